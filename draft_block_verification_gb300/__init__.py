@@ -81,6 +81,15 @@ def lib():
         L.sv_packed_topk_step.argtypes = [vp, vp, i32, i64, i32, i32, i32, i32, i32, i32, vp, vp,
                                           vp, vp, vp, f32, u64, u64, vp, i32, vp, vp, vp, vp, vp,
                                           vp, vp, vp, vp, vp, vp]
+        L.sv_kv_plan.restype = i32
+        L.sv_kv_plan.argtypes = [vp] + [i32] * 5 + [vp] * 13
+        L.sv_kv_append.restype = i32
+        L.sv_kv_append.argtypes = ([vp] * 3 + [i32] + [i64] * 4 + [i32] * 5 + [vp] * 6)
+        L.sv_kv_attention.restype = i32
+        L.sv_kv_attention.argtypes = ([vp] * 2 + [i64] * 2 + [i32] * 4 + [vp] * 4 + [i32] * 2 +
+                                      [vp, i32] + [vp] * 2 + [i32, vp, i32, f32] + [vp] * 3)
+        L.sv_sample_rows.restype = i32
+        L.sv_sample_rows.argtypes = [vp, vp, i32, i64, i32, i32] + [vp] * 9
         _lib = L
     return _lib
 
@@ -446,3 +455,145 @@ def sv_packed_topk_step(logits, K, W, kp, kq, prev_draft, prev_len, prev_q_ids, 
         _stream(stream, dev)), "sv_packed_topk_step")
     return out
 
+
+
+def _dense(t, dtype, shape, name, dev):
+    """Address of a contiguous tensor of this type and shape (None: any)."""
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor on %s" % (name, dtype, dev))
+    if len(shape) != t.dim() or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError("%s must have shape %s" % (name, shape))
+    return t.data_ptr()
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.device
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def sv_kv_plan(cached_len, new_len, held, table, free_ids, free_pos, block, max_tokens, *,
+               handle=None, stream=None):
+    """Places of new tokens in the paged cache (see sv.h): cached_len, new_len,
+    held [B] and table [B, cols], free_ids [ring] int32; free_pos [2] int64.
+    Updates table and free_ids in place and returns a dict of new tensors
+    (kv_len, cu_new, held, free_pos, slot, pos)."""
+    dev = _cuda(cached_len, "cached_len")
+    B = cached_len.shape[0]
+    i32 = torch.int32
+    h = handle or default_handle(dev)
+    out = {"kv_len": torch.empty(B, dtype=i32, device=dev),
+           "cu_new": torch.empty(B + 1, dtype=i32, device=dev),
+           "held": torch.empty(B, dtype=i32, device=dev),
+           "free_pos": torch.empty(2, dtype=torch.int64, device=dev),
+           "slot": torch.empty(int(max_tokens), dtype=i32, device=dev),
+           "pos": torch.empty(int(max_tokens), dtype=i32, device=dev)}
+    _check(lib().sv_kv_plan(
+        h.ptr, B, int(block), table.shape[1], free_ids.shape[0], int(max_tokens),
+        _dense(cached_len, i32, (B,), "cached_len", dev),
+        _dense(new_len, i32, (B,), "new_len", dev), _dense(held, i32, (B,), "held", dev),
+        _dense(free_pos, torch.int64, (2,), "free_pos", dev),
+        _dense(free_ids, i32, (None,), "free_ids", dev),
+        _dense(table, i32, (B, None), "table", dev), out["kv_len"].data_ptr(),
+        out["cu_new"].data_ptr(), out["held"].data_ptr(), out["free_pos"].data_ptr(),
+        out["slot"].data_ptr(), out["pos"].data_ptr(), _raw_stream(stream, dev)), "sv_kv_plan")
+    return out
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
+    """Shape (pages, Hkv, block, D) and addresses of a paged cache."""
+    if k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("k_cache must be float8_e4m3fn or uint8")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, Hkv, block, D]")
+    shape = tuple(k_cache.shape)
+    return shape, (_dense(k_cache, k_cache.dtype, shape, "k_cache", dev),
+                   _dense(v_cache, k_cache.dtype, shape, "v_cache", dev),
+                   _dense(k_scale, torch.float32, shape[:2], "k_scale", dev),
+                   _dense(v_scale, torch.float32, shape[:2], "v_scale", dev))
+
+
+def sv_kv_append(k, v, slot, k_cache, v_cache, k_scale, v_scale, *, handle=None, stream=None):
+    """Write k, v [T, Hkv, D] (float32 or bfloat16) to the cache's slots
+    slot [T] int32 in place (see sv.h); caches [pages, Hkv, block, D]
+    float8_e4m3fn, scales [pages, Hkv] float32."""
+    dev = _cuda(k, "k")
+    (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
+    if k.dtype != v.dtype or v.device != dev or k.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("k and v must both be bfloat16 or float32, on one device")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v: the last dimension must be contiguous")
+    h = handle or default_handle(dev)
+    _check(lib().sv_kv_append(
+        h.ptr, k.data_ptr(), v.data_ptr(), SV_BF16 if k.dtype == torch.bfloat16 else SV_F32,
+        k.stride(0), k.stride(1), v.stride(0), v.stride(1), T, H, D, block, pages,
+        _dense(slot, torch.int32, (T,), "slot", dev), *cache, _raw_stream(stream, dev)),
+        "sv_kv_append")
+
+
+def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new, *, scale=None,
+                    mask=None, want_lse=False, handle=None, stream=None):
+    """Attention of the new tokens' queries q [T, Hq, D] (bfloat16) over the
+    paged cache (see sv.h); table [B, cols], kv_len [B], cu_new [B + 1] int32;
+    mask [T, words] int32 bits over the sequence's new tokens, or None for
+    causal.  scale defaults to D ** -0.5.  Returns a dict (out, and lse)."""
+    dev = _cuda(q, "q")
+    (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+        raise ValueError("q must be a bfloat16 [T, Hq, D] tensor with the cache's D, contiguous "
+                         "in its last dimension")
+    T, Hq, _ = q.shape
+    B = kv_len.shape[0]
+    i32 = torch.int32
+    words = 0
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError("mask must be [T, words]")
+        words = mask.shape[1]
+    h = handle or default_handle(dev)
+    out = {"out": torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)}
+    if want_lse:
+        out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    _check(lib().sv_kv_attention(
+        h.ptr, q.data_ptr(), q.stride(0), q.stride(1), T, Hq, H, D, *cache, block, pages,
+        _dense(table, i32, (B, None), "table", dev), table.shape[1],
+        _dense(kv_len, i32, (B,), "kv_len", dev), _dense(cu_new, i32, (B + 1,), "cu_new", dev), B,
+        None if mask is None else _dense(mask, i32, (T, words), "mask", dev), words,
+        float(D ** -0.5 if scale is None else scale), out["out"].data_ptr(),
+        out["lse"].data_ptr() if want_lse else None, _raw_stream(stream, dev)),
+        "sv_kv_attention")
+    return out
+
+
+def sv_sample_rows(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
+                   handle=None, stream=None):
+    """One draw from each row of logits [R, V] with the filters of sv.h; u,
+    temperature, top_p, min_p [R] float32 and top_k [R] int32 (None: off; for
+    the temperature 1).  Returns a dict (token, prob, kept)."""
+    dev = _cuda(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [R, V]")
+    code, rs = _rows(logits, "logits")
+    R, V = logits.shape
+    f32 = torch.float32
+    opt = lambda t, dt, n: None if t is None else _dense(t, dt, (R,), n, dev)
+    h = handle or default_handle(dev)
+    out = {"token": torch.empty(R, dtype=torch.int32, device=dev),
+           "prob": torch.empty(R, dtype=f32, device=dev),
+           "kept": torch.empty(R, dtype=torch.int32, device=dev)}
+    _check(lib().sv_sample_rows(
+        h.ptr, logits.data_ptr(), code, rs if R > 1 else max(rs, V), R, V,
+        _dense(u, f32, (R,), "u", dev), opt(temperature, f32, "temperature"),
+        opt(top_k, torch.int32, "top_k"), opt(top_p, f32, "top_p"), opt(min_p, f32, "min_p"),
+        out["token"].data_ptr(), out["prob"].data_ptr(), out["kept"].data_ptr(),
+        _raw_stream(stream, dev)), "sv_sample_rows")
+    return out

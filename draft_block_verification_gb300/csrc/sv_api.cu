@@ -10,6 +10,8 @@
 
 #include "sv_gumbel.cuh"
 #include "sv_job.cuh"
+#include "sv_kv.cuh"
+#include "sv_rows.cuh"
 #include "sv_topk.cuh"
 
 namespace sv {
@@ -249,6 +251,16 @@ bool logits_ok(const void *p, sv_dtype dt, int64_t rs, int V)
     return true;
 }
 
+// Page sizes of the cache, and a cache's pointers.
+bool kv_block_ok(int block)
+{
+    return block == 16 || block == 32 || block == 64 || block == 128;
+}
+bool kv_cache_ok(const void *cache, const float *scale)
+{
+    return cache && scale && aligned16(cache);
+}
+
 void fill_common(Job &j, sv_handle *h, const void *src0, sv_dtype dt, int64_t rs, int V)
 {
     memset(&j, 0, sizeof j);
@@ -400,6 +412,8 @@ sv_status sv_create(sv_handle **out)
     int sb = 0;
     if (e == cudaSuccess) e = seed_setup(&sb);
     h->seed_blocks = std::max(1, sb);
+    if (e == cudaSuccess) e = plan_setup();
+    if (e == cudaSuccess) e = rows_setup();
     if (e == cudaSuccess) e = cudaMalloc(&h->d_err, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_ctl, C_NCTL * sizeof(unsigned));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_gtab, kGTab * sizeof(float));
@@ -863,6 +877,108 @@ sv_status sv_packed_topk_step(sv_handle *h, const void *logits, sv_dtype dtype,
     if (h->timing) cudaEventRecord(h->ev[1], s);
     if (e == cudaSuccess) e = topk_decide_launch(t, s);
     return cuda_status(e);
+}
+
+sv_status sv_kv_plan(sv_handle *h, int B, int block, int cols, int ring, int max_tokens,
+                     const int32_t *cached_len, const int32_t *new_len, const int32_t *held,
+                     const int64_t *free_pos, int32_t *free_ids, int32_t *table, int32_t *kv_len,
+                     int32_t *cu_new, int32_t *held_out, int64_t *free_pos_out, int32_t *slot,
+                     int32_t *pos, void *stream)
+{
+    if (!h || B < 0 || cols < 1 || ring < 1 || max_tokens < 0 || !kv_block_ok(block))
+        return SV_ERR_INVALID_ARG;
+    if (!free_pos || !free_ids || !cu_new || !free_pos_out ||
+        (B > 0 && (!cached_len || !new_len || !held || !table || !kv_len || !held_out)) ||
+        (max_tokens > 0 && (!slot || !pos)))
+        return SV_ERR_INVALID_ARG;
+    // these are read by every CTA while others write the outputs
+    if (free_pos_out == free_pos || (B > 0 && (held_out == held || kv_len == cached_len)))
+        return SV_ERR_INVALID_ARG;
+    if (B > kPlanMaxB) return SV_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_kv_plan")) return fi;
+    PlanJob j = {B, block, cols, ring, max_tokens, cached_len, new_len, held, free_pos, free_ids,
+                 table, kv_len, cu_new, held_out, free_pos_out, slot, pos, h->d_err};
+    return cuda_status(plan_launch(j, h->sms, (cudaStream_t)stream));
+}
+
+sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtype,
+                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, int T, int H, int D, int block, int pages,
+                       const int32_t *slot, void *k_cache, void *v_cache, float *k_scale,
+                       float *v_scale, void *stream)
+{
+    if (!h || T < 0 || H < 1 || pages < 1 || !kv_block_ok(block)) return SV_ERR_INVALID_ARG;
+    if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SV_ERR_UNSUPPORTED;
+    if (H > 32767 || (int64_t)pages * block > 0x7FFFFFFF) return SV_ERR_UNSUPPORTED;
+    if (!kv_cache_ok(k_cache, k_scale) || !kv_cache_ok(v_cache, v_scale))
+        return SV_ERR_INVALID_ARG;
+    if (T == 0) return SV_OK;
+    const int esz = dtype == SV_BF16 ? 2 : 4;
+    if (!k || !v || !slot || (uintptr_t)k % esz || (uintptr_t)v % esz || k_token_stride < 0 ||
+        k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+        return SV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_kv_append")) return fi;
+    AppendJob j = {{(const char *)k, (const char *)v},
+                   {k_token_stride * esz, v_token_stride * esz},
+                   {k_head_stride * esz, v_head_stride * esz},
+                   dtype, T, H, D, block, pages, slot,
+                   {(uint8_t *)k_cache, (uint8_t *)v_cache},
+                   {k_scale, v_scale}, h->d_err};
+    return cuda_status(append_launch(j, h->sms, (cudaStream_t)stream));
+}
+
+sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, int T, int Hq, int H, int D,
+                          const void *k_cache, const void *v_cache, const float *k_scale,
+                          const float *v_scale, int block, int pages, const int32_t *table,
+                          int cols, const int32_t *kv_len, const int32_t *cu_new, int B,
+                          const uint32_t *mask, int mask_words, float scale, void *out,
+                          float *lse, void *stream)
+{
+    if (!h || T < 0 || B < 0 || Hq < 1 || H < 1 || Hq % H || pages < 1 || cols < 1 ||
+        !kv_block_ok(block))
+        return SV_ERR_INVALID_ARG;
+    if (!isfinite(scale) || q_token_stride < 0 || q_head_stride < 0 ||
+        (mask && mask_words < 1))
+        return SV_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SV_ERR_UNSUPPORTED;
+    if ((int64_t)T * Hq > 0x7FFFFFFF || (int64_t)pages * block > 0x7FFFFFFF ||
+        (int64_t)cols * block > 0x7FFFFFFF)
+        return SV_ERR_UNSUPPORTED;
+    if (!kv_cache_ok(k_cache, k_scale) || !kv_cache_ok(v_cache, v_scale))
+        return SV_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return SV_OK;
+    if (!q || !table || !kv_len || !cu_new || !out || (uintptr_t)q % 2 || !aligned16(out))
+        return SV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_kv_attention")) return fi;
+    AttendJob j = {(const uint16_t *)q, q_token_stride, q_head_stride,
+                   {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
+                   {k_scale, v_scale}, table, kv_len, cu_new, mask, B, T, Hq, H, Hq / H, D,
+                   block, pages, cols, mask_words, scale, (uint16_t *)out, lse, h->d_err};
+    return cuda_status(attend_launch(j, h->sms, (cudaStream_t)stream));
+}
+
+sv_status sv_sample_rows(sv_handle *h, const void *logits, sv_dtype dtype, int64_t row_stride,
+                         int R, int V, const float *u, const float *temperature,
+                         const int32_t *top_k, const float *top_p, const float *min_p,
+                         int32_t *token, float *prob, int32_t *kept, void *stream)
+{
+    if (!h || R < 0 || V < 1 || row_stride < V) return SV_ERR_INVALID_ARG;
+    if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (V > kRowsMaxV) return SV_ERR_UNSUPPORTED;
+    if (R == 0) return SV_OK;
+    const int esz = dtype == SV_BF16 ? 2 : 4;
+    if (!logits || (uintptr_t)logits % esz || !u || !token || !prob || !kept)
+        return SV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_sample_rows")) return fi;
+    RowsJob j = {(const char *)logits, row_stride * esz, dtype, R, V, u, temperature, top_k,
+                 top_p, min_p, token, kept, prob, h->d_err};
+    return cuda_status(rows_launch(j, h->sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -49,7 +49,8 @@
  *   each listed entry point (sv_create, sv_verify_greedy,
  *   sv_verify_greedy_static, sv_verify_sample, sv_verify_tree,
  *   sv_verify_spot, sv_packed_step, sv_packed_topk_step,
- *   sv_packed_anyorder_step) return the
+ *   sv_packed_anyorder_step, sv_kv_plan, sv_kv_append, sv_kv_attention,
+ *   sv_sample_rows) return the
  *   status `code` (1..6) at its launch point,
  *   after its argument checks and before anything is enqueued.  It is read
  *   at every call; unset, nothing is injected.
@@ -377,6 +378,124 @@ sv_status sv_packed_anyorder_step(sv_handle *h, const void *logits, sv_dtype dty
                                   int32_t *accept_len, int32_t *commit_len, int32_t *commit_pos,
                                   int32_t *commit_tok, int32_t *end_out, int32_t *next_draft,
                                   float *score, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged 8-bit key/value cache.  Between two verify calls a draft block is
+ * given its places (sv_kv_plan), its keys and values are written
+ * (sv_kv_append) and its queries read the cache (sv_kv_attention).
+ *
+ * A cache is [pages, Hkv, block, D] bytes (e4m3; keys and values apart, bases
+ * 16-byte aligned) with fp32 scales [pages, Hkv]: the value of a byte is its
+ * e4m3 value times its page's and head's scale.  block is 16, 32, 64 or 128;
+ * D is 64 or 128; pages * block <= 2^31 - 1 (offsets are 64-bit throughout).
+ * Sequence b's token at position p is row p % block of page
+ * table[b, p / block] of the int32 table [B, cols]; its slot is
+ * table[b, p / block] * block + p % block.
+ *
+ * sv_kv_plan.  Sequence b has cached_len[b] tokens in the cache, holds
+ * held[b] pages (table[b, 0 .. held)), and gets new_len[b] tokens.  It needs
+ * w = ceil((cached_len + new_len) / block) pages: it takes what is missing
+ * from the queue of free pages, or gives back what is over (drafts that were
+ * rejected; a sequence that ended, both lengths 0).  The queue holds
+ * free_ids[i mod ring] for free_pos[0] <= i < free_pos[1] (int64 [2]); pages
+ * are taken at its front and given at its end, in order of b, then of the
+ * place in the table; pages given in a call are taken by later calls only.
+ * Outputs:
+ *   kv_len [B] cached_len + new_len;  cu_new [B + 1] exclusive sums of
+ *   new_len;  held_out [B] w;  free_pos_out [2];
+ *   slot, pos [max_tokens] slot and position of each new token, in order of
+ *   b, then position; -1 beyond cu_new[B].
+ *   table (in place): entries [held, w) are written; those from w on are dead.
+ *   free_ids (in place): written only outside the queue.
+ * held_out, free_pos_out and kv_len must not be held, free_pos and cached_len
+ * themselves.  So a call whose outputs were dropped may be repeated.
+ * A call that cannot be served changes nothing (outputs: kv_len = cached_len,
+ * held_out = held, free_pos_out = free_pos, cu_new = 0, slot = pos = -1) and
+ * latches SV_ERR_OOM (too few free pages) or SV_ERR_DEVICE_BOUNDS (a negative
+ * length, held or w beyond cols, more than max_tokens new tokens, a queue
+ * that does not fit its ring).
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED for B > 16384.
+ * ------------------------------------------------------------------------- */
+sv_status sv_kv_plan(sv_handle *h, int B, int block, int cols, int ring, int max_tokens,
+                     const int32_t *cached_len, const int32_t *new_len, const int32_t *held,
+                     const int64_t *free_pos, int32_t *free_ids, int32_t *table, int32_t *kv_len,
+                     int32_t *cu_new, int32_t *held_out, int64_t *free_pos_out, int32_t *slot,
+                     int32_t *pos, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_kv_append.  Writes k, v [T, H, D] (fp32 or bf16, strides in elements, D
+ * contiguous) to the slots slot [T]; a negative slot is skipped.  Tokens with
+ * consecutive slots in one page form a run; a call writes each page with one
+ * run at most, and what the page holds after the run is dead.
+ *   Scale of a page and head: the least power of two s in [2^-40, 2^40] with
+ *   |x| <= 448 s over the run (NaN aside), and, when the run starts past the
+ *   page's first row, at least the scale it had.  Where that grows, the rows
+ *   before the run are rounded again at the new scale.  Bytes: round to
+ *   nearest even, saturating at 448; NaN stays NaN.
+ * Writing the same tokens to the same slots again changes nothing.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D, H > 32767); a slot
+ * beyond the cache latches SV_ERR_DEVICE_BOUNDS and is skipped.
+ * ------------------------------------------------------------------------- */
+sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtype,
+                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, int T, int H, int D, int block, int pages,
+                       const int32_t *slot, void *k_cache, void *v_cache, float *k_scale,
+                       float *v_scale, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_kv_attention.  q [T, Hq, D] bf16 (strides in elements, D contiguous);
+ * rows cu_new[b] .. cu_new[b+1] - 1 are sequence b's n_b new tokens, the last
+ * n_b of its kv_len[b] tokens, all in the cache.  Query head g reads cache
+ * head g / (Hq / H).  Token i sees
+ *   mask == NULL: the positions up to its own;
+ *   mask [T, mask_words]: every position before the new tokens, and new token
+ *     j where bit j % 32 of word j / 32 of its row is set (draft trees; a
+ *     token's own bit counts like any other).
+ *   out [T, Hq, D] bf16 (16-byte aligned) = softmax(scale q.k) v; 0 where a
+ *     token sees nothing.  Softmax and sums are fp32.
+ *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
+ *     where a token sees nothing.
+ * Rows from cu_new[B] on are not written.  Bytes past kv_len may hold
+ * anything; those of visible tokens are finite, with scales in [2^-40, 2^40].
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D); latched
+ * SV_ERR_DEVICE_BOUNDS for lengths or pages out of range (the sequence's
+ * output is then not meaningful).
+ * ------------------------------------------------------------------------- */
+sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
+                          int64_t q_head_stride, int T, int Hq, int H, int D,
+                          const void *k_cache, const void *v_cache, const float *k_scale,
+                          const float *v_scale, int block, int pages, const int32_t *table,
+                          int cols, const int32_t *kv_len, const int32_t *cu_new, int B,
+                          const uint32_t *mask, int mask_words, float scale, void *out,
+                          float *lse, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_sample_rows.  One draw from each of R logit rows (any V <= 2^20, any row
+ * stride >= V; rows that start on 16 bytes are read in vectors).  With the
+ * row's maximum m, w_v = exp((x_v - m) / T); tokens are ordered by logit, the
+ * lower id first among equals, and each filter keeps a prefix:
+ *   top_k  the first k (0, or k >= V: off);
+ *   top_p  the shortest whose weight reaches p times the weight of the top k
+ *          (p >= 1: off; at least one token);
+ *   min_p  the tokens with w_v >= min_p (0: off).
+ * The shortest is kept, and the draw is the first kept token by id whose
+ * running weight exceeds u times the kept weight.  T = 0: the argmax, lowest
+ * id on ties.  -inf and NaN logits are never kept; +inf logits share all the
+ * weight.
+ *   u [R] in [0, 1];  temperature, top_k, top_p, min_p [R], each or NULL for
+ *   1, off, off, off.
+ *   token [R] (-1: the row has no finite logit);  prob [R] the token's share
+ *   of the kept weight;  kept [R] the number of kept tokens.
+ * Ranks, weights and the draw are decided exactly (weights to 2^-44).
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (V); a row whose parameters
+ * are out of range (u outside [0, 1], a negative or NaN filter, min_p > 1,
+ * T < 2^-20 other than 0, T infinite) gets token -1, prob NaN, kept 0 and
+ * latches SV_ERR_DEVICE_BOUNDS.
+ * ------------------------------------------------------------------------- */
+sv_status sv_sample_rows(sv_handle *h, const void *logits, sv_dtype dtype, int64_t row_stride,
+                         int R, int V, const float *u, const float *temperature,
+                         const int32_t *top_k, const float *top_p, const float *min_p,
+                         int32_t *token, float *prob, int32_t *kept, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Options (testing and measurement).
