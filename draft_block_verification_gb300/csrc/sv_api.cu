@@ -50,6 +50,7 @@ struct sv_handle {
     unsigned *cnt = nullptr;  // completion counters: always zero between calls
     int cnt_B = 0;            // sequences the counter arena holds
     int force_rescue = 0;
+    char *kv_ws = nullptr;    // sv_kv_attention's partial sums and counters
     cudaEvent_t ev[2] = {nullptr, nullptr};  // caller-owned (SV_OPT_TIMING_EVENTS)
     bool timing = false;
     std::mutex mu;
@@ -414,6 +415,7 @@ sv_status sv_create(sv_handle **out)
     h->seed_blocks = std::max(1, sb);
     if (e == cudaSuccess) e = plan_setup();
     if (e == cudaSuccess) e = rows_setup();
+    if (e == cudaSuccess) e = attend_setup();
     if (e == cudaSuccess) e = cudaMalloc(&h->d_err, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_ctl, C_NCTL * sizeof(unsigned));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_gtab, kGTab * sizeof(float));
@@ -445,6 +447,7 @@ sv_status sv_destroy(sv_handle *h)
     cudaDeviceSynchronize();
     if (h->ws) cudaFree(h->ws);
     if (h->cnt) cudaFree(h->cnt);
+    if (h->kv_ws) cudaFree(h->kv_ws);
     if (h->d_err) cudaFree(h->d_err);
     if (h->d_ctl) cudaFree(h->d_ctl);
     if (h->d_gtab) cudaFree(h->d_gtab);
@@ -472,6 +475,7 @@ sv_status sv_sync_status(sv_handle *h, void *stream)
         cudaMemset(h->d_ctl, 0, C_NCTL * sizeof(unsigned));
         cudaMemcpy(h->d_ctl + C_RESCUED, &keep, sizeof(unsigned), cudaMemcpyHostToDevice);
         if (h->cnt) cudaMemset(h->cnt, 0, (size_t)h->cnt_B * kCntPerSeq * sizeof(unsigned));
+        if (h->kv_ws) cudaMemset(h->kv_ws, 0, attend_counter_bytes(h->sms));
         cudaDeviceSynchronize();
     }
     return (sv_status)code;
@@ -946,7 +950,7 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
         return SV_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return SV_ERR_UNSUPPORTED;
     if ((int64_t)T * Hq > 0x7FFFFFFF || (int64_t)pages * block > 0x7FFFFFFF ||
-        (int64_t)cols * block > 0x7FFFFFFF)
+        (int64_t)cols * block > 0x7FFFFFFF || (int64_t)pages * H > 0x7FFFFFFF)
         return SV_ERR_UNSUPPORTED;
     if (!kv_cache_ok(k_cache, k_scale) || !kv_cache_ok(v_cache, v_scale))
         return SV_ERR_INVALID_ARG;
@@ -955,11 +959,31 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
         return SV_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_attention")) return fi;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (!h->kv_ws) {
+        // once a handle; an allocation does not belong into a captured graph
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(s, &cap);
+        if (e != cudaSuccess) return cuda_status(e);
+        if (cap != cudaStreamCaptureStatusNone) return SV_ERR_UNSUPPORTED;
+        void *p = nullptr;
+        const size_t n = attend_counter_bytes(h->sms);
+        e = cudaMalloc(&p, n + attend_ws_bytes(h->sms));
+        if (e != cudaSuccess) return cuda_status(e);
+        e = cudaMemsetAsync(p, 0, n, s);
+        if (e != cudaSuccess) {
+            cudaFree(p);
+            return cuda_status(e);
+        }
+        h->kv_ws = (char *)p;
+    }
     AttendJob j = {(const uint16_t *)q, q_token_stride, q_head_stride,
                    {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
                    {k_scale, v_scale}, table, kv_len, cu_new, mask, B, T, Hq, H, Hq / H, D,
-                   block, pages, cols, mask_words, scale, (uint16_t *)out, lse, h->d_err};
-    return cuda_status(attend_launch(j, h->sms, (cudaStream_t)stream));
+                   block, pages, cols, mask_words, scale, (uint16_t *)out, lse,
+                   (float *)(h->kv_ws + attend_counter_bytes(h->sms)), (unsigned *)h->kv_ws,
+                   h->d_err};
+    return cuda_status(attend_launch(j, h->sms, s));
 }
 
 sv_status sv_sample_rows(sv_handle *h, const void *logits, sv_dtype dtype, int64_t row_stride,

@@ -51,8 +51,13 @@ struct AttendJob {
     float softmax_scale;
     uint16_t *out;             // [T, Hq, D]
     float *lse;                // [T, Hq] or null
+    float *part;               // partial sums of shared units (workspace)
+    unsigned *arrived;         // a counter a CTA, zero between calls
     int *err;
 };
+size_t attend_ws_bytes(int sms);       // partial sums
+size_t attend_counter_bytes(int sms);  // counters, before them
+cudaError_t attend_setup();
 cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s);
 
 }  // namespace sv

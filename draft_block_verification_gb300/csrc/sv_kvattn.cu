@@ -7,92 +7,908 @@
 //   o = sum_p w_p (v_p s^v) / sum_p w_p
 // over the positions it sees: those up to its own, or, with a mask, every
 // position before the new tokens and the new tokens whose bit is set.
+//
+// Shape of the work.  A sequence's n_b G query rows of one cache head read the
+// same keys and values, so they are handled together, up to 128 at a time.
+// Reading the cache bounds the call up to about 64 rows a head (256 bytes a
+// token and head at D = 128); the tensor cores take both products:
+//   S^T [128 tokens x N rows] = K Q^T     (K is the A operand, as it lies)
+//   O^T [D x N rows]         += V^T P^T   (V is the A operand, as it lies)
+// With tokens and head elements on the 128 rows of the product, N is the number
+// of query rows rounded to 16: a single token pays for 16 rows, not for 128.
+//
+// The cache's bytes go from TMA to the tensor cores untouched (e4m3); so the
+// other operand is e4m3 as well, in two parts.  A bf16 query (8 significant
+// bits, scaled by a power of two per row) is the sum of two e4m3 values (4 bits
+// each): q = hi + lo exactly, up to 2^-19 of the row's largest element.  A
+// weight p is rounded to hi + lo with a relative error of 2^-8 at most (2^-10
+// in the mean square), down to 2^-22 of the largest; lo carries a scale of its
+// own and accumulates apart.  Sums, maxima and the rescaling are fp32.
+//
+// Scales of pages differ from token to token, which is a row of S^T: the key's
+// scale multiplies there, and the value's scale goes into the exponent,
+//   w'_p = 2^(z_p log2 e + log2 s^v_p - M),  M = max over the same sum,
+// so that O needs no scale; the sum of weights takes w'_p / s^v_p.
+//
+// Split.  The tiles (128 tokens of one unit: sequence, head, row block) of the
+// whole call, laid end to end, are cut into equal spans, one per CTA of one
+// wave.  A unit that several CTAs share leaves partial sums in the workspace;
+// the last of them to finish joins them in the order of the CTAs, so the result
+// does not depend on who that is.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "sv_common.cuh"
 #include "sv_kv.cuh"
 
 namespace sv {
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t v)
+constexpr int kTile = 128;             // tokens of a tile
+constexpr int kRowsMax = 128;          // query rows of a unit
+constexpr int kAtStages = 4;           // tiles in flight
+constexpr int kSoftWarps = 8;          // two warpgroups, each half of the rows
+constexpr int kAtThreads = kSoftWarps * 32 + 64;  // + producer and issuer
+constexpr float kNone = -1e30f;        // running maximum before any token
+constexpr uint32_t kAtSpin = 1u << 20; // tries of a wait (a tile takes microseconds)
+
+struct AttnShared {
+    uint64_t full_k[kAtStages], full_v[kAtStages], empty_k[kAtStages], empty_v[kAtStages];
+    uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, drained;
+    uint32_t tmem;
+    int abort;
+    int last;                          // this CTA joins the unit's parts
+    int first_b;
+    long long first_x, total;          // the span's first tile in sequence first_b; all tiles
+    float ks[kAtStages][8], vs[kAtStages][8];  // scales of the tile's pages
+    float c[kRowsMax];                 // factor from S to log2 units, per row
+    float wmax[2][kSoftWarps][64];     // tile maxima per warp and row
+    float mu[kSoftWarps][64];          // running maximum in use, per warp
+    float sum[4][kRowsMax];            // sums of weights per quarter of a tile
+    long long scan[kAtThreads / 32];
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05 wrappers.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_after()
 {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-    return __low2float(*reinterpret_cast<__half2 *>(&h));
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_ld8(uint32_t addr, float *v)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const float *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                     addr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])),
+                 "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+                 "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
+// The registers of the loads before it may be read after it: they pass through.
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(float (&v)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tc_wait_st()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-constexpr int kAttThreads = 128;
-
-// One warp per token and query head, the head's elements over the lanes.
-template <int D>
-__global__ void __launch_bounds__(kAttThreads) attend_kernel(const AttendJob j)
+// Shared-memory operand descriptors.  layout: 2 = 128-byte swizzle, 4 = 64-byte.
+// Operands whose products' dimension is contiguous: stride = 8 rows.  Operands
+// whose rows (tokens) are the products' dimension: stride = 8 tokens, lead =
+// the next 128 (64) bytes of the other dimension.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead, uint32_t stride,
+                                            uint32_t layout)
 {
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (kAttThreads / 32) + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_trigger();
-    const int t = (int)(item / j.Hq), g = (int)(item % j.Hq);
-    if (t >= j.T) return;
-    int lo = 0, hi = j.B;  // the last b with cu[b] <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (j.cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int b = lo;
-    const int n = j.cu[b + 1] - j.cu[b], L = j.kv_len[b], ctx = L - n, i = t - j.cu[b];
-    if (i >= n || i < 0) return;
-    bool bad = ctx < 0 || (long long)(L + j.block - 1) / j.block > j.cols;
-    float q[N], o[N];
-    for (int k = 0; k < N; ++k) {
-        q[k] = __uint_as_float((uint32_t)j.q[t * j.qts + g * j.qhs + lane + 32 * k] << 16) *
-               j.softmax_scale * 1.4426950408889634f;
-        o[k] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    const int h = g / j.G;
-    for (int p = 0; p < (bad ? 0 : L); ++p) {
-        bool sees = p <= ctx + i;
-        if (j.mask && p >= ctx) {
-            const int k = p - ctx;
-            sees = k < 32 * j.words && ((j.mask[(int64_t)t * j.words + (k >> 5)] >> (k & 31)) & 1);
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lead >> 4) & 0x3FFF) << 16) |
+           ((uint64_t)((stride >> 4) & 0x3FFF) << 32) | (1ull << 46) | ((uint64_t)layout << 61);
+}
+
+__device__ __forceinline__ void fence_async()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Barrier over `n` threads with an or over a flag.
+__device__ __forceinline__ bool bar_or(int id, int n, bool flag)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+        " barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"((uint32_t)flag), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+// Bounded wait that also ends when another role has given up.
+__device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < kAtSpin; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if ((i & 63) == 63) {
+            if (*(volatile int *)&sh->abort) return false;
+            __nanosleep(64);
         }
-        if (!sees) continue;
-        const int page = j.table[(int64_t)b * j.cols + p / j.block];
-        if (page < 0 || page >= j.pages) {
-            bad = true;
+    }
+    *(volatile int *)&sh->abort = 1;
+    latch(err, SV_ERR_TIMEOUT);
+    return false;
+}
+
+// ---------------------------------------------------------------------------
+// The units of a call.
+// ---------------------------------------------------------------------------
+struct SeqWork {
+    int n, L, first;         // new tokens, tokens, first row of q
+    int tiles, blocks, rows; // tiles of a unit, row blocks, rows of a block
+    long long work;          // tiles of the sequence
+    bool bad;
+};
+__device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
+{
+    SeqWork s;
+    s.first = j.cu[b];
+    const int end = j.cu[b + 1];
+    s.L = j.kv_len[b];
+    s.n = end - s.first;
+    s.bad = s.first < 0 || end > j.T || s.n < 0 || s.L < s.n ||
+            (s.L + (long long)j.block - 1) / j.block > j.cols;
+    if (s.bad) s.n = 0;
+    const long long all = (long long)s.n * j.G;
+    s.tiles = (int)(((long long)s.L + kTile - 1) / kTile);
+    s.blocks = (int)((all + kRowsMax - 1) / kRowsMax);
+    s.rows = s.blocks ? (int)((all + s.blocks - 1) / s.blocks) : 0;
+    s.work = (long long)s.tiles * s.blocks * j.H;
+    return s;
+}
+
+// A CTA's share of one unit, walked alike by every role.
+struct Piece {
+    int b, h, row0, rows;    // sequence, cache head, first row (of n G) and rows
+    int t0, t1, tiles;       // tiles [t0, t1) of the unit's
+    long long unit0;         // the unit's first tile in the call's order
+    int L, n, first;
+};
+struct PieceWalk {
+    long long pos, end, x;   // next tile, the span's end, next tile within b
+    int b;
+    SeqWork s;
+    __device__ __forceinline__ void start(const AttendJob &j, const AttnShared *sh,
+                                          long long from, long long to)
+    {
+        pos = from;
+        end = to;
+        b = sh->first_b;
+        x = sh->first_x;
+        if (pos < end) s = seq_work(j, b);
+    }
+    __device__ __forceinline__ bool next(const AttendJob &j, Piece &p)
+    {
+        if (pos >= end) return false;
+        while (x >= s.work) {
+            x -= s.work;
+            s = seq_work(j, ++b);
+        }
+        const long long u = x / s.tiles;
+        p.t0 = (int)(x - u * s.tiles);
+        const long long left = end - pos;
+        p.t1 = (int)(s.tiles - p.t0 < left ? s.tiles : p.t0 + left);
+        p.b = b;
+        p.h = (int)(u / s.blocks);
+        p.row0 = (int)(u - (long long)p.h * s.blocks) * s.rows;
+        p.rows = min(s.rows, s.n * j.G - p.row0);
+        p.tiles = s.tiles;
+        p.unit0 = pos - p.t0;
+        p.L = s.L;
+        p.n = s.n;
+        p.first = s.first;
+        pos += p.t1 - p.t0;
+        x += p.t1 - p.t0;
+        return true;
+    }
+};
+
+// Span of CTA i of `ctas` over `total` tiles, and the CTA that owns a tile.
+__device__ __forceinline__ long long span_at(long long total, int ctas, int i)
+{
+    return total * i / ctas;
+}
+__device__ __forceinline__ int span_owner(long long total, int ctas, long long x)
+{
+    int i = (int)(x * ctas / total);
+    while (i + 1 < ctas && span_at(total, ctas, i + 1) <= x) ++i;
+    while (i > 0 && span_at(total, ctas, i) > x) --i;
+    return i;
+}
+
+// Workspace of a CTA: two parts (its first and its last unit), each kRowsMax
+// rows of D sums, then the rows' maxima and sums of weights.
+__host__ __device__ constexpr size_t part_floats(int D) { return (size_t)kRowsMax * (D + 2); }
+
+// ---------------------------------------------------------------------------
+// Softmax side of one piece.  Thread: one token of the tile (TMEM lane) for
+// the weights, one head element for the output; C8 * 8 rows a warpgroup.
+// ---------------------------------------------------------------------------
+template <int D, int C8>
+__device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, char *smem_v,
+                                           char *smem_p, const Piece &pc, uint32_t &it,
+                                           int stage_bytes, int ctas, bool ok)
+{
+    constexpr int R = C8 * 8;      // rows of this warpgroup
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = warp >> 2, quarter = warp & 3;
+    const int tk = quarter * 32 + lane;
+    const uint32_t lanes = sh->tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t o_col = lanes + 256 + g * 2 * R;   // R hi columns, then R lo
+    const int ctx = pc.L - pc.n;
+    const int pages_in = tk / j.block;
+
+    float mu[2] = {kNone, kNone};  // rows lane and lane + 32 of this warpgroup
+    float l[R];
+#pragma unroll
+    for (int n = 0; n < R; ++n) l[n] = 0.f;
+
+    for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+        const int st = it % kAtStages, sb = it & 1;
+        ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
+        ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
+        tc_fence_after();
+        float y[R];
+#pragma unroll
+        for (int c = 0; c < C8; ++c) tc_ld8(lanes + sb * 128 + g * R + c * 8, y + c * 8);
+        tc_wait_ld(y);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->s_empty[sb]);
+
+        // log2 units, the value's scale included
+        const int p0 = t * kTile, pos = p0 + tk;
+        const float ks = sh->ks[st][pages_in];
+        const float vs = fminf(fmaxf(sh->vs[st][pages_in], 0x1p-60f), 0x1p60f);
+        const float vl = log2f(vs), ivs = 1.f / vs;
+        {
+            const float2 a2 = make_float2(ks, ks), v2 = make_float2(vl, vl);
+            const float *cr = sh->c + g * R;
+#pragma unroll
+            for (int n = 0; n < R; n += 4) {
+                const float4 c4 = *reinterpret_cast<const float4 *>(cr + n);
+                float2 u = make_float2(y[n] * c4.x, y[n + 1] * c4.y);
+                float2 w = make_float2(y[n + 2] * c4.z, y[n + 3] * c4.w);
+                u = fma2(u, a2, v2);
+                w = fma2(w, a2, v2);
+                y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
+            }
+        }
+        // tiles that reach the new tokens: which rows see this token
+        if (p0 + kTile > ctx || p0 + kTile > pc.L) {
+            unsigned long long sees = 0;
+            if (pos < pc.L) {
+                if (pos < ctx) {
+                    sees = ~0ull;
+                } else if (!j.mask) {
+                    // rows (row0 + n) / G >= pos - ctx
+                    const long long from = (long long)(pos - ctx) * j.G - pc.row0 - g * R;
+                    sees = from <= 0 ? ~0ull : from >= 64 ? 0ull : ~0ull << from;
+                } else {
+                    const int k = pos - ctx;
+                    if ((k >> 5) < j.words) {
+                        for (int n = 0; n < R; ++n) {
+                            const int row = pc.row0 + g * R + n;
+                            if (row < pc.row0 + pc.rows) {
+                                const int64_t tok = pc.first + row / j.G;
+                                const uint32_t m = j.mask[tok * j.words + (k >> 5)];
+                                sees |= (unsigned long long)((m >> (k & 31)) & 1u) << n;
+                            }
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < R; ++n)
+                if (!((sees >> n) & 1ull)) y[n] = -INFINITY;
+        }
+        // the tile's maximum of each row: over the warp's tokens, then four warps
+        float keep[2] = {kNone, kNone};
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            float m;
+            asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(y[n]));
+            if (lane == (n & 31)) keep[n >> 5] = m;
+        }
+        sh->wmax[it & 1][warp][lane] = keep[0];
+        if (R > 32) sh->wmax[it & 1][warp][lane + 32] = keep[1];
+        if (bar_or(1 + g, 128, !ok)) {
+            ok = false;
             break;
         }
-        const int64_t ph = (int64_t)page * j.H + h;
-        const int64_t at = (ph * j.block + p % j.block) * D + lane;
-        float z = 0.f;
-        for (int k = 0; k < N; ++k) z += q[k] * e4m3_to_f32(j.cache[0][at + 32 * k]);
-        z = warp_sum(z) * j.scale[0][ph];
-        const float top = fmaxf(m, z), c = ex2f(m - top), w = ex2f(z - top);
-        l = l * c + w;
-        m = top;
-        const float vs = j.scale[1][ph] * w;
-        for (int k = 0; k < N; ++k) o[k] = o[k] * c + vs * e4m3_to_f32(j.cache[1][at + 32 * k]);
+        float f[2] = {1.f, 1.f};
+        bool moved = false;
+#pragma unroll
+        for (int k = 0; k < (R > 32 ? 2 : 1); ++k) {
+            float m = mu[k];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, sh->wmax[it & 1][g * 4 + w][lane + 32 * k]);
+            if (lane + 32 * k < R && m > mu[k]) {
+                f[k] = ex2f(mu[k] - m);
+                mu[k] = m;
+                moved = true;
+            }
+            sh->mu[warp][lane + 32 * k] = mu[k] - 8.f;  // weights in units of 2^-8
+        }
+        moved = __any_sync(0xFFFFFFFFu, moved);  // (orders the writes of mu as well)
+        __syncwarp();
+        if (t > pc.t0) ok = ok && at_wait(sh, j.err, &sh->pv_done, (it - 1) & 1);
+        if (moved) {
+#pragma unroll
+            for (int n = 0; n < R; ++n) l[n] *= __shfl_sync(0xFFFFFFFFu, f[n >> 5], n & 31);
+            if (t > pc.t0) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2 * C8; ++c) {
+                    float o[8];
+                    tc_ld8(o_col + c * 8, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int n = (c % C8) * 8 + i;
+                        o[i] *= __shfl_sync(0xFFFFFFFFu, f[n >> 5], n & 31);
+                    }
+                    tc_st8(o_col + c * 8, o);
+                }
+                tc_wait_st();
+                tc_fence_before();
+            }
+        }
+        // weights: 8 rows at a time, hi and lo
+        {
+            const float2 i2 = make_float2(ivs, ivs);
+            char *row = smem_p + tk * 128;
+#pragma unroll
+            for (int c = 0; c < C8; ++c) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int n = c * 8 + k * 2;
+                    const float2 m2 = *reinterpret_cast<const float2 *>(&sh->mu[warp][n]);
+                    const float2 p =
+                        make_float2(ex2f(y[n] - m2.x), ex2f(y[n + 1] - m2.y));
+                    const float2 s = fma2(p, i2, make_float2(l[n], l[n + 1]));
+                    l[n] = s.x;
+                    l[n + 1] = s.y;
+                    uint16_t h8;
+                    uint32_t h16, p16;
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(p.y), "f"(p.x));
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p16) : "f"(p.y), "f"(p.x));
+                    // (p - hi) * 16: exact in fp16
+                    __half2 d = __hsub2(*reinterpret_cast<__half2 *>(&p16),
+                                        *reinterpret_cast<__half2 *>(&h16));
+                    d = __hmul2(d, __floats2half2_rn(16.f, 16.f));
+                    uint16_t l8;
+                    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+                        : "=h"(l8)
+                        : "r"(*reinterpret_cast<uint32_t *>(&d)));
+                    hi[k] = h8;
+                    lo[k] = l8;
+                }
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const uint32_t *v = part ? lo : hi;
+                    const int col = g * 2 * R + part * R + c * 8;
+                    uint2 w;
+                    w.x = v[0] | (v[1] << 16);
+                    w.y = v[2] | (v[3] << 16);
+                    *reinterpret_cast<uint2 *>(row + (col >> 7) * (kTile * 128) +
+                                               ((((col & 127) >> 4) ^ (tk & 7)) << 4) +
+                                               (col & 15)) = w;
+                }
+            }
+        }
+        // values past the sequence's end may be anything (NaN times a weight of
+        // 0 would stay): clear them
+        const int valid = pc.L - p0;
+        if (valid < kTile) {
+            char *v = smem_v + (size_t)st * stage_bytes;
+            for (int i = valid * (D / 16) + tid; i < kTile * (D / 16); i += kSoftWarps * 32)
+                reinterpret_cast<uint4 *>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full);
     }
-    if (bad && lane == 0) latch(j.err, SV_ERR_DEVICE_BOUNDS);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int k = 0; k < N; ++k)
-        j.out[((int64_t)t * j.Hq + g) * D + lane + 32 * k] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(o[k] * inv));
-    if (j.lse && lane == 0)
-        j.lse[(int64_t)t * j.Hq + g] =
-            l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+
+    // ---- the piece's sums
+    if (ok && pc.t1 > pc.t0) ok = at_wait(sh, j.err, &sh->pv_done, (it - 1) & 1);
+    tc_fence_after();
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        const float s = warp_sum(l[n]);
+        if (lane == 0) sh->sum[quarter][g * R + n] = s;
+    }
+    if (lane < R) sh->mu[warp][lane] = mu[0];
+    if (lane + 32 < R) sh->mu[warp][lane + 32] = mu[1];
+    if (bar_or(3, kSoftWarps * 32, !ok)) return false;
+
+    const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
+    const int c0 = span_owner(sh->total, ctas, pc.unit0);
+    const int c1 = span_owner(sh->total, ctas, pc.unit0 + pc.tiles - 1);
+    const int me = blockIdx.x;
+    const size_t pf = part_floats(D);
+    // a unit that starts before this CTA's span is its first, else its last
+    float *part = j.part + ((size_t)me * 2 + (me == c0 ? 1 : 0)) * pf;
+    const int d = tk;  // head element of this lane (D = 64: lanes 64.. hold copies)
+#pragma unroll
+    for (int c = 0; c < C8; ++c) {
+        float hi[8], lo[8];
+        tc_ld8(o_col + c * 8, hi);
+        tc_ld8(o_col + R + c * 8, lo);
+        tc_wait_ld(hi);
+        tc_wait_ld(lo);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = g * R + c * 8 + i;
+            if (n >= pc.rows || d >= D) continue;
+            const float o = fmaf(lo[i], 0.0625f, hi[i]);
+            if (whole) {
+                const float s = (sh->sum[0][n] + sh->sum[1][n]) + (sh->sum[2][n] + sh->sum[3][n]);
+                const int row = pc.row0 + n;
+                const int64_t at = (int64_t)(pc.first + row / j.G) * j.Hq + pc.h * j.G + row % j.G;
+                j.out[at * D + d] = __bfloat16_as_ushort(
+                    __float2bfloat16_rn(s > 0.f ? o / s : 0.f));
+                if (d == 0 && j.lse)
+                    j.lse[at] = s > 0.f ? (sh->mu[g * 4][c * 8 + i] - 8.f + log2f(s)) *
+                                              0.6931471805599453f
+                                        : -INFINITY;
+            } else {
+                part[(size_t)n * D + d] = o;
+                if (d == 0) {
+                    part[(size_t)kRowsMax * D + n] = sh->mu[g * 4][c * 8 + i];
+                    part[(size_t)kRowsMax * (D + 1) + n] =
+                        (sh->sum[0][n] + sh->sum[1][n]) + (sh->sum[2][n] + sh->sum[3][n]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    if (whole) {
+        bar_or(3, kSoftWarps * 32, false);  // sum and mu are free again
+        return true;
+    }
+    // ---- a shared unit: the last CTA to arrive joins the parts
+    __threadfence();
+    bar_or(3, kSoftWarps * 32, false);
+    if (tid == 0) {
+        const unsigned seen = atomicAdd(&j.arrived[c0], 1u);
+        sh->last = seen == (unsigned)(c1 - c0);
+        if (sh->last) j.arrived[c0] = 0;
+        __threadfence();
+    }
+    bar_or(3, kSoftWarps * 32, false);
+    if (!sh->last) return true;
+    for (int i = tid; i < pc.rows * D; i += kSoftWarps * 32) {
+        const int n = i / D, e = i - n * D;
+        float m = kNone, s = 0.f, o = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float *q = j.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * pf;
+            const float mc = __ldcg(q + (size_t)kRowsMax * D + n);
+            const float sc = __ldcg(q + (size_t)kRowsMax * (D + 1) + n);
+            const float oc = __ldcg(q + (size_t)n * D + e);
+            const float top = fmaxf(m, mc), fo = ex2f(m - top), fc = ex2f(mc - top);
+            s = s * fo + sc * fc;
+            o = o * fo + oc * fc;
+            m = top;
+        }
+        const int row = pc.row0 + n;
+        const int64_t at = (int64_t)(pc.first + row / j.G) * j.Hq + pc.h * j.G + row % j.G;
+        j.out[at * D + e] = __bfloat16_as_ushort(__float2bfloat16_rn(s > 0.f ? o / s : 0.f));
+        if (e == 0 && j.lse)
+            j.lse[at] = s > 0.f ? (m - 8.f + log2f(s)) * 0.6931471805599453f : -INFINITY;
+    }
+    return true;
+}
+
+// The piece's queries: hi and lo parts to shared memory, rows of D bytes in the
+// swizzle of the keys; one row a warp at a time.
+template <int D>
+__device__ __forceinline__ void load_queries(const AttendJob &j, AttnShared *sh, char *smem_q,
+                                             const Piece &pc, int N)
+{
+    constexpr int E = D / 32;  // elements a lane
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int n = warp; n < N; n += kSoftWarps) {
+        float x[E];
+        float amax = 0.f;
+        const int row = pc.row0 + n;
+        if (n < pc.rows) {
+            const uint16_t *q = j.q + (int64_t)(pc.first + row / j.G) * j.qts +
+                                (int64_t)(pc.h * j.G + row % j.G) * j.qhs + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                x[i] = __uint_as_float((uint32_t)q[i] << 16);
+                amax = fmaxf(amax, fabsf(x[i]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] = 0.f;
+        }
+        amax = warp_max(amax);
+        // 2^e brings the largest element to [128, 256)
+        const int e = amax > 0.f ? min(134 - (int)(__float_as_uint(amax) >> 23), 126) : 0;
+        const float up = __int_as_float((127 + e) << 23);
+        if (lane == 0)
+            sh->c[n] = n < pc.rows ? j.softmax_scale * 1.4426950408889634f / up : 0.f;
+        uint32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            uint16_t h8, l8;
+            const float a = x[i] * up, b = x[i + 1] * up;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(b), "f"(a));
+            uint32_t h16;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
+            const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&h16));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l8) : "f"(b - h.y), "f"(a - h.x));
+            hi |= (uint32_t)h8 << (8 * i);
+            lo |= (uint32_t)l8 << (8 * i);
+        }
+        const int byte = lane * E;
+        const int sw = D == 128 ? n & 7 : (n >> 1) & 3;
+        char *at = smem_q + n * D + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+        if (E == 4) {
+            *reinterpret_cast<uint32_t *>(at) = hi;
+            *reinterpret_cast<uint32_t *>(at + kRowsMax * D) = lo;
+        } else {
+            *reinterpret_cast<uint16_t *>(at) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t *>(at + kRowsMax * D) = (uint16_t)lo;
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1)
+attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v)
+{
+    extern __shared__ char attn_raw[];
+    __shared__ AttnShared shared;
+    AttnShared *sh = &shared;
+    constexpr int kSide = kTile * D;            // bytes of a tile's keys (or values)
+    constexpr uint32_t kSwz = D == 128 ? 2 : 4;
+    char *base = attn_raw + ((1024 - (smem_u32(attn_raw) & 1023)) & 1023);
+    char *s_k = base, *s_v = base + kSide, *s_q = base + 2 * kAtStages * kSide;
+    char *s_p = s_q + 2 * kRowsMax * D;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < kAtStages; ++i) {
+            mbar_init(&sh->full_k[i], 1);
+            mbar_init(&sh->full_v[i], 1);
+            mbar_init(&sh->empty_k[i], 1);
+            mbar_init(&sh->empty_v[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->s_empty[i], kSoftWarps);
+        }
+        mbar_init(&sh->p_full, kSoftWarps);
+        mbar_init(&sh->pv_done, 1);
+        mbar_init(&sh->q_full, kSoftWarps);
+        mbar_init(&sh->drained, 1);
+        mbar_fence_init();
+        sh->abort = 0;
+        sh->first_b = 0;
+        sh->first_x = 0;
+    }
+    if (warp == kSoftWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&sh->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's span: each thread sums a run of sequences
+    const int per = (j.B + kAtThreads - 1) / kAtThreads;
+    const int b0 = min(tid * per, j.B), b1 = min(b0 + per, j.B);
+    long long own = 0;
+    for (int b = b0; b < b1; ++b) {
+        const SeqWork s = seq_work(j, b);
+        own += s.work;
+        if (s.bad && blockIdx.x == 0) latch(j.err, SV_ERR_DEVICE_BOUNDS);
+    }
+    long long run = own;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long a = __shfl_up_sync(0xFFFFFFFFu, run, k);
+        if (lane >= k) run += a;
+    }
+    if (lane == 31) sh->scan[warp] = run;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kAtThreads / 32; ++w) {
+        if (w < warp) run += sh->scan[w];
+        total += sh->scan[w];
+    }
+    const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+    const int me = blockIdx.x;
+    const long long from = me < ctas ? span_at(total, ctas, me) : 0;
+    const long long to = me < ctas ? span_at(total, ctas, me + 1) : 0;
+    if (from < to && run > from && run - own <= from) {
+        long long x = from - (run - own);
+        int b = b0;
+        for (;; ++b) {
+            const long long w = seq_work(j, b).work;
+            if (x < w) break;
+            x -= w;
+        }
+        sh->first_b = b;
+        sh->first_x = x;
+    }
+    if (tid == 0) sh->total = total;
+    __syncthreads();
+
+    PieceWalk walk;
+    Piece pc;
+    walk.start(j, sh, from, to);
+    uint32_t it = 0;
+    if (warp < kSoftWarps) {
+        bool ok = true;
+        while (ok && walk.next(j, pc)) {
+            const int N = (pc.rows + 15) & ~15;
+            load_queries<D>(j, sh, s_q, pc, N);
+            fence_async();
+            bar_or(3, kSoftWarps * 32, false);  // the rows' factors are there
+            if (lane == 0) mbar_arrive(&sh->q_full);
+#define SV_SOFT(C)                                                                              \
+    case C:                                                                                     \
+        ok = soft_piece<D, C>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, ok);                    \
+        break;
+            switch (N / 16) {
+                SV_SOFT(1) SV_SOFT(2) SV_SOFT(3) SV_SOFT(4) SV_SOFT(5) SV_SOFT(6) SV_SOFT(7)
+                SV_SOFT(8)
+            }
+#undef SV_SOFT
+        }
+    } else if (warp == kSoftWarps) {
+        // ---- producer: the pages of each tile, looked up 32 at a time
+        const int per_tile = kTile / j.block;
+        const int inner = lane & (per_tile - 1);
+        bool ok = true;
+        while (ok && walk.next(j, pc)) {
+            const int last = (pc.L + j.block - 1) / j.block;  // pages of the sequence
+            const int32_t *tab = j.table + (int64_t)pc.b * j.cols;
+            auto window = [&](int w0, int &page, float &ks, float &vs) {
+                page = w0 + lane < last ? tab[w0 + lane] : -1;
+                if (w0 + lane < last && (page < 0 || page >= j.pages)) {
+                    latch(j.err, SV_ERR_DEVICE_BOUNDS);
+                    page = -1;
+                }
+                ks = vs = 1.f;
+                if (page >= 0) {
+                    const int64_t ph = (int64_t)page * j.H + pc.h;
+                    ks = j.scale[0][ph];
+                    vs = j.scale[1][ph];
+                }
+            };
+            int w0 = (pc.t0 * per_tile) & ~31, page, npage;
+            float ks, vs, nks, nvs;
+            window(w0, page, ks, vs);
+            window(w0 + 32, npage, nks, nvs);
+            for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+                const int st = it % kAtStages;
+                const uint32_t ph = ((it / kAtStages) & 1) ^ 1;
+                const int p0 = t * per_tile;
+                if (p0 >= w0 + 32) {
+                    w0 += 32;
+                    page = npage;
+                    ks = nks;
+                    vs = nvs;
+                    window(w0 + 32, npage, nks, nvs);
+                }
+                const bool mine = lane - (p0 - w0) >= 0 && lane - (p0 - w0) < per_tile;
+                const bool copy = mine && page >= 0;
+                const uint32_t bytes =
+                    (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copy)) * j.block * D;
+                ok = at_wait(sh, j.err, &sh->empty_k[st], ph);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_tx(&sh->full_k[st], bytes);
+                __syncwarp();
+                const int64_t row = (int64_t)page * j.H + pc.h;
+                auto fetch = [&](const CUtensorMap *map, char *dst, uint64_t *bar) {
+                    asm volatile(
+                        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
+                        "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                        "l"(map), "r"(0), "r"(0), "r"((int)row), "r"(smem_u32(bar))
+                        : "memory");
+                };
+                if (copy)
+                    fetch(&map_k, s_k + (size_t)st * 2 * kSide + inner * j.block * D,
+                          &sh->full_k[st]);
+                ok = at_wait(sh, j.err, &sh->empty_v[st], ph);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (mine) {
+                    sh->ks[st][inner] = ks;
+                    sh->vs[st][inner] = vs;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_tx(&sh->full_v[st], bytes);
+                __syncwarp();
+                if (copy)
+                    fetch(&map_v, s_v + (size_t)st * 2 * kSide + inner * j.block * D,
+                          &sh->full_v[st]);
+            }
+        }
+        // after a wait that ran out: copies still in flight land before the exit
+        if (!ok)
+            for (int i = 0; i < kAtStages; ++i) {
+                mbar_wait_n(&sh->full_k[i], (it / kAtStages) & 1, 1u << 12);
+                mbar_wait_n(&sh->full_v[i], (it / kAtStages) & 1, 1u << 12);
+            }
+    } else if (lane == 0) {
+        // ---- issuer of the products
+        constexpr uint32_t kKinds = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);  // fp32 sums, M = 128
+        const uint32_t tmem = sh->tmem;
+        bool ok = true;
+        uint32_t pieces = 0;
+        while (ok && walk.next(j, pc)) {
+            const int N = (pc.rows + 15) & ~15;
+            const uint32_t id_s = kKinds | ((uint32_t)(N >> 3) << 17);
+            const uint32_t id_o = kKinds | (3u << 15) | ((uint32_t)(2 * N >> 3) << 17);
+            ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
+            ++pieces;
+            const uint32_t aq = smem_u32(s_q), ap = smem_u32(s_p);
+            auto scores = [&](uint32_t i) {
+                const int st = i % kAtStages, sb = i & 1;
+                ok = ok && at_wait(sh, j.err, &sh->full_k[st], (i / kAtStages) & 1);
+                ok = ok && at_wait(sh, j.err, &sh->s_empty[sb], ((i >> 1) & 1) ^ 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t ak = smem_u32(s_k) + st * 2 * kSide;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k)
+                        tc_mma(tmem + sb * 128, tc_desc(ak + k * 32, 16, 8 * D, kSwz),
+                               tc_desc(aq + part * kRowsMax * D + k * 32, 16, 8 * D, kSwz), id_s,
+                               part || k);
+                tc_commit(&sh->empty_k[st]);
+                tc_commit(&sh->s_full[sb]);
+            };
+            const int nt = pc.t1 - pc.t0;
+            if (ok) scores(it);
+            for (int i = 0; i < nt && ok; ++i) {
+                const uint32_t x = it + i;
+                if (i + 1 < nt) scores(x + 1);
+                const int st = x % kAtStages;
+                ok = ok && at_wait(sh, j.err, &sh->full_v[st], (x / kAtStages) & 1);
+                ok = ok && at_wait(sh, j.err, &sh->p_full, x & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t av = smem_u32(s_v) + st * 2 * kSide;
+                // D = 64: the second 64 rows read the same values again
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    tc_mma(tmem + 256, tc_desc(av + k * 32 * D, 0, 8 * D, kSwz),
+                           tc_desc(ap + k * 32 * 128, kTile * 128, 1024, 2), id_o, i || k);
+                tc_commit(&sh->empty_v[st]);
+                tc_commit(&sh->pv_done);
+            }
+            it += nt;
+        }
+        // after a wait that ran out: products still in flight end before the exit
+        if (!ok) {
+            tc_commit(&sh->drained);
+            mbar_wait_n(&sh->drained, 0, 1u << 12);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sh->tmem));
+    }
+}
+
+constexpr size_t attend_smem(int D)
+{
+    return 1024 + (size_t)2 * kAtStages * kTile * D + 2 * kRowsMax * D + 2 * kTile * 128;
+}
+
+size_t attend_ws_bytes(int sms) { return (size_t)sms * 2 * part_floats(128) * sizeof(float); }
+size_t attend_counter_bytes(int sms) { return ((size_t)sms * sizeof(unsigned) + 255) & ~(size_t)255; }
+
+cudaError_t attend_setup()
+{
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<64>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)attend_smem(128));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)attend_smem(128));
+    return e;
+}
+
+// Map of one side of the cache: [pages * H][block][D] bytes, a page's head at a
+// time, in the swizzle that the products read.
+static bool cache_map(CUtensorMap *m, const AttendJob &j, int side)
+{
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                               const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                               const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &r) != cudaSuccess)
+            f = nullptr;
+        return (Encode)f;
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)j.D, (cuuint64_t)j.block,
+                                (cuuint64_t)j.pages * j.H};
+    const cuuint64_t strides[2] = {(cuuint64_t)j.D, (cuuint64_t)j.D * j.block};
+    const cuuint32_t box[3] = {(cuuint32_t)j.D, (cuuint32_t)j.block, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void *)j.cache[side], dims, strides, box,
+                  step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  j.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s)
 {
+    CUtensorMap mk, mv;
+    if (!cache_map(&mk, j, 0) || !cache_map(&mv, j, 1)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
-    const int64_t items = (int64_t)j.T * j.Hq;
-    pdl_config(cfg, at, dim3((unsigned)((items + 3) / 4)), dim3(kAttThreads), 0, s);
-    return j.D == 64 ? cudaLaunchKernelEx(&cfg, attend_kernel<64>, j)
-                     : cudaLaunchKernelEx(&cfg, attend_kernel<128>, j);
+    // (one CTA an SM, also where the shared memory of D = 64 would allow two:
+    // each holds all of the SM's tensor memory)
+    pdl_config(cfg, at, dim3(sms), dim3(kAtThreads), attend_smem(128), s);
+    return j.D == 64 ? cudaLaunchKernelEx(&cfg, attend_kernel<64>, j, mk, mv)
+                     : cudaLaunchKernelEx(&cfg, attend_kernel<128>, j, mk, mv);
 }
 
 }  // namespace sv

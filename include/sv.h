@@ -455,6 +455,8 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  *     token sees nothing.  Softmax and sums are fp32.
  *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
  *     where a token sees nothing.
+ * The handle's first call allocates its workspace (20 MB, of fixed size): make
+ * it before any stream capture (SV_ERR_UNSUPPORTED inside one).
  * Rows from cu_new[B] on are not written.  Bytes past kv_len may hold
  * anything; those of visible tokens are finite, with scales in [2^-40, 2^40].
  * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D); latched
