@@ -48,23 +48,34 @@ constexpr int kTile = 128;             // tokens of a tile
 constexpr int kRowsMax = 128;          // query rows of a unit
 constexpr int kAtStages = 4;           // tiles in flight
 constexpr int kSoftWarps = 8;          // two warpgroups, each half of the rows
-constexpr int kAtThreads = kSoftWarps * 32 + 64;  // + producer and issuer
+// + producer and issuer, and two idle warps that make up a warpgroup with them
+constexpr int kAtThreads = kSoftWarps * 32 + 128;
+// Registers: the launch gives each thread 168 of the SM's 65,536; the softmax
+// warps keep up to 128 scores and sums each and take what the others leave
+// (128 * 72 + 256 * 216 = 384 * 168).
+constexpr int kAtRegs = 168, kSideRegs = 72, kSoftRegs = 216;
+static_assert(128 * kSideRegs + kSoftWarps * 32 * kSoftRegs <= kAtThreads * kAtRegs, "registers");
 constexpr float kNone = -1e30f;        // running maximum before any token
 constexpr uint32_t kAtSpin = 1u << 20; // tries of a wait (a tile takes microseconds)
 
 struct AttnShared {
     uint64_t full_k[kAtStages], full_v[kAtStages], empty_k[kAtStages], empty_v[kAtStages];
-    uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, drained;
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, drained;
     uint32_t tmem;
     int abort;
     int last;                          // this CTA joins the unit's parts
     int first_b;
-    long long first_x, total;          // the span's first tile in sequence first_b; all tiles
+    long long first_x, total;          // where the span starts in sequence first_b; the call's cost
     float ks[kAtStages][8], vs[kAtStages][8];  // scales of the tile's pages
-    float c[kRowsMax];                 // factor from S to log2 units, per row
-    float wmax[2][kSoftWarps][64];     // tile maxima per warp and row
-    float mu[kSoftWarps][64];          // running maximum in use, per warp
-    float sum[4][kRowsMax];            // sums of weights per quarter of a tile
+    int at[kRowsMax];                  // output row (token * Hq + head), per row
+    alignas(16) float c[kRowsMax];     // factor from S to log2 units, per row
+    float wmax[kSoftWarps][64];        // tile maxima per warp and row
+    alignas(16) float mu[kSoftWarps][64];    // running maximum in use, a copy per warp
+    alignas(16) float down[kSoftWarps][64];  // its last move, and the factor 2^-move
+    alignas(16) float fac[kSoftWarps][64];
+    float sum[2][4][kRowsMax];         // sums of weights: warpgroup, quarter of a tile, row
+    float top[2][kRowsMax];            // maximum that they are against
+    short owner[256];                  // CTAs of a shared unit's tiles (spans below a tile)
     long long scan[kAtThreads / 32];
 };
 
@@ -177,9 +188,13 @@ __device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar,
 struct SeqWork {
     int n, L, first;         // new tokens, tokens, first row of q
     int tiles, blocks, rows; // tiles of a unit, row blocks, rows of a block
-    long long work;          // tiles of the sequence
+    int cost;                // of a tile
+    long long work;          // cost of the sequence
     bool bad;
 };
+// Time of a tile by its rows, as measured: even spans of it are even in time.
+__device__ __forceinline__ int tile_cost(int N) { return 16 + N / 4; }
+
 __device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
 {
     SeqWork s;
@@ -194,19 +209,23 @@ __device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
     s.tiles = (int)(((long long)s.L + kTile - 1) / kTile);
     s.blocks = (int)((all + kRowsMax - 1) / kRowsMax);
     s.rows = s.blocks ? (int)((all + s.blocks - 1) / s.blocks) : 0;
-    s.work = (long long)s.tiles * s.blocks * j.H;
+    s.cost = tile_cost((s.rows + 15) & ~15);
+    s.work = (long long)s.tiles * s.blocks * j.H * s.cost;
     return s;
 }
 
-// A CTA's share of one unit, walked alike by every role.
+// A CTA's share of one unit, walked alike by every role.  Costs of tiles, laid
+// end to end, are cut into equal spans; a tile belongs to the span that its
+// first unit of cost lies in.
 struct Piece {
     int b, h, row0, rows;    // sequence, cache head, first row (of n G) and rows
     int t0, t1, tiles;       // tiles [t0, t1) of the unit's
-    long long unit0;         // the unit's first tile in the call's order
+    int cost;                // of a tile
+    long long unit0;         // where the unit starts in the call's cost
     int L, n, first;
 };
 struct PieceWalk {
-    long long pos, end, x;   // next tile, the span's end, next tile within b
+    long long pos, end, x;   // a tile's start, the span's end, the tile's start within b
     int b;
     SeqWork s;
     __device__ __forceinline__ void start(const AttendJob &j, const AttnShared *sh,
@@ -216,7 +235,13 @@ struct PieceWalk {
         end = to;
         b = sh->first_b;
         x = sh->first_x;
-        if (pos < end) s = seq_work(j, b);
+        if (pos < end) {
+            s = seq_work(j, b);
+            // on to the first tile that starts within the span
+            const long long on = (s.cost - x % s.cost) % s.cost;
+            x += on;
+            pos += on;
+        }
     }
     __device__ __forceinline__ bool next(const AttendJob &j, Piece &p)
     {
@@ -225,21 +250,22 @@ struct PieceWalk {
             x -= s.work;
             s = seq_work(j, ++b);
         }
-        const long long u = x / s.tiles;
-        p.t0 = (int)(x - u * s.tiles);
-        const long long left = end - pos;
+        const long long tile = x / s.cost, u = tile / s.tiles;
+        p.t0 = (int)(tile - u * s.tiles);
+        const long long left = (end - pos + s.cost - 1) / s.cost;
         p.t1 = (int)(s.tiles - p.t0 < left ? s.tiles : p.t0 + left);
         p.b = b;
         p.h = (int)(u / s.blocks);
         p.row0 = (int)(u - (long long)p.h * s.blocks) * s.rows;
         p.rows = min(s.rows, s.n * j.G - p.row0);
         p.tiles = s.tiles;
-        p.unit0 = pos - p.t0;
+        p.cost = s.cost;
+        p.unit0 = pos - (long long)p.t0 * s.cost;
         p.L = s.L;
         p.n = s.n;
         p.first = s.first;
-        pos += p.t1 - p.t0;
-        x += p.t1 - p.t0;
+        pos += (long long)(p.t1 - p.t0) * s.cost;
+        x += (long long)(p.t1 - p.t0) * s.cost;
         return true;
     }
 };
@@ -263,151 +289,227 @@ __host__ __device__ constexpr size_t part_floats(int D) { return (size_t)kRowsMa
 
 // ---------------------------------------------------------------------------
 // Softmax side of one piece.  Thread: one token of the tile (TMEM lane) for
-// the weights, one head element for the output; C8 * 8 rows a warpgroup.
+// the weights, one head element for the output.
+//
+// Up to 64 rows (TURNS) the two warpgroups take the tiles in turn, each with
+// all the rows, sums and a running maximum of its own, so that one tile's chain
+// (scores, maximum, weights, products) runs under the other's; above, they
+// share each tile, half of the rows each.  (All rows of a tile in one
+// warpgroup would not fit the registers.)
+//
+// The running maximum M moves lazily: weights are taken as 2^(y - M + 4.5), and
+// M moves only when one would pass 2^8.5 (e4m3 ends at 448).  So most tiles
+// need no maximum at all, only a vote of the warpgroup that nothing passes;
+// a tile that does is looked at again from its scores.
 // ---------------------------------------------------------------------------
-template <int D, int C8>
+constexpr float kUnit = 4.5f;  // log2 of the weight at the running maximum
+constexpr float kMost = 8.5f;  // log2 of the largest weight
+
+// Sum v[0 .. N) over the warp's lanes: three halvings leave each lane N / 8
+// rows, those from index (lane / 4) * N / 8 on (a quarter of the shuffles of
+// whole sums).
+template <int N>
+__device__ __forceinline__ void warp_sum_rows(float (&v)[N], int lane)
+{
+#pragma unroll
+    for (int level = 0; level < 3; ++level) {
+        const int half = N >> (level + 1), bit = 16 >> level;
+        const bool up = lane & bit;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if (i >= half) break;
+            const float give = up ? v[i] : v[i + half];
+            const float keep = up ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, bit);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+        v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 2);
+        v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 1);
+    }
+}
+
+template <int D, int C8, bool TURNS>
 __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, char *smem_v,
                                            char *smem_p, const Piece &pc, uint32_t &it,
                                            int stage_bytes, int ctas, bool ok)
 {
-    constexpr int R = C8 * 8;      // rows of this warpgroup
+    constexpr int R = C8 * 8;                   // rows of this warpgroup
+    constexpr int kWays = TURNS ? 1 : 2;        // warpgroups of a tile
+    constexpr int kHalf = TURNS ? R / 2 : R;    // rows of the output of this warpgroup
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = warp >> 2, quarter = warp & 3;
     const int tk = quarter * 32 + lane;
+    const int r0 = TURNS ? 0 : g * R;           // first row of this warpgroup
     const uint32_t lanes = sh->tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t o_col = lanes + 256 + g * 2 * R;   // R hi columns, then R lo
+    const uint32_t o_own = lanes + 256 + g * (TURNS ? 128 : 2 * R);  // R hi columns, then R lo
     const int ctx = pc.L - pc.n;
-    const int pages_in = tk / j.block;
+    const int page_in = tk >> (31 - __clz(j.block));
+    char *p_row = smem_p + (TURNS ? g * (kTile * 128) : 0) + tk * 128;
+    float *mu = sh->mu[warp];
 
-    float mu[2] = {kNone, kNone};  // rows lane and lane + 32 of this warpgroup
     float l[R];
 #pragma unroll
     for (int n = 0; n < R; ++n) l[n] = 0.f;
+    mu[lane] = kNone;                           // (kept less kUnit)
+    mu[lane + 32] = kNone;
+    __syncwarp();
+    uint32_t mine = 0;                          // tiles this warpgroup has taken
+    bool unset = true;                          // a row has seen no token yet
+    const uint32_t it0 = it;
 
     for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = it % kAtStages, sb = it & 1;
+        if (TURNS && sb != g) continue;
         ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
         ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
         tc_fence_after();
         float y[R];
 #pragma unroll
-        for (int c = 0; c < C8; ++c) tc_ld8(lanes + sb * 128 + g * R + c * 8, y + c * 8);
-        tc_wait_ld(y);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->s_empty[sb]);
-
-        // log2 units, the value's scale included
+        for (int c = 0; c < C8; ++c) tc_ld8(lanes + sb * 128 + r0 + c * 8, y + c * 8);
         const int p0 = t * kTile, pos = p0 + tk;
-        const float ks = sh->ks[st][pages_in];
-        const float vs = fminf(fmaxf(sh->vs[st][pages_in], 0x1p-60f), 0x1p60f);
-        const float vl = log2f(vs), ivs = 1.f / vs;
-        {
-            const float2 a2 = make_float2(ks, ks), v2 = make_float2(vl, vl);
-            const float *cr = sh->c + g * R;
-#pragma unroll
-            for (int n = 0; n < R; n += 4) {
-                const float4 c4 = *reinterpret_cast<const float4 *>(cr + n);
-                float2 u = make_float2(y[n] * c4.x, y[n + 1] * c4.y);
-                float2 w = make_float2(y[n + 2] * c4.z, y[n + 3] * c4.w);
-                u = fma2(u, a2, v2);
-                w = fma2(w, a2, v2);
-                y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
-            }
-        }
+        const float ks = sh->ks[st][page_in];
+        const float vs = fminf(fmaxf(sh->vs[st][page_in], 0x1p-60f), 0x1p60f);
+        float vl, ivs;
+        asm("lg2.approx.f32 %0, %1;" : "=f"(vl) : "f"(vs));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));
         // tiles that reach the new tokens: which rows see this token
-        if (p0 + kTile > ctx || p0 + kTile > pc.L) {
-            unsigned long long sees = 0;
+        unsigned long long sees = ~0ull;
+        const bool edge = p0 + kTile > ctx;
+        if (edge) {
+            sees = 0;
             if (pos < pc.L) {
                 if (pos < ctx) {
                     sees = ~0ull;
                 } else if (!j.mask) {
                     // rows (row0 + n) / G >= pos - ctx
-                    const long long from = (long long)(pos - ctx) * j.G - pc.row0 - g * R;
+                    const long long from = (long long)(pos - ctx) * j.G - pc.row0 - r0;
                     sees = from <= 0 ? ~0ull : from >= 64 ? 0ull : ~0ull << from;
                 } else {
                     const int k = pos - ctx;
                     if ((k >> 5) < j.words) {
-                        for (int n = 0; n < R; ++n) {
-                            const int row = pc.row0 + g * R + n;
-                            if (row < pc.row0 + pc.rows) {
-                                const int64_t tok = pc.first + row / j.G;
-                                const uint32_t m = j.mask[tok * j.words + (k >> 5)];
-                                sees |= (unsigned long long)((m >> (k & 31)) & 1u) << n;
-                            }
+                        const int rows = min(R, pc.rows - r0);
+#pragma unroll 1
+                        for (int n = 0; n < rows; ++n) {
+                            const int64_t tok = pc.first + (pc.row0 + r0 + n) / j.G;
+                            const uint32_t m = j.mask[tok * j.words + (k >> 5)];
+                            sees |= (unsigned long long)((m >> (k & 31)) & 1u) << n;
                         }
                     }
                 }
             }
-#pragma unroll
-            for (int n = 0; n < R; ++n)
-                if (!((sees >> n) & 1ull)) y[n] = -INFINITY;
         }
-        // the tile's maximum of each row: over the warp's tokens, then four warps
-        float keep[2] = {kNone, kNone};
+        // scores in log2 units, the value's scale included, against the maximum in use
+        auto scale_scores = [&](bool against) {
+            tc_wait_ld(y);
+            const float2 a2 = make_float2(ks, ks), v2 = make_float2(vl, vl);
 #pragma unroll
-        for (int n = 0; n < R; ++n) {
-            float m;
-            asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(y[n]));
-            if (lane == (n & 31)) keep[n >> 5] = m;
-        }
-        sh->wmax[it & 1][warp][lane] = keep[0];
-        if (R > 32) sh->wmax[it & 1][warp][lane + 32] = keep[1];
-        if (bar_or(1 + g, 128, !ok)) {
-            ok = false;
-            break;
-        }
-        float f[2] = {1.f, 1.f};
-        bool moved = false;
-#pragma unroll
-        for (int k = 0; k < (R > 32 ? 2 : 1); ++k) {
-            float m = mu[k];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) m = fmaxf(m, sh->wmax[it & 1][g * 4 + w][lane + 32 * k]);
-            if (lane + 32 * k < R && m > mu[k]) {
-                f[k] = ex2f(mu[k] - m);
-                mu[k] = m;
-                moved = true;
+            for (int n = 0; n < R; n += 4) {
+                const float4 c4 = *reinterpret_cast<const float4 *>(&sh->c[r0 + n]);
+                float2 u = make_float2(y[n] * c4.x, y[n + 1] * c4.y);
+                float2 w = make_float2(y[n + 2] * c4.z, y[n + 3] * c4.w);
+                u = fma2(u, a2, v2);
+                w = fma2(w, a2, v2);
+                if (against) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(&mu[n]);
+                    u = add2(u, make_float2(-m4.x, -m4.y));
+                    w = add2(w, make_float2(-m4.z, -m4.w));
+                }
+                y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
             }
-            sh->mu[warp][lane + 32 * k] = mu[k] - 8.f;  // weights in units of 2^-8
-        }
-        moved = __any_sync(0xFFFFFFFFu, moved);  // (orders the writes of mu as well)
-        __syncwarp();
-        if (t > pc.t0) ok = ok && at_wait(sh, j.err, &sh->pv_done, (it - 1) & 1);
-        if (moved) {
+            if (edge) {
+                const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
 #pragma unroll
-            for (int n = 0; n < R; ++n) l[n] *= __shfl_sync(0xFFFFFFFFu, f[n >> 5], n & 31);
-            if (t > pc.t0) {
+                for (int n = 0; n < R; ++n)
+                    if (!((n < 32 ? s0 : s1) & (1u << (n & 31)))) y[n] = -INFINITY;
+            }
+        };
+        scale_scores(true);
+        float top = y[0];
+#pragma unroll
+        for (int n = 1; n < R; ++n) top = fmaxf(top, y[n]);
+        if (bar_or(1 + g, 128, !ok || top > kMost)) {
+            // a row without a maximum: its scores against none
+            if (unset) {
+#pragma unroll
+                for (int c = 0; c < C8; ++c) tc_ld8(lanes + sb * 128 + r0 + c * 8, y + c * 8);
+                scale_scores(false);
+            }
+            // the tile's maximum of each row: over the warp's tokens, then four warps
+            float keep[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                float m;
+                asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(y[n]));
+                if (lane == (n & 31)) keep[n >> 5] = m;
+            }
+            sh->wmax[warp][lane] = keep[0];
+            if (R > 32) sh->wmax[warp][lane + 32] = keep[1];
+            if (bar_or(1 + g, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            float *down = sh->down[warp], *fac = sh->fac[warp];
+            bool none = false;
+#pragma unroll
+            for (int k = 0; k < (R > 32 ? 2 : 1); ++k) {
+                const int n = lane + 32 * k;
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) m = fmaxf(m, sh->wmax[g * 4 + w][n]);
+                // (n >= R: padding of the arrays, not used)
+                const float old = mu[n];
+                const float now = unset ? fmaxf(old, m - kUnit) : old + fmaxf(m - kUnit, 0.f);
+                mu[n] = now;
+                down[n] = unset ? now : now - old;  // from the scores at hand
+                fac[n] = ex2f(old - now);
+                none = none || (n < R && now == kNone);
+            }
+            unset = __any_sync(0xFFFFFFFFu, none);
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < R; n += 4) {
+                const float4 d4 = *reinterpret_cast<const float4 *>(&down[n]);
+                const float4 f4 = *reinterpret_cast<const float4 *>(&fac[n]);
+                y[n] -= d4.x; y[n + 1] -= d4.y; y[n + 2] -= d4.z; y[n + 3] -= d4.w;
+                l[n] *= f4.x; l[n + 1] *= f4.y; l[n + 2] *= f4.z; l[n + 3] *= f4.w;
+            }
+            if (mine > 0) {
+                const uint32_t before = TURNS ? it - 2 : it - 1;
+                ok = at_wait(sh, j.err, &sh->pv_done[before & 1], (before >> 1) & 1);
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 2 * C8; ++c) {
+                    const float *f = fac + (c < C8 ? c : c - C8) * 8;
                     float o[8];
-                    tc_ld8(o_col + c * 8, o);
+                    tc_ld8(o_own + c * 8, o);
                     tc_wait_ld(o);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int n = (c % C8) * 8 + i;
-                        o[i] *= __shfl_sync(0xFFFFFFFFu, f[n >> 5], n & 31);
-                    }
-                    tc_st8(o_col + c * 8, o);
+                    for (int i = 0; i < 8; ++i) o[i] *= f[i];
+                    tc_st8(o_own + c * 8, o);
                 }
                 tc_wait_st();
-                tc_fence_before();
             }
         }
-        // weights: 8 rows at a time, hi and lo
+        tc_fence_before();
+        __syncwarp();
+        if (lane < 3 - kWays) mbar_arrive(&sh->s_empty[sb]);
+        // the weights' place is free once the products before have read it
+        if (mine > 0) {
+            const uint32_t before = TURNS ? it - 2 : it - 1;
+            ok = ok && at_wait(sh, j.err, &sh->pv_done[before & 1], (before >> 1) & 1);
+        }
+        ++mine;
         {
             const float2 i2 = make_float2(ivs, ivs);
-            char *row = smem_p + tk * 128;
 #pragma unroll
             for (int c = 0; c < C8; ++c) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int n = c * 8 + k * 2;
-                    const float2 m2 = *reinterpret_cast<const float2 *>(&sh->mu[warp][n]);
-                    const float2 p =
-                        make_float2(ex2f(y[n] - m2.x), ex2f(y[n + 1] - m2.y));
+                    const float2 p = make_float2(ex2f(y[n]), ex2f(y[n + 1]));
                     const float2 s = fma2(p, i2, make_float2(l[n], l[n + 1]));
                     l[n] = s.x;
                     l[n + 1] = s.y;
@@ -430,11 +532,11 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
                     const uint32_t *v = part ? lo : hi;
-                    const int col = g * 2 * R + part * R + c * 8;
+                    const int col = r0 * 2 + part * R + c * 8;
                     uint2 w;
                     w.x = v[0] | (v[1] << 16);
                     w.y = v[2] | (v[3] << 16);
-                    *reinterpret_cast<uint2 *>(row + (col >> 7) * (kTile * 128) +
+                    *reinterpret_cast<uint2 *>(p_row + (col >> 7) * (kTile * 128) +
                                                ((((col & 127) >> 4) ^ (tk & 7)) << 4) +
                                                (col & 15)) = w;
                 }
@@ -445,69 +547,108 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         const int valid = pc.L - p0;
         if (valid < kTile) {
             char *v = smem_v + (size_t)st * stage_bytes;
-            for (int i = valid * (D / 16) + tid; i < kTile * (D / 16); i += kSoftWarps * 32)
+            const int at = TURNS ? tk : tid;
+            for (int i = valid * (D / 16) + at; i < kTile * (D / 16); i += 128 * kWays)
                 reinterpret_cast<uint4 *>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full);
+        if (lane < 3 - kWays) mbar_arrive(&sh->p_full[sb]);
     }
 
     // ---- the piece's sums
-    if (ok && pc.t1 > pc.t0) ok = at_wait(sh, j.err, &sh->pv_done, (it - 1) & 1);
-    tc_fence_after();
-#pragma unroll
-    for (int n = 0; n < R; ++n) {
-        const float s = warp_sum(l[n]);
-        if (lane == 0) sh->sum[quarter][g * R + n] = s;
+    it = it0 + (uint32_t)(pc.t1 - pc.t0);
+    if (mine > 0 && ok) {
+        // the last tile of this warpgroup
+        const uint32_t last = TURNS && ((it - 1) & 1) != (uint32_t)g ? it - 2 : it - 1;
+        ok = at_wait(sh, j.err, &sh->pv_done[last & 1], (last >> 1) & 1);
     }
-    if (lane < R) sh->mu[warp][lane] = mu[0];
-    if (lane + 32 < R) sh->mu[warp][lane + 32] = mu[1];
+    warp_sum_rows(l, lane);
+    if ((lane & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < C8; ++i) {
+            // which row the halvings left here: bits 4, 3, 2 of the lane
+            const int n = ((lane >> 4) & 1) * (R / 2) + ((lane >> 3) & 1) * (R / 4) +
+                          ((lane >> 2) & 1) * (R / 8) + i;
+            sh->sum[TURNS ? g : 0][quarter][r0 + n] = l[i];
+        }
+    }
+    if (quarter == 0) {
+        if (lane < R) sh->top[TURNS ? g : 0][r0 + lane] = mu[lane];
+        if (lane + 32 < R) sh->top[TURNS ? g : 0][r0 + lane + 32] = mu[lane + 32];
+    }
     if (bar_or(3, kSoftWarps * 32, !ok)) return false;
+    tc_fence_after();
 
     const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
     const int c0 = span_owner(sh->total, ctas, pc.unit0);
-    const int c1 = span_owner(sh->total, ctas, pc.unit0 + pc.tiles - 1);
+    const int c1 = span_owner(sh->total, ctas, pc.unit0 + (long long)(pc.tiles - 1) * pc.cost);
+    // Spans at least a tile long leave no CTA between c0 and c1 without a tile;
+    // in shorter ones every tile has a CTA of its own.
+    const bool each = pc.cost > sh->total / ctas;
+    const int owners = each ? pc.tiles : c1 - c0 + 1;
     const int me = blockIdx.x;
     const size_t pf = part_floats(D);
     // a unit that starts before this CTA's span is its first, else its last
     float *part = j.part + ((size_t)me * 2 + (me == c0 ? 1 : 0)) * pf;
     const int d = tk;  // head element of this lane (D = 64: lanes 64.. hold copies)
+    const int w0 = g * kHalf;  // rows that this warpgroup writes
+    // (a warpgroup that had no tile has no sums)
+    const bool has[2] = {!TURNS || pc.t1 - pc.t0 > 1 || (it0 & 1) == 0,
+                         TURNS && (pc.t1 - pc.t0 > 1 || (it0 & 1) == 1)};
+#pragma unroll 1
+    for (int c = 0; c < kHalf / 8; ++c) {
+        float o[8];
+        float hi[8], lo[8], fac[2][8];
 #pragma unroll
-    for (int c = 0; c < C8; ++c) {
-        float hi[8], lo[8];
-        tc_ld8(o_col + c * 8, hi);
-        tc_ld8(o_col + R + c * 8, lo);
-        tc_wait_ld(hi);
-        tc_wait_ld(lo);
+        for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll
+        for (int way = 0; way < 3 - kWays; ++way) {
+            const uint32_t col = TURNS ? lanes + 256 + way * 128 + w0 + c * 8 : o_own + c * 8;
+            if (!has[way]) continue;
+            tc_ld8(col, hi);
+            tc_ld8(col + R, lo);
+            tc_wait_ld(hi);
+            tc_wait_ld(lo);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int n = w0 + c * 8 + i;
+                const float m = TURNS ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
+                fac[way][i] = TURNS ? ex2f(sh->top[way][n] - m) : 1.f;
+                o[i] = fmaf(fac[way][i], fmaf(lo[i], 0.0625f, hi[i]), o[i]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int n = g * R + c * 8 + i;
+            const int n = w0 + c * 8 + i;
             if (n >= pc.rows || d >= D) continue;
-            const float o = fmaf(lo[i], 0.0625f, hi[i]);
+            float s = 0.f;
+#pragma unroll
+            for (int way = 0; way < 3 - kWays; ++way)
+                if (has[way])
+                    s = fmaf(fac[way][i],
+                             (sh->sum[way][0][n] + sh->sum[way][1][n]) +
+                                 (sh->sum[way][2][n] + sh->sum[way][3][n]),
+                             s);
+            const float m = TURNS ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
             if (whole) {
-                const float s = (sh->sum[0][n] + sh->sum[1][n]) + (sh->sum[2][n] + sh->sum[3][n]);
-                const int row = pc.row0 + n;
-                const int64_t at = (int64_t)(pc.first + row / j.G) * j.Hq + pc.h * j.G + row % j.G;
+                const int64_t at = sh->at[n];
                 j.out[at * D + d] = __bfloat16_as_ushort(
-                    __float2bfloat16_rn(s > 0.f ? o / s : 0.f));
+                    __float2bfloat16_rn(s > 0.f ? __fdividef(o[i], s) : 0.f));
                 if (d == 0 && j.lse)
-                    j.lse[at] = s > 0.f ? (sh->mu[g * 4][c * 8 + i] - 8.f + log2f(s)) *
-                                              0.6931471805599453f
-                                        : -INFINITY;
+                    j.lse[at] = s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
             } else {
-                part[(size_t)n * D + d] = o;
+                part[(size_t)n * D + d] = o[i];
                 if (d == 0) {
-                    part[(size_t)kRowsMax * D + n] = sh->mu[g * 4][c * 8 + i];
-                    part[(size_t)kRowsMax * (D + 1) + n] =
-                        (sh->sum[0][n] + sh->sum[1][n]) + (sh->sum[2][n] + sh->sum[3][n]);
+                    part[(size_t)kRowsMax * D + n] = m;
+                    part[(size_t)kRowsMax * (D + 1) + n] = s;
                 }
             }
         }
     }
     tc_fence_before();
     if (whole) {
-        bar_or(3, kSoftWarps * 32, false);  // sum and mu are free again
+        bar_or(3, kSoftWarps * 32, false);  // sum and top are free again
         return true;
     }
     // ---- a shared unit: the last CTA to arrive joins the parts
@@ -515,16 +656,21 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     bar_or(3, kSoftWarps * 32, false);
     if (tid == 0) {
         const unsigned seen = atomicAdd(&j.arrived[c0], 1u);
-        sh->last = seen == (unsigned)(c1 - c0);
+        sh->last = seen == (unsigned)(owners - 1);
         if (sh->last) j.arrived[c0] = 0;
         __threadfence();
     }
+    if (each)
+        for (int k = tid; k < owners; k += kSoftWarps * 32)
+            sh->owner[k] = (short)span_owner(sh->total, ctas, pc.unit0 + (long long)k * pc.cost);
     bar_or(3, kSoftWarps * 32, false);
     if (!sh->last) return true;
+#pragma unroll 1
     for (int i = tid; i < pc.rows * D; i += kSoftWarps * 32) {
         const int n = i / D, e = i - n * D;
         float m = kNone, s = 0.f, o = 0.f;
-        for (int c = c0; c <= c1; ++c) {
+        for (int k = 0; k < owners; ++k) {
+            const int c = each ? sh->owner[k] : c0 + k;
             const float *q = j.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * pf;
             const float mc = __ldcg(q + (size_t)kRowsMax * D + n);
             const float sc = __ldcg(q + (size_t)kRowsMax * (D + 1) + n);
@@ -534,11 +680,10 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             o = o * fo + oc * fc;
             m = top;
         }
-        const int row = pc.row0 + n;
-        const int64_t at = (int64_t)(pc.first + row / j.G) * j.Hq + pc.h * j.G + row % j.G;
+        const int64_t at = sh->at[n];
         j.out[at * D + e] = __bfloat16_as_ushort(__float2bfloat16_rn(s > 0.f ? o / s : 0.f));
         if (e == 0 && j.lse)
-            j.lse[at] = s > 0.f ? (m - 8.f + log2f(s)) * 0.6931471805599453f : -INFINITY;
+            j.lse[at] = s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
     }
     return true;
 }
@@ -556,8 +701,9 @@ __device__ __forceinline__ void load_queries(const AttendJob &j, AttnShared *sh,
         float amax = 0.f;
         const int row = pc.row0 + n;
         if (n < pc.rows) {
-            const uint16_t *q = j.q + (int64_t)(pc.first + row / j.G) * j.qts +
-                                (int64_t)(pc.h * j.G + row % j.G) * j.qhs + lane * E;
+            const int tok = pc.first + row / j.G, head = pc.h * j.G + row % j.G;
+            if (lane == 0) sh->at[n] = tok * j.Hq + head;
+            const uint16_t *q = j.q + (int64_t)tok * j.qts + (int64_t)head * j.qhs + lane * E;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 x[i] = __uint_as_float((uint32_t)q[i] << 16);
@@ -623,10 +769,11 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->s_full[i], 1);
+            // (a warp of a tile's only warpgroup arrives twice)
             mbar_init(&sh->s_empty[i], kSoftWarps);
+            mbar_init(&sh->p_full[i], kSoftWarps);
+            mbar_init(&sh->pv_done[i], 1);
         }
-        mbar_init(&sh->p_full, kSoftWarps);
-        mbar_init(&sh->pv_done, 1);
         mbar_init(&sh->q_full, kSoftWarps);
         mbar_init(&sh->drained, 1);
         mbar_fence_init();
@@ -668,10 +815,9 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         if (w < warp) run += sh->scan[w];
         total += sh->scan[w];
     }
-    const int ctas = (int)(total < (long long)gridDim.x ? total : (long long)gridDim.x);
+    const int ctas = gridDim.x;
     const int me = blockIdx.x;
-    const long long from = me < ctas ? span_at(total, ctas, me) : 0;
-    const long long to = me < ctas ? span_at(total, ctas, me + 1) : 0;
+    const long long from = span_at(total, ctas, me), to = span_at(total, ctas, me + 1);
     if (from < to && run > from && run - own <= from) {
         long long x = from - (run - own);
         int b = b0;
@@ -691,6 +837,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
     walk.start(j, sh, from, to);
     uint32_t it = 0;
     if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         bool ok = true;
         while (ok && walk.next(j, pc)) {
             const int N = (pc.rows + 15) & ~15;
@@ -698,17 +845,20 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
             fence_async();
             bar_or(3, kSoftWarps * 32, false);  // the rows' factors are there
             if (lane == 0) mbar_arrive(&sh->q_full);
-#define SV_SOFT(C)                                                                              \
-    case C:                                                                                     \
-        ok = soft_piece<D, C>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, ok);                    \
+#define SV_SOFT(N16, C, TURNS)                                                                   \
+    case N16:                                                                                   \
+        ok = soft_piece<D, C, TURNS>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, ok);             \
         break;
             switch (N / 16) {
-                SV_SOFT(1) SV_SOFT(2) SV_SOFT(3) SV_SOFT(4) SV_SOFT(5) SV_SOFT(6) SV_SOFT(7)
-                SV_SOFT(8)
+                SV_SOFT(1, 2, true) SV_SOFT(2, 4, true) SV_SOFT(3, 6, true) SV_SOFT(4, 8, true)
+                SV_SOFT(5, 5, false) SV_SOFT(6, 6, false) SV_SOFT(7, 7, false) SV_SOFT(8, 8, false)
             }
 #undef SV_SOFT
         }
-    } else if (warp == kSoftWarps) {
+    } else if (warp >= kSoftWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+    }
+    if (warp == kSoftWarps) {
         // ---- producer: the pages of each tile, looked up 32 at a time
         const int per_tile = kTile / j.block;
         const int inner = lane & (per_tile - 1);
@@ -785,7 +935,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 mbar_wait_n(&sh->full_k[i], (it / kAtStages) & 1, 1u << 12);
                 mbar_wait_n(&sh->full_v[i], (it / kAtStages) & 1, 1u << 12);
             }
-    } else if (lane == 0) {
+    } else if (warp == kSoftWarps + 1 && lane == 0) {
         // ---- issuer of the products
         constexpr uint32_t kKinds = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);  // fp32 sums, M = 128
         const uint32_t tmem = sh->tmem;
@@ -797,12 +947,10 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
             const uint32_t id_o = kKinds | (3u << 15) | ((uint32_t)(2 * N >> 3) << 17);
             ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
             ++pieces;
+            if (!ok) break;
             const uint32_t aq = smem_u32(s_q), ap = smem_u32(s_p);
             auto scores = [&](uint32_t i) {
                 const int st = i % kAtStages, sb = i & 1;
-                ok = ok && at_wait(sh, j.err, &sh->full_k[st], (i / kAtStages) & 1);
-                ok = ok && at_wait(sh, j.err, &sh->s_empty[sb], ((i >> 1) & 1) ^ 1);
-                if (!ok) return;
                 tc_fence_after();
                 const uint32_t ak = smem_u32(s_k) + st * 2 * kSide;
 #pragma unroll
@@ -816,23 +964,59 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 tc_commit(&sh->s_full[sb]);
             };
             const int nt = pc.t1 - pc.t0;
-            if (ok) scores(it);
-            for (int i = 0; i < nt && ok; ++i) {
-                const uint32_t x = it + i;
-                if (i + 1 < nt) scores(x + 1);
-                const int st = x % kAtStages;
-                ok = ok && at_wait(sh, j.err, &sh->full_v[st], (x / kAtStages) & 1);
-                ok = ok && at_wait(sh, j.err, &sh->p_full, x & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t av = smem_u32(s_v) + st * 2 * kSide;
-                // D = 64: the second 64 rows read the same values again
+            const bool turns = N <= 64;
+            // Whichever is ready first: the next tile's scores (its keys have
+            // landed, and a score buffer is free) or the next tile's output.
+            // (Waiting for the keys of a later tile here would hold back the
+            // products that free the places of the ones before.)
+            int si = 0, oi = 0;
+            uint32_t tries = 0;
+            while (oi < nt) {
+                bool did = false;
+                if (si < nt) {
+                    const uint32_t x = it + si;
+                    const int st = x % kAtStages, sb = x & 1;
+                    if (mbar_test(&sh->full_k[st], (x / kAtStages) & 1) &&
+                        mbar_test(&sh->s_empty[sb], ((x >> 1) & 1) ^ 1)) {
+                        scores(x);
+                        ++si;
+                        did = true;
+                    }
+                }
+                if (oi < si) {
+                    const uint32_t x = it + oi;
+                    const int st = x % kAtStages, sb = x & 1;
+                    if (mbar_test(&sh->p_full[sb], (x >> 1) & 1) &&
+                        mbar_test(&sh->full_v[st], (x / kAtStages) & 1)) {
+                        tc_fence_after();
+                        const uint32_t av = smem_u32(s_v) + st * 2 * kSide;
+                        const uint32_t apx = ap + (turns ? sb * kTile * 128 : 0);
+                        const uint32_t o = tmem + 256 + (turns ? sb * 128 : 0);
+                        const bool sum = turns ? oi > 1 : oi > 0;
+                        // D = 64: the second 64 rows read the same values again
 #pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    tc_mma(tmem + 256, tc_desc(av + k * 32 * D, 0, 8 * D, kSwz),
-                           tc_desc(ap + k * 32 * 128, kTile * 128, 1024, 2), id_o, i || k);
-                tc_commit(&sh->empty_v[st]);
-                tc_commit(&sh->pv_done);
+                        for (int k = 0; k < kTile / 32; ++k)
+                            tc_mma(o, tc_desc(av + k * 32 * D, 0, 8 * D, kSwz),
+                                   tc_desc(apx + k * 32 * 128, kTile * 128, 1024, 2), id_o,
+                                   sum || k);
+                        tc_commit(&sh->empty_v[st]);
+                        tc_commit(&sh->pv_done[sb]);
+                        ++oi;
+                        did = true;
+                    }
+                }
+                if (did) {
+                    tries = 0;
+                } else if (++tries > kAtSpin || ((tries & 63) == 0 && *(volatile int *)&sh->abort)) {
+                    if (tries > kAtSpin) {
+                        *(volatile int *)&sh->abort = 1;
+                        latch(j.err, SV_ERR_TIMEOUT);
+                    }
+                    ok = false;
+                    break;
+                } else if (tries > 64) {
+                    __nanosleep(32);
+                }
             }
             it += nt;
         }
@@ -900,6 +1084,7 @@ static bool cache_map(CUtensorMap *m, const AttendJob &j, int side)
 
 cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s)
 {
+    sms = sms < 256 ? sms : 256;  // (AttnShared::owner)
     CUtensorMap mk, mv;
     if (!cache_map(&mk, j, 0) || !cache_map(&mv, j, 1)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
