@@ -47,13 +47,13 @@ namespace sv {
 constexpr int kTile = 128;             // tokens of a tile
 constexpr int kRowsMax = 128;          // query rows of a unit
 constexpr int kAtStages = 4;           // tiles in flight
-constexpr int kSoftWarps = 8;          // two warpgroups, each half of the rows
+constexpr int kSoftWarps = 16;         // four warpgroups
 // + producer and issuer, and two idle warps that make up a warpgroup with them
 constexpr int kAtThreads = kSoftWarps * 32 + 128;
-// Registers: the launch gives each thread 168 of the SM's 65,536; the softmax
-// warps keep up to 128 scores and sums each and take what the others leave
-// (128 * 72 + 256 * 216 = 384 * 168).
-constexpr int kAtRegs = 168, kSideRegs = 72, kSoftRegs = 216;
+// Registers: the launch gives each thread 96 of the SM's 65,536; the softmax
+// warps hold up to 32 scores and 32 sums each and take what the others leave
+// (128 * 56 + 512 * 104 <= 640 * 96).
+constexpr int kAtRegs = 96, kSideRegs = 56, kSoftRegs = 104;
 static_assert(128 * kSideRegs + kSoftWarps * 32 * kSoftRegs <= kAtThreads * kAtRegs, "registers");
 constexpr float kNone = -1e30f;        // running maximum before any token
 constexpr uint32_t kAtSpin = 1u << 20; // tries of a wait (a tile takes microseconds)
@@ -69,10 +69,10 @@ struct AttnShared {
     float ks[kAtStages][8], vs[kAtStages][8];  // scales of the tile's pages
     int at[kRowsMax];                  // output row (token * Hq + head), per row
     alignas(16) float c[kRowsMax];     // factor from S to log2 units, per row
-    float wmax[kSoftWarps][64];        // tile maxima per warp and row
-    alignas(16) float mu[kSoftWarps][64];    // running maximum in use, a copy per warp
-    alignas(16) float down[kSoftWarps][64];  // its last move, and the factor 2^-move
-    alignas(16) float fac[kSoftWarps][64];
+    float wmax[kSoftWarps][32];        // tile maxima per warp and row
+    alignas(16) float mu[kSoftWarps][32];    // running maximum in use, a copy per warp
+    alignas(16) float down[kSoftWarps][32];  // its last move, and the factor 2^-move
+    alignas(16) float fac[kSoftWarps][32];
     float sum[2][4][kRowsMax];         // sums of weights: warpgroup, quarter of a tile, row
     float top[2][kRowsMax];            // maximum that they are against
     short owner[256];                  // CTAs of a shared unit's tiles (spans below a tile)
@@ -126,6 +126,15 @@ __device__ __forceinline__ void tc_st8(uint32_t addr, const float *v)
                  : "memory");
 }
 // The registers of the loads before it may be read after it: they pass through.
+__device__ __forceinline__ void tc_ld4(uint32_t addr, float *v)
+{
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
 template <int N>
 __device__ __forceinline__ void tc_wait_ld(float (&v)[N])
 {
@@ -192,6 +201,12 @@ struct SeqWork {
     long long work;          // cost of the sequence
     bool bad;
 };
+// Rows of the products for this many query rows: the two (up to 64) or four
+// warpgroups of a tile have 8 rows each, or 16, 24, 32.
+__device__ __forceinline__ int round_rows(int rows)
+{
+    return rows <= 64 ? (rows + 15) & ~15 : (rows + 31) & ~31;
+}
 // Time of a tile by its rows, as measured: even spans of it are even in time.
 __device__ __forceinline__ int tile_cost(int N) { return 16 + N / 4; }
 
@@ -209,7 +224,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
     s.tiles = (int)(((long long)s.L + kTile - 1) / kTile);
     s.blocks = (int)((all + kRowsMax - 1) / kRowsMax);
     s.rows = s.blocks ? (int)((all + s.blocks - 1) / s.blocks) : 0;
-    s.cost = tile_cost((s.rows + 15) & ~15);
+    s.cost = tile_cost(round_rows(s.rows));
     s.work = (long long)s.tiles * s.blocks * j.H * s.cost;
     return s;
 }
@@ -291,11 +306,14 @@ __host__ __device__ constexpr size_t part_floats(int D) { return (size_t)kRowsMa
 // Softmax side of one piece.  Thread: one token of the tile (TMEM lane) for
 // the weights, one head element for the output.
 //
-// Up to 64 rows (TURNS) the two warpgroups take the tiles in turn, each with
-// all the rows, sums and a running maximum of its own, so that one tile's chain
-// (scores, maximum, weights, products) runs under the other's; above, they
-// share each tile, half of the rows each.  (All rows of a tile in one
-// warpgroup would not fit the registers.)
+// Four warpgroups.  Up to 64 rows (turns) two of them take the even tiles and
+// two the odd ones, each pair with sums and a running maximum of its own, so
+// that one tile's chain (scores, maximum, weights, products) runs under the
+// other's; a warpgroup of a pair has half of the rows.  Above, all four share
+// each tile, a quarter of the rows each (a second set of sums would not fit the
+// tensor memory).  So a thread holds 8 to 32 rows, and four warps hide each
+// other's latencies on every scheduler: two warpgroups with up to 64 rows a
+// thread took 1.4 to 1.9 times as long.
 //
 // The running maximum M moves lazily: weights are taken as 2^(y - M + 4.5), and
 // M moves only when one would pass 2^8.5 (e4m3 ends at 448).  So most tiles
@@ -330,30 +348,29 @@ __device__ __forceinline__ void warp_sum_rows(float (&v)[N], int lane)
     }
 }
 
-template <int D, int C8, bool TURNS>
+template <int D, int C8>
 __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, char *smem_v,
                                            char *smem_p, const Piece &pc, uint32_t &it,
-                                           int stage_bytes, int ctas, bool ok)
+                                           int stage_bytes, int ctas, bool turns, bool ok)
 {
     constexpr int R = C8 * 8;                   // rows of this warpgroup
-    constexpr int kWays = TURNS ? 1 : 2;        // warpgroups of a tile
-    constexpr int kHalf = TURNS ? R / 2 : R;    // rows of the output of this warpgroup
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = warp >> 2, quarter = warp & 3;
+    const int part_no = turns ? g & 1 : g, par = turns ? g >> 1 : 0;
     const int tk = quarter * 32 + lane;
-    const int r0 = TURNS ? 0 : g * R;           // first row of this warpgroup
+    const int r0 = part_no * R;                 // first row of this warpgroup
     const uint32_t lanes = sh->tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t o_own = lanes + 256 + g * (TURNS ? 128 : 2 * R);  // R hi columns, then R lo
+    const uint32_t o_own = lanes + 256 + par * 128 + r0 * 2;  // R hi columns, then R lo
+    const uint32_t arrivals = turns ? 2 : 1;    // of a warp: 16 a tile
     const int ctx = pc.L - pc.n;
     const int page_in = tk >> (31 - __clz(j.block));
-    char *p_row = smem_p + (TURNS ? g * (kTile * 128) : 0) + tk * 128;
+    char *p_row = smem_p + par * (kTile * 128) + tk * 128;
     float *mu = sh->mu[warp];
 
     float l[R];
 #pragma unroll
     for (int n = 0; n < R; ++n) l[n] = 0.f;
     mu[lane] = kNone;                           // (kept less kUnit)
-    mu[lane + 32] = kNone;
     __syncwarp();
     uint32_t mine = 0;                          // tiles this warpgroup has taken
     bool unset = true;                          // a row has seen no token yet
@@ -361,7 +378,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
 
     for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = it % kAtStages, sb = it & 1;
-        if (TURNS && sb != g) continue;
+        if (turns && sb != par) continue;
         ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
         ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
         tc_fence_after();
@@ -375,17 +392,17 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         asm("lg2.approx.f32 %0, %1;" : "=f"(vl) : "f"(vs));
         asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));
         // tiles that reach the new tokens: which rows see this token
-        unsigned long long sees = ~0ull;
+        uint32_t sees = ~0u;
         const bool edge = p0 + kTile > ctx;
         if (edge) {
             sees = 0;
             if (pos < pc.L) {
                 if (pos < ctx) {
-                    sees = ~0ull;
+                    sees = ~0u;
                 } else if (!j.mask) {
                     // rows (row0 + n) / G >= pos - ctx
                     const long long from = (long long)(pos - ctx) * j.G - pc.row0 - r0;
-                    sees = from <= 0 ? ~0ull : from >= 64 ? 0ull : ~0ull << from;
+                    sees = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << (int)from;
                 } else {
                     const int k = pos - ctx;
                     if ((k >> 5) < j.words) {
@@ -394,7 +411,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                         for (int n = 0; n < rows; ++n) {
                             const int64_t tok = pc.first + (pc.row0 + r0 + n) / j.G;
                             const uint32_t m = j.mask[tok * j.words + (k >> 5)];
-                            sees |= (unsigned long long)((m >> (k & 31)) & 1u) << n;
+                            sees |= ((m >> (k & 31)) & 1u) << n;
                         }
                     }
                 }
@@ -419,10 +436,9 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
             }
             if (edge) {
-                const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
 #pragma unroll
                 for (int n = 0; n < R; ++n)
-                    if (!((n < 32 ? s0 : s1) & (1u << (n & 31)))) y[n] = -INFINITY;
+                    if (!(sees & (1u << n))) y[n] = -INFINITY;
             }
         };
         scale_scores(true);
@@ -437,35 +453,29 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 scale_scores(false);
             }
             // the tile's maximum of each row: over the warp's tokens, then four warps
-            float keep[2] = {-INFINITY, -INFINITY};
+            float keep = -INFINITY;
 #pragma unroll
             for (int n = 0; n < R; ++n) {
                 float m;
                 asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(y[n]));
-                if (lane == (n & 31)) keep[n >> 5] = m;
+                if (lane == n) keep = m;
             }
-            sh->wmax[warp][lane] = keep[0];
-            if (R > 32) sh->wmax[warp][lane + 32] = keep[1];
+            sh->wmax[warp][lane] = keep;
             if (bar_or(1 + g, 128, !ok)) {
                 ok = false;
                 break;
             }
             float *down = sh->down[warp], *fac = sh->fac[warp];
-            bool none = false;
+            float m = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < (R > 32 ? 2 : 1); ++k) {
-                const int n = lane + 32 * k;
-                float m = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) m = fmaxf(m, sh->wmax[g * 4 + w][n]);
-                // (n >= R: padding of the arrays, not used)
-                const float old = mu[n];
-                const float now = unset ? fmaxf(old, m - kUnit) : old + fmaxf(m - kUnit, 0.f);
-                mu[n] = now;
-                down[n] = unset ? now : now - old;  // from the scores at hand
-                fac[n] = ex2f(old - now);
-                none = none || (n < R && now == kNone);
-            }
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, sh->wmax[g * 4 + w][lane]);
+            // (lanes from R on: padding of the arrays, not used)
+            const float old = mu[lane];
+            const float now = unset ? fmaxf(old, m - kUnit) : old + fmaxf(m - kUnit, 0.f);
+            mu[lane] = now;
+            down[lane] = unset ? now : now - old;  // from the scores at hand
+            fac[lane] = ex2f(old - now);
+            const bool none = lane < R && now == kNone;
             unset = __any_sync(0xFFFFFFFFu, none);
             __syncwarp();
 #pragma unroll
@@ -476,7 +486,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 l[n] *= f4.x; l[n + 1] *= f4.y; l[n + 2] *= f4.z; l[n + 3] *= f4.w;
             }
             if (mine > 0) {
-                const uint32_t before = TURNS ? it - 2 : it - 1;
+                const uint32_t before = turns ? it - 2 : it - 1;
                 ok = at_wait(sh, j.err, &sh->pv_done[before & 1], (before >> 1) & 1);
                 tc_fence_after();
 #pragma unroll 1
@@ -494,10 +504,10 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         }
         tc_fence_before();
         __syncwarp();
-        if (lane < 3 - kWays) mbar_arrive(&sh->s_empty[sb]);
+        if (lane < arrivals) mbar_arrive(&sh->s_empty[sb]);
         // the weights' place is free once the products before have read it
         if (mine > 0) {
-            const uint32_t before = TURNS ? it - 2 : it - 1;
+            const uint32_t before = turns ? it - 2 : it - 1;
             ok = ok && at_wait(sh, j.err, &sh->pv_done[before & 1], (before >> 1) & 1);
         }
         ++mine;
@@ -547,20 +557,20 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         const int valid = pc.L - p0;
         if (valid < kTile) {
             char *v = smem_v + (size_t)st * stage_bytes;
-            const int at = TURNS ? tk : tid;
-            for (int i = valid * (D / 16) + at; i < kTile * (D / 16); i += 128 * kWays)
+            const int at = turns ? part_no * 128 + tk : tid;
+            for (int i = valid * (D / 16) + at; i < kTile * (D / 16); i += turns ? 256 : 512)
                 reinterpret_cast<uint4 *>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async();
         __syncwarp();
-        if (lane < 3 - kWays) mbar_arrive(&sh->p_full[sb]);
+        if (lane < arrivals) mbar_arrive(&sh->p_full[sb]);
     }
 
     // ---- the piece's sums
     it = it0 + (uint32_t)(pc.t1 - pc.t0);
     if (mine > 0 && ok) {
         // the last tile of this warpgroup
-        const uint32_t last = TURNS && ((it - 1) & 1) != (uint32_t)g ? it - 2 : it - 1;
+        const uint32_t last = turns && ((it - 1) & 1) != (uint32_t)par ? it - 2 : it - 1;
         ok = at_wait(sh, j.err, &sh->pv_done[last & 1], (last >> 1) & 1);
     }
     warp_sum_rows(l, lane);
@@ -570,14 +580,11 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             // which row the halvings left here: bits 4, 3, 2 of the lane
             const int n = ((lane >> 4) & 1) * (R / 2) + ((lane >> 3) & 1) * (R / 4) +
                           ((lane >> 2) & 1) * (R / 8) + i;
-            sh->sum[TURNS ? g : 0][quarter][r0 + n] = l[i];
+            sh->sum[par][quarter][r0 + n] = l[i];
         }
     }
-    if (quarter == 0) {
-        if (lane < R) sh->top[TURNS ? g : 0][r0 + lane] = mu[lane];
-        if (lane + 32 < R) sh->top[TURNS ? g : 0][r0 + lane + 32] = mu[lane + 32];
-    }
-    if (bar_or(3, kSoftWarps * 32, !ok)) return false;
+    if (quarter == 0 && lane < R) sh->top[par][r0 + lane] = mu[lane];
+    if (bar_or(5, kSoftWarps * 32, !ok)) return false;
     tc_fence_after();
 
     const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
@@ -592,45 +599,54 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     // a unit that starts before this CTA's span is its first, else its last
     float *part = j.part + ((size_t)me * 2 + (me == c0 ? 1 : 0)) * pf;
     const int d = tk;  // head element of this lane (D = 64: lanes 64.. hold copies)
-    const int w0 = g * kHalf;  // rows that this warpgroup writes
-    // (a warpgroup that had no tile has no sums)
-    const bool has[2] = {!TURNS || pc.t1 - pc.t0 > 1 || (it0 & 1) == 0,
-                         TURNS && (pc.t1 - pc.t0 > 1 || (it0 & 1) == 1)};
+    // (a pair that had no tile has no sums)
+    const int nt = pc.t1 - pc.t0;
+    const bool has0 = !turns || nt > 1 || (it0 & 1) == 0;
+    const bool has1 = turns && (nt > 1 || (it0 & 1) == 1);
+    // rows this warpgroup writes, 4 at a time: all of its own, or half of those
+    // that it shares with the other pair
+    const int w0 = r0 + (turns ? par * (R / 2) : 0), w1 = w0 + (turns ? R / 2 : R);
 #pragma unroll 1
-    for (int c = 0; c < kHalf / 8; ++c) {
-        float o[8];
-        float hi[8], lo[8], fac[2][8];
+    for (int w = w0; w < w1; w += 4) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f}, f0[4], f1[4], v[8];
+        const uint32_t col = lanes + 256 + r0 * 2 + (w - r0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = 0.f;
-#pragma unroll
-        for (int way = 0; way < 3 - kWays; ++way) {
-            const uint32_t col = TURNS ? lanes + 256 + way * 128 + w0 + c * 8 : o_own + c * 8;
-            if (!has[way]) continue;
-            tc_ld8(col, hi);
-            tc_ld8(col + R, lo);
-            tc_wait_ld(hi);
-            tc_wait_ld(lo);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int n = w0 + c * 8 + i;
-                const float m = TURNS ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
-                fac[way][i] = TURNS ? ex2f(sh->top[way][n] - m) : 1.f;
-                o[i] = fmaf(fac[way][i], fmaf(lo[i], 0.0625f, hi[i]), o[i]);
+        for (int i = 0; i < 4; ++i) {
+            f0[i] = has0 ? 1.f : 0.f;
+            f1[i] = 0.f;
+            if (turns) {
+                const float m = fmaxf(sh->top[0][w + i], sh->top[1][w + i]);
+                f0[i] = has0 ? ex2f(sh->top[0][w + i] - m) : 0.f;
+                f1[i] = has1 ? ex2f(sh->top[1][w + i] - m) : 0.f;
             }
         }
+        if (has0) {
+            tc_ld4(col, v);
+            tc_ld4(col + R, v + 4);
+            tc_wait_ld(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int n = w0 + c * 8 + i;
+            for (int i = 0; i < 4; ++i) o[i] = f0[i] * fmaf(v[4 + i], 0.0625f, v[i]);
+        }
+        if (has1) {
+            tc_ld4(col + 128, v);
+            tc_ld4(col + 128 + R, v + 4);
+            tc_wait_ld(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = fmaf(f1[i], fmaf(v[4 + i], 0.0625f, v[i]), o[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = w + i;
             if (n >= pc.rows || d >= D) continue;
             float s = 0.f;
-#pragma unroll
-            for (int way = 0; way < 3 - kWays; ++way)
-                if (has[way])
-                    s = fmaf(fac[way][i],
-                             (sh->sum[way][0][n] + sh->sum[way][1][n]) +
-                                 (sh->sum[way][2][n] + sh->sum[way][3][n]),
-                             s);
-            const float m = TURNS ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
+            if (has0)
+                s = f0[i] * ((sh->sum[0][0][n] + sh->sum[0][1][n]) +
+                             (sh->sum[0][2][n] + sh->sum[0][3][n]));
+            if (has1)
+                s = fmaf(f1[i], (sh->sum[1][0][n] + sh->sum[1][1][n]) +
+                                    (sh->sum[1][2][n] + sh->sum[1][3][n]), s);
+            const float m = turns ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
             if (whole) {
                 const int64_t at = sh->at[n];
                 j.out[at * D + d] = __bfloat16_as_ushort(
@@ -648,12 +664,12 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     }
     tc_fence_before();
     if (whole) {
-        bar_or(3, kSoftWarps * 32, false);  // sum and top are free again
+        bar_or(5, kSoftWarps * 32, false);  // sum and top are free again
         return true;
     }
     // ---- a shared unit: the last CTA to arrive joins the parts
     __threadfence();
-    bar_or(3, kSoftWarps * 32, false);
+    bar_or(5, kSoftWarps * 32, false);
     if (tid == 0) {
         const unsigned seen = atomicAdd(&j.arrived[c0], 1u);
         sh->last = seen == (unsigned)(owners - 1);
@@ -663,7 +679,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     if (each)
         for (int k = tid; k < owners; k += kSoftWarps * 32)
             sh->owner[k] = (short)span_owner(sh->total, ctas, pc.unit0 + (long long)k * pc.cost);
-    bar_or(3, kSoftWarps * 32, false);
+    bar_or(5, kSoftWarps * 32, false);
     if (!sh->last) return true;
 #pragma unroll 1
     for (int i = tid; i < pc.rows * D; i += kSoftWarps * 32) {
@@ -769,7 +785,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->s_full[i], 1);
-            // (a warp of a tile's only warpgroup arrives twice)
+            // (a warp arrives twice where two warpgroups have a tile)
             mbar_init(&sh->s_empty[i], kSoftWarps);
             mbar_init(&sh->p_full[i], kSoftWarps);
             mbar_init(&sh->pv_done[i], 1);
@@ -840,18 +856,18 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         bool ok = true;
         while (ok && walk.next(j, pc)) {
-            const int N = (pc.rows + 15) & ~15;
+            const int N = round_rows(pc.rows);
             load_queries<D>(j, sh, s_q, pc, N);
             fence_async();
-            bar_or(3, kSoftWarps * 32, false);  // the rows' factors are there
+            bar_or(5, kSoftWarps * 32, false);  // the rows' factors are there
             if (lane == 0) mbar_arrive(&sh->q_full);
-#define SV_SOFT(N16, C, TURNS)                                                                   \
-    case N16:                                                                                   \
-        ok = soft_piece<D, C, TURNS>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, ok);             \
+            const bool turns = N <= 64;
+#define SV_SOFT(C)                                                                              \
+    case C:                                                                                     \
+        ok = soft_piece<D, C>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, turns, ok);             \
         break;
-            switch (N / 16) {
-                SV_SOFT(1, 2, true) SV_SOFT(2, 4, true) SV_SOFT(3, 6, true) SV_SOFT(4, 8, true)
-                SV_SOFT(5, 5, false) SV_SOFT(6, 6, false) SV_SOFT(7, 7, false) SV_SOFT(8, 8, false)
+            switch (N / (turns ? 16 : 32)) {
+                SV_SOFT(1) SV_SOFT(2) SV_SOFT(3) SV_SOFT(4)
             }
 #undef SV_SOFT
         }
@@ -942,7 +958,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         bool ok = true;
         uint32_t pieces = 0;
         while (ok && walk.next(j, pc)) {
-            const int N = (pc.rows + 15) & ~15;
+            const int N = round_rows(pc.rows);
             const uint32_t id_s = kKinds | ((uint32_t)(N >> 3) << 17);
             const uint32_t id_o = kKinds | (3u << 15) | ((uint32_t)(2 * N >> 3) << 17);
             ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
