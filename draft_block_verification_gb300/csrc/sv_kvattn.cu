@@ -44,11 +44,11 @@
 
 namespace sv {
 
-constexpr int kTile = 128;             // tokens of a tile
+constexpr int kTile = 128;             // tokens of a tile (>> 7 below)
 constexpr int kRowsMax = 128;          // query rows of a unit
 constexpr int kAtStages = 4;           // tiles in flight
 constexpr int kSoftWarps = 16;         // four warpgroups
-// + producer and issuer, and two idle warps that make up a warpgroup with them
+// + a producer, two issuers, and an idle warp that makes up a warpgroup with them
 constexpr int kAtThreads = kSoftWarps * 32 + 128;
 // Registers: the launch gives each thread 96 of the SM's 65,536; the softmax
 // warps hold up to 32 scores and 32 sums each and take what the others leave
@@ -60,7 +60,7 @@ constexpr uint32_t kAtSpin = 1u << 20; // tries of a wait (a tile takes microsec
 
 struct AttnShared {
     uint64_t full_k[kAtStages], full_v[kAtStages], empty_k[kAtStages], empty_v[kAtStages];
-    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, drained;
+    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, drained[2];
     uint32_t tmem;
     int abort;
     int last;                          // this CTA joins the unit's parts
@@ -194,6 +194,13 @@ __device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar,
 // ---------------------------------------------------------------------------
 // The units of a call.
 // ---------------------------------------------------------------------------
+// Quotient of non-negative numbers; 64-bit division costs thousands of cycles.
+__device__ __forceinline__ long long div_pos(long long a, long long b)
+{
+    if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 struct SeqWork {
     int n, L, first;         // new tokens, tokens, first row of q
     int tiles, blocks, rows; // tiles of a unit, row blocks, rows of a block
@@ -218,12 +225,12 @@ __device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
     s.L = j.kv_len[b];
     s.n = end - s.first;
     s.bad = s.first < 0 || end > j.T || s.n < 0 || s.L < s.n ||
-            (s.L + (long long)j.block - 1) / j.block > j.cols;
+            ((s.L + (long long)j.block - 1) >> (31 - __clz(j.block))) > j.cols;
     if (s.bad) s.n = 0;
     const long long all = (long long)s.n * j.G;
-    s.tiles = (int)(((long long)s.L + kTile - 1) / kTile);
-    s.blocks = (int)((all + kRowsMax - 1) / kRowsMax);
-    s.rows = s.blocks ? (int)((all + s.blocks - 1) / s.blocks) : 0;
+    s.tiles = (int)(((long long)s.L + kTile - 1) >> 7);
+    s.blocks = (int)((all + kRowsMax - 1) >> 7);
+    s.rows = s.blocks <= 1 ? (int)all : (int)div_pos(all + s.blocks - 1, s.blocks);
     s.cost = tile_cost(round_rows(s.rows));
     s.work = (long long)s.tiles * s.blocks * j.H * s.cost;
     return s;
@@ -240,8 +247,8 @@ struct Piece {
     int L, n, first;
 };
 struct PieceWalk {
-    long long pos, end, x;   // a tile's start, the span's end, the tile's start within b
-    int b;
+    long long pos, end;      // the next tile's start, the span's end
+    int b, h, block, tile;   // the next tile
     SeqWork s;
     __device__ __forceinline__ void start(const AttendJob &j, const AttnShared *sh,
                                           long long from, long long to)
@@ -249,38 +256,49 @@ struct PieceWalk {
         pos = from;
         end = to;
         b = sh->first_b;
-        x = sh->first_x;
+        h = block = tile = 0;
         if (pos < end) {
             s = seq_work(j, b);
             // on to the first tile that starts within the span
-            const long long on = (s.cost - x % s.cost) % s.cost;
-            x += on;
-            pos += on;
+            const long long x = sh->first_x;
+            long long t = div_pos(x + s.cost - 1, s.cost);
+            pos += t * s.cost - x;
+            const long long u = div_pos(t, s.tiles);
+            tile = (int)(t - u * s.tiles);
+            h = (int)div_pos(u, s.blocks);
+            block = (int)(u - (long long)h * s.blocks);
         }
     }
     __device__ __forceinline__ bool next(const AttendJob &j, Piece &p)
     {
         if (pos >= end) return false;
-        while (x >= s.work) {
-            x -= s.work;
+        while (h >= j.H || s.work == 0) {
             s = seq_work(j, ++b);
+            h = 0;
         }
-        const long long tile = x / s.cost, u = tile / s.tiles;
-        p.t0 = (int)(tile - u * s.tiles);
-        const long long left = (end - pos + s.cost - 1) / s.cost;
-        p.t1 = (int)(s.tiles - p.t0 < left ? s.tiles : p.t0 + left);
+        const long long left = end - pos, all = (long long)(s.tiles - tile) * s.cost;
+        const int n = left >= all ? s.tiles - tile : (int)div_pos(left + s.cost - 1, s.cost);
+        p.t0 = tile;
+        p.t1 = tile + n;
         p.b = b;
-        p.h = (int)(u / s.blocks);
-        p.row0 = (int)(u - (long long)p.h * s.blocks) * s.rows;
+        p.h = h;
+        p.row0 = block * s.rows;
         p.rows = min(s.rows, s.n * j.G - p.row0);
         p.tiles = s.tiles;
         p.cost = s.cost;
-        p.unit0 = pos - (long long)p.t0 * s.cost;
+        p.unit0 = pos - (long long)tile * s.cost;
         p.L = s.L;
         p.n = s.n;
         p.first = s.first;
-        pos += (long long)(p.t1 - p.t0) * s.cost;
-        x += (long long)(p.t1 - p.t0) * s.cost;
+        pos += (long long)n * s.cost;
+        tile += n;
+        if (tile == s.tiles) {
+            tile = 0;
+            if (++block == s.blocks) {
+                block = 0;
+                ++h;
+            }
+        }
         return true;
     }
 };
@@ -288,11 +306,11 @@ struct PieceWalk {
 // Span of CTA i of `ctas` over `total` tiles, and the CTA that owns a tile.
 __device__ __forceinline__ long long span_at(long long total, int ctas, int i)
 {
-    return total * i / ctas;
+    return div_pos(total * i, ctas);
 }
 __device__ __forceinline__ int span_owner(long long total, int ctas, long long x)
 {
-    int i = (int)(x * ctas / total);
+    int i = (int)div_pos(x * ctas, total);
     while (i + 1 < ctas && span_at(total, ctas, i + 1) <= x) ++i;
     while (i > 0 && span_at(total, ctas, i) > x) --i;
     return i;
@@ -348,6 +366,37 @@ __device__ __forceinline__ void warp_sum_rows(float (&v)[N], int lane)
     }
 }
 
+// R scores of this token: one product, or (lo > 0) the sum of the products with
+// the queries' hi and lo parts, lo columns further.
+template <int C8>
+__device__ __forceinline__ void load_scores(float (&y)[C8 * 8], uint32_t col, uint32_t lo)
+{
+    if (!lo) {
+#pragma unroll
+        for (int c = 0; c < C8; ++c) tc_ld8(col + c * 8, y + c * 8);
+        tc_wait_ld(y);
+        return;
+    }
+    constexpr int kStep = C8 % 2 ? 8 : 16;
+#pragma unroll
+    for (int n = 0; n < C8 * 8; n += kStep) {
+        float h[kStep], l[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; i += 8) {
+            tc_ld8(col + n + i, h + i);
+            tc_ld8(col + lo + n + i, l + i);
+        }
+        tc_wait_ld(h);
+        tc_wait_ld(l);
+#pragma unroll
+        for (int i = 0; i < kStep; i += 2) {
+            const float2 s = add2(make_float2(h[i], h[i + 1]), make_float2(l[i], l[i + 1]));
+            y[n + i] = s.x;
+            y[n + i + 1] = s.y;
+        }
+    }
+}
+
 template <int D, int C8>
 __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, char *smem_v,
                                            char *smem_p, const Piece &pc, uint32_t &it,
@@ -383,8 +432,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
         tc_fence_after();
         float y[R];
-#pragma unroll
-        for (int c = 0; c < C8; ++c) tc_ld8(lanes + sb * 128 + r0 + c * 8, y + c * 8);
+        load_scores<C8>(y, lanes + sb * 128 + r0, turns ? 2 * R : 0);
         const int p0 = t * kTile, pos = p0 + tk;
         const float ks = sh->ks[st][page_in];
         const float vs = fminf(fmaxf(sh->vs[st][page_in], 0x1p-60f), 0x1p60f);
@@ -419,7 +467,6 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         }
         // scores in log2 units, the value's scale included, against the maximum in use
         auto scale_scores = [&](bool against) {
-            tc_wait_ld(y);
             const float2 a2 = make_float2(ks, ks), v2 = make_float2(vl, vl);
 #pragma unroll
             for (int n = 0; n < R; n += 4) {
@@ -448,8 +495,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         if (bar_or(1 + g, 128, !ok || top > kMost)) {
             // a row without a maximum: its scores against none
             if (unset) {
-#pragma unroll
-                for (int c = 0; c < C8; ++c) tc_ld8(lanes + sb * 128 + r0 + c * 8, y + c * 8);
+                load_scores<C8>(y, lanes + sb * 128 + r0, turns ? 2 * R : 0);
                 scale_scores(false);
             }
             // the tile's maximum of each row: over the warp's tokens, then four warps
@@ -588,16 +634,19 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     tc_fence_after();
 
     const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
-    const int c0 = span_owner(sh->total, ctas, pc.unit0);
-    const int c1 = span_owner(sh->total, ctas, pc.unit0 + (long long)(pc.tiles - 1) * pc.cost);
-    // Spans at least a tile long leave no CTA between c0 and c1 without a tile;
-    // in shorter ones every tile has a CTA of its own.
-    const bool each = pc.cost > sh->total / ctas;
-    const int owners = each ? pc.tiles : c1 - c0 + 1;
-    const int me = blockIdx.x;
-    const size_t pf = part_floats(D);
-    // a unit that starts before this CTA's span is its first, else its last
-    float *part = j.part + ((size_t)me * 2 + (me == c0 ? 1 : 0)) * pf;
+    int c0 = 0, c1 = 0, owners = 0;  // the CTAs that share the unit
+    bool each = false;
+    float *part = nullptr;
+    if (!whole) {
+        c0 = span_owner(sh->total, ctas, pc.unit0);
+        c1 = span_owner(sh->total, ctas, pc.unit0 + (long long)(pc.tiles - 1) * pc.cost);
+        // Spans at least a tile long leave no CTA between c0 and c1 without a
+        // tile; in shorter ones every tile has a CTA of its own.
+        each = pc.cost > div_pos(sh->total, ctas);
+        owners = each ? pc.tiles : c1 - c0 + 1;
+        // a unit that starts before this CTA's span is its first, else its last
+        part = j.part + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * part_floats(D);
+    }
     const int d = tk;  // head element of this lane (D = 64: lanes 64.. hold copies)
     // (a pair that had no tile has no sums)
     const int nt = pc.t1 - pc.t0;
@@ -687,7 +736,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         float m = kNone, s = 0.f, o = 0.f;
         for (int k = 0; k < owners; ++k) {
             const int c = each ? sh->owner[k] : c0 + k;
-            const float *q = j.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * pf;
+            const float *q = j.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * part_floats(D);
             const float mc = __ldcg(q + (size_t)kRowsMax * D + n);
             const float sc = __ldcg(q + (size_t)kRowsMax * (D + 1) + n);
             const float oc = __ldcg(q + (size_t)n * D + e);
@@ -753,10 +802,10 @@ __device__ __forceinline__ void load_queries(const AttendJob &j, AttnShared *sh,
         char *at = smem_q + n * D + (((byte >> 4) ^ sw) << 4) + (byte & 15);
         if (E == 4) {
             *reinterpret_cast<uint32_t *>(at) = hi;
-            *reinterpret_cast<uint32_t *>(at + kRowsMax * D) = lo;
+            *reinterpret_cast<uint32_t *>(at + N * D) = lo;
         } else {
             *reinterpret_cast<uint16_t *>(at) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t *>(at + kRowsMax * D) = (uint16_t)lo;
+            *reinterpret_cast<uint16_t *>(at + N * D) = (uint16_t)lo;
         }
     }
 }
@@ -791,7 +840,8 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
             mbar_init(&sh->pv_done[i], 1);
         }
         mbar_init(&sh->q_full, kSoftWarps);
-        mbar_init(&sh->drained, 1);
+        mbar_init(&sh->drained[0], 1);
+        mbar_init(&sh->drained[1], 1);
         mbar_fence_init();
         sh->abort = 0;
         sh->first_b = 0;
@@ -876,11 +926,11 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
     }
     if (warp == kSoftWarps) {
         // ---- producer: the pages of each tile, looked up 32 at a time
-        const int per_tile = kTile / j.block;
+            const int per_tile = kTile >> (31 - __clz(j.block));
         const int inner = lane & (per_tile - 1);
         bool ok = true;
         while (ok && walk.next(j, pc)) {
-            const int last = (pc.L + j.block - 1) / j.block;  // pages of the sequence
+                const int last = (int)((pc.L + (long long)j.block - 1) >> (31 - __clz(j.block)));  // pages of the sequence
             const int32_t *tab = j.table + (int64_t)pc.b * j.cols;
             auto window = [&](int w0, int &page, float &ks, float &vs) {
                 page = w0 + lane < last ? tab[w0 + lane] : -1;
@@ -952,94 +1002,83 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 mbar_wait_n(&sh->full_v[i], (it / kAtStages) & 1, 1u << 12);
             }
     } else if (warp == kSoftWarps + 1 && lane == 0) {
-        // ---- issuer of the products
+        // ---- issuer of the scores.  (One thread for both products would wait
+        // with each for the other's inputs; issuing a product takes it some
+        // seventy cycles, a commit almost as many.)
         constexpr uint32_t kKinds = (1u << 4) | ((uint32_t)(kTile >> 4) << 24);  // fp32 sums, M = 128
         const uint32_t tmem = sh->tmem;
+        const uint64_t dk0 = tc_desc(smem_u32(s_k), 16, 8 * D, kSwz);
+        const uint64_t dq = tc_desc(smem_u32(s_q), 16, 8 * D, kSwz);
         bool ok = true;
         uint32_t pieces = 0;
         while (ok && walk.next(j, pc)) {
             const int N = round_rows(pc.rows);
-            const uint32_t id_s = kKinds | ((uint32_t)(N >> 3) << 17);
-            const uint32_t id_o = kKinds | (3u << 15) | ((uint32_t)(2 * N >> 3) << 17);
+            // Up to 64 rows the queries' two parts stand side by side in one
+            // product: with few rows a product's time is that of reading the
+            // keys from shared memory (64 bytes a cycle), not of its rows.
+            const bool turns = N <= 64;
+            const uint32_t id_s = kKinds | ((uint32_t)((turns ? 2 * N : N) >> 3) << 17);
+            const uint64_t dlo = dq + (uint32_t)(N * D >> 4);
             ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
             ++pieces;
-            if (!ok) break;
-            const uint32_t aq = smem_u32(s_q), ap = smem_u32(s_p);
-            auto scores = [&](uint32_t i) {
-                const int st = i % kAtStages, sb = i & 1;
+#pragma unroll 1
+            for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+                const uint32_t st = it % kAtStages, sb = it & 1;
+                ok = ok && at_wait(sh, j.err, &sh->full_k[st], (it / kAtStages) & 1);
+                ok = ok && at_wait(sh, j.err, &sh->s_empty[sb], ((it >> 1) & 1) ^ 1);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t ak = smem_u32(s_k) + st * 2 * kSide;
+                const uint64_t dk = dk0 + st * (2 * kSide >> 4);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int k = 0; k < D / 32; ++k)
+                    tc_mma(tmem + sb * 128, dk + 2 * k, dq + 2 * k, id_s, k);
+                if (!turns)
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k)
-                        tc_mma(tmem + sb * 128, tc_desc(ak + k * 32, 16, 8 * D, kSwz),
-                               tc_desc(aq + part * kRowsMax * D + k * 32, 16, 8 * D, kSwz), id_s,
-                               part || k);
-                tc_commit(&sh->empty_k[st]);
+                        tc_mma(tmem + sb * 128, dk + 2 * k, dlo + 2 * k, id_s, 1);
                 tc_commit(&sh->s_full[sb]);
-            };
-            const int nt = pc.t1 - pc.t0;
-            const bool turns = N <= 64;
-            // Whichever is ready first: the next tile's scores (its keys have
-            // landed, and a score buffer is free) or the next tile's output.
-            // (Waiting for the keys of a later tile here would hold back the
-            // products that free the places of the ones before.)
-            int si = 0, oi = 0;
-            uint32_t tries = 0;
-            while (oi < nt) {
-                bool did = false;
-                if (si < nt) {
-                    const uint32_t x = it + si;
-                    const int st = x % kAtStages, sb = x & 1;
-                    if (mbar_test(&sh->full_k[st], (x / kAtStages) & 1) &&
-                        mbar_test(&sh->s_empty[sb], ((x >> 1) & 1) ^ 1)) {
-                        scores(x);
-                        ++si;
-                        did = true;
-                    }
-                }
-                if (oi < si) {
-                    const uint32_t x = it + oi;
-                    const int st = x % kAtStages, sb = x & 1;
-                    if (mbar_test(&sh->p_full[sb], (x >> 1) & 1) &&
-                        mbar_test(&sh->full_v[st], (x / kAtStages) & 1)) {
-                        tc_fence_after();
-                        const uint32_t av = smem_u32(s_v) + st * 2 * kSide;
-                        const uint32_t apx = ap + (turns ? sb * kTile * 128 : 0);
-                        const uint32_t o = tmem + 256 + (turns ? sb * 128 : 0);
-                        const bool sum = turns ? oi > 1 : oi > 0;
-                        // D = 64: the second 64 rows read the same values again
-#pragma unroll
-                        for (int k = 0; k < kTile / 32; ++k)
-                            tc_mma(o, tc_desc(av + k * 32 * D, 0, 8 * D, kSwz),
-                                   tc_desc(apx + k * 32 * 128, kTile * 128, 1024, 2), id_o,
-                                   sum || k);
-                        tc_commit(&sh->empty_v[st]);
-                        tc_commit(&sh->pv_done[sb]);
-                        ++oi;
-                        did = true;
-                    }
-                }
-                if (did) {
-                    tries = 0;
-                } else if (++tries > kAtSpin || ((tries & 63) == 0 && *(volatile int *)&sh->abort)) {
-                    if (tries > kAtSpin) {
-                        *(volatile int *)&sh->abort = 1;
-                        latch(j.err, SV_ERR_TIMEOUT);
-                    }
-                    ok = false;
-                    break;
-                } else if (tries > 64) {
-                    __nanosleep(32);
-                }
+                tc_commit(&sh->empty_k[st]);
             }
-            it += nt;
         }
         // after a wait that ran out: products still in flight end before the exit
         if (!ok) {
-            tc_commit(&sh->drained);
-            mbar_wait_n(&sh->drained, 0, 1u << 12);
+            tc_commit(&sh->drained[0]);
+            mbar_wait_n(&sh->drained[0], 0, 1u << 12);
+        }
+    } else if (warp == kSoftWarps + 2 && lane == 0) {
+        // ---- issuer of the outputs
+        constexpr uint32_t kKinds = (1u << 4) | ((uint32_t)(kTile >> 4) << 24) | (3u << 15);
+        const uint32_t tmem = sh->tmem;
+        // D = 64: the second 64 rows read the same values again
+        const uint64_t dv0 = tc_desc(smem_u32(s_v), 0, 8 * D, kSwz);
+        const uint64_t dp0 = tc_desc(smem_u32(s_p), kTile * 128, 1024, 2);
+        bool ok = true;
+        while (ok && walk.next(j, pc)) {
+            const int N = round_rows(pc.rows);
+            const bool turns = N <= 64;
+            const uint32_t id_o = kKinds | ((uint32_t)(2 * N >> 3) << 17);
+            uint32_t done = 0;
+#pragma unroll 1
+            for (int t = pc.t0; t < pc.t1; ++t, ++it, ++done) {
+                const uint32_t st = it % kAtStages, sb = it & 1;
+                ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
+                ok = ok && at_wait(sh, j.err, &sh->p_full[sb], (it >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t dv = dv0 + st * (2 * kSide >> 4);
+                const uint64_t dp = dp0 + (turns ? sb * (kTile * 128 >> 4) : 0u);
+                const uint32_t o = tmem + 256 + (turns ? sb * 128 : 0);
+                const bool sum = done > (turns ? 1u : 0u);
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    tc_mma(o, dv + 2 * D * k, dp + 256 * k, id_o, sum || k);
+                tc_commit(&sh->pv_done[sb]);
+                tc_commit(&sh->empty_v[st]);
+            }
+        }
+        if (!ok) {
+            tc_commit(&sh->drained[1]);
+            mbar_wait_n(&sh->drained[1], 0, 1u << 12);
         }
     }
     tc_fence_before();
