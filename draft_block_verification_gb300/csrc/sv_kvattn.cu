@@ -176,8 +176,10 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool flag)
     return r != 0;
 }
 
-// Bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar, uint32_t parity)
+// Bounded wait that also ends when another role has given up.  (The roles'
+// loops share the instruction caches: what is rarely run is marked so, to lie
+// outside them.)
+__device__ __forceinline__ bool at_wait_on(AttnShared *sh, int *err, uint64_t *bar, uint32_t parity)
 {
     for (uint32_t i = 0; i < kAtSpin; ++i) {
         if (mbar_try(bar, parity)) return true;
@@ -189,6 +191,11 @@ __device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar,
     *(volatile int *)&sh->abort = 1;
     latch(err, SV_ERR_TIMEOUT);
     return false;
+}
+__device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar, uint32_t parity)
+{
+    if (__builtin_expect(mbar_try(bar, parity), 1)) return true;
+    return at_wait_on(sh, err, bar, parity);
 }
 
 // ---------------------------------------------------------------------------
@@ -442,7 +449,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         // tiles that reach the new tokens: which rows see this token
         uint32_t sees = ~0u;
         const bool edge = p0 + kTile > ctx;
-        if (edge) {
+        if (__builtin_expect(edge, 0)) {
             sees = 0;
             if (pos < pc.L) {
                 if (pos < ctx) {
@@ -482,7 +489,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 }
                 y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
             }
-            if (edge) {
+            if (__builtin_expect(edge, 0)) {
 #pragma unroll
                 for (int n = 0; n < R; ++n)
                     if (!(sees & (1u << n))) y[n] = -INFINITY;
@@ -492,7 +499,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         float top = y[0];
 #pragma unroll
         for (int n = 1; n < R; ++n) top = fmaxf(top, y[n]);
-        if (bar_or(1 + g, 128, !ok || top > kMost)) {
+        if (__builtin_expect(bar_or(1 + g, 128, !ok || top > kMost), 0)) {
             // a row without a maximum: its scores against none
             if (unset) {
                 load_scores<C8>(y, lanes + sb * 128 + r0, turns ? 2 * R : 0);
@@ -601,7 +608,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         // values past the sequence's end may be anything (NaN times a weight of
         // 0 would stay): clear them
         const int valid = pc.L - p0;
-        if (valid < kTile) {
+        if (__builtin_expect(valid < kTile, 0)) {
             char *v = smem_v + (size_t)st * stage_bytes;
             const int at = turns ? part_no * 128 + tk : tid;
             for (int i = valid * (D / 16) + at; i < kTile * (D / 16); i += turns ? 256 : 512)
@@ -1032,10 +1039,11 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
                     tc_mma(tmem + sb * 128, dk + 2 * k, dq + 2 * k, id_s, k);
-                if (!turns)
-#pragma unroll
+                if (__builtin_expect(!turns, 0)) {
+#pragma unroll 1
                     for (int k = 0; k < D / 32; ++k)
                         tc_mma(tmem + sb * 128, dk + 2 * k, dlo + 2 * k, id_s, 1);
+                }
                 tc_commit(&sh->s_full[sb]);
                 tc_commit(&sh->empty_k[st]);
             }
