@@ -71,8 +71,7 @@ struct AttnShared {
     alignas(16) float c[kRowsMax];     // factor from S to log2 units, per row
     float wmax[kSoftWarps][32];        // tile maxima per warp and row
     alignas(16) float mu[kSoftWarps][32];    // running maximum in use, a copy per warp
-    alignas(16) float down[kSoftWarps][32];  // its last move, and the factor 2^-move
-    alignas(16) float fac[kSoftWarps][32];
+    alignas(16) float fac[kSoftWarps][32];   // factor of its last move
     float sum[2][4][kRowsMax];         // sums of weights: warpgroup, quarter of a tile, row
     float top[2][kRowsMax];            // maximum that they are against
     short owner[256];                  // CTAs of a shared unit's tiles (spans below a tile)
@@ -373,34 +372,34 @@ __device__ __forceinline__ void warp_sum_rows(float (&v)[N], int lane)
     }
 }
 
-// R scores of this token: one product, or (lo > 0) the sum of the products with
-// the queries' hi and lo parts, lo columns further.
+// Queries' two parts.  Up to 32 rows they stand side by side in one product:
+// with few rows a product's time is that of reading the keys from shared memory
+// (64 bytes a cycle), whatever its rows.  Above, the second part's product adds
+// to the first's, which saves the softmax warps reading and adding it.
+__host__ __device__ constexpr bool stacked(int N) { return N <= 32; }
+
+// R scores of this token; with stacked queries the sum of both parts' products,
+// 2 R columns apart.
 template <int C8>
-__device__ __forceinline__ void load_scores(float (&y)[C8 * 8], uint32_t col, uint32_t lo)
+__device__ __forceinline__ void load_scores(float (&y)[C8 * 8], uint32_t col)
 {
-    if (!lo) {
+    constexpr int R = C8 * 8;
 #pragma unroll
-        for (int c = 0; c < C8; ++c) tc_ld8(col + c * 8, y + c * 8);
+    for (int n = 0; n < R; n += 8) tc_ld8(col + n, y + n);
+    if (stacked(2 * R)) {
+        float l[R];
+#pragma unroll
+        for (int n = 0; n < R; n += 8) tc_ld8(col + 2 * R + n, l + n);
         tc_wait_ld(y);
-        return;
-    }
-    constexpr int kStep = C8 % 2 ? 8 : 16;
-#pragma unroll
-    for (int n = 0; n < C8 * 8; n += kStep) {
-        float h[kStep], l[kStep];
-#pragma unroll
-        for (int i = 0; i < kStep; i += 8) {
-            tc_ld8(col + n + i, h + i);
-            tc_ld8(col + lo + n + i, l + i);
-        }
-        tc_wait_ld(h);
         tc_wait_ld(l);
 #pragma unroll
-        for (int i = 0; i < kStep; i += 2) {
-            const float2 s = add2(make_float2(h[i], h[i + 1]), make_float2(l[i], l[i + 1]));
-            y[n + i] = s.x;
-            y[n + i + 1] = s.y;
+        for (int n = 0; n < R; n += 2) {
+            const float2 s = add2(make_float2(y[n], y[n + 1]), make_float2(l[n], l[n + 1]));
+            y[n] = s.x;
+            y[n + 1] = s.y;
         }
+    } else {
+        tc_wait_ld(y);
     }
 }
 
@@ -426,10 +425,11 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     float l[R];
 #pragma unroll
     for (int n = 0; n < R; ++n) l[n] = 0.f;
-    mu[lane] = kNone;                           // (kept less kUnit)
+    mu[lane] = 0.f;                             // (kept less kUnit)
     __syncwarp();
     uint32_t mine = 0;                          // tiles this warpgroup has taken
-    bool unset = true;                          // a row has seen no token yet
+    bool none = lane < R;                       // row `lane` has seen no token yet
+    bool unset = true;                          // some row has not
     const uint32_t it0 = it;
 
     for (int t = pc.t0; t < pc.t1; ++t, ++it) {
@@ -438,8 +438,6 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
         ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
         tc_fence_after();
-        float y[R];
-        load_scores<C8>(y, lanes + sb * 128 + r0, turns ? 2 * R : 0);
         const int p0 = t * kTile, pos = p0 + tk;
         const float ks = sh->ks[st][page_in];
         const float vs = fminf(fmaxf(sh->vs[st][page_in], 0x1p-60f), 0x1p60f);
@@ -472,21 +470,23 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 }
             }
         }
-        // scores in log2 units, the value's scale included, against the maximum in use
-        auto scale_scores = [&](bool against) {
+        // Scores in log2 units, the value's scale included, against the maximum
+        // in use; again, where that has to move.
+        float y[R];
+        bool stop = false;  // alike in the whole warpgroup
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+            load_scores<C8>(y, lanes + sb * 128 + r0);
             const float2 a2 = make_float2(ks, ks), v2 = make_float2(vl, vl);
+            float top = -INFINITY;
 #pragma unroll
             for (int n = 0; n < R; n += 4) {
                 const float4 c4 = *reinterpret_cast<const float4 *>(&sh->c[r0 + n]);
-                float2 u = make_float2(y[n] * c4.x, y[n + 1] * c4.y);
-                float2 w = make_float2(y[n + 2] * c4.z, y[n + 3] * c4.w);
-                u = fma2(u, a2, v2);
-                w = fma2(w, a2, v2);
-                if (against) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(&mu[n]);
-                    u = add2(u, make_float2(-m4.x, -m4.y));
-                    w = add2(w, make_float2(-m4.z, -m4.w));
-                }
+                const float4 m4 = *reinterpret_cast<const float4 *>(&mu[n]);
+                float2 u = mul2(make_float2(y[n], y[n + 1]), make_float2(c4.x, c4.y));
+                float2 w = mul2(make_float2(y[n + 2], y[n + 3]), make_float2(c4.z, c4.w));
+                u = add2(fma2(u, a2, v2), make_float2(-m4.x, -m4.y));
+                w = add2(fma2(w, a2, v2), make_float2(-m4.z, -m4.w));
                 y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
             }
             if (__builtin_expect(edge, 0)) {
@@ -494,17 +494,11 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 for (int n = 0; n < R; ++n)
                     if (!(sees & (1u << n))) y[n] = -INFINITY;
             }
-        };
-        scale_scores(true);
-        float top = y[0];
+            if (again) break;
 #pragma unroll
-        for (int n = 1; n < R; ++n) top = fmaxf(top, y[n]);
-        if (__builtin_expect(bar_or(1 + g, 128, !ok || top > kMost), 0)) {
-            // a row without a maximum: its scores against none
-            if (unset) {
-                load_scores<C8>(y, lanes + sb * 128 + r0, turns ? 2 * R : 0);
-                scale_scores(false);
-            }
+            for (int n = 0; n < R; ++n) top = fmaxf(top, y[n]);
+            if (__builtin_expect(!bar_or(1 + g, 128, !ok || unset || top > kMost), 1)) break;
+
             // the tile's maximum of each row: over the warp's tokens, then four warps
             float keep = -INFINITY;
 #pragma unroll
@@ -516,26 +510,28 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             sh->wmax[warp][lane] = keep;
             if (bar_or(1 + g, 128, !ok)) {
                 ok = false;
+                stop = true;
                 break;
             }
-            float *down = sh->down[warp], *fac = sh->fac[warp];
+            float *fac = sh->fac[warp];
             float m = -INFINITY;
 #pragma unroll
             for (int w = 0; w < 4; ++w) m = fmaxf(m, sh->wmax[g * 4 + w][lane]);
-            // (lanes from R on: padding of the arrays, not used)
-            const float old = mu[lane];
-            const float now = unset ? fmaxf(old, m - kUnit) : old + fmaxf(m - kUnit, 0.f);
-            mu[lane] = now;
-            down[lane] = unset ? now : now - old;  // from the scores at hand
-            fac[lane] = ex2f(old - now);
-            const bool none = lane < R && now == kNone;
+            // a row's first maximum is taken as it is; later ones only rise.
+            // (Lanes from R on: padding of the arrays, not used.)
+            float move = none ? (m > -INFINITY ? m - kUnit : 0.f) : fmaxf(m - kUnit, 0.f);
+            const float f = none ? 1.f : ex2f(-move);
+            none = none && !(m > -INFINITY);
+            if (lane >= R) move = 0.f;
+            mu[lane] += move;
+            fac[lane] = f;
             unset = __any_sync(0xFFFFFFFFu, none);
+            const unsigned moved = __ballot_sync(0xFFFFFFFFu, lane < R && f != 1.f);
             __syncwarp();
+            if (!moved) continue;
 #pragma unroll
             for (int n = 0; n < R; n += 4) {
-                const float4 d4 = *reinterpret_cast<const float4 *>(&down[n]);
                 const float4 f4 = *reinterpret_cast<const float4 *>(&fac[n]);
-                y[n] -= d4.x; y[n + 1] -= d4.y; y[n + 2] -= d4.z; y[n + 3] -= d4.w;
                 l[n] *= f4.x; l[n + 1] *= f4.y; l[n + 2] *= f4.z; l[n + 3] *= f4.w;
             }
             if (mine > 0) {
@@ -544,17 +540,19 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < 2 * C8; ++c) {
-                    const float *f = fac + (c < C8 ? c : c - C8) * 8;
+                    const int n = (c < C8 ? c : c - C8) * 8;
+                    if (!((moved >> n) & 0xFFu)) continue;
                     float o[8];
                     tc_ld8(o_own + c * 8, o);
                     tc_wait_ld(o);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] *= f[i];
+                    for (int i = 0; i < 8; ++i) o[i] *= fac[n + i];
                     tc_st8(o_own + c * 8, o);
                 }
                 tc_wait_st();
             }
         }
+        if (stop) break;
         tc_fence_before();
         __syncwarp();
         if (lane < arrivals) mbar_arrive(&sh->s_empty[sb]);
@@ -566,42 +564,46 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         ++mine;
         {
             const float2 i2 = make_float2(ivs, ivs);
+            constexpr int kStep = C8 % 2 ? 8 : 16;  // rows of a store
 #pragma unroll
-            for (int c = 0; c < C8; ++c) {
-                uint32_t hi[4], lo[4];
+            for (int c = 0; c < R; c += kStep) {
+                uint32_t hi[kStep / 4], lo[kStep / 4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int n = c * 8 + k * 2;
-                    const float2 p = make_float2(ex2f(y[n]), ex2f(y[n + 1]));
-                    const float2 s = fma2(p, i2, make_float2(l[n], l[n + 1]));
-                    l[n] = s.x;
-                    l[n + 1] = s.y;
-                    uint16_t h8;
-                    uint32_t h16, p16;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(p.y), "f"(p.x));
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p16) : "f"(p.y), "f"(p.x));
-                    // (p - hi) * 16: exact in fp16
-                    __half2 d = __hsub2(*reinterpret_cast<__half2 *>(&p16),
-                                        *reinterpret_cast<__half2 *>(&h16));
-                    d = __hmul2(d, __floats2half2_rn(16.f, 16.f));
-                    uint16_t l8;
-                    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
-                        : "=h"(l8)
-                        : "r"(*reinterpret_cast<uint32_t *>(&d)));
-                    hi[k] = h8;
-                    lo[k] = l8;
+                for (int k = 0; k < kStep / 4; ++k) {
+                    uint16_t h8[2], l8[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int n = c + k * 4 + i * 2;
+                        const float2 p = make_float2(ex2f(y[n]), ex2f(y[n + 1]));
+                        const float2 s = fma2(p, i2, make_float2(l[n], l[n + 1]));
+                        l[n] = s.x;
+                        l[n + 1] = s.y;
+                        uint32_t h16, p16;
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+                            : "=h"(h8[i]) : "f"(p.y), "f"(p.x));
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8[i]));
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p16) : "f"(p.y), "f"(p.x));
+                        // (p - hi) * 16: exact in fp16
+                        __half2 d = __hsub2(*reinterpret_cast<__half2 *>(&p16),
+                                            *reinterpret_cast<__half2 *>(&h16));
+                        d = __hmul2(d, __floats2half2_rn(16.f, 16.f));
+                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+                            : "=h"(l8[i])
+                            : "r"(*reinterpret_cast<uint32_t *>(&d)));
+                    }
+                    hi[k] = h8[0] | ((uint32_t)h8[1] << 16);
+                    lo[k] = l8[0] | ((uint32_t)l8[1] << 16);
                 }
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    const uint32_t *v = part ? lo : hi;
-                    const int col = r0 * 2 + part * R + c * 8;
-                    uint2 w;
-                    w.x = v[0] | (v[1] << 16);
-                    w.y = v[2] | (v[3] << 16);
-                    *reinterpret_cast<uint2 *>(p_row + (col >> 7) * (kTile * 128) +
-                                               ((((col & 127) >> 4) ^ (tk & 7)) << 4) +
-                                               (col & 15)) = w;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t *v = half ? lo : hi;
+                    const int col = r0 * 2 + half * R + c;
+                    char *at = p_row + (col >> 7) * (kTile * 128) +
+                               ((((col & 127) >> 4) ^ (tk & 7)) << 4) + (col & 15);
+                    if (kStep == 16)
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(v[0], v[1], v[kStep / 8], v[kStep / 4 - 1]);
+                    else
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(v[0], v[1]);
                 }
             }
         }
@@ -1020,11 +1022,8 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         uint32_t pieces = 0;
         while (ok && walk.next(j, pc)) {
             const int N = round_rows(pc.rows);
-            // Up to 64 rows the queries' two parts stand side by side in one
-            // product: with few rows a product's time is that of reading the
-            // keys from shared memory (64 bytes a cycle), not of its rows.
-            const bool turns = N <= 64;
-            const uint32_t id_s = kKinds | ((uint32_t)((turns ? 2 * N : N) >> 3) << 17);
+            const bool one = stacked(N);
+            const uint32_t id_s = kKinds | ((uint32_t)((one ? 2 * N : N) >> 3) << 17);
             const uint64_t dlo = dq + (uint32_t)(N * D >> 4);
             ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
             ++pieces;
@@ -1039,8 +1038,8 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)
                     tc_mma(tmem + sb * 128, dk + 2 * k, dq + 2 * k, id_s, k);
-                if (__builtin_expect(!turns, 0)) {
-#pragma unroll 1
+                if (!one) {
+#pragma unroll
                     for (int k = 0; k < D / 32; ++k)
                         tc_mma(tmem + sb * 128, dk + 2 * k, dlo + 2 * k, id_s, 1);
                 }
