@@ -39,6 +39,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "sv_common.cuh"
 #include "sv_kv.cuh"
 
@@ -432,9 +434,16 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     bool unset = true;                          // some row has not
     const uint32_t it0 = it;
 
-    for (int t = pc.t0; t < pc.t1; ++t, ++it) {
-        const int st = it % kAtStages, sb = it & 1;
-        if (turns && sb != par) continue;
+    bool stop = false;                          // alike in the whole warpgroup
+    // The loop over tiles, in a copy for those that every row sees whole and
+    // one for the last ones, which reach the new tokens.  (The code between the
+    // hot instructions of a loop costs instruction cache.)
+    auto tiles = [&](auto is_edge, int from, int to) {
+    constexpr bool edge = decltype(is_edge)::value;
+#pragma unroll 1
+    for (int t = from; t < to && !stop; t += turns ? 2 : 1) {
+        const uint32_t it = it0 + (uint32_t)(t - pc.t0);
+        const uint32_t st = it % kAtStages, sb = it & 1;
         ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
         ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
         tc_fence_after();
@@ -444,10 +453,8 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         float vl, ivs;
         asm("lg2.approx.f32 %0, %1;" : "=f"(vl) : "f"(vs));
         asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));
-        // tiles that reach the new tokens: which rows see this token
-        uint32_t sees = ~0u;
-        const bool edge = p0 + kTile > ctx;
-        if (__builtin_expect(edge, 0)) {
+        uint32_t sees = ~0u;  // which rows see this token
+        if (edge) {
             sees = 0;
             if (pos < pc.L) {
                 if (pos < ctx) {
@@ -473,7 +480,6 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         // Scores in log2 units, the value's scale included, against the maximum
         // in use; again, where that has to move.
         float y[R];
-        bool stop = false;  // alike in the whole warpgroup
 #pragma unroll 1
         for (bool again = false;; again = true) {
             load_scores<C8>(y, lanes + sb * 128 + r0);
@@ -489,7 +495,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
                 w = add2(fma2(w, a2, v2), make_float2(-m4.z, -m4.w));
                 y[n] = u.x; y[n + 1] = u.y; y[n + 2] = w.x; y[n + 3] = w.y;
             }
-            if (__builtin_expect(edge, 0)) {
+            if (edge) {
 #pragma unroll
                 for (int n = 0; n < R; ++n)
                     if (!(sees & (1u << n))) y[n] = -INFINITY;
@@ -610,7 +616,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         // values past the sequence's end may be anything (NaN times a weight of
         // 0 would stay): clear them
         const int valid = pc.L - p0;
-        if (__builtin_expect(valid < kTile, 0)) {
+        if (edge && valid < kTile) {
             char *v = smem_v + (size_t)st * stage_bytes;
             const int at = turns ? part_no * 128 + tk : tid;
             for (int i = valid * (D / 16) + at; i < kTile * (D / 16); i += turns ? 256 : 512)
@@ -619,6 +625,15 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         fence_async();
         __syncwarp();
         if (lane < arrivals) mbar_arrive(&sh->p_full[sb]);
+    }
+    };
+    {
+        // (it0 and t0 may differ in parity: a pair's tiles are those of its it)
+        const int own = pc.t0 + (turns ? (int)((par ^ it0) & 1) : 0);
+        const int reach = min(max(ctx >> 7, pc.t0), pc.t1);  // first tile that reaches them
+        const int on = reach > own ? (turns ? own + ((reach - own + 1) & ~1) : reach) : own;
+        tiles(std::false_type{}, own, reach);
+        tiles(std::true_type{}, on, pc.t1);
     }
 
     // ---- the piece's sums
@@ -1027,25 +1042,30 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
             const uint64_t dlo = dq + (uint32_t)(N * D >> 4);
             ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
             ++pieces;
+            auto tiles = [&](auto is_one) {
 #pragma unroll 1
-            for (int t = pc.t0; t < pc.t1; ++t, ++it) {
-                const uint32_t st = it % kAtStages, sb = it & 1;
-                ok = ok && at_wait(sh, j.err, &sh->full_k[st], (it / kAtStages) & 1);
-                ok = ok && at_wait(sh, j.err, &sh->s_empty[sb], ((it >> 1) & 1) ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t dk = dk0 + st * (2 * kSide >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    tc_mma(tmem + sb * 128, dk + 2 * k, dq + 2 * k, id_s, k);
-                if (!one) {
+                for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+                    const uint32_t st = it % kAtStages, sb = it & 1;
+                    ok = ok && at_wait(sh, j.err, &sh->full_k[st], (it / kAtStages) & 1);
+                    ok = ok && at_wait(sh, j.err, &sh->s_empty[sb], ((it >> 1) & 1) ^ 1);
+                    if (__builtin_expect(!ok, 0)) break;
+                    tc_fence_after();
+                    const uint64_t dk = dk0 + st * (2 * kSide >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k)
-                        tc_mma(tmem + sb * 128, dk + 2 * k, dlo + 2 * k, id_s, 1);
+                        tc_mma(tmem + sb * 128, dk + 2 * k, dq + 2 * k, id_s, k);
+                    if (!decltype(is_one)::value)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            tc_mma(tmem + sb * 128, dk + 2 * k, dlo + 2 * k, id_s, 1);
+                    tc_commit(&sh->s_full[sb]);
+                    tc_commit(&sh->empty_k[st]);
                 }
-                tc_commit(&sh->s_full[sb]);
-                tc_commit(&sh->empty_k[st]);
-            }
+            };
+            if (one)
+                tiles(std::true_type{});
+            else
+                tiles(std::false_type{});
         }
         // after a wait that ran out: products still in flight end before the exit
         if (!ok) {
@@ -1070,7 +1090,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 const uint32_t st = it % kAtStages, sb = it & 1;
                 ok = ok && at_wait(sh, j.err, &sh->full_v[st], (it / kAtStages) & 1);
                 ok = ok && at_wait(sh, j.err, &sh->p_full[sb], (it >> 1) & 1);
-                if (!ok) break;
+                if (__builtin_expect(!ok, 0)) break;
                 tc_fence_after();
                 const uint64_t dv = dv0 + st * (2 * kSide >> 4);
                 const uint64_t dp = dp0 + (turns ? sb * (kTile * 128 >> 4) : 0u);
