@@ -458,11 +458,11 @@ def sv_packed_topk_step(logits, K, W, kp, kq, prev_draft, prev_len, prev_q_ids, 
 
 
 def _dense(t, dtype, shape, name, dev):
-    """Address of a contiguous tensor of this type and shape (None: any)."""
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    """Address of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor on %s" % (name, dtype, dev))
-    if len(shape) != t.dim() or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError("%s must have shape %s" % (name, shape))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
     return t.data_ptr()
 
 
@@ -472,10 +472,14 @@ def _cuda(t, name):
     return t.device
 
 
-def _raw_stream(stream, dev):
+def _call_on(handle, stream, dev):
+    """(handle pointer, raw stream): the given ones, or the device's default
+    handle and torch's current stream."""
+    if handle is None:
+        handle = _handles.get(dev.index) or default_handle(dev)
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return handle.ptr, torch._C._cuda_getCurrentRawStream(dev.index)
+    return handle.ptr, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def sv_kv_plan(cached_len, new_len, held, table, free_ids, free_pos, block, max_tokens, *,
@@ -485,25 +489,28 @@ def sv_kv_plan(cached_len, new_len, held, table, free_ids, free_pos, block, max_
     Updates table and free_ids in place and returns a dict of new tensors
     (kv_len, cu_new, held, free_pos, slot, pos)."""
     dev = _cuda(cached_len, "cached_len")
-    B = cached_len.shape[0]
-    i32 = torch.int32
-    h = handle or default_handle(dev)
-    out = {"kv_len": torch.empty(B, dtype=i32, device=dev),
-           "cu_new": torch.empty(B + 1, dtype=i32, device=dev),
-           "held": torch.empty(B, dtype=i32, device=dev),
-           "free_pos": torch.empty(2, dtype=torch.int64, device=dev),
-           "slot": torch.empty(int(max_tokens), dtype=i32, device=dev),
-           "pos": torch.empty(int(max_tokens), dtype=i32, device=dev)}
+    i32, empty = torch.int32, torch.empty
+    B, cap = cached_len.shape[0], int(max_tokens)
+    if table.dim() != 2 or free_ids.dim() != 1:
+        raise ValueError("table must be [B, cols] and free_ids [ring]")
+    cols, ring = table.shape[1], free_ids.shape[0]
+    row = (B,)
+    ptr, raw = _call_on(handle, stream, dev)
+    kv_len, held_out = torch.empty_like(cached_len), torch.empty_like(held)
+    free_out = torch.empty_like(free_pos)
+    cu_new = empty(B + 1, dtype=i32, device=dev)
+    slot = empty(cap, dtype=i32, device=dev)
+    pos = torch.empty_like(slot)
     _check(lib().sv_kv_plan(
-        h.ptr, B, int(block), table.shape[1], free_ids.shape[0], int(max_tokens),
-        _dense(cached_len, i32, (B,), "cached_len", dev),
-        _dense(new_len, i32, (B,), "new_len", dev), _dense(held, i32, (B,), "held", dev),
+        ptr, B, int(block), cols, ring, cap, _dense(cached_len, i32, row, "cached_len", dev),
+        _dense(new_len, i32, row, "new_len", dev), _dense(held, i32, row, "held", dev),
         _dense(free_pos, torch.int64, (2,), "free_pos", dev),
-        _dense(free_ids, i32, (None,), "free_ids", dev),
-        _dense(table, i32, (B, None), "table", dev), out["kv_len"].data_ptr(),
-        out["cu_new"].data_ptr(), out["held"].data_ptr(), out["free_pos"].data_ptr(),
-        out["slot"].data_ptr(), out["pos"].data_ptr(), _raw_stream(stream, dev)), "sv_kv_plan")
-    return out
+        _dense(free_ids, i32, (ring,), "free_ids", dev),
+        _dense(table, i32, (B, cols), "table", dev), kv_len.data_ptr(), cu_new.data_ptr(),
+        held_out.data_ptr(), free_out.data_ptr(), slot.data_ptr(), pos.data_ptr(), raw),
+        "sv_kv_plan")
+    return {"kv_len": kv_len, "cu_new": cu_new, "held": held_out, "free_pos": free_out,
+            "slot": slot, "pos": pos}
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
@@ -512,7 +519,7 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
         raise ValueError("k_cache must be float8_e4m3fn or uint8")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, Hkv, block, D]")
-    shape = tuple(k_cache.shape)
+    shape = k_cache.shape
     return shape, (_dense(k_cache, k_cache.dtype, shape, "k_cache", dev),
                    _dense(v_cache, k_cache.dtype, shape, "v_cache", dev),
                    _dense(k_scale, torch.float32, shape[:2], "k_scale", dev),
@@ -526,17 +533,17 @@ def sv_kv_append(k, v, slot, k_cache, v_cache, k_scale, v_scale, *, handle=None,
     dev = _cuda(k, "k")
     (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     T = k.shape[0]
-    if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
+    if k.shape != (T, H, D) or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
     if k.dtype != v.dtype or v.device != dev or k.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("k and v must both be bfloat16 or float32, on one device")
     if k.stride(2) != 1 or v.stride(2) != 1:
         raise ValueError("k and v: the last dimension must be contiguous")
-    h = handle or default_handle(dev)
+    ptr, raw = _call_on(handle, stream, dev)
     _check(lib().sv_kv_append(
-        h.ptr, k.data_ptr(), v.data_ptr(), SV_BF16 if k.dtype == torch.bfloat16 else SV_F32,
+        ptr, k.data_ptr(), v.data_ptr(), SV_BF16 if k.dtype == torch.bfloat16 else SV_F32,
         k.stride(0), k.stride(1), v.stride(0), v.stride(1), T, H, D, block, pages,
-        _dense(slot, torch.int32, (T,), "slot", dev), *cache, _raw_stream(stream, dev)),
+        _dense(slot, torch.int32, (T,), "slot", dev), *cache, raw),
         "sv_kv_append")
 
 
@@ -551,25 +558,27 @@ def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
         raise ValueError("q must be a bfloat16 [T, Hq, D] tensor with the cache's D, contiguous "
                          "in its last dimension")
+    if table.dim() != 2:
+        raise ValueError("table must be [B, cols]")
     T, Hq, _ = q.shape
-    B = kv_len.shape[0]
+    B, cols = kv_len.shape[0], table.shape[1]
     i32 = torch.int32
     words = 0
     if mask is not None:
         if mask.dim() != 2:
             raise ValueError("mask must be [T, words]")
         words = mask.shape[1]
-    h = handle or default_handle(dev)
+    ptr, raw = _call_on(handle, stream, dev)
     out = {"out": torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)}
     if want_lse:
         out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     _check(lib().sv_kv_attention(
-        h.ptr, q.data_ptr(), q.stride(0), q.stride(1), T, Hq, H, D, *cache, block, pages,
-        _dense(table, i32, (B, None), "table", dev), table.shape[1],
+        ptr, q.data_ptr(), q.stride(0), q.stride(1), T, Hq, H, D, *cache, block, pages,
+        _dense(table, i32, (B, cols), "table", dev), cols,
         _dense(kv_len, i32, (B,), "kv_len", dev), _dense(cu_new, i32, (B + 1,), "cu_new", dev), B,
         None if mask is None else _dense(mask, i32, (T, words), "mask", dev), words,
         float(D ** -0.5 if scale is None else scale), out["out"].data_ptr(),
-        out["lse"].data_ptr() if want_lse else None, _raw_stream(stream, dev)),
+        out["lse"].data_ptr() if want_lse else None, raw),
         "sv_kv_attention")
     return out
 
@@ -584,16 +593,14 @@ def sv_sample_rows(logits, u, *, temperature=None, top_k=None, top_p=None, min_p
         raise ValueError("logits must be [R, V]")
     code, rs = _rows(logits, "logits")
     R, V = logits.shape
-    f32 = torch.float32
-    opt = lambda t, dt, n: None if t is None else _dense(t, dt, (R,), n, dev)
-    h = handle or default_handle(dev)
-    out = {"token": torch.empty(R, dtype=torch.int32, device=dev),
-           "prob": torch.empty(R, dtype=f32, device=dev),
-           "kept": torch.empty(R, dtype=torch.int32, device=dev)}
+    f32, row = torch.float32, (R,)
+    opt = lambda t, dt, n: None if t is None else _dense(t, dt, row, n, dev)
+    ptr, raw = _call_on(handle, stream, dev)
+    token, prob = torch.empty(R, dtype=torch.int32, device=dev), torch.empty_like(u)
+    kept = torch.empty_like(token)
     _check(lib().sv_sample_rows(
-        h.ptr, logits.data_ptr(), code, rs if R > 1 else max(rs, V), R, V,
-        _dense(u, f32, (R,), "u", dev), opt(temperature, f32, "temperature"),
+        ptr, logits.data_ptr(), code, rs if R > 1 else max(rs, V), R, V,
+        _dense(u, f32, row, "u", dev), opt(temperature, f32, "temperature"),
         opt(top_k, torch.int32, "top_k"), opt(top_p, f32, "top_p"), opt(min_p, f32, "min_p"),
-        out["token"].data_ptr(), out["prob"].data_ptr(), out["kept"].data_ptr(),
-        _raw_stream(stream, dev)), "sv_sample_rows")
-    return out
+        token.data_ptr(), prob.data_ptr(), kept.data_ptr(), raw), "sv_sample_rows")
+    return {"token": token, "prob": prob, "kept": kept}
