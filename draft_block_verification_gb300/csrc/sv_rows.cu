@@ -17,12 +17,11 @@
 // first taken in fp32 with a bound on its error, and taken again in fixed
 // point where a decision falls inside the bound.
 //
-// The boundary of the kept prefix is found by counting, not by sorting: a
-// sample of 4096 logits tells about where it lies, one pass over the row
-// collects the tokens around it into a shared list (all tokens above it where
-// they fit), and bisection over the list's keys finds it exactly.  A row comes
-// from DRAM once; the later passes hit L2, since the rows in flight (two a SM)
-// take a fraction of it.
+// Only the tokens around the boundary of the kept prefix are ordered: a sample
+// of 4096 logits tells about where it lies, one pass over the row collects the
+// tokens around it into a shared list (all tokens above it where they fit), and
+// the list is sorted.  A row comes from DRAM once; the later passes hit L2,
+// since the rows in flight (two a SM) take a fraction of it.
 #include <float.h>
 #include <math.h>
 
@@ -46,7 +45,16 @@ static_assert(kRowsMaxV / kIdBlock <= kListCap, "block sums share the list's mem
 // ex2 2^-22, and 11 additions of 2^-24: under 2^-18.
 constexpr double kMassEps = 0x1p-18;
 
+// (key, id) of a listed token: larger pairs come first in the order.
+__device__ __forceinline__ unsigned long long pair_of(uint32_t key, int id)
+{
+    return ((unsigned long long)key << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ uint32_t pair_key(unsigned long long p) { return (uint32_t)(p >> 32); }
+__device__ __forceinline__ int pair_id(unsigned long long p) { return (int)~(uint32_t)p; }
+
 struct RowShared {
+    float queue[kRwWarps][64];
     unsigned long long mass[2][kRwWarps];
     unsigned cnt[2][kRwWarps];
     double dred[kRwWarps];
@@ -200,20 +208,21 @@ __device__ __forceinline__ unsigned long long scale_mass(float f, unsigned long 
     return r + (up && rest ? 1 : 0);
 }
 
-// Visit the row in steps of 8 logits a thread: f(v0, logits).
+// Visit the row in steps of 8 logits a thread: f(v0, logits).  Every lane of a
+// warp takes part in every step (logits past the row's end are -inf).
 template <typename In, bool VEC, typename F>
 __device__ __forceinline__ void each8(const RowCtx &c, F f)
 {
-    constexpr int kStep = kRwThreads * 8;
+    constexpr int kStep = kRwThreads * 8, kDeep = sizeof(In) == 2 ? 4 : 2;  // loads in flight
     int v0 = c.tid * 8;
-    for (; v0 + kStep < c.V; v0 += 2 * kStep) {  // two loads in flight
-        float a[8], b[8];
-        load8<In, VEC>(c, v0, a);
-        load8<In, VEC>(c, v0 + kStep, b);
-        f(v0, a);
-        f(v0 + kStep, b);
+    for (; v0 - c.lane * 8 + (kDeep - 1) * kStep < c.V; v0 += kDeep * kStep) {
+        float a[kDeep][8];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) load8<In, VEC>(c, v0 + i * kStep, a[i]);
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) f(v0 + i * kStep, a[i]);
     }
-    if (v0 < c.V) {
+    for (; v0 - c.lane * 8 < c.V; v0 += kStep) {
         float a[8];
         load8<In, VEC>(c, v0, a);
         f(v0, a);
@@ -291,6 +300,45 @@ __device__ float row_max_mass(RowCtx &c, double *mass)
     return m;
 }
 
+// A warp's queue of logits whose weights are to be summed: the few lanes of a
+// step that have one put it there, and a full warp's worth is weighed at once.
+struct WeightQueue {
+    float *buf;   // 64 of this warp's
+    int n;
+    unsigned long long sum;
+    __device__ __forceinline__ void init(RowCtx &c)
+    {
+        buf = c.sh->queue[c.warp];
+        n = 0;
+        sum = 0;
+    }
+    __device__ __forceinline__ void put(const RowCtx &c, float x, bool on)
+    {
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
+        if (on) buf[n + __popc(m & ((1u << c.lane) - 1))] = x;
+        n += __popc(m);
+        if (n >= 32) {
+            __syncwarp();
+            sum += row_weight(c, buf[c.lane]);
+            const float rest = buf[32 + c.lane];
+            __syncwarp();
+            n -= 32;
+            if (c.lane < n) buf[c.lane] = rest;
+        }
+    }
+    // the lane's part of everything put so far
+    __device__ __forceinline__ unsigned long long take(const RowCtx &c)
+    {
+        __syncwarp();
+        if (c.lane < n) sum += row_weight(c, buf[c.lane]);
+        __syncwarp();
+        const unsigned long long s = sum;
+        n = 0;
+        sum = 0;
+        return s;
+    }
+};
+
 // Exact mass and count of the logits with key >= k.
 template <typename In, bool VEC>
 __device__ void row_above(RowCtx &c, uint32_t k, bool want_mass, unsigned *cnt,
@@ -298,27 +346,30 @@ __device__ void row_above(RowCtx &c, uint32_t k, bool want_mass, unsigned *cnt,
 {
     const float t = ord2f(k);
     unsigned n = 0;
-    unsigned long long w = 0;
+    WeightQueue q;
+    q.init(c);
     each8<In, VEC>(c, [&](int, const float (&f)[8]) {
-        if (max8(f) >= t) {
+        if (__any_sync(0xFFFFFFFFu, max8(f) >= t)) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (row_key(f[i]) >= k && f[i] > -INFINITY) {
-                    ++n;
-                    if (want_mass) w += row_weight(c, f[i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                const bool on = row_key(f[i]) >= k && f[i] > -INFINITY;
+                n += on;
+                if (want_mass) q.put(c, f[i], on);
+            }
         }
     });
+    const unsigned long long w = want_mass ? q.take(c) : 0;
     *cnt = cta_count(c, n);
     *mass = want_mass ? cta_mass(c, w) : 0;
 }
 
-// Collect the logits with lo <= key < hi (hi = 0: no upper end) as (key, id);
-// returns how many there are, of which the first kListCap are listed.
+// Collect the logits with lo <= key < hi (hi = 0: no upper end); returns how
+// many there are, of which the first kListCap are listed.
 template <typename In, bool VEC>
-__device__ unsigned row_collect(RowCtx &c, uint32_t lo, uint32_t hi, uint32_t *key, uint32_t *id)
+__device__ unsigned row_collect(RowCtx &c, uint32_t lo, uint32_t hi, unsigned long long *list)
 {
     const float t = ord2f(lo);
+    __syncthreads();
     if (c.tid == 0) c.sh->list_n = 0;
     __syncthreads();
     each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
@@ -328,16 +379,66 @@ __device__ unsigned row_collect(RowCtx &c, uint32_t lo, uint32_t hi, uint32_t *k
                 const uint32_t k = row_key(f[i]);
                 if (k >= lo && (hi == 0 || k < hi) && f[i] > -INFINITY) {
                     const unsigned at = atomicAdd(&c.sh->list_n, 1u);
-                    if (at < (unsigned)kListCap) {
-                        key[at] = k;
-                        id[at] = (uint32_t)(v0 + i);
-                    }
+                    if (at < (unsigned)kListCap) list[at] = pair_of(k, v0 + i);
                 }
             }
         }
     });
     __syncthreads();
     return c.sh->list_n;
+}
+
+// Sort list[0 .. n) downwards (bitonic; padded to a power of two with zeros).
+// Stages of distance 32 and less stay within a warp's 64 entries.
+__device__ void list_sort(const RowCtx &c, unsigned long long *list, unsigned n)
+{
+    unsigned size = 64;
+    while (size < n) size *= 2;
+    for (unsigned i = n + c.tid; i < size; i += kRwThreads) list[i] = 0;
+    __syncthreads();
+    for (unsigned k = 2; k <= size; k *= 2) {
+        for (unsigned d = k / 2; d > 0; d /= 2) {
+            for (unsigned p = c.tid; p < size / 2; p += kRwThreads) {
+                const unsigned i = 2 * p - (p & (d - 1)), o = i + d;
+                const unsigned long long a = list[i], b = list[o];
+                if ((a < b) == ((i & k) == 0)) {
+                    list[i] = b;
+                    list[o] = a;
+                }
+            }
+            if (d > 32 || (d == 1 && k >= 64))
+                __syncthreads();
+            else
+                __syncwarp();
+        }
+    }
+    __syncthreads();
+}
+
+// Running sums of the sorted list's weights, inclusive, to sum[0 .. n).
+__device__ void list_sums(RowCtx &c, const unsigned long long *list, unsigned long long *sum,
+                          unsigned n)
+{
+    const unsigned each = (n + kRwThreads - 1) / kRwThreads, from = c.tid * each;
+    unsigned long long own = 0;
+    for (unsigned i = from; i < min(from + each, n); ++i) {
+        own += row_weight(c, ord2f(pair_key(list[i])));
+        sum[i] = own;
+    }
+    unsigned long long run = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, run, d);
+        if (c.lane >= d) run += a;
+    }
+    const int par = c.par;
+    c.par ^= 1;
+    if (c.lane == 31) c.sh->mass[par][c.warp] = run;
+    __syncthreads();
+    for (int i = 0; i < c.warp; ++i) run += c.sh->mass[par][i];
+    run -= own;
+    for (unsigned i = from; i < min(from + each, n); ++i) sum[i] += run;
+    __syncthreads();
 }
 
 // What the kept prefix has to reach: `rank` tokens, or a mass known to lie in
@@ -359,11 +460,10 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
 {
     extern __shared__ unsigned long long rows_smem[];
     __shared__ RowShared sh;
-    unsigned long long *s_w = rows_smem;                              // [kListCap]
-    uint32_t *s_key = reinterpret_cast<uint32_t *>(s_w + kListCap);   // [kListCap]
-    uint32_t *s_id = s_key + kListCap;                                // [kListCap]
-    unsigned *s_hist = reinterpret_cast<unsigned *>(s_w);             // [kBins], before the list
-    float *s_tail = reinterpret_cast<float *>(s_hist + kBins);        // [kBins]
+    unsigned long long *s_w = rows_smem;              // [kListCap] running weights
+    unsigned long long *s_list = s_w + kListCap;      // [kListCap] pairs
+    unsigned *s_hist = reinterpret_cast<unsigned *>(s_w);       // [kBins], before the list
+    float *s_tail = reinterpret_cast<float *>(s_hist + kBins);  // [kBins]
 
     RowCtx c;
     c.tid = threadIdx.x;
@@ -483,7 +583,8 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     unsigned base_n = 0;            // tokens and mass at or above hi
     unsigned long long base_w = 0;
     unsigned list_n = 0;
-    bool listed = false;
+    bool listed = false;   // the list holds every kept token
+    bool one_key = false, p_exact = false;
     Goal goal;
     goal.by_mass = !by_k && by_p;
     goal.rank = by_k ? (unsigned)top_k : 0xFFFFFFFFu;
@@ -582,23 +683,67 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         est = (float)s_hist[bl] * per;
         __syncthreads();
     }
+    // ---- otherwise narrow [lo, hi) until its tokens fit the list
+    auto narrow = [&](Goal &g) {
+        unsigned in_n;  // tokens at or above lo
+        unsigned long long w;
+        row_above<In, VEC>(c, lo, false, &in_n, &w);
+        uint32_t top = row_key(c.m) + 1;
+        base_n = 0;
+        base_w = 0;
+        int tries = 0;
+        while (in_n - base_n > (unsigned)kListCap && top - lo > 1) {
+            // first around the guess, then by halves of the key range
+            uint32_t mid = lo + (top - lo) / 2;
+            const uint32_t k = tries == 0 ? guess_hi : guess_lo;
+            if (tries < 2 && k > lo && k < top) mid = k;
+            ++tries;
+            unsigned n;
+            row_above<In, VEC>(c, mid, g.by_mass, &n, &w);
+            int got = g.reached(n, w);
+            if (got < 0) {
+                refine();
+                set_goal();
+                got = g.reached(n, w);
+            }
+            if (got) {
+                lo = mid;
+                in_n = n;
+            } else {
+                top = mid;
+                base_n = n;
+                base_w = w;
+            }
+        }
+        hi = top;
+        // (more equal logits than the list holds: none is listed)
+        list_n = in_n - base_n <= (unsigned)kListCap ? row_collect<In, VEC>(c, lo, hi, s_list) : 0;
+        one_key = in_n - base_n > (unsigned)kListCap;
+    };
+    // entries of the list whose running weight, with the mass above, is below x
+    auto below = [&](unsigned long long x) {
+        unsigned n = 0;
+        for (int i = c.tid; i < (int)list_n; i += kRwThreads) n += base_w + s_w[i] < x;
+        return cta_count(c, n);
+    };
+
+    // ---- the boundary: the last kept token's key t and id (id_cut), and the
+    // number of kept tokens
+    uint32_t t = key_min;
+    int id_cut = j.V;
+    unsigned kept = 0, kept_list = 0;  // all; those in the list, its first ones
     if (filtered) {
-        // ---- small kept sets: list everything from the guess on
         if (est < 0.9f * kListCap || j.V <= kListCap) {
+            // small kept sets: everything from the guess on
             const uint32_t from = max(guess_lo, lo);
-            list_n = row_collect<In, VEC>(c, from, 0, s_key, s_id);
+            list_n = row_collect<In, VEC>(c, from, 0, s_list);
             if (list_n <= (unsigned)kListCap) {
-                bool enough = from <= lo;
-                if (!enough) {
-                    if (by_k) {
-                        enough = list_n >= (unsigned)top_k;
-                    } else {
-                        unsigned long long w = 0;
-                        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                            w += row_weight(c, ord2f(s_key[i]));
-                        w = cta_mass(c, w);
-                        enough = goal.reached(0, w) == 1;
-                    }
+                bool enough = from <= lo || (by_k && list_n >= (unsigned)top_k);
+                if (!enough && goal.by_mass) {
+                    unsigned long long w = 0;
+                    for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+                        w += row_weight(c, ord2f(pair_key(s_list[i])));
+                    enough = goal.reached(0, cta_mass(c, w)) == 1;
                 }
                 if (enough) {
                     lo = from;
@@ -606,208 +751,121 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 }
             }
         }
-        // ---- otherwise narrow [lo, hi) until its tokens fit the list (min-p
-        // alone needs no list: its boundary is known)
-        if (!listed && (by_k || by_p)) {
-            unsigned in_n;  // tokens at or above lo
+        if (!listed && !by_k && !by_p) {
+            // min-p alone needs no list: its boundary is known
             unsigned long long w;
-            row_above<In, VEC>(c, lo, false, &in_n, &w);
-            uint32_t top = row_key(c.m) + 1;
-            int tries = 0;
-            while (in_n - base_n > (unsigned)kListCap && top - lo > 1) {
-                // first around the guess, then by halves of the key range
-                uint32_t mid = lo + (top - lo) / 2;
-                const uint32_t k = tries == 0 ? guess_hi : guess_lo;
-                if (tries < 2 && k > lo && k < top) mid = k;
-                ++tries;
-                unsigned n;
-                row_above<In, VEC>(c, mid, goal.by_mass, &n, &w);
-                int got = goal.reached(n, w);
-                if (got < 0) {
-                    refine();
-                    set_goal();
-                    got = goal.reached(n, w);
-                }
-                if (got) {
-                    lo = mid;
-                    in_n = n;
-                } else {
-                    top = mid;
-                    base_n = n;
-                    base_w = w;
-                }
-            }
-            hi = top;
-            if (in_n - base_n <= (unsigned)kListCap) {
-                list_n = row_collect<In, VEC>(c, lo, hi, s_key, s_id);
-            } else {
-                list_n = 0;  // more equal logits than fit: one key, known count
-            }
-            // with top-k beyond the list, the mass above the list is still open
-            if (by_k && by_p) row_above<In, VEC>(c, hi, true, &base_n, &base_w);
-        }
-    }
-
-    // ---- the boundary: key t and how many of its tokens (lowest ids first)
-    uint32_t t = kKeyNegInf + 1;
-    unsigned ties_kept = 0xFFFFFFFFu, kept = 0;
-    int id_cut = 0x7FFFFFFF;
-    const bool one_key = (by_k || by_p) && !listed && list_n == 0;
-    if (filtered) {
-        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-            s_w[i] = row_weight(c, ord2f(s_key[i]));
-        __syncthreads();
-        auto above = [&](uint32_t k, bool want, unsigned *n, unsigned long long *w) {
-            unsigned a = 0;
-            unsigned long long b = 0;
-            for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                if (s_key[i] >= k) {
-                    ++a;
-                    if (want) b += s_w[i];
-                }
-            *n = base_n + cta_count(c, a);
-            *w = want ? base_w + cta_mass(c, b) : 0;
-        };
-        unsigned one_n = 0;
-        if (one_key) {
-            unsigned long long w;
-            row_above<In, VEC>(c, lo, false, &one_n, &w);
-        }
-        // the largest key whose tokens and those above reach the goal; the
-        // list's lowest key where none does
-        auto boundary = [&](Goal &g, uint32_t *key, unsigned *n_at, unsigned long long *w_at,
-                            unsigned *n_over, unsigned long long *w_over) {
-            const bool want = g.by_mass;
-            uint32_t a = lo, b = hi ? hi : row_key(c.m) + 1;  // reached at a, not at b
-            unsigned n;
-            unsigned long long w;
-            if (one_key) {
-                *key = lo;
-                *n_at = one_n;
-                *n_over = base_n;
-                *w_over = base_w;
-                *w_at = base_w + (one_n - base_n) * row_weight(c, ord2f(lo));
-                return;
-            }
-            while (b - a > 1) {
-                const uint32_t mid = a + (b - a) / 2;
-                above(mid, want, &n, &w);
-                int got = g.reached(n, w);
-                if (got < 0) {
-                    refine();
-                    set_goal();
-                    g = goal;
-                    got = g.reached(n, w);
-                }
-                if (got)
-                    a = mid;
-                else
-                    b = mid;
-            }
-            *key = a;
-            above(a, true, n_at, w_at);
-            above(b, true, n_over, w_over);
-        };
-        t = lo;
-        unsigned n_at = 0, n_over = 0;
-        unsigned long long w_at, w_over;
-        if (by_k) {
-            boundary(goal, &t, &n_at, &w_at, &n_over, &w_over);
-            // (fewer than k finite logits: every one of them)
-            ties_kept = min((unsigned)top_k, n_at) - n_over;
-            if (by_p) {
-                const unsigned long long wt = row_weight(c, ord2f(t));
-                Goal g;
-                g.by_mass = true;
-                g.rank = 0;
-                const unsigned long long M = w_over + ties_kept * wt;
-                g.lo = g.hi = scale_mass(top_p, M, true);
-                uint32_t tp;
-                unsigned pn_at, pn_over;
-                unsigned long long pw_at, pw_over;
-                if (g.lo <= base_w && base_n > 0) {
-                    // the boundary of p lies above the list: narrow again over the row
-                    uint32_t a = hi, b = row_key(c.m) + 1;
-                    unsigned n;
+            list_n = 0;
+            row_above<In, VEC>(c, key_min, false, &kept, &w);
+        } else {
+            if (!listed) {
+                narrow(goal);
+                if (by_k && by_p) {
+                    // the mass of the top k, and with it the boundary of p
                     unsigned long long w;
-                    while (b - a > 1) {
-                        const uint32_t mid = a + (b - a) / 2;
-                        row_above<In, VEC>(c, mid, true, &n, &w);
-                        if (w >= g.lo)
-                            a = mid;
-                        else
-                            b = mid;
+                    row_above<In, VEC>(c, hi, true, &base_n, &w);
+                    const unsigned r = (unsigned)min(top_k, 0x7FFFFFFF) - base_n;
+                    unsigned long long M;
+                    if (one_key) {
+                        M = w + r * row_weight(c, ord2f(lo));
+                    } else {
+                        list_sort(c, s_list, list_n);
+                        list_sums(c, s_list, s_w, list_n);
+                        const unsigned at = min(r, list_n);
+                        M = w + (at ? s_w[at - 1] : 0);
                     }
-                    tp = a;
-                    row_above<In, VEC>(c, a, true, &pn_at, &pw_at);
-                    row_above<In, VEC>(c, b, true, &pn_over, &pw_over);
-                } else {
-                    boundary(g, &tp, &pn_at, &pw_at, &pn_over, &pw_over);
-                }
-                const unsigned long long wp = row_weight(c, ord2f(tp));
-                unsigned rp = pn_at - pn_over;
-                if (wp) rp = (unsigned)min((unsigned long long)rp,
-                                           (g.lo - min(pw_over, g.lo) + wp - 1) / wp);
-                rp = max(rp, 1u);
-                if (tp > t || (tp == t && rp < ties_kept)) {
-                    t = tp;
-                    ties_kept = rp;
-                    n_over = pn_over;
-                    n_at = pn_at;
+                    Goal g;
+                    g.by_mass = true;
+                    g.rank = 0;
+                    g.lo = g.hi = scale_mass(top_p, M, true);
+                    goal = g;
+                    lo = kKeyNegInf + 1;
+                    guess_lo = guess_hi = 0;
+                    p_exact = true;
+                    narrow(goal);
                 }
             }
-        } else if (by_p) {
-            boundary(goal, &t, &n_at, &w_at, &n_over, &w_over);
-            const unsigned long long wt = row_weight(c, ord2f(t));
-            unsigned rp = n_at - n_over;
-            if (wt) {
-                // tokens of this key until the goal is reached: both ends of its bounds
-                auto until = [&](unsigned long long g) {
-                    return (g - min(w_over, g) + wt - 1) / wt;
-                };
-                if (until(goal.lo) != until(goal.hi) && until(goal.lo) < rp) {
-                    refine();
-                    set_goal();
+            if (one_key) {
+                // one logit fills the bracket: how many of its tokens, lowest ids first
+                const unsigned long long wt = row_weight(c, ord2f(lo));
+                unsigned n_at;
+                unsigned long long w;
+                row_above<In, VEC>(c, lo, false, &n_at, &w);
+                unsigned r = n_at - base_n;
+                if (goal.by_mass) {
+                    auto until = [&](unsigned long long x) -> unsigned {
+                        if (!wt) return r;
+                        return (unsigned)min((unsigned long long)r,
+                                             (x - min(base_w, x) + wt - 1) / wt);
+                    };
+                    if (until(goal.lo) != until(goal.hi)) {
+                        refine();
+                        set_goal();
+                    }
+                    r = until(goal.hi);
                 }
-                rp = (unsigned)min((unsigned long long)rp, until(goal.hi));
-            }
-            ties_kept = max(rp, 1u);
-        }
-        // min-p cuts at a logit, with all its equals (and never above the maximum)
-        if (t < key_min || !(by_k || by_p)) {
-            t = key_min;
-            ties_kept = 0xFFFFFFFFu;
-            unsigned long long w;
-            if (listed)
-                above(t, false, &n_at, &w);
-            else
-                row_above<In, VEC>(c, t, false, &n_at, &w);
-            n_over = 0;
-        }
-        const unsigned ties = n_at - n_over;
-        kept = n_over + min(ties_kept, ties);
-        if (ties_kept < ties) {
-            // the id of the ties_kept-th lowest id among the boundary's equals
-            int a = -1, b = j.V - 1;
-            const bool in_list = list_n && t >= lo && (hi == 0 || t < hi);
-            while (b - a > 1) {
-                const int mid = a + (b - a) / 2;
-                unsigned n = 0;
-                if (in_list) {
-                    for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                        n += s_key[i] == t && (int)s_id[i] <= mid;
-                } else {
-                    each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
+                if (by_k) r = min(r, (unsigned)top_k - base_n);
+                r = max(r, 1u);
+                t = lo;
+                kept = base_n + r;
+                if (r < n_at - base_n) {
+                    // the id of the r-th lowest among the equals
+                    int a = -1, b = j.V - 1;
+                    while (b - a > 1) {
+                        const int mid = a + (b - a) / 2;
+                        unsigned n = 0;
+                        each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) n += row_key(f[i]) == t && v0 + i <= mid;
-                    });
+                            for (int i = 0; i < 8; ++i) n += row_key(f[i]) == t && v0 + i <= mid;
+                        });
+                        if (cta_count(c, n) >= r)
+                            b = mid;
+                        else
+                            a = mid;
+                    }
+                    id_cut = b;
                 }
-                if (cta_count(c, n) >= ties_kept)
-                    b = mid;
-                else
-                    a = mid;
+            } else {
+                list_sort(c, s_list, list_n);
+                list_sums(c, s_list, s_w, list_n);
+                unsigned n = list_n;
+                if (by_k) n = min(n, (unsigned)top_k - base_n);
+                if (by_k && by_p && !p_exact) {
+                    // (the list starts at the maximum here)
+                    n = min(n, below(scale_mass(top_p, s_w[n - 1], true)) + 1);
+                } else if (by_p) {
+                    if (below(goal.lo) != below(goal.hi)) {
+                        refine();
+                        set_goal();
+                    }
+                    n = min(n, below(goal.hi) + 1);
+                }
+                // min-p cuts at a logit, with all its equals
+                unsigned m = 0;
+                for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+                    m += pair_key(s_list[i]) >= key_min;
+                m = cta_count(c, m);
+                if (m < n && min_p > 0.f) {
+                    n = m;
+                    if (n == 0 && base_n > 0) {
+                        // its boundary lies above the list
+                        unsigned long long w;
+                        row_above<In, VEC>(c, key_min, false, &kept, &w);
+                    }
+                }
+                kept_list = n;
+                if (n > 0) {
+                    kept = base_n + n;
+                    t = pair_key(s_list[n - 1]);
+                    id_cut = pair_id(s_list[n - 1]);
+                }
             }
-            id_cut = b;
+            // (a bracket of one key below min-p's boundary)
+            if (t < key_min) {
+                unsigned long long w;
+                t = key_min;
+                id_cut = j.V;
+                row_above<In, VEC>(c, t, false, &kept, &w);
+            }
         }
     }
 
@@ -828,13 +886,20 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     int end_id = -1;
     if (u == 0.f || u == 1.f) {
         int best = u == 0.f ? 0x7FFFFFFF : -1;
-        each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
+        auto see = [&](float x, int id) {
+            if (((double)x - (double)c.m) / (double)T > -745.0)
+                best = u == 0.f ? min(best, id) : max(best, id);
+        };
+        if (listed) {
+            for (int i = c.tid; i < (int)kept_list; i += kRwThreads)
+                see(ord2f(pair_key(s_list[i])), pair_id(s_list[i]));
+        } else {
+            each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (is_kept(f[i], v0 + i) &&
-                    ((double)f[i] - (double)c.m) / (double)T > -745.0)
-                    best = u == 0.f ? min(best, v0 + i) : max(best, v0 + i);
-        });
+                for (int i = 0; i < 8; ++i)
+                    if (is_kept(f[i], v0 + i)) see(f[i], v0 + i);
+            });
+        }
         best = u == 0.f ? __reduce_min_sync(0xFFFFFFFFu, best)
                         : __reduce_max_sync(0xFFFFFFFFu, best);
         __syncthreads();
@@ -847,28 +912,38 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         __syncthreads();
     }
     if (listed) {
-        unsigned long long w = 0;
-        for (int i = c.tid; i < (int)list_n; i += kRwThreads) {
-            const bool on = s_key[i] > t || (s_key[i] == t && (int)s_id[i] <= id_cut);
-            if (!on) s_w[i] = 0;
-            w += s_w[i];
-        }
-        const unsigned long long M = cta_mass(c, w);
+        const unsigned long long M = s_w[kept_list - 1];
         const unsigned long long g = min(scale_mass(u, M, false), M - 1);
+        auto weight = [&](unsigned i) { return s_w[i] - (i ? s_w[i - 1] : 0ull); };
+        if (end_id < 0 && kept_list <= 512u) {
+            // each kept token's running weight by id
+            const unsigned i = c.tid;
+            if (i < kept_list) {
+                const int id = pair_id(s_list[i]);
+                unsigned long long run = 0, last = 0;
+                for (unsigned k = 0; k < kept_list; ++k) {
+                    const unsigned long long next = s_w[k];
+                    if (pair_id(s_list[k]) <= id) run += next - last;
+                    last = next;
+                }
+                if (run > g && run - weight(i) <= g) drawn(id, ord2f(pair_key(s_list[i])), M);
+            }
+            return;
+        }
         // running weight at most g at a, above it at b
         int a = end_id < 0 ? -1 : end_id - 1, b = end_id < 0 ? j.V - 1 : end_id;
         while (b - a > 1) {
             const int mid = a + (b - a) / 2;
-            w = 0;
-            for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                if ((int)s_id[i] <= mid) w += s_w[i];
+            unsigned long long w = 0;
+            for (unsigned i = c.tid; i < kept_list; i += kRwThreads)
+                if (pair_id(s_list[i]) <= mid) w += weight(i);
             if (cta_mass(c, w) > g)
                 b = mid;
             else
                 a = mid;
         }
-        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-            if ((int)s_id[i] == b) drawn(b, ord2f(s_key[i]), M);
+        for (unsigned i = c.tid; i < kept_list; i += kRwThreads)
+            if (pair_id(s_list[i]) == b) drawn(b, ord2f(pair_key(s_list[i])), M);
         return;
     }
     // Sums of kept weights over blocks of 256 ids, one warp a block.
@@ -879,18 +954,19 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     if (all) t = kKeyNegInf + 1;
     __syncthreads();
     unsigned finite = 0;
+    WeightQueue q;
+    q.init(c);
     for (int b = c.warp; b < blocks; b += kRwWarps) {
         float f[8];
         load8<In, VEC>(c, b * kIdBlock + c.lane * 8, f);
-        unsigned long long w = 0;
-        if (max8(f) >= ord2f(t)) {
+        if (__any_sync(0xFFFFFFFFu, max8(f) >= ord2f(t))) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                w += kept_weight(f[i], b * kIdBlock + c.lane * 8 + i);
+                q.put(c, f[i], is_kept(f[i], b * kIdBlock + c.lane * 8 + i));
                 finite += f[i] > -INFINITY;
             }
         }
-        w = warp_sum64(w);
+        const unsigned long long w = warp_sum64(q.take(c));
         if (c.lane == 0) s_w[b] = w;
     }
     if (all) kept = cta_count(c, finite);
@@ -963,7 +1039,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     }
 }
 
-constexpr size_t kRowsSmem = (size_t)kListCap * (8 + 4 + 4);
+constexpr size_t kRowsSmem = (size_t)kListCap * 16;
 
 template <typename In, bool VEC>
 static cudaError_t rows_attr()
