@@ -17,11 +17,13 @@
 // first taken in fp32 with a bound on its error, and taken again in fixed
 // point where a decision falls inside the bound.
 //
-// Only the tokens around the boundary of the kept prefix are ordered: a sample
-// of 4096 logits tells about where it lies, one pass over the row collects the
-// tokens around it into a shared list (all tokens above it where they fit), and
-// the list is sorted.  A row comes from DRAM once; the later passes hit L2,
-// since the rows in flight (two a SM) take a fraction of it.
+// Only the tokens around the boundary of the kept prefix are ordered.  A sample
+// of 8192 logits tells about where it lies.  Where the tokens above it should
+// fit a shared list, the row's only pass collects them while it takes the
+// maximum and the mass.  Otherwise a second pass (in L2: the rows in flight,
+// two a SM, take a fraction of it) lists those near the boundary, sums those
+// above exactly, by blocks of ids for the draw, and those below in fp32.  The
+// list is sorted, and the boundary is an entry of it.
 #include <float.h>
 #include <math.h>
 
@@ -33,9 +35,9 @@ namespace sv {
 constexpr int kRwThreads = 512;
 constexpr int kRwWarps = kRwThreads / 32;
 constexpr int kListCap = 4096;
-constexpr int kBins = 1024;        // of 1/16 in log2 of the weight
-constexpr float kBinsPer = 16.f;
-constexpr int kSampled = kRwThreads * 8;
+constexpr int kBins = 2048;        // of 1/32 in log2 of the weight
+constexpr float kBinsPer = 32.f;
+constexpr int kSampled = kRwThreads * 16;
 constexpr int kIdBlock = 256;      // ids of one warp's block: 8 a lane
 static_assert(kRowsMaxV / kIdBlock <= kListCap, "block sums share the list's memory");
 
@@ -44,6 +46,9 @@ static_assert(kRowsMaxV / kIdBlock <= kListCap, "block sums share the list's mem
 // maximum in log2, on average at most log2 V <= 20 (twice 20 * ln2 * 2^-24),
 // ex2 2^-22, and 11 additions of 2^-24: under 2^-18.
 constexpr double kMassEps = 0x1p-18;
+// The same for the tokens below the bracket alone, whose distances are larger
+// (up to 35 in log2; beyond, a row's tokens weigh less than 2^-15 of its maximum).
+constexpr double kTailEps = 0x1p-17;
 
 // (key, id) of a listed token: larger pairs come first in the order.
 __device__ __forceinline__ unsigned long long pair_of(uint32_t key, int id)
@@ -235,33 +240,34 @@ __device__ __forceinline__ float max8(const float (&f)[8])
                  fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
 }
 
-// The row's maximum.
+// The row's first pass: its maximum (with the lowest id that has it, where
+// `top_id` is given), its mass sum_v 2^((x_v - m) ch) within kMassEps (`mass`),
+// and the logits at or above `from` in the list (`list`; counted in
+// sh.list_n, which is 0 before).
 template <typename In, bool VEC>
-__device__ float row_max(RowCtx &c)
-{
-    float m = -INFINITY;
-    each8<In, VEC>(c, [&](int, const float (&f)[8]) { m = fmaxf(m, max8(f)); });
-    m = warp_max(m);
-    if (c.lane == 0) c.sh->fred[c.warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRwWarps; ++i) m = fmaxf(m, c.sh->fred[i]);
-    return m;
-}
-
-// The row's maximum and its mass sum_v 2^((x_v - m) ch) within kMassEps.
-template <typename In, bool VEC>
-__device__ float row_max_mass(RowCtx &c, double *mass)
+__device__ float row_first(RowCtx &c, double *mass, int *top_id, float from,
+                           unsigned long long *list)
 {
     // terms against an integer reference e (a multiple of the exponent): a
     // larger reference moves the sum by an exact power of two
     float m = -INFINITY, e = -FLT_MAX, s = 0.f;
     double total = 0.0;
-    int n = 0;
-    each8<In, VEC>(c, [&](int, const float (&f)[8]) {
+    int n = 0, at = -1;
+    each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
         const float top = max8(f);
-        m = fmaxf(m, top);
-        if (top > -INFINITY && top < INFINITY) {
+        if (top > m) {  // (a thread's ids rise)
+            m = top;
+            at = v0;
+        }
+        if (list && top >= from) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (f[i] >= from && f[i] > -INFINITY) {
+                    const unsigned k = atomicAdd(&c.sh->list_n, 1u);
+                    if (k < (unsigned)kListCap) list[k] = pair_of(row_key(f[i]), v0 + i);
+                }
+        }
+        if (mass && top > -INFINITY && top < INFINITY) {
             const float r = ceilf(top * c.ch);
             if (r > e) {
                 const float k = e == -FLT_MAX ? 0.f : pow2_int(fmaxf(e - r, -127.f));
@@ -280,23 +286,41 @@ __device__ float row_max_mass(RowCtx &c, double *mass)
             }
         }
     });
-    total += (double)s;
-    float wm = warp_max(m);
-    if (c.lane == 0) c.sh->fred[c.warp] = wm;
+    const float own = m;
+    m = warp_max(m);
+    if (c.lane == 0) c.sh->fred[c.warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRwWarps; ++i) wm = fmaxf(wm, c.sh->fred[i]);
-    m = wm;
-    // this thread's sum in units of 2^(m ch): e - m ch in fp64, its power in fp32
-    const double y = e == -FLT_MAX ? -1000.0 : (double)e - (double)m * (double)c.ch;
-    total *= y < -126.0 ? 0.0 : (double)exp2f((float)y);
-    total = warp_sumd(total);
-    if (c.lane == 0) c.sh->dred[c.warp] = total;
-    __syncthreads();
-    double z = 0.0;
+    for (int i = 0; i < kRwWarps; ++i) m = fmaxf(m, c.sh->fred[i]);
+    if (top_id) {
+        int best = 0x7FFFFFFF;
+        if (own == m && at >= 0) {
+            float f[8];
+            load8<In, VEC>(c, at, f);
 #pragma unroll
-    for (int i = 0; i < kRwWarps; ++i) z += c.sh->dred[i];
-    *mass = z;
+            for (int i = 7; i >= 0; --i)
+                if (f[i] == m) best = at + i;
+        }
+        best = __reduce_min_sync(0xFFFFFFFFu, best);
+        if (c.lane == 0) c.sh->cnt[0][c.warp] = (unsigned)best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)c.sh->cnt[0][i]);
+        *top_id = best;
+    }
+    if (mass) {
+        total += (double)s;
+        // this thread's sum in units of 2^(m ch): e - m ch in fp64, its power in fp32
+        const double y = e == -FLT_MAX ? -1000.0 : (double)e - (double)m * (double)c.ch;
+        total *= y < -126.0 ? 0.0 : (double)exp2f((float)y);
+        total = warp_sumd(total);
+        if (c.lane == 0) c.sh->dred[c.warp] = total;
+        __syncthreads();
+        double z = 0.0;
+#pragma unroll
+        for (int i = 0; i < kRwWarps; ++i) z += c.sh->dred[i];
+        *mass = z;
+    }
     return m;
 }
 
@@ -388,6 +412,75 @@ __device__ unsigned row_collect(RowCtx &c, uint32_t lo, uint32_t hi, unsigned lo
     return c.sh->list_n;
 }
 
+// The row in three by key: below lo its mass in fp32 (`tail`, within kTailEps,
+// in units of the maximum's weight), from lo to hi the list, from hi on exact
+// masses of blocks of 256 ids (`block`) and the count.  Returns the length of
+// the list (of which the first kListCap are there).
+template <typename In, bool VEC>
+__device__ unsigned row_split(RowCtx &c, uint32_t lo, uint32_t hi, unsigned long long *list,
+                              unsigned long long *block, unsigned *above, double *tail)
+{
+    const float flo = ord2f(lo), fhi = ord2f(hi);
+    __syncthreads();
+    if (c.tid == 0) c.sh->list_n = 0;
+    __syncthreads();
+    const int blocks = (c.V + kIdBlock - 1) / kIdBlock;
+    WeightQueue q;
+    q.init(c);
+    unsigned n = 0;
+    float s = 0.f;
+    double total = 0.0;
+    int steps = 0;
+    constexpr int kDeep = 2;  // blocks in flight
+    for (int b0 = c.warp; b0 < blocks; b0 += kDeep * kRwWarps) {
+        float f[kDeep][8];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+            load8<In, VEC>(c, (b0 + d * kRwWarps) * kIdBlock + c.lane * 8, f[d]);
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int b = b0 + d * kRwWarps, v0 = b * kIdBlock + c.lane * 8;
+            if (b >= blocks) break;
+            const float top = max8(f[d]);
+            if (__any_sync(0xFFFFFFFFu, top >= fhi)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool on = f[d][i] >= fhi;
+                    n += on;
+                    q.put(c, f[d][i], on);
+                }
+            }
+            const unsigned long long w = warp_sum64(q.take(c));
+            if (c.lane == 0) block[b] = w;
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = f[d][i];
+                if (x >= flo && x < fhi && x > -INFINITY) {
+                    const unsigned at = atomicAdd(&c.sh->list_n, 1u);
+                    if (at < (unsigned)kListCap) list[at] = pair_of(row_key(x), v0 + i);
+                }
+                t[i] = x < flo ? ex2f((x - c.m) * c.ch) : 0.f;
+            }
+            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+            if (++steps == 8) {
+                total += (double)s;
+                s = 0.f;
+                steps = 0;
+            }
+        }
+    }
+    total = warp_sumd(total + (double)s);
+    if (c.lane == 0) c.sh->dred[c.warp] = total;
+    *above = cta_count(c, n);
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < kRwWarps; ++i) z += c.sh->dred[i];
+    *tail = z;
+    __syncthreads();
+    return c.sh->list_n;
+}
+
 // Sort list[0 .. n) downwards (bitonic; padded to a power of two with zeros).
 // Stages of distance 32 and less stay within a warp's 64 entries.
 __device__ void list_sort(const RowCtx &c, unsigned long long *list, unsigned n)
@@ -462,6 +555,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     __shared__ RowShared sh;
     unsigned long long *s_w = rows_smem;              // [kListCap] running weights
     unsigned long long *s_list = s_w + kListCap;      // [kListCap] pairs
+    unsigned long long *s_block = s_list + kListCap;  // [kListCap] masses of id blocks
     unsigned *s_hist = reinterpret_cast<unsigned *>(s_w);       // [kBins], before the list
     float *s_tail = reinterpret_cast<float *>(s_hist + kBins);  // [kBins]
 
@@ -511,32 +605,147 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     c.ch = sh.ch;
     c.cl = sh.cl;
 
-    // ---- the maximum, and the row's mass where a filter or the draw needs it
-    const bool need_mass = T > 0.f && !by_k;
+    if (T == 0.f) {
+        int id;
+        const float m = row_first<In, VEC>(c, nullptr, &id, 0.f, nullptr);
+        answer(m > -INFINITY ? id : -1, m > -INFINITY ? 1.f : 0.f, m > -INFINITY);
+        return;
+    }
+
+    // ---- where the boundary lies, from a sample: bins of log2 weights below
+    // the sample's maximum
+    const bool filtered = by_k || by_p || min_p > 0.f;
+    const bool sampled = filtered && j.V > kListCap;
+    const float per = (float)j.V / (float)kSampled;  // tokens a sampled one stands for
+    float s_max = -INFINITY, s_all = 0.f;            // the sample's maximum and mass
+    if (sampled) {
+        for (int i = c.tid; i < kBins; i += kRwThreads) s_hist[i] = 0;
+        // twice 8 consecutive logits a thread, spread evenly over the row
+        float f[2][8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            load8<In, VEC>(c, (int)((int64_t)(c.tid + k * kRwThreads) * (j.V / 8) /
+                                    (2 * kRwThreads)) * 8, f[k]);
+        s_max = warp_max(fmaxf(max8(f[0]), max8(f[1])));
+        if (c.lane == 0) sh.fred[c.warp] = s_max;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRwWarps; ++i) s_max = fmaxf(s_max, sh.fred[i]);
+        if (s_max > -INFINITY && s_max < INFINITY) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = (s_max - f[k][i]) * c.ch * kBinsPer;
+                    atomicAdd(&s_hist[y < (float)(kBins - 1) ? (int)y : kBins - 1], 1u);
+                }
+        }
+        __syncthreads();
+        // Counts from the top and masses from the bottom, four bins a thread.
+        const int b = 4 * c.tid;
+        unsigned n[4];
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            n[i] = s_hist[b + i];
+            w[i] = (float)n[i] * ex2f(-((float)(b + i) + 0.5f) / kBinsPer);
+        }
+        unsigned cs = n[0] + n[1] + n[2] + n[3];
+        float ws = (w[0] + w[1]) + (w[2] + w[3]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned a = __shfl_up_sync(0xFFFFFFFFu, cs, d);
+            const float q = __shfl_up_sync(0xFFFFFFFFu, ws, d);
+            if (c.lane >= d) {
+                cs += a;
+                ws += q;
+            }
+        }
+        if (c.lane == 31) {
+            sh.cnt[0][c.warp] = cs;
+            sh.fred[c.warp] = ws;
+        }
+        __syncthreads();
+        for (int i = 0; i < kRwWarps; ++i) {
+            if (i < c.warp) {
+                cs += sh.cnt[0][i];
+                ws += sh.fred[i];
+            }
+            s_all += sh.fred[i];
+        }
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            s_hist[b + i] = cs;
+            s_tail[b + i] = s_all - ws;  // mass of the bins after it
+            cs -= n[i];
+            ws -= w[i];
+        }
+        __syncthreads();
+    }
+    // the first bin that is past a limit, by counts or by masses of the rest
+    auto first_bin = [&](auto past) {
+        int best = kBins - 1;
+        for (int b = 4 * c.tid + 3; b >= 4 * c.tid; --b)
+            if (past(b)) best = min(best, b);
+        best = __reduce_min_sync(0xFFFFFFFFu, best);
+        __syncthreads();
+        if (c.lane == 0) sh.cnt[0][c.warp] = (unsigned)best;
+        __syncthreads();
+        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)sh.cnt[0][i]);
+        return best;
+    };
+    const bool bins = sampled && s_max > -INFINITY && s_max < INFINITY;
+    auto bin_end = [&](int b) {  // the logit at which bin b - 1 ends and b starts
+        return b >= kBins - 1 ? -INFINITY : s_max - (float)b / kBinsPer / c.ch;
+    };
+    // surely (to several deviations) past the boundary, and surely before it;
+    // rest: the mass that top-p leaves out, in the sample's terms
+    auto guess = [&](float rest, float *from, float *to) {
+        int lo = kBins - 1, hi = 0;
+        if (by_k) {
+            const float want = (float)top_k / per, off = 4.f * sqrtf(want) + 8.f;
+            lo = first_bin([&](int b) { return (float)s_hist[b] >= want + off; });
+            hi = first_bin([&](int b) { return (float)s_hist[b] >= want - off; });
+        } else if (by_p) {
+            lo = first_bin([&](int b) { return s_tail[b] <= 0.95f * rest; });
+            hi = first_bin([&](int b) { return s_tail[b] <= 1.05f * rest; });
+        }
+        *from = bin_end(lo + 1);
+        *to = bin_end(hi);
+    };
+    auto tokens_from = [&](float x) {  // how many, by the sample
+        const float y = (s_max - x) * c.ch * kBinsPer;
+        return (float)s_hist[y < (float)(kBins - 1) ? max((int)y, 0) : kBins - 1] * per;
+    };
+    // With both k and p the mass of the top k is needed, whatever min-p keeps.
+    const bool min_cuts = min_p > 0.f && !(by_k && by_p);
+    float g_lo = -INFINITY, g_hi = INFINITY;
+    bool collect = filtered && !sampled;
+    if (bins) {
+        guess((1.f - top_p) * s_all, &g_lo, &g_hi);
+        // (the sample's maximum and mass are at most the row's: this is early)
+        if (min_cuts) g_lo = fmaxf(g_lo, s_max + T * logf(min_p) * 1.0001f - 1e-6f);
+        collect = tokens_from(g_lo) < 0.8f * kListCap;
+    }
+
+    // ---- the first pass
+    const bool need_mass = !by_k;
     double z = 1.0;
-    c.m = need_mass ? row_max_mass<In, VEC>(c, &z) : row_max<In, VEC>(c);
+    if (c.tid == 0) sh.list_n = 0;
+    __syncthreads();
+    c.m = row_first<In, VEC>(c, need_mass ? &z : nullptr, nullptr, g_lo,
+                             collect ? s_list : nullptr);
     if (c.m == -INFINITY) {  // nothing is left of the row
         answer(-1, 0.f, 0);
         return;
     }
-    if (T == 0.f) {
-        int best = 0x7FFFFFFF;
-        each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
-#pragma unroll
-            for (int i = 7; i >= 0; --i)
-                if (f[i] == c.m) best = min(best, v0 + i);
-        });
-        best = __reduce_min_sync(0xFFFFFFFFu, best);
-        if (c.lane == 0) sh.cnt[0][c.warp] = (unsigned)best;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)sh.cnt[0][i]);
-        answer(best, 1.f, 1);
-        return;
-    }
+    unsigned list_n = collect ? sh.list_n : 0;
+    if (list_n > (unsigned)kListCap) collect = false;
     if (c.m == INFINITY) {
         c.top_inf = true;
         c.m = 0.f;
+        collect = false;
+        g_lo = -INFINITY;
         unsigned n;
         unsigned long long w;
         row_above<In, VEC>(c, kKeyNegInf + 1, false, &n, &w);
@@ -576,15 +785,13 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         key_min = row_key(sh.xmin);
     }
 
-    // ---- where the boundary lies, from a sample
-    // With both k and p the mass of the top k is needed, whatever min-p keeps.
-    uint32_t lo = by_k && by_p ? kKeyNegInf + 1 : key_min;
+    uint32_t lo = min_cuts ? key_min : kKeyNegInf + 1;
     uint32_t hi = 0;  // the boundary's key is in [lo, hi); 0: open
     unsigned base_n = 0;            // tokens and mass at or above hi
     unsigned long long base_w = 0;
-    unsigned list_n = 0;
     bool listed = false;   // the list holds every kept token
     bool one_key = false, p_exact = false;
+    bool have_blocks = false;  // s_block holds the masses above hi
     Goal goal;
     goal.by_mass = !by_k && by_p;
     goal.rank = by_k ? (unsigned)top_k : 0xFFFFFFFFu;
@@ -593,96 +800,8 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         goal.hi = scale_mass(top_p, zhi, true);
     };
     set_goal();
-    const bool filtered = by_k || by_p || min_p > 0.f;
-    uint32_t guess_lo = lo, guess_hi = 0;
-    float est = (float)j.V;
-    if (filtered && j.V > kListCap) {
-        for (int i = c.tid; i < kBins; i += kRwThreads) s_hist[i] = 0;
-        __syncthreads();
-        {
-            // 8 consecutive logits a thread, spread evenly over the row
-            const int v0 = (int)((int64_t)c.tid * (j.V / 8) / kRwThreads) * 8;
-            float f[8];
-            load8<In, VEC>(c, v0, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = (c.m - f[i]) * c.ch * kBinsPer;
-                atomicAdd(&s_hist[y < (float)(kBins - 1) ? (int)y : kBins - 1], 1u);
-            }
-        }
-        __syncthreads();
-        const float per = (float)j.V / (float)kSampled;  // tokens a sampled one stands for
-        // Counts from the top and masses from the bottom, two bins a thread.
-        {
-            const int b = 2 * c.tid;
-            const unsigned n0 = s_hist[b], n1 = s_hist[b + 1];
-            const float w0 = (float)n0 * ex2f(-((float)b + 0.5f) / kBinsPer);
-            const float w1 = (float)n1 * ex2f(-((float)b + 1.5f) / kBinsPer);
-            unsigned cs = n0 + n1;
-            float ws = w0 + w1;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned a = __shfl_up_sync(0xFFFFFFFFu, cs, d);
-                const float q = __shfl_up_sync(0xFFFFFFFFu, ws, d);
-                if (c.lane >= d) {
-                    cs += a;
-                    ws += q;
-                }
-            }
-            if (c.lane == 31) {
-                sh.cnt[0][c.warp] = cs;
-                sh.fred[c.warp] = ws;
-            }
-            __syncthreads();
-            float all = 0.f;
-            for (int i = 0; i < kRwWarps; ++i) {
-                if (i < c.warp) {
-                    cs += sh.cnt[0][i];
-                    ws += sh.fred[i];
-                }
-                all += sh.fred[i];
-            }
-            s_hist[b] = cs - n1;
-            s_hist[b + 1] = cs;
-            s_tail[b] = all - (ws - w1);      // mass of the bins after b
-            s_tail[b + 1] = all - ws;
-            __syncthreads();
-        }
-        // the first bin whose end surely (to several deviations) lies past the boundary
-        auto first_bin = [&](auto past) {
-            int best = kBins - 1;
-            for (int b = 2 * c.tid + 1; b >= 2 * c.tid; --b)
-                if (past(b)) best = min(best, b);
-            best = __reduce_min_sync(0xFFFFFFFFu, best);
-            __syncthreads();
-            if (c.lane == 0) sh.cnt[0][c.warp] = (unsigned)best;
-            __syncthreads();
-            for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)sh.cnt[0][i]);
-            return best;
-        };
-        int bin = kBins - 1, bin_hi = 0;
-        if (by_k) {
-            const float want = (float)top_k / per;
-            const float margin = want + 4.f * sqrtf(want) + 8.f;
-            const float under = want - 4.f * sqrtf(want) - 8.f;
-            bin = first_bin([&](int b) { return (float)s_hist[b] >= margin; });
-            bin_hi = first_bin([&](int b) { return (float)s_hist[b] >= under; });
-        } else if (by_p) {
-            const float left = (1.f - top_p) * (float)z * 0.85f / per;
-            bin = first_bin([&](int b) { return s_tail[b] <= left; });
-            bin_hi = first_bin([&](int b) { return s_tail[b] * 0.72f <= left; });
-        }
-        if (bin < kBins - 1) {
-            const uint32_t k = row_key(c.m - (float)(bin + 1) / kBinsPer / c.ch);
-            guess_lo = max(k, lo);
-            guess_hi = row_key(c.m - (float)bin_hi / kBinsPer / c.ch);
-        }
-        // tokens in the list, if it starts there (a bin too many is no harm)
-        const float yl = (c.m - ord2f(guess_lo)) * c.ch * kBinsPer;
-        const int bl = yl < (float)(kBins - 1) ? (int)yl : kBins - 1;
-        est = (float)s_hist[bl] * per;
-        __syncthreads();
-    }
+    uint32_t guess_lo = max(row_key(g_lo), lo), guess_hi = 0;
+
     // ---- otherwise narrow [lo, hi) until its tokens fit the list
     auto narrow = [&](Goal &g) {
         unsigned in_n;  // tokens at or above lo
@@ -733,21 +852,60 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     int id_cut = j.V;
     unsigned kept = 0, kept_list = 0;  // all; those in the list, its first ones
     if (filtered) {
-        if (est < 0.9f * kListCap || j.V <= kListCap) {
-            // small kept sets: everything from the guess on
-            const uint32_t from = max(guess_lo, lo);
-            list_n = row_collect<In, VEC>(c, from, 0, s_list);
-            if (list_n <= (unsigned)kListCap) {
-                bool enough = from <= lo || (by_k && list_n >= (unsigned)top_k);
-                if (!enough && goal.by_mass) {
-                    unsigned long long w = 0;
+        // is what the list starts from past the boundary?
+        auto try_list = [&](uint32_t from) {
+            bool enough = from <= lo || (by_k && list_n >= (unsigned)top_k);
+            if (!enough && goal.by_mass) {
+                unsigned long long w = 0;
+                for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+                    w += row_weight(c, ord2f(pair_key(s_list[i])));
+                enough = goal.reached(0, cta_mass(c, w)) == 1;
+            }
+            if (enough) {
+                lo = min(from, lo);
+                listed = true;
+            }
+        };
+        if (collect) try_list(g_lo == -INFINITY ? kKeyNegInf + 1 : row_key(g_lo));
+        if (!listed && bins && !c.top_inf) {
+            // again, with the row's maximum and mass in place of the sample's
+            const float up = exp2f(fminf((c.m - s_max) * c.ch, 100.f));
+            guess((1.f - top_p) * (float)z * up / per, &g_lo, &g_hi);
+            guess_lo = max(row_key(g_lo), lo);
+            guess_hi = row_key(g_hi);
+            const float x = ord2f(guess_lo);
+            if (tokens_from(x) < 0.9f * kListCap) {
+                list_n = row_collect<In, VEC>(c, guess_lo, 0, s_list);
+                if (list_n <= (unsigned)kListCap) try_list(guess_lo);
+            } else if (goal.by_mass && guess_hi > guess_lo && z_known) {
+                double tail;
+                unsigned above;
+                list_n = row_split<In, VEC>(c, guess_lo, guess_hi, s_list, s_block, &above, &tail);
+                if (list_n <= (unsigned)kListCap) {
+                    const int blocks = (j.V + kIdBlock - 1) / kIdBlock;
+                    unsigned long long a = 0, l = 0;
+                    for (int i = c.tid; i < blocks; i += kRwThreads) a += s_block[i];
                     for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                        w += row_weight(c, ord2f(pair_key(s_list[i])));
-                    enough = goal.reached(0, cta_mass(c, w)) == 1;
-                }
-                if (enough) {
-                    lo = from;
-                    listed = true;
+                        l += row_weight(c, ord2f(pair_key(s_list[i])));
+                    a = cta_mass(c, a);
+                    l = cta_mass(c, l);
+                    // the row's mass again: only the tail is not exact
+                    const double ts = ldexp(tail, c.S);
+                    const unsigned long long old_lo = zlo, old_hi = zhi;
+                    zlo = a + l + (unsigned long long)(ts * (1.0 - kTailEps));
+                    zhi = a + l + (unsigned long long)(ts * (1.0 + kTailEps)) + 1;
+                    set_goal();
+                    if (a < goal.lo && a + l >= goal.hi && guess_lo >= lo) {
+                        lo = guess_lo;
+                        hi = guess_hi;
+                        base_n = above;
+                        base_w = a;
+                        have_blocks = true;
+                    } else {
+                        zlo = max(zlo, old_lo);
+                        zhi = min(zhi, old_hi);
+                        set_goal();
+                    }
                 }
             }
         }
@@ -757,7 +915,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
             list_n = 0;
             row_above<In, VEC>(c, key_min, false, &kept, &w);
         } else {
-            if (!listed) {
+            if (!listed && !have_blocks) {
                 narrow(goal);
                 if (by_k && by_p) {
                     // the mass of the top k, and with it the boundary of p
@@ -953,30 +1111,36 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     };
     if (all) t = kKeyNegInf + 1;
     __syncthreads();
-    unsigned finite = 0;
-    WeightQueue q;
-    q.init(c);
-    for (int b = c.warp; b < blocks; b += kRwWarps) {
-        float f[8];
-        load8<In, VEC>(c, b * kIdBlock + c.lane * 8, f);
-        if (__any_sync(0xFFFFFFFFu, max8(f) >= ord2f(t))) {
+    // (the masses above the list are there already: its own tokens are missing)
+    if (have_blocks && kept_list > 0) {
+        for (unsigned i = c.tid; i < kept_list; i += kRwThreads)
+            atomicAdd(&s_block[pair_id(s_list[i]) / kIdBlock], s_w[i] - (i ? s_w[i - 1] : 0ull));
+    } else {
+        unsigned finite = 0;
+        WeightQueue q;
+        q.init(c);
+        for (int b = c.warp; b < blocks; b += kRwWarps) {
+            float f[8];
+            load8<In, VEC>(c, b * kIdBlock + c.lane * 8, f);
+            if (__any_sync(0xFFFFFFFFu, max8(f) >= ord2f(t))) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q.put(c, f[i], is_kept(f[i], b * kIdBlock + c.lane * 8 + i));
-                finite += f[i] > -INFINITY;
+                for (int i = 0; i < 8; ++i) {
+                    q.put(c, f[i], is_kept(f[i], b * kIdBlock + c.lane * 8 + i));
+                    finite += f[i] > -INFINITY;
+                }
             }
+            const unsigned long long w = warp_sum64(q.take(c));
+            if (c.lane == 0) s_block[b] = w;
         }
-        const unsigned long long w = warp_sum64(q.take(c));
-        if (c.lane == 0) s_w[b] = w;
+        if (all) kept = cta_count(c, finite);
     }
-    if (all) kept = cta_count(c, finite);
     __syncthreads();
     // each thread takes consecutive blocks
     const int each = (blocks + kRwThreads - 1) / kRwThreads;
     unsigned long long own = 0;
     for (int i = 0; i < each; ++i) {
         const int b = c.tid * each + i;
-        if (b < blocks) own += s_w[b];
+        if (b < blocks) own += s_block[b];
     }
     const unsigned long long M = cta_mass(c, own);
     const unsigned long long g = min(scale_mass(u, M, false), M - 1);
@@ -992,7 +1156,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     if (run > g && run - own <= g) {  // exactly one thread
         unsigned long long at = run - own;
         int b = c.tid * each;
-        while (at + s_w[b] <= g) at += s_w[b++];
+        while (at + s_block[b] <= g) at += s_block[b++];
         sh.pick = b;
         sh.base = at;
     }
@@ -1039,7 +1203,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     }
 }
 
-constexpr size_t kRowsSmem = (size_t)kListCap * 16;
+constexpr size_t kRowsSmem = (size_t)kListCap * 24;
 
 template <typename In, bool VEC>
 static cudaError_t rows_attr()
