@@ -21,9 +21,14 @@
 // of 8192 logits tells about where it lies.  Where the tokens above it should
 // fit a shared list, the row's only pass collects them while it takes the
 // maximum and the mass.  Otherwise a second pass (in L2: the rows in flight,
-// two a SM, take a fraction of it) lists those near the boundary, sums those
-// above exactly, by blocks of ids for the draw, and those below in fp32.  The
-// list is sorted, and the boundary is an entry of it.
+// two a SM, take a fraction of it) lists those near the boundary and sums the
+// others: those above by blocks of ids, for the draw.  In the list the boundary,
+// and later the drawn id, are found by histograms over 9 bits at a time.
+//
+// A bf16 logit of magnitude 2^-10 to 2^12 is one of 5,632; so a pass that sums
+// many weights takes them from a table of the row's, 45 KB, and computes only
+// the others (a weight costs some 90 instructions, a look-up 8).  fp32 logits
+// are queued, and a warp weighs 32 of them at once.
 #include <float.h>
 #include <math.h>
 
@@ -38,8 +43,12 @@ constexpr int kListCap = 4096;
 constexpr int kBins = 2048;        // of 1/32 in log2 of the weight
 constexpr float kBinsPer = 32.f;
 constexpr int kSampled = kRwThreads * 16;
-constexpr int kIdBlock = 256;      // ids of one warp's block: 8 a lane
-static_assert(kRowsMaxV / kIdBlock <= kListCap, "block sums share the list's memory");
+constexpr int kIdStep = 256;       // ids of a warp's step: 8 a lane
+constexpr int kIdBlock = 1024;     // ids of a block: 4 steps
+constexpr int kMaxBlocks = kRowsMaxV / kIdBlock;
+constexpr int kTabMag = 117 << 7;  // bits of 2^-10, the table's least magnitude
+constexpr int kTabHalf = 22 << 7;  // its magnitudes, up to 2^12
+constexpr int kDigits = 512;       // bins of a selection step: 9 bits
 
 // Bound on the relative error of the fp32 mass of a row: the argument's
 // rounding and that of log2(e)/T weigh a term by its distance below the
@@ -58,14 +67,19 @@ __device__ __forceinline__ unsigned long long pair_of(uint32_t key, int id)
 __device__ __forceinline__ uint32_t pair_key(unsigned long long p) { return (uint32_t)(p >> 32); }
 __device__ __forceinline__ int pair_id(unsigned long long p) { return (int)~(uint32_t)p; }
 
+struct Digits {  // counts and masses (16 bits a word) of a selection step
+    unsigned n[kDigits], w[4][kDigits];
+};
+
 struct RowShared {
     float queue[kRwWarps][64];
-    unsigned long long mass[2][kRwWarps];
-    unsigned cnt[2][kRwWarps];
+    unsigned long long mass[kRwWarps];
+    unsigned cnt[kRwWarps];
     double dred[kRwWarps];
     float fred[kRwWarps];
     unsigned list_n;
     int pick;
+    unsigned pick_n, pick_at, sel_from, sel_to;
     unsigned long long base;
     float ch, cl, xmin;
     float2 exp2_tab[64];
@@ -78,13 +92,12 @@ struct RowCtx {
     float ch, cl;     // log2(e) / T as a pair
     int S;            // weights are multiples of 2^-S
     bool top_inf;     // the maximum is +inf: those logits share the mass
-    int par;          // buffer of the next reduction
     RowShared *sh;
 };
 
 // 8 logits from id v0 on; -inf past the row's end and in place of NaN.
 template <typename In, bool VEC>
-__device__ __forceinline__ void load8(const RowCtx &c, int v0, float (&f)[8])
+__device__ __forceinline__ void load8(const RowCtx c, int v0, float (&f)[8])
 {
     if (VEC && v0 + 8 <= c.V) {
         if (sizeof(In) == 2) {
@@ -113,18 +126,21 @@ __device__ __forceinline__ uint32_t row_key(float x) { return f2ord(x + 0.f); }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // f2ord(-inf)
 
 // w = exp((x - m) / T) as a multiple of 2^-S, to the nearest within 2^-44 w.
-__device__ __forceinline__ unsigned long long row_weight(const RowCtx &c, float x)
+// (One copy of it, and one of each pass below: copied into the loops that use
+// them they were several times the instruction caches.)
+__device__ __noinline__ unsigned long long row_weight(float x, float m, float ch, float cl, int S,
+                                                      const float2 *tab)
 {
     if (x == -INFINITY) return 0;
     // x - m = d + dl exactly
-    const float d = x - c.m, bb = d - x;
-    const float dl = (x - (d - bb)) + (-c.m - bb);
+    const float d = x - m, bb = d - x;
+    const float dl = (x - (d - bb)) + (-m - bb);
     // log2 w = p + e
-    const float p = d * c.ch;
+    const float p = d * ch;
     if (!(p > -100.f)) return 0;
-    float e = fmaf(d, c.ch, -p);
-    e = fmaf(d, c.cl, e);
-    e = fmaf(dl, c.ch, e);
+    float e = fmaf(d, ch, -p);
+    e = fmaf(d, cl, e);
+    e = fmaf(dl, ch, e);
     const float n = rintf(p * 64.f);
     const float f = fmaf(n, -0.015625f, p);  // exact
     // (f + e) ln 2 = rh + rl
@@ -142,7 +158,7 @@ __device__ __forceinline__ unsigned long long row_weight(const RowCtx &c, float 
     const float h = fmaf(0.5f, s, rh);
     const float l = ((rh - h) + 0.5f * s) + (fmaf(0.5f, se, rl) + q);
     const int ni = (int)n;
-    const float2 t = c.sh->exp2_tab[ni & 63];
+    const float2 t = tab[ni & 63];
     const float ph = t.x * h;
     float pl = fmaf(t.x, h, -ph);
     pl = fmaf(t.x, l, pl);
@@ -151,10 +167,14 @@ __device__ __forceinline__ unsigned long long row_weight(const RowCtx &c, float 
     const float wl = ((t.x - wh) + ph) + pl;
     // 48 fraction bits (wh has at most 24)
     const long long I = ((long long)(int)(wh * 16777216.f) << 24) + (int)rintf(wl * 0x1p48f);
-    const int sh = c.S - 48 + (ni >> 6);
+    const int sh = S - 48 + (ni >> 6);
     if (sh >= 0) return (unsigned long long)I << sh;
     if (sh < -62) return 0;
     return (unsigned long long)((I + (1ll << (-sh - 1))) >> -sh);
+}
+__device__ __forceinline__ unsigned long long row_weight(const RowCtx c, float x)
+{
+    return row_weight(x, c.m, c.ch, c.cl, c.S, c.sh->exp2_tab);
 }
 
 // Sum of up to 2^62 over the CTA, in every thread.
@@ -165,28 +185,26 @@ __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v)
     const unsigned d = __reduce_add_sync(0xFFFFFFFFu, (unsigned)(v >> 44));
     return (unsigned long long)a + ((unsigned long long)b << 22) + ((unsigned long long)d << 44);
 }
-__device__ __forceinline__ unsigned long long cta_mass(RowCtx &c, unsigned long long v)
+__device__ __forceinline__ unsigned long long cta_mass(const RowCtx c, unsigned long long v)
 {
     v = warp_sum64(v);
-    const int par = c.par;
-    c.par ^= 1;
-    if (c.lane == 0) c.sh->mass[par][c.warp] = v;
+    __syncthreads();
+    if (c.lane == 0) c.sh->mass[c.warp] = v;
     __syncthreads();
     unsigned long long r = 0;
 #pragma unroll
-    for (int i = 0; i < kRwWarps; ++i) r += c.sh->mass[par][i];
+    for (int i = 0; i < kRwWarps; ++i) r += c.sh->mass[i];
     return r;
 }
-__device__ __forceinline__ unsigned cta_count(RowCtx &c, unsigned v)
+__device__ __forceinline__ unsigned cta_count(const RowCtx c, unsigned v)
 {
     v = __reduce_add_sync(0xFFFFFFFFu, v);
-    const int par = c.par;
-    c.par ^= 1;
-    if (c.lane == 0) c.sh->cnt[par][c.warp] = v;
+    __syncthreads();
+    if (c.lane == 0) c.sh->cnt[c.warp] = v;
     __syncthreads();
     unsigned r = 0;
 #pragma unroll
-    for (int i = 0; i < kRwWarps; ++i) r += c.sh->cnt[par][i];
+    for (int i = 0; i < kRwWarps; ++i) r += c.sh->cnt[i];
     return r;
 }
 
@@ -216,7 +234,7 @@ __device__ __forceinline__ unsigned long long scale_mass(float f, unsigned long 
 // Visit the row in steps of 8 logits a thread: f(v0, logits).  Every lane of a
 // warp takes part in every step (logits past the row's end are -inf).
 template <typename In, bool VEC, typename F>
-__device__ __forceinline__ void each8(const RowCtx &c, F f)
+__device__ __forceinline__ void each8(const RowCtx c, F f)
 {
     constexpr int kStep = kRwThreads * 8, kDeep = sizeof(In) == 2 ? 4 : 2;  // loads in flight
     int v0 = c.tid * 8;
@@ -245,7 +263,7 @@ __device__ __forceinline__ float max8(const float (&f)[8])
 // and the logits at or above `from` in the list (`list`; counted in
 // sh.list_n, which is 0 before).
 template <typename In, bool VEC>
-__device__ float row_first(RowCtx &c, double *mass, int *top_id, float from,
+__device__ __forceinline__ float row_first(const RowCtx c, double *mass, int *top_id, float from,
                            unsigned long long *list)
 {
     // terms against an integer reference e (a multiple of the exponent): a
@@ -302,10 +320,10 @@ __device__ float row_first(RowCtx &c, double *mass, int *top_id, float from,
                 if (f[i] == m) best = at + i;
         }
         best = __reduce_min_sync(0xFFFFFFFFu, best);
-        if (c.lane == 0) c.sh->cnt[0][c.warp] = (unsigned)best;
+        if (c.lane == 0) c.sh->cnt[c.warp] = (unsigned)best;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)c.sh->cnt[0][i]);
+        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)c.sh->cnt[i]);
         *top_id = best;
     }
     if (mass) {
@@ -330,13 +348,13 @@ struct WeightQueue {
     float *buf;   // 64 of this warp's
     int n;
     unsigned long long sum;
-    __device__ __forceinline__ void init(RowCtx &c)
+    __device__ __forceinline__ void init(const RowCtx c)
     {
         buf = c.sh->queue[c.warp];
         n = 0;
         sum = 0;
     }
-    __device__ __forceinline__ void put(const RowCtx &c, float x, bool on)
+    __device__ __forceinline__ void put(const RowCtx c, float x, bool on)
     {
         const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
         if (on) buf[n + __popc(m & ((1u << c.lane) - 1))] = x;
@@ -351,7 +369,7 @@ struct WeightQueue {
         }
     }
     // the lane's part of everything put so far
-    __device__ __forceinline__ unsigned long long take(const RowCtx &c)
+    __device__ __forceinline__ unsigned long long take(const RowCtx c)
     {
         __syncwarp();
         if (c.lane < n) sum += row_weight(c, buf[c.lane]);
@@ -365,7 +383,7 @@ struct WeightQueue {
 
 // Exact mass and count of the logits with key >= k.
 template <typename In, bool VEC>
-__device__ void row_above(RowCtx &c, uint32_t k, bool want_mass, unsigned *cnt,
+__device__ __noinline__ void row_above(const RowCtx c, uint32_t k, bool want_mass, unsigned *cnt,
                           unsigned long long *mass)
 {
     const float t = ord2f(k);
@@ -390,7 +408,7 @@ __device__ void row_above(RowCtx &c, uint32_t k, bool want_mass, unsigned *cnt,
 // Collect the logits with lo <= key < hi (hi = 0: no upper end); returns how
 // many there are, of which the first kListCap are listed.
 template <typename In, bool VEC>
-__device__ unsigned row_collect(RowCtx &c, uint32_t lo, uint32_t hi, unsigned long long *list)
+__device__ __noinline__ unsigned row_collect(const RowCtx c, uint32_t lo, uint32_t hi, unsigned long long *list)
 {
     const float t = ord2f(lo);
     __syncthreads();
@@ -412,15 +430,37 @@ __device__ unsigned row_collect(RowCtx &c, uint32_t lo, uint32_t hi, unsigned lo
     return c.sh->list_n;
 }
 
-// The row in three by key: below lo its mass in fp32 (`tail`, within kTailEps,
-// in units of the maximum's weight), from lo to hi the list, from hi on exact
-// masses of blocks of 256 ids (`block`) and the count.  Returns the length of
-// the list (of which the first kListCap are there).
-template <typename In, bool VEC>
-__device__ unsigned row_split(RowCtx &c, uint32_t lo, uint32_t hi, unsigned long long *list,
-                              unsigned long long *block, unsigned *above, double *tail)
+// The row's table of bf16 weights (negative magnitudes in its second half).
+__device__ __noinline__ void row_table(const RowCtx c, unsigned long long *tab)
 {
-    const float flo = ord2f(lo), fhi = ord2f(hi);
+    __syncthreads();
+    for (int e = c.tid; e < 2 * kTabHalf; e += kRwThreads) {
+        const uint32_t bits = e < kTabHalf ? (uint32_t)(kTabMag + e)
+                                           : 0x8000u | (uint32_t)(kTabMag + e - kTabHalf);
+        const float x = __uint_as_float(bits << 16);
+        tab[e] = x <= c.m ? row_weight(c, x) : 0;
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ unsigned long long table_weight(const RowCtx c,
+                                                           const unsigned long long *tab, float x)
+{
+    const uint32_t bits = __float_as_uint(x) >> 16;
+    const uint32_t off = (bits & 0x7FFFu) - (uint32_t)kTabMag;
+    if (off < (uint32_t)kTabHalf) return tab[off + (bits >> 15) * (uint32_t)kTabHalf];
+    return row_weight(c, x);
+}
+
+// The row in three: from hi on exact masses of blocks of ids (`block`) and the
+// count; from lo to hi the list (its length is returned; the first kListCap are
+// there); below lo the mass (`tail`): exact for bf16, else in fp32 within
+// kTailEps (`ftail`, in units of the maximum's weight).
+template <typename In, bool VEC>
+__device__ __noinline__ unsigned row_split(const RowCtx c, float lo, float hi, const unsigned long long *tab,
+                              unsigned long long *list, unsigned long long *block,
+                              unsigned *above, unsigned long long *tail, double *ftail)
+{
+    constexpr bool kTab = sizeof(In) == 2;
     __syncthreads();
     if (c.tid == 0) c.sh->list_n = 0;
     __syncthreads();
@@ -428,110 +468,57 @@ __device__ unsigned row_split(RowCtx &c, uint32_t lo, uint32_t hi, unsigned long
     WeightQueue q;
     q.init(c);
     unsigned n = 0;
-    float s = 0.f;
+    unsigned long long below = 0;
     double total = 0.0;
-    int steps = 0;
-    constexpr int kDeep = 2;  // blocks in flight
-    for (int b0 = c.warp; b0 < blocks; b0 += kDeep * kRwWarps) {
-        float f[kDeep][8];
+    for (int b = c.warp; b < blocks; b += kRwWarps) {
+        unsigned long long own = 0;
+        float s = 0.f;
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d)
-            load8<In, VEC>(c, (b0 + d * kRwWarps) * kIdBlock + c.lane * 8, f[d]);
+        for (int half = 0; half < 2; ++half) {
+            float f[2][8];  // two steps in flight
 #pragma unroll
-        for (int d = 0; d < kDeep; ++d) {
-            const int b = b0 + d * kRwWarps, v0 = b * kIdBlock + c.lane * 8;
-            if (b >= blocks) break;
-            const float top = max8(f[d]);
-            if (__any_sync(0xFFFFFFFFu, top >= fhi)) {
+            for (int k = 0; k < 2; ++k)
+                load8<In, VEC>(c, b * kIdBlock + (half * 2 + k) * kIdStep + c.lane * 8, f[k]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int v0 = b * kIdBlock + (half * 2 + k) * kIdStep + c.lane * 8;
+                float t[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const bool on = f[d][i] >= fhi;
+                    const float x = f[k][i];
+                    const bool on = x >= hi;
                     n += on;
-                    q.put(c, f[d][i], on);
+                    t[i] = 0.f;
+                    if (kTab) {
+                        const unsigned long long w = table_weight(c, tab, x);
+                        own += on ? w : 0;
+                        below += x < lo ? w : 0;
+                    } else {
+                        q.put(c, x, on);
+                        if (x < lo) t[i] = ex2f((x - c.m) * c.ch);
+                    }
+                    if (x >= lo && !on) {
+                        const unsigned at = atomicAdd(&c.sh->list_n, 1u);
+                        if (at < (unsigned)kListCap) list[at] = pair_of(row_key(x), v0 + i);
+                    }
                 }
-            }
-            const unsigned long long w = warp_sum64(q.take(c));
-            if (c.lane == 0) block[b] = w;
-            float t[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = f[d][i];
-                if (x >= flo && x < fhi && x > -INFINITY) {
-                    const unsigned at = atomicAdd(&c.sh->list_n, 1u);
-                    if (at < (unsigned)kListCap) list[at] = pair_of(row_key(x), v0 + i);
-                }
-                t[i] = x < flo ? ex2f((x - c.m) * c.ch) : 0.f;
-            }
-            s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
-            if (++steps == 8) {
-                total += (double)s;
-                s = 0.f;
-                steps = 0;
+                if (!kTab) s += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
             }
         }
+        const unsigned long long w = warp_sum64(kTab ? own : q.take(c));
+        if (c.lane == 0) block[b] = w;
+        total += (double)s;
     }
-    total = warp_sumd(total + (double)s);
+    total = warp_sumd(total);
     if (c.lane == 0) c.sh->dred[c.warp] = total;
     *above = cta_count(c, n);
     double z = 0.0;
 #pragma unroll
     for (int i = 0; i < kRwWarps; ++i) z += c.sh->dred[i];
-    *tail = z;
+    *ftail = z;
+    *tail = cta_mass(c, below);
     __syncthreads();
     return c.sh->list_n;
-}
-
-// Sort list[0 .. n) downwards (bitonic; padded to a power of two with zeros).
-// Stages of distance 32 and less stay within a warp's 64 entries.
-__device__ void list_sort(const RowCtx &c, unsigned long long *list, unsigned n)
-{
-    unsigned size = 64;
-    while (size < n) size *= 2;
-    for (unsigned i = n + c.tid; i < size; i += kRwThreads) list[i] = 0;
-    __syncthreads();
-    for (unsigned k = 2; k <= size; k *= 2) {
-        for (unsigned d = k / 2; d > 0; d /= 2) {
-            for (unsigned p = c.tid; p < size / 2; p += kRwThreads) {
-                const unsigned i = 2 * p - (p & (d - 1)), o = i + d;
-                const unsigned long long a = list[i], b = list[o];
-                if ((a < b) == ((i & k) == 0)) {
-                    list[i] = b;
-                    list[o] = a;
-                }
-            }
-            if (d > 32 || (d == 1 && k >= 64))
-                __syncthreads();
-            else
-                __syncwarp();
-        }
-    }
-    __syncthreads();
-}
-
-// Running sums of the sorted list's weights, inclusive, to sum[0 .. n).
-__device__ void list_sums(RowCtx &c, const unsigned long long *list, unsigned long long *sum,
-                          unsigned n)
-{
-    const unsigned each = (n + kRwThreads - 1) / kRwThreads, from = c.tid * each;
-    unsigned long long own = 0;
-    for (unsigned i = from; i < min(from + each, n); ++i) {
-        own += row_weight(c, ord2f(pair_key(list[i])));
-        sum[i] = own;
-    }
-    unsigned long long run = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, run, d);
-        if (c.lane >= d) run += a;
-    }
-    const int par = c.par;
-    c.par ^= 1;
-    if (c.lane == 31) c.sh->mass[par][c.warp] = run;
-    __syncthreads();
-    for (int i = 0; i < c.warp; ++i) run += c.sh->mass[par][i];
-    run -= own;
-    for (unsigned i = from; i < min(from + each, n); ++i) sum[i] += run;
-    __syncthreads();
 }
 
 // What the kept prefix has to reach: `rank` tokens, or a mass known to lie in
@@ -548,14 +535,228 @@ struct Goal {
     }
 };
 
+// What select_step looks at: the keys of the listed tokens (downwards), the ids
+// of those with one key, or the ids of the kept ones (both upwards).
+enum : int { kByKey, kIdsOfKey, kKeptIds };
+enum : int { kFound, kOn, kPast, kAgain };
+
+// One step of finding the value in [from, to) at which counts and masses, on
+// top of n and w, reach the goal: 9 bits of it.  Narrows [from, to) to the
+// step's bin, with n and w what comes before it and n_at the tokens in it.
+// kFound: the bin is one value; kPast: the goal is beyond all; kAgain: bounds
+// that do not tell (nothing is changed).
+__device__ __noinline__ int select_step(const RowCtx c, Digits *dig, const unsigned long long *list,
+                                        const unsigned long long *weight, int len, int what,
+                                        uint32_t key, int cut, uint32_t *from, uint32_t *to,
+                                        const Goal g, unsigned *n, unsigned long long *w,
+                                        unsigned *n_at)
+{
+    RowShared &sh = *c.sh;
+    const uint32_t lo = *from, span = *to - lo;
+    const int shift = span <= 1 ? 0 : max(32 - __clz(span - 1) - 9, 0);
+    const uint32_t last = span <= 1 ? 0 : (span - 1) >> shift;
+    dig->n[c.tid] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dig->w[k][c.tid] = 0;
+    if (c.tid == 0) sh.pick = -1;
+    __syncthreads();
+    for (int i = c.tid; i < len; i += kRwThreads) {
+        const unsigned long long p = list[i];
+        const uint32_t x = what == kByKey ? pair_key(p) : (uint32_t)pair_id(p);
+        const bool on = what == kByKey || (what == kIdsOfKey && pair_key(p) == key) ||
+                        (what == kKeptIds && (pair_key(p) > key ||
+                                              (pair_key(p) == key && pair_id(p) <= cut)));
+        if (on && x >= lo && x - lo < span) {
+            const uint32_t b = (x - lo) >> shift, d = what == kByKey ? last - b : b;
+            atomicAdd(&dig->n[d], 1u);
+            if (g.by_mass || what == kByKey) {
+                const unsigned long long y = weight[i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    atomicAdd(&dig->w[k][d], (unsigned)(y >> (16 * k)) & 0xFFFFu);
+            }
+        }
+    }
+    __syncthreads();
+    const unsigned own_n = dig->n[c.tid];
+    unsigned long long own_w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) own_w += (unsigned long long)dig->w[k][c.tid] << (16 * k);
+    unsigned run_n = own_n;
+    unsigned long long run_w = own_w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned a = __shfl_up_sync(0xFFFFFFFFu, run_n, d);
+        const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, run_w, d);
+        if (c.lane >= d) {
+            run_n += a;
+            run_w += b;
+        }
+    }
+    if (c.lane == 31) {
+        sh.cnt[c.warp] = run_n;
+        sh.mass[c.warp] = run_w;
+    }
+    __syncthreads();
+    run_n += *n;
+    run_w += *w;
+    for (int i = 0; i < c.warp; ++i) {
+        run_n += sh.cnt[i];
+        run_w += sh.mass[i];
+    }
+    const int got = g.reached(run_n, run_w), had = g.reached(run_n - own_n, run_w - own_w);
+    // (a goal that needs nothing is reached by the first token)
+    if (got == 1 && own_n > 0 && (had == 0 || run_n - own_n == *n)) {
+        sh.pick = c.tid;
+        sh.pick_n = run_n - own_n;
+        sh.base = run_w - own_w;
+        sh.pick_at = own_n;
+    }
+    if (__syncthreads_or(own_n > 0 && (got < 0 || had < 0))) return kAgain;
+    const int pick = sh.pick;
+    if (pick < 0) return kPast;
+    *n = sh.pick_n;
+    *w = sh.base;
+    *n_at = sh.pick_at;
+    const uint32_t b = what == kByKey ? last - (uint32_t)pick : (uint32_t)pick;
+    *from = lo + (b << shift);
+    *to = *from + min(*to - *from, 1u << shift);
+    __syncthreads();
+    return shift == 0 ? kFound : kOn;
+}
+
+// The same by one warp, 6 bits a step, for short lists: the other warps wait,
+// which costs less than sixteen warps' share of such a step.
+__device__ __noinline__ int select_warp(const RowCtx c, Digits *dig,
+                                        const unsigned long long *list,
+                                        const unsigned long long *weight, int len, int what,
+                                        uint32_t key, int cut, uint32_t *from, uint32_t *to,
+                                        const Goal g, unsigned *n, unsigned long long *w,
+                                        unsigned *n_at)
+{
+    RowShared &sh = *c.sh;
+    __syncthreads();
+    if (c.warp == 0) {
+        uint32_t lo = *from, end = *to;
+        unsigned before_n = *n, at_n = 0;
+        unsigned long long before_w = *w;
+        int state = kOn;
+        while (state == kOn) {
+            const uint32_t span = end - lo;
+            const int shift = span <= 1 ? 0 : max(32 - __clz(span - 1) - 6, 0);
+            const uint32_t last = span <= 1 ? 0 : (span - 1) >> shift;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                dig->n[c.lane + 32 * h] = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dig->w[k][c.lane + 32 * h] = 0;
+            }
+            __syncwarp();
+            for (int i = c.lane; i < len; i += 32) {
+                const unsigned long long p = list[i];
+                const uint32_t x = what == kByKey ? pair_key(p) : (uint32_t)pair_id(p);
+                const bool on = what == kByKey || (what == kIdsOfKey && pair_key(p) == key) ||
+                                (what == kKeptIds && (pair_key(p) > key ||
+                                                      (pair_key(p) == key && pair_id(p) <= cut)));
+                if (on && x >= lo && x - lo < span) {
+                    const uint32_t b = (x - lo) >> shift, d = what == kByKey ? last - b : b;
+                    atomicAdd(&dig->n[d], 1u);
+                    const unsigned long long y = weight[i];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        atomicAdd(&dig->w[k][d], (unsigned)(y >> (16 * k)) & 0xFFFFu);
+                }
+            }
+            __syncwarp();
+            // two neighbouring bins a lane
+            unsigned own_n[2], run_n;
+            unsigned long long own_w[2], run_w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                own_n[h] = dig->n[2 * c.lane + h];
+                own_w[h] = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    own_w[h] += (unsigned long long)dig->w[k][2 * c.lane + h] << (16 * k);
+            }
+            run_n = own_n[0] + own_n[1];
+            run_w = own_w[0] + own_w[1];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned a = __shfl_up_sync(0xFFFFFFFFu, run_n, d);
+                const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, run_w, d);
+                if (c.lane >= d) {
+                    run_n += a;
+                    run_w += b;
+                }
+            }
+            unsigned a_n = before_n + run_n - own_n[0] - own_n[1];
+            unsigned long long a_w = before_w + run_w - own_w[0] - own_w[1];
+            int pick = -1;
+            bool open = false;
+            unsigned pick_n = 0, pick_at = 0;
+            unsigned long long pick_w = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int had = g.reached(a_n, a_w), got = g.reached(a_n + own_n[h], a_w + own_w[h]);
+                open = open || (own_n[h] > 0 && (got < 0 || had < 0));
+                if (got == 1 && own_n[h] > 0 && (had == 0 || a_n == before_n)) {
+                    pick = 2 * c.lane + h;
+                    pick_n = a_n;
+                    pick_w = a_w;
+                    pick_at = own_n[h];
+                }
+                a_n += own_n[h];
+                a_w += own_w[h];
+            }
+            if (__any_sync(0xFFFFFFFFu, open)) {
+                state = kAgain;
+                break;
+            }
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, pick >= 0);
+            if (!who) {
+                state = kPast;
+                break;
+            }
+            const int src = __ffs(who) - 1;
+            pick = __shfl_sync(0xFFFFFFFFu, pick, src);
+            before_n = __shfl_sync(0xFFFFFFFFu, pick_n, src);
+            before_w = __shfl_sync(0xFFFFFFFFu, pick_w, src);
+            at_n = __shfl_sync(0xFFFFFFFFu, pick_at, src);
+            const uint32_t b = what == kByKey ? last - (uint32_t)pick : (uint32_t)pick;
+            lo += b << shift;
+            end = lo + min(end - lo, 1u << shift);  // (the keys end near 2^32)
+            if (shift == 0) state = kFound;
+            __syncwarp();
+        }
+        if (c.lane == 0) {
+            sh.pick = state;
+            sh.sel_from = lo;
+            sh.sel_to = end;
+            sh.pick_n = before_n;
+            sh.base = before_w;
+            sh.pick_at = at_n;
+        }
+    }
+    __syncthreads();
+    *from = sh.sel_from;
+    *to = sh.sel_to;
+    *n = sh.pick_n;
+    *w = sh.base;
+    *n_at = sh.pick_at;
+    return sh.pick;
+}
+
 template <typename In, bool VEC>
 __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
 {
     extern __shared__ unsigned long long rows_smem[];
     __shared__ RowShared sh;
-    unsigned long long *s_w = rows_smem;              // [kListCap] running weights
-    unsigned long long *s_list = s_w + kListCap;      // [kListCap] pairs
-    unsigned long long *s_block = s_list + kListCap;  // [kListCap] masses of id blocks
+    unsigned long long *s_w = rows_smem;              // [kListCap] weights of the list
+    unsigned long long *s_tab = s_w;                  // [2 kTabHalf] before them: the table
+    unsigned long long *s_list = s_w + 2 * kTabHalf;  // [kListCap] pairs
+    unsigned long long *s_block = s_list + kListCap;  // [kMaxBlocks] masses of id blocks
+    Digits *s_dig = reinterpret_cast<Digits *>(s_block + kMaxBlocks);
     unsigned *s_hist = reinterpret_cast<unsigned *>(s_w);       // [kBins], before the list
     float *s_tail = reinterpret_cast<float *>(s_hist + kBins);  // [kBins]
 
@@ -564,7 +765,6 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     c.lane = c.tid & 31;
     c.warp = c.tid >> 5;
     c.V = j.V;
-    c.par = 0;
     c.top_inf = false;
     c.sh = &sh;
     c.S = 0;
@@ -662,13 +862,13 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
             }
         }
         if (c.lane == 31) {
-            sh.cnt[0][c.warp] = cs;
+            sh.cnt[c.warp] = cs;
             sh.fred[c.warp] = ws;
         }
         __syncthreads();
         for (int i = 0; i < kRwWarps; ++i) {
             if (i < c.warp) {
-                cs += sh.cnt[0][i];
+                cs += sh.cnt[i];
                 ws += sh.fred[i];
             }
             s_all += sh.fred[i];
@@ -689,9 +889,9 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
             if (past(b)) best = min(best, b);
         best = __reduce_min_sync(0xFFFFFFFFu, best);
         __syncthreads();
-        if (c.lane == 0) sh.cnt[0][c.warp] = (unsigned)best;
+        if (c.lane == 0) sh.cnt[c.warp] = (unsigned)best;
         __syncthreads();
-        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)sh.cnt[0][i]);
+        for (int i = 0; i < kRwWarps; ++i) best = min(best, (int)sh.cnt[i]);
         return best;
     };
     const bool bins = sampled && s_max > -INFINITY && s_max < INFINITY;
@@ -700,15 +900,15 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     };
     // surely (to several deviations) past the boundary, and surely before it;
     // rest: the mass that top-p leaves out, in the sample's terms
-    auto guess = [&](float rest, float *from, float *to) {
+    auto guess = [&](float rest, float margin, float *from, float *to) {
         int lo = kBins - 1, hi = 0;
         if (by_k) {
             const float want = (float)top_k / per, off = 4.f * sqrtf(want) + 8.f;
             lo = first_bin([&](int b) { return (float)s_hist[b] >= want + off; });
             hi = first_bin([&](int b) { return (float)s_hist[b] >= want - off; });
         } else if (by_p) {
-            lo = first_bin([&](int b) { return s_tail[b] <= 0.95f * rest; });
-            hi = first_bin([&](int b) { return s_tail[b] <= 1.05f * rest; });
+            lo = first_bin([&](int b) { return s_tail[b] <= (1.f - margin) * rest; });
+            hi = first_bin([&](int b) { return s_tail[b] <= (1.f + margin) * rest; });
         }
         *from = bin_end(lo + 1);
         *to = bin_end(hi);
@@ -722,7 +922,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     float g_lo = -INFINITY, g_hi = INFINITY;
     bool collect = filtered && !sampled;
     if (bins) {
-        guess((1.f - top_p) * s_all, &g_lo, &g_hi);
+        guess((1.f - top_p) * s_all, 0.1f, &g_lo, &g_hi);
         // (the sample's maximum and mass are at most the row's: this is early)
         if (min_cuts) g_lo = fmaxf(g_lo, s_max + T * logf(min_p) * 1.0001f - 1e-6f);
         collect = tokens_from(g_lo) < 0.8f * kListCap;
@@ -767,10 +967,22 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         zlo = (unsigned long long)(zs * (1.0 - kMassEps));
         zhi = (unsigned long long)(zs * (1.0 + kMassEps)) + 1;
     }
-    auto refine = [&]() {  // the row's mass in fixed point
+    // The row's mass in fixed point.  (The list's weights are lost: the table
+    // takes their place.)
+    auto refine = [&]() {
         unsigned n;
-        unsigned long long w;
-        row_above<In, VEC>(c, kKeyNegInf + 1, true, &n, &w);
+        unsigned long long w = 0;
+        if (sizeof(In) == 2 && !c.top_inf) {
+            unsigned long long none;
+            double f;
+            row_table(c, s_tab);
+            row_split<In, VEC>(c, -FLT_MAX, -FLT_MAX, s_tab, s_list, s_block, &n, &none, &f);
+            const int blocks = (j.V + kIdBlock - 1) / kIdBlock;
+            for (int i = c.tid; i < blocks; i += kRwThreads) w += s_block[i];
+            w = cta_mass(c, w);
+        } else {
+            row_above<In, VEC>(c, kKeyNegInf + 1, true, &n, &w);
+        }
         zlo = zhi = w;
     };
     if (!z_known && by_p) refine();
@@ -839,18 +1051,38 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         list_n = in_n - base_n <= (unsigned)kListCap ? row_collect<In, VEC>(c, lo, hi, s_list) : 0;
         one_key = in_n - base_n > (unsigned)kListCap;
     };
-    // entries of the list whose running weight, with the mass above, is below x
-    auto below = [&](unsigned long long x) {
-        unsigned n = 0;
-        for (int i = c.tid; i < (int)list_n; i += kRwThreads) n += base_w + s_w[i] < x;
-        return cta_count(c, n);
+    // Weights of the listed tokens.
+    auto weigh = [&]() {
+        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+            s_w[i] = row_weight(c, ord2f(pair_key(s_list[i])));
+        __syncthreads();
+    };
+    // select_step with the bounds on the row's mass refined where they do not tell
+    auto select = [&](int what, uint32_t from, uint32_t to, Goal &g, uint32_t key, int cut,
+                      uint32_t *v, unsigned *n, unsigned long long *w, unsigned *n_at) -> bool {
+        for (;;) {
+            const int r = list_n <= 1024u
+                              ? select_warp(c, s_dig, s_list, s_w, (int)list_n, what, key, cut,
+                                            &from, &to, g, n, w, n_at)
+                              : select_step(c, s_dig, s_list, s_w, (int)list_n, what, key, cut,
+                                            &from, &to, g, n, w, n_at);
+            if (r == kAgain) {
+                refine();
+                set_goal();
+                weigh();
+                g = goal;
+            } else if (r != kOn) {
+                *v = from;
+                return r == kFound;
+            }
+        }
     };
 
     // ---- the boundary: the last kept token's key t and id (id_cut), and the
     // number of kept tokens
     uint32_t t = key_min;
     int id_cut = j.V;
-    unsigned kept = 0, kept_list = 0;  // all; those in the list, its first ones
+    unsigned kept = 0;
     if (filtered) {
         // is what the list starts from past the boundary?
         auto try_list = [&](uint32_t from) {
@@ -867,10 +1099,14 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
             }
         };
         if (collect) try_list(g_lo == -INFINITY ? kKeyNegInf + 1 : row_key(g_lo));
-        if (!listed && bins && !c.top_inf) {
-            // again, with the row's maximum and mass in place of the sample's
+        // again, with the row's maximum and mass in place of the sample's; and
+        // with other margins where that missed or was too wide
+        float margin = 0.05f;
+        for (int time = 0; time < (goal.by_mass ? 3 : 1) && !listed && !have_blocks && bins &&
+                           !c.top_inf; ++time) {
             const float up = exp2f(fminf((c.m - s_max) * c.ch, 100.f));
-            guess((1.f - top_p) * (float)z * up / per, &g_lo, &g_hi);
+            guess((1.f - top_p) * (float)z * up / per, margin, &g_lo, &g_hi);
+            margin = 0.4f;
             guess_lo = max(row_key(g_lo), lo);
             guess_hi = row_key(g_hi);
             const float x = ord2f(guess_lo);
@@ -878,22 +1114,31 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 list_n = row_collect<In, VEC>(c, guess_lo, 0, s_list);
                 if (list_n <= (unsigned)kListCap) try_list(guess_lo);
             } else if (goal.by_mass && guess_hi > guess_lo && z_known) {
-                double tail;
+                double ftail;
+                unsigned long long tail;
                 unsigned above;
-                list_n = row_split<In, VEC>(c, guess_lo, guess_hi, s_list, s_block, &above, &tail);
-                if (list_n <= (unsigned)kListCap) {
+                if (sizeof(In) == 2) row_table(c, s_tab);
+                list_n = row_split<In, VEC>(c, ord2f(guess_lo), ord2f(guess_hi), s_tab, s_list,
+                                            s_block, &above, &tail, &ftail);
+                if (list_n > (unsigned)kListCap) {
+                    margin = 0.02f;
+                } else {
                     const int blocks = (j.V + kIdBlock - 1) / kIdBlock;
                     unsigned long long a = 0, l = 0;
                     for (int i = c.tid; i < blocks; i += kRwThreads) a += s_block[i];
-                    for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                        l += row_weight(c, ord2f(pair_key(s_list[i])));
+                    weigh();
+                    for (int i = c.tid; i < (int)list_n; i += kRwThreads) l += s_w[i];
                     a = cta_mass(c, a);
                     l = cta_mass(c, l);
-                    // the row's mass again: only the tail is not exact
-                    const double ts = ldexp(tail, c.S);
+                    // the row's mass again: at most the tail is not exact
+                    const double ts = ldexp(ftail, c.S);
                     const unsigned long long old_lo = zlo, old_hi = zhi;
-                    zlo = a + l + (unsigned long long)(ts * (1.0 - kTailEps));
-                    zhi = a + l + (unsigned long long)(ts * (1.0 + kTailEps)) + 1;
+                    if (sizeof(In) == 2) {
+                        zlo = zhi = a + l + tail;
+                    } else {
+                        zlo = max(old_lo, a + l + (unsigned long long)(ts * (1.0 - kTailEps)));
+                        zhi = min(old_hi, a + l + (unsigned long long)(ts * (1.0 + kTailEps)) + 1);
+                    }
                     set_goal();
                     if (a < goal.lo && a + l >= goal.hi && guess_lo >= lo) {
                         lo = guess_lo;
@@ -901,19 +1146,19 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                         base_n = above;
                         base_w = a;
                         have_blocks = true;
-                    } else {
-                        zlo = max(zlo, old_lo);
-                        zhi = min(zhi, old_hi);
-                        set_goal();
                     }
                 }
             }
         }
-        if (!listed && !by_k && !by_p) {
-            // min-p alone needs no list: its boundary is known
+        // min-p's boundary is known; it needs no list where it comes first
+        bool min_first = !listed && !by_k && !by_p;
+        if (min_first || (!listed && !have_blocks && goal.by_mass && min_cuts)) {
             unsigned long long w;
+            row_above<In, VEC>(c, key_min, by_p, &kept, &w);
+            min_first = min_first || goal.reached(kept, w) == 0;
+        }
+        if (min_first) {
             list_n = 0;
-            row_above<In, VEC>(c, key_min, false, &kept, &w);
         } else {
             if (!listed && !have_blocks) {
                 narrow(goal);
@@ -921,21 +1166,21 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                     // the mass of the top k, and with it the boundary of p
                     unsigned long long w;
                     row_above<In, VEC>(c, hi, true, &base_n, &w);
-                    const unsigned r = (unsigned)min(top_k, 0x7FFFFFFF) - base_n;
-                    unsigned long long M;
+                    const unsigned r = (unsigned)top_k - base_n;
                     if (one_key) {
-                        M = w + r * row_weight(c, ord2f(lo));
+                        w += r * row_weight(c, ord2f(lo));
                     } else {
-                        list_sort(c, s_list, list_n);
-                        list_sums(c, s_list, s_w, list_n);
-                        const unsigned at = min(r, list_n);
-                        M = w + (at ? s_w[at - 1] : 0);
+                        weigh();
+                        uint32_t v;
+                        unsigned n = base_n, n_at;
+                        if (select(kByKey, lo, hi, goal, 0u, 0, &v, &n, &w, &n_at))
+                            w += ((unsigned)top_k - n) * row_weight(c, ord2f(v));
+                        else
+                            for (int i = 0; i < (int)list_n; ++i) w += s_w[i];
                     }
-                    Goal g;
-                    g.by_mass = true;
-                    g.rank = 0;
-                    g.lo = g.hi = scale_mass(top_p, M, true);
-                    goal = g;
+                    goal.by_mass = true;
+                    goal.rank = 0;
+                    goal.lo = goal.hi = scale_mass(top_p, w, true);
                     lo = kKeyNegInf + 1;
                     guess_lo = guess_hi = 0;
                     p_exact = true;
@@ -983,46 +1228,95 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                     id_cut = b;
                 }
             } else {
-                list_sort(c, s_list, list_n);
-                list_sums(c, s_list, s_w, list_n);
-                unsigned n = list_n;
-                if (by_k) n = min(n, (unsigned)top_k - base_n);
-                if (by_k && by_p && !p_exact) {
-                    // (the list starts at the maximum here)
-                    n = min(n, below(scale_mass(top_p, s_w[n - 1], true)) + 1);
-                } else if (by_p) {
-                    if (below(goal.lo) != below(goal.hi)) {
+                if (!have_blocks) weigh();
+                const uint32_t end = hi ? hi : row_key(c.m) + 1;
+                unsigned n = base_n, n_at = 0;
+                unsigned long long w = base_w;
+                t = lo;
+                kept = base_n + list_n;
+                // tokens of the boundary's key until the goal, lowest ids first
+                auto until = [&](const Goal &g, unsigned long long wt) -> unsigned {
+                    if (!g.by_mass) return g.rank - n;
+                    if (!wt) return n_at;
+                    return (unsigned)min((unsigned long long)n_at,
+                                         (g.hi - min(w, g.hi) + wt - 1) / wt);
+                };
+                unsigned r = 0xFFFFFFFFu;
+                if (select(kByKey, lo, end, goal, 0u, 0, &t, &n, &w, &n_at)) {
+                    const unsigned long long wt = row_weight(c, ord2f(t));
+                    if (goal.lo != goal.hi && goal.by_mass && wt &&
+                        (goal.lo - min(w, goal.lo) + wt - 1) / wt !=
+                            (goal.hi - min(w, goal.hi) + wt - 1) / wt) {
                         refine();
                         set_goal();
+                        weigh();
                     }
-                    n = min(n, below(goal.hi) + 1);
+                    r = max(until(goal, wt), 1u);
+                    kept = n + min(r, n_at);
+                    if (by_k && p_exact) kept = min(kept, (unsigned)top_k);
+                } else {
+                    // (the goal is past the list's end: fewer than k finite
+                    // logits, or min-p's boundary comes first)
+                    n = kept;
+                    w = base_w;
+                    unsigned long long l = 0;
+                    for (int i = c.tid; i < (int)list_n; i += kRwThreads) l += s_w[i];
+                    w += cta_mass(c, l);
+                    n_at = 0;
                 }
-                // min-p cuts at a logit, with all its equals
-                unsigned m = 0;
-                for (int i = c.tid; i < (int)list_n; i += kRwThreads)
-                    m += pair_key(s_list[i]) >= key_min;
-                m = cta_count(c, m);
-                if (m < n && min_p > 0.f) {
-                    n = m;
-                    if (n == 0 && base_n > 0) {
-                        // its boundary lies above the list
-                        unsigned long long w;
-                        row_above<In, VEC>(c, key_min, false, &kept, &w);
+                if (by_k && by_p && !p_exact) {
+                    // the same over the top k, for p of their mass
+                    const unsigned long long wt = n_at ? row_weight(c, ord2f(t)) : 0;
+                    const unsigned long long M = w + (n_at ? min(r, n_at) * wt : 0);
+                    Goal g;
+                    g.by_mass = true;
+                    g.rank = 0;
+                    g.lo = g.hi = scale_mass(top_p, M, true);
+                    uint32_t tp;
+                    unsigned pn = 0, p_at;
+                    unsigned long long pw = 0;
+                    if (select(kByKey, lo, end, g, 0u, 0, &tp, &pn, &pw, &p_at)) {
+                        n = pn;
+                        w = pw;
+                        const unsigned all_at = n_at;
+                        n_at = p_at;
+                        const unsigned rp = max(until(g, row_weight(c, ord2f(tp))), 1u);
+                        if (tp > t || r == 0xFFFFFFFFu || rp < r) {
+                            r = rp;
+                            kept = pn + min(rp, p_at);
+                        } else {
+                            n_at = all_at;
+                        }
+                        t = tp;
                     }
                 }
-                kept_list = n;
-                if (n > 0) {
-                    kept = base_n + n;
-                    t = pair_key(s_list[n - 1]);
-                    id_cut = pair_id(s_list[n - 1]);
+                if (r < n_at) {
+                    // the id of the r-th lowest among the boundary's equals
+                    Goal g;
+                    g.by_mass = false;
+                    g.rank = r;
+                    g.lo = g.hi = 0;
+                    uint32_t id;
+                    unsigned in = 0, i_at;
+                    unsigned long long iw = 0;
+                    select(kIdsOfKey, 0u, (uint32_t)j.V, g, t, 0, &id, &in, &iw, &i_at);
+                    id_cut = (int)id;
                 }
             }
-            // (a bracket of one key below min-p's boundary)
+            // min-p cuts at a logit, with all its equals
             if (t < key_min) {
                 unsigned long long w;
                 t = key_min;
                 id_cut = j.V;
-                row_above<In, VEC>(c, t, false, &kept, &w);
+                if (hi && key_min >= hi) have_blocks = false;
+                if (listed) {
+                    unsigned n = 0;
+                    for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+                        n += pair_key(s_list[i]) >= t;
+                    kept = cta_count(c, n);
+                } else {
+                    row_above<In, VEC>(c, t, false, &kept, &w);
+                }
             }
         }
     }
@@ -1049,8 +1343,10 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 best = u == 0.f ? min(best, id) : max(best, id);
         };
         if (listed) {
-            for (int i = c.tid; i < (int)kept_list; i += kRwThreads)
-                see(ord2f(pair_key(s_list[i])), pair_id(s_list[i]));
+            for (int i = c.tid; i < (int)list_n; i += kRwThreads) {
+                const float x = ord2f(pair_key(s_list[i]));
+                if (is_kept(x, pair_id(s_list[i]))) see(x, pair_id(s_list[i]));
+            }
         } else {
             each8<In, VEC>(c, [&](int v0, const float (&f)[8]) {
 #pragma unroll
@@ -1061,72 +1357,71 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         best = u == 0.f ? __reduce_min_sync(0xFFFFFFFFu, best)
                         : __reduce_max_sync(0xFFFFFFFFu, best);
         __syncthreads();
-        if (c.lane == 0) sh.cnt[0][c.warp] = (unsigned)best;
+        if (c.lane == 0) sh.cnt[c.warp] = (unsigned)best;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRwWarps; ++i)
-            best = u == 0.f ? min(best, (int)sh.cnt[0][i]) : max(best, (int)sh.cnt[0][i]);
+            best = u == 0.f ? min(best, (int)sh.cnt[i]) : max(best, (int)sh.cnt[i]);
         end_id = best;
         __syncthreads();
     }
+    auto kept_at = [&](int i, uint32_t *x) {
+        const int id = pair_id(s_list[i]);
+        *x = (uint32_t)id;
+        return is_kept(ord2f(pair_key(s_list[i])), id);
+    };
     if (listed) {
-        const unsigned long long M = s_w[kept_list - 1];
-        const unsigned long long g = min(scale_mass(u, M, false), M - 1);
-        auto weight = [&](unsigned i) { return s_w[i] - (i ? s_w[i - 1] : 0ull); };
-        if (end_id < 0 && kept_list <= 512u) {
-            // each kept token's running weight by id
-            const unsigned i = c.tid;
-            if (i < kept_list) {
-                const int id = pair_id(s_list[i]);
-                unsigned long long run = 0, last = 0;
-                for (unsigned k = 0; k < kept_list; ++k) {
-                    const unsigned long long next = s_w[k];
-                    if (pair_id(s_list[k]) <= id) run += next - last;
-                    last = next;
-                }
-                if (run > g && run - weight(i) <= g) drawn(id, ord2f(pair_key(s_list[i])), M);
-            }
-            return;
-        }
-        // running weight at most g at a, above it at b
-        int a = end_id < 0 ? -1 : end_id - 1, b = end_id < 0 ? j.V - 1 : end_id;
-        while (b - a > 1) {
-            const int mid = a + (b - a) / 2;
+        unsigned long long M = 0;
+        uint32_t id;
+        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+            if (kept_at(i, &id)) M += s_w[i];
+        M = cta_mass(c, M);
+        id = (uint32_t)end_id;
+        if (end_id < 0) {
+            // the first id whose running weight exceeds u M
+            Goal g;
+            g.by_mass = true;
+            g.rank = 0;
+            g.lo = g.hi = min(scale_mass(u, M, false), M - 1) + 1;
+            unsigned n = 0, n_at;
             unsigned long long w = 0;
-            for (unsigned i = c.tid; i < kept_list; i += kRwThreads)
-                if (pair_id(s_list[i]) <= mid) w += weight(i);
-            if (cta_mass(c, w) > g)
-                b = mid;
-            else
-                a = mid;
+            select(kKeptIds, 0u, (uint32_t)j.V, g, t, id_cut, &id, &n, &w, &n_at);
         }
-        for (unsigned i = c.tid; i < kept_list; i += kRwThreads)
-            if (pair_id(s_list[i]) == b) drawn(b, ord2f(pair_key(s_list[i])), M);
+        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+            if ((uint32_t)pair_id(s_list[i]) == id) drawn((int)id, ord2f(pair_key(s_list[i])), M);
         return;
     }
-    // Sums of kept weights over blocks of 256 ids, one warp a block.
+    // Sums of kept weights over blocks of ids, one warp a block.
     const int blocks = (j.V + kIdBlock - 1) / kIdBlock;
     auto kept_weight = [&](float x, int id) -> unsigned long long {
         return is_kept(x, id) ? row_weight(c, x) : 0;
     };
-    if (all) t = kKeyNegInf + 1;
     __syncthreads();
-    // (the masses above the list are there already: its own tokens are missing)
-    if (have_blocks && kept_list > 0) {
-        for (unsigned i = c.tid; i < kept_list; i += kRwThreads)
-            atomicAdd(&s_block[pair_id(s_list[i]) / kIdBlock], s_w[i] - (i ? s_w[i - 1] : 0ull));
+    if (have_blocks) {
+        // (the masses above the list are there: the list's own kept tokens are missing)
+        uint32_t id;
+        for (int i = c.tid; i < (int)list_n; i += kRwThreads)
+            if (kept_at(i, &id)) atomicAdd(&s_block[id / kIdBlock], s_w[i]);
+    } else if (all && !c.top_inf) {
+        unsigned long long none;
+        double f;
+        if (sizeof(In) == 2) row_table(c, s_tab);
+        row_split<In, VEC>(c, -FLT_MAX, -FLT_MAX, s_tab, s_list, s_block, &kept, &none, &f);
     } else {
         unsigned finite = 0;
         WeightQueue q;
         q.init(c);
         for (int b = c.warp; b < blocks; b += kRwWarps) {
-            float f[8];
-            load8<In, VEC>(c, b * kIdBlock + c.lane * 8, f);
-            if (__any_sync(0xFFFFFFFFu, max8(f) >= ord2f(t))) {
+            for (int k = 0; k < kIdBlock / kIdStep; ++k) {
+                const int v0 = b * kIdBlock + k * kIdStep + c.lane * 8;
+                float f[8];
+                load8<In, VEC>(c, v0, f);
+                if (__any_sync(0xFFFFFFFFu, all || max8(f) >= ord2f(t))) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    q.put(c, f[i], is_kept(f[i], b * kIdBlock + c.lane * 8 + i));
-                    finite += f[i] > -INFINITY;
+                    for (int i = 0; i < 8; ++i) {
+                        q.put(c, f[i], is_kept(f[i], v0 + i));
+                        finite += f[i] > -INFINITY;
+                    }
                 }
             }
             const unsigned long long w = warp_sum64(q.take(c));
@@ -1150,9 +1445,10 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, run, d);
         if (c.lane >= d) run += a;
     }
-    if (c.lane == 31) sh.mass[c.par][c.warp] = run;
     __syncthreads();
-    for (int i = 0; i < c.warp; ++i) run += sh.mass[c.par][i];
+    if (c.lane == 31) sh.mass[c.warp] = run;
+    __syncthreads();
+    for (int i = 0; i < c.warp; ++i) run += sh.mass[i];
     if (run > g && run - own <= g) {  // exactly one thread
         unsigned long long at = run - own;
         int b = c.tid * each;
@@ -1173,37 +1469,44 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         return;
     }
     if (c.warp == 0) {
-        const int v0 = sh.pick * kIdBlock + c.lane * 8;
-        float f[8];
-        load8<In, VEC>(c, v0, f);
-        unsigned long long w[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = kept_weight(f[i], v0 + i);
-            sum += w[i];
-        }
-        unsigned long long before = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, before, d);
-            if (c.lane >= d) before += a;
-        }
-        before += sh.base - sum;
-        if (before <= g && before + sum > g) {
-            bool done = false;
+        unsigned long long at = sh.base;
+        for (int k = 0; k < kIdBlock / kIdStep; ++k) {
+            const int v0 = sh.pick * kIdBlock + k * kIdStep + c.lane * 8;
+            float f[8];
+            load8<In, VEC>(c, v0, f);
+            unsigned long long w[8], sum = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                before += w[i];
-                if (!done && before > g) {
-                    done = true;
-                    drawn(v0 + i, f[i], M);
+                w[i] = kept_weight(f[i], v0 + i);
+                sum += w[i];
+            }
+            unsigned long long before = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned long long a = __shfl_up_sync(0xFFFFFFFFu, before, d);
+                if (c.lane >= d) before += a;
+            }
+            const unsigned long long step = __shfl_sync(0xFFFFFFFFu, before, 31);
+            before += at - sum;
+            if (before <= g && before + sum > g) {
+                bool done = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    before += w[i];
+                    if (!done && before > g) {
+                        done = true;
+                        drawn(v0 + i, f[i], M);
+                    }
                 }
             }
+            at += step;
+            if (at > g) break;
         }
     }
 }
 
-constexpr size_t kRowsSmem = (size_t)kListCap * 24;
+constexpr size_t kRowsSmem = (size_t)(2 * kTabHalf + kListCap + kMaxBlocks) * 8 + sizeof(Digits);
+static_assert(2 * kTabHalf >= kListCap, "the list's weights take the table's place");
 
 template <typename In, bool VEC>
 static cudaError_t rows_attr()
