@@ -40,7 +40,7 @@ namespace sv {
 constexpr int kRwThreads = 512;
 constexpr int kRwWarps = kRwThreads / 32;
 constexpr int kListCap = 4096;
-constexpr int kBins = 2048;        // of 1/32 in log2 of the weight
+constexpr int kBins = 1024;        // of 1/32 in log2 of the weight
 constexpr float kBinsPer = 32.f;
 constexpr int kSampled = kRwThreads * 16;
 constexpr int kIdStep = 256;       // ids of a warp's step: 8 a lane
@@ -79,7 +79,7 @@ struct RowShared {
     float fred[kRwWarps];
     unsigned list_n;
     int pick;
-    unsigned pick_n, pick_at, sel_from, sel_to;
+    unsigned pick_n, pick_at;
     unsigned long long base;
     float ch, cl, xmin;
     float2 exp2_tab[64];
@@ -625,128 +625,6 @@ __device__ __noinline__ int select_step(const RowCtx c, Digits *dig, const unsig
     return shift == 0 ? kFound : kOn;
 }
 
-// The same by one warp, 6 bits a step, for short lists: the other warps wait,
-// which costs less than sixteen warps' share of such a step.
-__device__ __noinline__ int select_warp(const RowCtx c, Digits *dig,
-                                        const unsigned long long *list,
-                                        const unsigned long long *weight, int len, int what,
-                                        uint32_t key, int cut, uint32_t *from, uint32_t *to,
-                                        const Goal g, unsigned *n, unsigned long long *w,
-                                        unsigned *n_at)
-{
-    RowShared &sh = *c.sh;
-    __syncthreads();
-    if (c.warp == 0) {
-        uint32_t lo = *from, end = *to;
-        unsigned before_n = *n, at_n = 0;
-        unsigned long long before_w = *w;
-        int state = kOn;
-        while (state == kOn) {
-            const uint32_t span = end - lo;
-            const int shift = span <= 1 ? 0 : max(32 - __clz(span - 1) - 6, 0);
-            const uint32_t last = span <= 1 ? 0 : (span - 1) >> shift;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                dig->n[c.lane + 32 * h] = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) dig->w[k][c.lane + 32 * h] = 0;
-            }
-            __syncwarp();
-            for (int i = c.lane; i < len; i += 32) {
-                const unsigned long long p = list[i];
-                const uint32_t x = what == kByKey ? pair_key(p) : (uint32_t)pair_id(p);
-                const bool on = what == kByKey || (what == kIdsOfKey && pair_key(p) == key) ||
-                                (what == kKeptIds && (pair_key(p) > key ||
-                                                      (pair_key(p) == key && pair_id(p) <= cut)));
-                if (on && x >= lo && x - lo < span) {
-                    const uint32_t b = (x - lo) >> shift, d = what == kByKey ? last - b : b;
-                    atomicAdd(&dig->n[d], 1u);
-                    const unsigned long long y = weight[i];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        atomicAdd(&dig->w[k][d], (unsigned)(y >> (16 * k)) & 0xFFFFu);
-                }
-            }
-            __syncwarp();
-            // two neighbouring bins a lane
-            unsigned own_n[2], run_n;
-            unsigned long long own_w[2], run_w;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                own_n[h] = dig->n[2 * c.lane + h];
-                own_w[h] = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    own_w[h] += (unsigned long long)dig->w[k][2 * c.lane + h] << (16 * k);
-            }
-            run_n = own_n[0] + own_n[1];
-            run_w = own_w[0] + own_w[1];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned a = __shfl_up_sync(0xFFFFFFFFu, run_n, d);
-                const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, run_w, d);
-                if (c.lane >= d) {
-                    run_n += a;
-                    run_w += b;
-                }
-            }
-            unsigned a_n = before_n + run_n - own_n[0] - own_n[1];
-            unsigned long long a_w = before_w + run_w - own_w[0] - own_w[1];
-            int pick = -1;
-            bool open = false;
-            unsigned pick_n = 0, pick_at = 0;
-            unsigned long long pick_w = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int had = g.reached(a_n, a_w), got = g.reached(a_n + own_n[h], a_w + own_w[h]);
-                open = open || (own_n[h] > 0 && (got < 0 || had < 0));
-                if (got == 1 && own_n[h] > 0 && (had == 0 || a_n == before_n)) {
-                    pick = 2 * c.lane + h;
-                    pick_n = a_n;
-                    pick_w = a_w;
-                    pick_at = own_n[h];
-                }
-                a_n += own_n[h];
-                a_w += own_w[h];
-            }
-            if (__any_sync(0xFFFFFFFFu, open)) {
-                state = kAgain;
-                break;
-            }
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, pick >= 0);
-            if (!who) {
-                state = kPast;
-                break;
-            }
-            const int src = __ffs(who) - 1;
-            pick = __shfl_sync(0xFFFFFFFFu, pick, src);
-            before_n = __shfl_sync(0xFFFFFFFFu, pick_n, src);
-            before_w = __shfl_sync(0xFFFFFFFFu, pick_w, src);
-            at_n = __shfl_sync(0xFFFFFFFFu, pick_at, src);
-            const uint32_t b = what == kByKey ? last - (uint32_t)pick : (uint32_t)pick;
-            lo += b << shift;
-            end = lo + min(end - lo, 1u << shift);  // (the keys end near 2^32)
-            if (shift == 0) state = kFound;
-            __syncwarp();
-        }
-        if (c.lane == 0) {
-            sh.pick = state;
-            sh.sel_from = lo;
-            sh.sel_to = end;
-            sh.pick_n = before_n;
-            sh.base = before_w;
-            sh.pick_at = at_n;
-        }
-    }
-    __syncthreads();
-    *from = sh.sel_from;
-    *to = sh.sel_to;
-    *n = sh.pick_n;
-    *w = sh.base;
-    *n_at = sh.pick_at;
-    return sh.pick;
-}
-
 template <typename In, bool VEC>
 __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
 {
@@ -757,8 +635,9 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     unsigned long long *s_list = s_w + 2 * kTabHalf;  // [kListCap] pairs
     unsigned long long *s_block = s_list + kListCap;  // [kMaxBlocks] masses of id blocks
     Digits *s_dig = reinterpret_cast<Digits *>(s_block + kMaxBlocks);
-    unsigned *s_hist = reinterpret_cast<unsigned *>(s_w);       // [kBins], before the list
+    unsigned *s_hist = reinterpret_cast<unsigned *>(s_dig);     // [kBins], before selections
     float *s_tail = reinterpret_cast<float *>(s_hist + kBins);  // [kBins]
+    static_assert(sizeof(Digits) >= kBins * 8 && kBins == 2 * kRwThreads, "the sample's bins");
 
     RowCtx c;
     c.tid = threadIdx.x;
@@ -841,17 +720,17 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 }
         }
         __syncthreads();
-        // Counts from the top and masses from the bottom, four bins a thread.
-        const int b = 4 * c.tid;
-        unsigned n[4];
-        float w[4];
+        // Counts from the top and masses from the bottom, two bins a thread.
+        const int b = 2 * c.tid;
+        unsigned n[2];
+        float w[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             n[i] = s_hist[b + i];
             w[i] = (float)n[i] * ex2f(-((float)(b + i) + 0.5f) / kBinsPer);
         }
-        unsigned cs = n[0] + n[1] + n[2] + n[3];
-        float ws = (w[0] + w[1]) + (w[2] + w[3]);
+        unsigned cs = n[0] + n[1];
+        float ws = w[0] + w[1];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const unsigned a = __shfl_up_sync(0xFFFFFFFFu, cs, d);
@@ -874,7 +753,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
             s_all += sh.fred[i];
         }
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
+        for (int i = 1; i >= 0; --i) {
             s_hist[b + i] = cs;
             s_tail[b + i] = s_all - ws;  // mass of the bins after it
             cs -= n[i];
@@ -885,7 +764,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     // the first bin that is past a limit, by counts or by masses of the rest
     auto first_bin = [&](auto past) {
         int best = kBins - 1;
-        for (int b = 4 * c.tid + 3; b >= 4 * c.tid; --b)
+        for (int b = 2 * c.tid + 1; b >= 2 * c.tid; --b)
             if (past(b)) best = min(best, b);
         best = __reduce_min_sync(0xFFFFFFFFu, best);
         __syncthreads();
@@ -903,7 +782,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     auto guess = [&](float rest, float margin, float *from, float *to) {
         int lo = kBins - 1, hi = 0;
         if (by_k) {
-            const float want = (float)top_k / per, off = 4.f * sqrtf(want) + 8.f;
+            const float want = (float)top_k / per, off = 4.f * sqrtf(want) + 6.f;
             lo = first_bin([&](int b) { return (float)s_hist[b] >= want + off; });
             hi = first_bin([&](int b) { return (float)s_hist[b] >= want - off; });
         } else if (by_p) {
@@ -1061,11 +940,8 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     auto select = [&](int what, uint32_t from, uint32_t to, Goal &g, uint32_t key, int cut,
                       uint32_t *v, unsigned *n, unsigned long long *w, unsigned *n_at) -> bool {
         for (;;) {
-            const int r = list_n <= 1024u
-                              ? select_warp(c, s_dig, s_list, s_w, (int)list_n, what, key, cut,
-                                            &from, &to, g, n, w, n_at)
-                              : select_step(c, s_dig, s_list, s_w, (int)list_n, what, key, cut,
-                                            &from, &to, g, n, w, n_at);
+            const int r = select_step(c, s_dig, s_list, s_w, (int)list_n, what, key, cut, &from,
+                                      &to, g, n, w, n_at);
             if (r == kAgain) {
                 refine();
                 set_goal();
@@ -1078,12 +954,21 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         }
     };
 
+    // Token `id` with logit x is drawn, of a kept mass M.
+    unsigned kept = 0;
+    auto drawn = [&](int id, float x, unsigned long long M) {
+        const double w = exp(((double)x - (double)c.m) / (double)T);
+        j.token[r] = id;
+        j.prob[r] = (float)(ldexp(w, c.S) / (double)M);
+        j.kept[r] = (int)kept;
+    };
+
     // ---- the boundary: the last kept token's key t and id (id_cut), and the
     // number of kept tokens
     uint32_t t = key_min;
     int id_cut = j.V;
-    unsigned kept = 0;
     if (filtered) {
+        unsigned long long list_mass = 0;
         // is what the list starts from past the boundary?
         auto try_list = [&](uint32_t from) {
             bool enough = from <= lo || (by_k && list_n >= (unsigned)top_k);
@@ -1091,7 +976,8 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 unsigned long long w = 0;
                 for (int i = c.tid; i < (int)list_n; i += kRwThreads)
                     w += row_weight(c, ord2f(pair_key(s_list[i])));
-                enough = goal.reached(0, cta_mass(c, w)) == 1;
+                list_mass = cta_mass(c, w);
+                enough = goal.reached(0, list_mass) == 1;
             }
             if (enough) {
                 lo = min(from, lo);
@@ -1099,20 +985,34 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
             }
         };
         if (collect) try_list(g_lo == -INFINITY ? kKeyNegInf + 1 : row_key(g_lo));
-        // again, with the row's maximum and mass in place of the sample's; and
-        // with other margins where that missed or was too wide
-        float margin = 0.05f;
-        for (int time = 0; time < (goal.by_mass ? 3 : 1) && !listed && !have_blocks && bins &&
+        // Again, with the row's maximum and mass in place of the sample's.  A pass
+        // that misses the boundary has told the exact mass above one logit: the
+        // sample's mass below that one, and how far the exact mass is from the
+        // goal, say where to look next.
+        const float unit =  // a weight's mass in the sample's terms
+            exp2f(fminf((c.m - s_max) * c.ch, 100.f)) / per;
+        float margin = 0.05f, rest = (1.f - top_p) * (float)z * unit;
+        auto learn = [&](float x, unsigned long long above) {
+            const float y = (s_max - x) * c.ch * kBinsPer;
+            const int b = y < (float)(kBins - 1) ? (int)y - 1 : kBins - 1;
+            const double off = (double)above - (double)goal.hi;
+            rest = (b < 0 ? s_all : s_tail[b]) + (float)ldexp(off, -c.S) * unit;
+            margin = 0.1f;
+        };
+        for (int time = 0; time < (goal.by_mass ? 5 : 1) && !listed && !have_blocks && bins &&
                            !c.top_inf; ++time) {
-            const float up = exp2f(fminf((c.m - s_max) * c.ch, 100.f));
-            guess((1.f - top_p) * (float)z * up / per, margin, &g_lo, &g_hi);
-            margin = 0.4f;
+            guess(rest, margin, &g_lo, &g_hi);
             guess_lo = max(row_key(g_lo), lo);
             guess_hi = row_key(g_hi);
             const float x = ord2f(guess_lo);
             if (tokens_from(x) < 0.9f * kListCap) {
                 list_n = row_collect<In, VEC>(c, guess_lo, 0, s_list);
-                if (list_n <= (unsigned)kListCap) try_list(guess_lo);
+                if (list_n <= (unsigned)kListCap) {
+                    try_list(guess_lo);
+                    if (!listed && goal.by_mass) learn(x, list_mass);
+                } else {
+                    margin = 0.02f;
+                }
             } else if (goal.by_mass && guess_hi > guess_lo && z_known) {
                 double ftail;
                 unsigned long long tail;
@@ -1120,15 +1020,16 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 if (sizeof(In) == 2) row_table(c, s_tab);
                 list_n = row_split<In, VEC>(c, ord2f(guess_lo), ord2f(guess_hi), s_tab, s_list,
                                             s_block, &above, &tail, &ftail);
+                const int blocks = (j.V + kIdBlock - 1) / kIdBlock;
+                unsigned long long a = 0, l = 0;
+                for (int i = c.tid; i < blocks; i += kRwThreads) a += s_block[i];
+                a = cta_mass(c, a);
                 if (list_n > (unsigned)kListCap) {
+                    learn(ord2f(guess_hi), a);
                     margin = 0.02f;
                 } else {
-                    const int blocks = (j.V + kIdBlock - 1) / kIdBlock;
-                    unsigned long long a = 0, l = 0;
-                    for (int i = c.tid; i < blocks; i += kRwThreads) a += s_block[i];
                     weigh();
                     for (int i = c.tid; i < (int)list_n; i += kRwThreads) l += s_w[i];
-                    a = cta_mass(c, a);
                     l = cta_mass(c, l);
                     // the row's mass again: at most the tail is not exact
                     const double ts = ldexp(ftail, c.S);
@@ -1146,9 +1047,70 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                         base_n = above;
                         base_w = a;
                         have_blocks = true;
+                    } else if (a >= goal.lo) {
+                        learn(ord2f(guess_hi), a);
+                    } else {
+                        learn(x, a + l);
                     }
                 }
             }
+        }
+        if (listed && list_n <= (unsigned)kRwThreads) {
+            // A list of at most a token a thread: each thread counts the tokens
+            // before its own, and their weights; then those of lower ids.
+            weigh();
+            const bool mine = c.tid < (int)list_n;
+            const unsigned long long p = mine ? s_list[c.tid] : 0, w = mine ? s_w[c.tid] : 0;
+            unsigned rank = 0;
+            unsigned long long before = 0;
+            if (c.warp * 32 < (int)list_n)
+                for (int i = 0; i < (int)list_n; ++i)
+                    if (s_list[i] > p) {
+                        ++rank;
+                        before += s_w[i];
+                    }
+            bool on = mine && (!by_k || rank < (unsigned)top_k);
+            if (by_k && by_p) {
+                const unsigned long long M = cta_mass(c, on ? w : 0);
+                on = on && (before < scale_mass(top_p, M, true) || rank == 0);
+            } else if (by_p) {
+                if (__syncthreads_or(mine && before >= goal.lo && before < goal.hi)) {
+                    refine();
+                    set_goal();
+                    weigh();
+                }
+                on = on && (before < goal.hi || rank == 0);
+            }
+            on = on && (pair_key(p) >= key_min || rank == 0);
+            kept = cta_count(c, on);
+            const unsigned long long M = cta_mass(c, on ? w : 0);
+            const int id = pair_id(p);
+            const float x = ord2f(pair_key(p));
+            if (u == 0.f || u == 1.f) {
+                // the first or the last kept token of any weight at all
+                const bool any = on && ((double)x - (double)c.m) / (double)T > -745.0;
+                int best = any ? id : u == 0.f ? 0x7FFFFFFF : -1;
+                best = u == 0.f ? __reduce_min_sync(0xFFFFFFFFu, best)
+                                : __reduce_max_sync(0xFFFFFFFFu, best);
+                __syncthreads();
+                if (c.lane == 0) sh.cnt[c.warp] = (unsigned)best;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kRwWarps; ++i)
+                    best = u == 0.f ? min(best, (int)sh.cnt[i]) : max(best, (int)sh.cnt[i]);
+                if (any && id == best) drawn(id, x, M);
+                return;
+            }
+            const unsigned long long g = min(scale_mass(u, M, false), M - 1);
+            if (mine && !on) s_w[c.tid] = 0;
+            __syncthreads();
+            if (__any_sync(0xFFFFFFFFu, on)) {
+                unsigned long long run = w;
+                for (int i = 0; i < (int)list_n; ++i)
+                    if (pair_id(s_list[i]) < id) run += s_w[i];
+                if (on && run > g && run - w <= g) drawn(id, x, M);
+            }
+            return;
         }
         // min-p's boundary is known; it needs no list where it comes first
         bool min_first = !listed && !by_k && !by_p;
@@ -1326,12 +1288,6 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
     auto is_kept = [&](float x, int id) {
         const uint32_t k = row_key(x);
         return all ? x > -INFINITY : k > t || (k == t && id <= id_cut);
-    };
-    auto drawn = [&](int id, float x, unsigned long long M) {
-        const double w = exp(((double)x - (double)c.m) / (double)T);
-        j.token[r] = id;
-        j.prob[r] = (float)(ldexp(w, c.S) / (double)M);
-        j.kept[r] = (int)kept;
     };
     // At the ends of u the answer is the first or the last kept token of any
     // weight at all (above the least double), however small.
