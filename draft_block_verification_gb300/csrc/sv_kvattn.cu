@@ -76,6 +76,7 @@ struct AttnShared {
     alignas(16) float fac[kSoftWarps][32];   // factor of its last move
     float sum[2][4][kRowsMax];         // sums of weights: warpgroup, quarter of a tile, row
     float top[2][kRowsMax];            // maximum that they are against
+    float out_f[2][kRowsMax];          // factors of the output's sums
     short owner[256];                  // CTAs of a shared unit's tiles (spans below a tile)
     long long scan[kAtThreads / 32];
 };
@@ -223,7 +224,11 @@ __device__ __forceinline__ int round_rows(int rows)
     return rows <= 64 ? (rows + 15) & ~15 : (rows + 31) & ~31;
 }
 // Time of a tile by its rows, as measured: even spans of it are even in time.
-__device__ __forceinline__ int tile_cost(int N) { return 16 + N / 4; }
+__device__ __forceinline__ int tile_cost(int N)
+{
+    // in units of 0.04 us (152 units of 4,096 and 16,384 tokens, D = 128)
+    return N <= 32 ? 18 : N <= 48 ? 20 : N <= 64 ? 22 : N <= 96 ? 34 : 42;
+}
 
 __device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
 {
@@ -341,12 +346,12 @@ __host__ __device__ constexpr size_t part_floats(int D) { return (size_t)kRowsMa
 // other's latencies on every scheduler: two warpgroups with up to 64 rows a
 // thread took 1.4 to 1.9 times as long.
 //
-// The running maximum M moves lazily: weights are taken as 2^(y - M + 4.5), and
+// The running maximum M moves lazily: weights are taken as 2^(y - M + 3.5), and
 // M moves only when one would pass 2^8.5 (e4m3 ends at 448).  So most tiles
 // need no maximum at all, only a vote of the warpgroup that nothing passes;
 // a tile that does is looked at again from its scores.
 // ---------------------------------------------------------------------------
-constexpr float kUnit = 4.5f;  // log2 of the weight at the running maximum
+constexpr float kUnit = 3.5f;  // log2 of the weight at the running maximum
 constexpr float kMost = 8.5f;  // log2 of the largest weight
 
 // Sum v[0 .. N) over the warp's lanes: three halvings leave each lane N / 8
@@ -676,62 +681,61 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     const int nt = pc.t1 - pc.t0;
     const bool has0 = !turns || nt > 1 || (it0 & 1) == 0;
     const bool has1 = turns && (nt > 1 || (it0 & 1) == 1);
-    // rows this warpgroup writes, 4 at a time: all of its own, or half of those
-    // that it shares with the other pair
+    // a thread for each row: the factors that its sums of the two pairs get
+    if (tid < (turns ? 2 : 4) * R) {
+        const int n = tid;
+        const float m = turns ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
+        float f0 = 0.f, f1 = 0.f, s = 0.f;
+        if (has0) {
+            f0 = turns ? ex2f(sh->top[0][n] - m) : 1.f;
+            s = f0 * ((sh->sum[0][0][n] + sh->sum[0][1][n]) + (sh->sum[0][2][n] + sh->sum[0][3][n]));
+        }
+        if (has1) {
+            f1 = ex2f(sh->top[1][n] - m);
+            s = fmaf(f1, (sh->sum[1][0][n] + sh->sum[1][1][n]) +
+                             (sh->sum[1][2][n] + sh->sum[1][3][n]), s);
+        }
+        const float inv = !whole ? 1.f : s > 0.f ? 1.f / s : 0.f;
+        sh->out_f[0][n] = f0 * inv;
+        sh->out_f[1][n] = f1 * inv;
+        if (n < pc.rows) {
+            if (whole) {
+                if (j.lse)
+                    j.lse[sh->at[n]] =
+                        s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                part[(size_t)kRowsMax * D + n] = m;
+                part[(size_t)kRowsMax * (D + 1) + n] = s;
+            }
+        }
+    }
+    bar_or(5, kSoftWarps * 32, false);
+    // rows this warpgroup writes: all of its own, or half of those that it
+    // shares with the other pair
     const int w0 = r0 + (turns ? par * (R / 2) : 0), w1 = w0 + (turns ? R / 2 : R);
 #pragma unroll 1
     for (int w = w0; w < w1; w += 4) {
-        float o[4] = {0.f, 0.f, 0.f, 0.f}, f0[4], f1[4], v[8];
-        const uint32_t col = lanes + 256 + r0 * 2 + (w - r0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f0[i] = has0 ? 1.f : 0.f;
-            f1[i] = 0.f;
-            if (turns) {
-                const float m = fmaxf(sh->top[0][w + i], sh->top[1][w + i]);
-                f0[i] = has0 ? ex2f(sh->top[0][w + i] - m) : 0.f;
-                f1[i] = has1 ? ex2f(sh->top[1][w + i] - m) : 0.f;
-            }
-        }
-        if (has0) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int way = has0 ? 0 : 1; way < (has1 ? 2 : 1); ++way) {
+            float v[8];  // hi and lo
+            const uint32_t col = lanes + 256 + way * 128 + r0 * 2 + (w - r0);
             tc_ld4(col, v);
             tc_ld4(col + R, v + 4);
             tc_wait_ld(v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = f0[i] * fmaf(v[4 + i], 0.0625f, v[i]);
-        }
-        if (has1) {
-            tc_ld4(col + 128, v);
-            tc_ld4(col + 128 + R, v + 4);
-            tc_wait_ld(v);
-#pragma unroll
             for (int i = 0; i < 4; ++i)
-                o[i] = fmaf(f1[i], fmaf(v[4 + i], 0.0625f, v[i]), o[i]);
+                o[i] = fmaf(sh->out_f[way][w + i], fmaf(v[4 + i], 0.0625f, v[i]), o[i]);
         }
+        if (d < D) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = w + i;
-            if (n >= pc.rows || d >= D) continue;
-            float s = 0.f;
-            if (has0)
-                s = f0[i] * ((sh->sum[0][0][n] + sh->sum[0][1][n]) +
-                             (sh->sum[0][2][n] + sh->sum[0][3][n]));
-            if (has1)
-                s = fmaf(f1[i], (sh->sum[1][0][n] + sh->sum[1][1][n]) +
-                                    (sh->sum[1][2][n] + sh->sum[1][3][n]), s);
-            const float m = turns ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
-            if (whole) {
-                const int64_t at = sh->at[n];
-                j.out[at * D + d] = __bfloat16_as_ushort(
-                    __float2bfloat16_rn(s > 0.f ? __fdividef(o[i], s) : 0.f));
-                if (d == 0 && j.lse)
-                    j.lse[at] = s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
-            } else {
-                part[(size_t)n * D + d] = o[i];
-                if (d == 0) {
-                    part[(size_t)kRowsMax * D + n] = m;
-                    part[(size_t)kRowsMax * (D + 1) + n] = s;
-                }
+            for (int i = 0; i < 4; ++i) {
+                if (w + i >= pc.rows) break;
+                if (whole)
+                    j.out[(int64_t)sh->at[w + i] * D + d] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
+                else
+                    part[(size_t)(w + i) * D + d] = o[i];
             }
         }
     }
@@ -785,51 +789,64 @@ __device__ __forceinline__ void load_queries(const AttendJob &j, AttnShared *sh,
 {
     constexpr int E = D / 32;  // elements a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int n = warp; n < N; n += kSoftWarps) {
-        float x[E];
-        float amax = 0.f;
-        const int row = pc.row0 + n;
-        if (n < pc.rows) {
-            const int tok = pc.first + row / j.G, head = pc.h * j.G + row % j.G;
-            if (lane == 0) sh->at[n] = tok * j.Hq + head;
-            const uint16_t *q = j.q + (int64_t)tok * j.qts + (int64_t)head * j.qhs + lane * E;
+#pragma unroll 1
+    for (int n0 = warp; n0 < N; n0 += 2 * kSoftWarps) {
+        uint16_t raw[2][E];  // two rows in flight
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int n = n0 + k * kSoftWarps, row = pc.row0 + n;
+#pragma unroll
+            for (int i = 0; i < E; ++i) raw[k][i] = 0;
+            if (n < pc.rows) {
+                const int tok = pc.first + row / j.G, head = pc.h * j.G + row % j.G;
+                if (lane == 0) sh->at[n] = tok * j.Hq + head;
+                const uint16_t *q = j.q + (int64_t)tok * j.qts + (int64_t)head * j.qhs + lane * E;
+#pragma unroll
+                for (int i = 0; i < E; ++i) raw[k][i] = q[i];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int n = n0 + k * kSoftWarps;
+            if (n >= N) break;
+            float x[E];
+            float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                x[i] = __uint_as_float((uint32_t)q[i] << 16);
+                x[i] = __uint_as_float((uint32_t)raw[k][i] << 16);
                 amax = fmaxf(amax, fabsf(x[i]));
             }
-        } else {
+            amax = warp_max(amax);
+            // 2^e brings the largest element to [128, 256)
+            const int e = amax > 0.f ? min(134 - (int)(__float_as_uint(amax) >> 23), 126) : 0;
+            const float up = __int_as_float((127 + e) << 23);
+            if (lane == 0)
+                sh->c[n] = n < pc.rows ? j.softmax_scale * 1.4426950408889634f / up : 0.f;
+            uint32_t hi = 0, lo = 0;
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = 0.f;
-        }
-        amax = warp_max(amax);
-        // 2^e brings the largest element to [128, 256)
-        const int e = amax > 0.f ? min(134 - (int)(__float_as_uint(amax) >> 23), 126) : 0;
-        const float up = __int_as_float((127 + e) << 23);
-        if (lane == 0)
-            sh->c[n] = n < pc.rows ? j.softmax_scale * 1.4426950408889634f / up : 0.f;
-        uint32_t hi = 0, lo = 0;
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            uint16_t h8, l8;
-            const float a = x[i] * up, b = x[i + 1] * up;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(b), "f"(a));
-            uint32_t h16;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
-            const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&h16));
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l8) : "f"(b - h.y), "f"(a - h.x));
-            hi |= (uint32_t)h8 << (8 * i);
-            lo |= (uint32_t)l8 << (8 * i);
-        }
-        const int byte = lane * E;
-        const int sw = D == 128 ? n & 7 : (n >> 1) & 3;
-        char *at = smem_q + n * D + (((byte >> 4) ^ sw) << 4) + (byte & 15);
-        if (E == 4) {
-            *reinterpret_cast<uint32_t *>(at) = hi;
-            *reinterpret_cast<uint32_t *>(at + N * D) = lo;
-        } else {
-            *reinterpret_cast<uint16_t *>(at) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t *>(at + N * D) = (uint16_t)lo;
+            for (int i = 0; i < E; i += 2) {
+                uint16_t h8, l8;
+                const float a = x[i] * up, b = x[i + 1] * up;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(b), "f"(a));
+                uint32_t h16;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
+                const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&h16));
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+                    : "=h"(l8)
+                    : "f"(b - h.y), "f"(a - h.x));
+                hi |= (uint32_t)h8 << (8 * i);
+                lo |= (uint32_t)l8 << (8 * i);
+            }
+            const int byte = lane * E;
+            const int sw = D == 128 ? n & 7 : (n >> 1) & 3;
+            char *at = smem_q + n * D + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+            if (E == 4) {
+                *reinterpret_cast<uint32_t *>(at) = hi;
+                *reinterpret_cast<uint32_t *>(at + N * D) = lo;
+            } else {
+                *reinterpret_cast<uint16_t *>(at) = (uint16_t)hi;
+                *reinterpret_cast<uint16_t *>(at + N * D) = (uint16_t)lo;
+            }
         }
     }
 }
