@@ -992,14 +992,15 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
         const float unit =  // a weight's mass in the sample's terms
             exp2f(fminf((c.m - s_max) * c.ch, 100.f)) / per;
         float margin = 0.05f, rest = (1.f - top_p) * (float)z * unit;
-        auto learn = [&](float x, unsigned long long above) {
+        auto learn = [&](float x, unsigned long long above, float step) {
             const float y = (s_max - x) * c.ch * kBinsPer;
             const int b = y < (float)(kBins - 1) ? (int)y - 1 : kBins - 1;
             const double off = (double)above - (double)goal.hi;
-            rest = (b < 0 ? s_all : s_tail[b]) + (float)ldexp(off, -c.S) * unit;
+            const float at = b < 0 ? s_all : s_tail[b];
+            rest = fmaxf(at + (float)ldexp(off, -c.S) * unit * step, 0.3f * at);
             margin = 0.1f;
         };
-        for (int time = 0; time < (goal.by_mass ? 5 : 1) && !listed && !have_blocks && bins &&
+        for (int time = 0; time < (goal.by_mass ? 8 : 1) && !listed && !have_blocks && bins &&
                            !c.top_inf; ++time) {
             guess(rest, margin, &g_lo, &g_hi);
             guess_lo = max(row_key(g_lo), lo);
@@ -1009,7 +1010,8 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 list_n = row_collect<In, VEC>(c, guess_lo, 0, s_list);
                 if (list_n <= (unsigned)kListCap) {
                     try_list(guess_lo);
-                    if (!listed && goal.by_mass) learn(x, list_mass);
+                    // (the sample misses heavy tokens: longer and longer steps)
+                    if (!listed && goal.by_mass) learn(x, list_mass, 1.f + (float)time);
                 } else {
                     margin = 0.02f;
                 }
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                 for (int i = c.tid; i < blocks; i += kRwThreads) a += s_block[i];
                 a = cta_mass(c, a);
                 if (list_n > (unsigned)kListCap) {
-                    learn(ord2f(guess_hi), a);
+                    learn(ord2f(guess_hi), a, 1.f);
                     margin = 0.02f;
                 } else {
                     weigh();
@@ -1048,9 +1050,9 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                         base_w = a;
                         have_blocks = true;
                     } else if (a >= goal.lo) {
-                        learn(ord2f(guess_hi), a);
+                        learn(ord2f(guess_hi), a, 1.f);
                     } else {
-                        learn(x, a + l);
+                        learn(x, a + l, 1.f);
                     }
                 }
             }
