@@ -21,9 +21,10 @@
 // other operand is e4m3 as well, in two parts.  A bf16 query (8 significant
 // bits, scaled by a power of two per row) is the sum of two e4m3 values (4 bits
 // each): q = hi + lo exactly, up to 2^-19 of the row's largest element.  A
-// weight p is rounded to hi + lo with a relative error of 2^-8 at most (2^-10
-// in the mean square), down to 2^-22 of the largest; lo carries a scale of its
-// own and accumulates apart.  Sums, maxima and the rescaling are fp32.
+// weight p is rounded to hi + lo with a relative error of 2^-8 at most (2^-10.5
+// in the mean square, under the output's own rounding to bf16), down to a step
+// of 2^-17 of the weight at the running maximum; lo carries a scale of its own
+// and accumulates apart.  Sums, maxima and the rescaling are fp32.
 //
 // Scales of pages differ from token to token, which is a row of S^T: the key's
 // scale multiplies there, and the value's scale goes into the exponent,
@@ -31,10 +32,17 @@
 // so that O needs no scale; the sum of weights takes w'_p / s^v_p.
 //
 // Split.  The tiles (128 tokens of one unit: sequence, head, row block) of the
-// whole call, laid end to end, are cut into equal spans, one per CTA of one
-// wave.  A unit that several CTAs share leaves partial sums in the workspace;
-// the last of them to finish joins them in the order of the CTAs, so the result
-// does not depend on who that is.
+// whole call, laid end to end by their cost, are cut into equal spans, one per
+// CTA of one wave.  A unit that several CTAs share leaves partial sums in the
+// workspace; the last of them to finish joins them in the order of the CTAs, so
+// the result does not depend on who that is.
+//
+// Measured at D = 128, 8 cache heads, 4 query heads each: a tile of 32 KB takes
+// 0.70 us on an SM for up to 32 rows (7.1 TB/s over all, the copy rate), 0.80
+// for 48, 0.87 for 64, 1.33 for 96, 1.65 for 128, where the softmax warps bound
+// it; a unit some 7 us more (queries, the first tiles' maxima, the output).
+// 128 single tokens over 4,096 to 8,192 take 300 us (5.4 TB/s, 80% of the copy
+// rate), 64 draft blocks of 9 to 17 over 2,048 to 4,096 195 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -80,6 +88,17 @@ struct AttnShared {
     short owner[256];                  // CTAs of a shared unit's tiles (spans below a tile)
     long long scan[kAtThreads / 32];
 };
+
+// Product of packed fp32 pairs.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 // ---------------------------------------------------------------------------
 // tcgen05 wrappers.

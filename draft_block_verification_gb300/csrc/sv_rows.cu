@@ -29,6 +29,12 @@
 // many weights takes them from a table of the row's, 45 KB, and computes only
 // the others (a weight costs some 90 instructions, a look-up 8).  fp32 logits
 // are queued, and a warp weighs 32 of them at once.
+//
+// Measured on 1,088 bf16 rows of 128,256 (41 us at the copy rate): T = 0 62 us
+// (4.5 TB/s), k = 50 230 us, p = 0.9 with 28,000 kept tokens 720 us, no filter
+// 500 us; a mix of them 410 us.  Filtered rows are bound by the chain of short
+// steps after the first pass, of which two rows an SM hide each other's; wide
+// ones by the instructions of their weights.
 #include <float.h>
 #include <math.h>
 
