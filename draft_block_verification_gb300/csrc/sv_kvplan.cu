@@ -216,9 +216,9 @@ cudaError_t plan_launch(const PlanJob &j, int sms, cudaStream_t s)
 // run's rows of one head and side; it looks at a window of tokens for the
 // first tokens of runs, so that neither many CTAs find nothing to do (long
 // prompts) nor one CTA works off many runs in turn (single tokens).  CTAs of
-// four warps, many on an SM, keep more loads in flight than wider ones: 36,900
-// bf16 tokens of 8 heads of 128 in pages of 32 take 44 us (5.2 TB/s, 76% of the
-// copy rate; 58 us with eight warps), 64 draft blocks of 17 tokens 8 us.
+// four warps, many on an SM, keep more loads in flight than wider ones: 38,152
+// bf16 tokens of 8 heads of 128 in pages of 32 take 44 us (5.4 TB/s, 79% of the
+// copy rate; 58 us with eight warps), 64 draft blocks of 9 to 17 tokens 8 us.
 // ---------------------------------------------------------------------------
 constexpr int kAppThreads = 128;
 constexpr int kScaleExp = 40;
