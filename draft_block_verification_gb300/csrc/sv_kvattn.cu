@@ -23,7 +23,7 @@
 // each): q = hi + lo exactly, up to 2^-19 of the row's largest element.  A
 // weight p is rounded to hi + lo with a relative error of 2^-8 at most (2^-10.5
 // in the mean square, under the output's own rounding to bf16), down to a step
-// of 2^-17 of the weight at the running maximum; lo carries a scale of its own
+// of 2^-16.5 of the weight at the running maximum; lo carries a scale of its own
 // and accumulates apart.  Sums, maxima and the rescaling are fp32.
 //
 // Scales of pages differ from token to token, which is a row of S^T: the key's
