@@ -489,7 +489,8 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
  *   token [R] (-1: the row has no finite logit);  prob [R] the token's share
  *   of the kept weight;  kept [R] the number of kept tokens.
  * Ranks, masses and the draw are decided exactly: weights within 2^-44, summed
- * in fixed point with a step of at most 2^-61 of a bound on the kept mass.
+ * in fixed point with steps of 2^-40 of the largest weight or less (2^-58 where
+ * the row's mass is near its largest weight).
  * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (V); a row whose parameters
  * are out of range (u outside [0, 1], a negative or NaN filter, min_p > 1,
  * T < 2^-20 other than 0, T infinite) gets token -1, prob NaN, kept 0 and
