@@ -797,6 +797,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         if (e == 0 && j.lse)
             j.lse[at] = s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
     }
+    bar_or(5, kSoftWarps * 32, false);  // the next piece's rows go where these are read from
     return true;
 }
 
