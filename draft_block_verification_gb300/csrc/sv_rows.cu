@@ -1151,7 +1151,9 @@ __global__ void __launch_bounds__(kRwThreads, 2) rows_kernel(const RowsJob j)
                     goal.by_mass = true;
                     goal.rank = 0;
                     goal.lo = goal.hi = scale_mass(top_p, w, true);
-                    lo = kKeyNegInf + 1;
+                    // It lies at the k-th token or before it: from the same lo on, only
+                    // the top k and the bracket's list are summed, which the weights'
+                    // unit has room for (a whole row of them it may not have).
                     guess_lo = guess_hi = 0;
                     p_exact = true;
                     narrow(goal);
