@@ -33,6 +33,15 @@ cudaError_t wait_selftest_run(int *err, const unsigned *word, uint32_t limit, cu
 
 using namespace sv;
 
+// sv_kv_attention's partial sums and counters, a set for each stream, so that
+// calls on different streams may overlap: the first for captured calls.
+constexpr int kKvSets = 17;
+constexpr unsigned long long kKvCaptured = ~0ull;
+struct KvSet {
+    unsigned long long stream;  // its id
+    char *mem;
+};
+
 struct sv_handle {
     int device = 0;
     int sms = 0;
@@ -50,7 +59,8 @@ struct sv_handle {
     unsigned *cnt = nullptr;  // completion counters: always zero between calls
     int cnt_B = 0;            // sequences the counter arena holds
     int force_rescue = 0;
-    char *kv_ws = nullptr;    // sv_kv_attention's partial sums and counters
+    KvSet kv[kKvSets] = {};
+    int kv_n = 0, kv_next = 1;  // sets in use; the one that a further stream takes over
     cudaEvent_t ev[2] = {nullptr, nullptr};  // caller-owned (SV_OPT_TIMING_EVENTS)
     bool timing = false;
     std::mutex mu;
@@ -235,6 +245,58 @@ sv_status ensure_cnt(sv_handle *h, int B, cudaStream_t s)
     if (e != cudaSuccess) return cuda_status(e);
     h->cnt = (unsigned *)p;
     h->cnt_B = nb;
+    return SV_OK;
+}
+
+// One more set, its counters zero in the order of stream s.
+sv_status kv_add(sv_handle *h, unsigned long long id, cudaStream_t s)
+{
+    void *p = nullptr;
+    const size_t n = attend_counter_bytes(h->sms);
+    cudaError_t e = cudaMallocAsync(&p, n + attend_ws_bytes(h->sms), s);
+    if (e != cudaSuccess) return cuda_status(e);
+    e = cudaMemsetAsync(p, 0, n, s);
+    // graphs are launched on any stream: theirs is ready before the call goes on
+    if (e == cudaSuccess && id == kKvCaptured) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) {
+        cudaFreeAsync(p, s);
+        return cuda_status(e);
+    }
+    h->kv[h->kv_n++] = {id, (char *)p};
+    return SV_OK;
+}
+
+// The set of a call on stream s.
+sv_status kv_workspace(sv_handle *h, cudaStream_t s, char **mem)
+{
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(s, &cap);
+    if (e != cudaSuccess) return cuda_status(e);
+    const bool captured = cap != cudaStreamCaptureStatusNone;
+    unsigned long long id = kKvCaptured;
+    if (!captured) e = cudaStreamGetId(s, &id);
+    if (e != cudaSuccess) return cuda_status(e);
+    for (int i = 0; i < h->kv_n; ++i)
+        if (h->kv[i].stream == id) {
+            *mem = h->kv[i].mem;
+            return SV_OK;
+        }
+    // an allocation does not belong into a captured graph
+    if (captured) return SV_ERR_UNSUPPORTED;
+    if (h->kv_n == 0)
+        if (sv_status st = kv_add(h, kKvCaptured, s)) return st;
+    if (h->kv_n < kKvSets) {
+        if (sv_status st = kv_add(h, id, s)) return st;
+        *mem = h->kv[h->kv_n - 1].mem;
+        return SV_OK;
+    }
+    // all are taken: another stream's, once its calls have ended
+    e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cuda_status(e);
+    KvSet &t = h->kv[h->kv_next];
+    h->kv_next = h->kv_next + 1 < kKvSets ? h->kv_next + 1 : 1;
+    t.stream = id;
+    *mem = t.mem;
     return SV_OK;
 }
 
@@ -447,7 +509,7 @@ sv_status sv_destroy(sv_handle *h)
     cudaDeviceSynchronize();
     if (h->ws) cudaFree(h->ws);
     if (h->cnt) cudaFree(h->cnt);
-    if (h->kv_ws) cudaFree(h->kv_ws);
+    for (int i = 0; i < h->kv_n; ++i) cudaFree(h->kv[i].mem);
     if (h->d_err) cudaFree(h->d_err);
     if (h->d_ctl) cudaFree(h->d_ctl);
     if (h->d_gtab) cudaFree(h->d_gtab);
@@ -475,7 +537,8 @@ sv_status sv_sync_status(sv_handle *h, void *stream)
         cudaMemset(h->d_ctl, 0, C_NCTL * sizeof(unsigned));
         cudaMemcpy(h->d_ctl + C_RESCUED, &keep, sizeof(unsigned), cudaMemcpyHostToDevice);
         if (h->cnt) cudaMemset(h->cnt, 0, (size_t)h->cnt_B * kCntPerSeq * sizeof(unsigned));
-        if (h->kv_ws) cudaMemset(h->kv_ws, 0, attend_counter_bytes(h->sms));
+        for (int i = 0; i < h->kv_n; ++i)
+            cudaMemset(h->kv[i].mem, 0, attend_counter_bytes(h->sms));
         cudaDeviceSynchronize();
     }
     return (sv_status)code;
@@ -960,29 +1023,13 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_attention")) return fi;
     cudaStream_t s = (cudaStream_t)stream;
-    if (!h->kv_ws) {
-        // once a handle; an allocation does not belong into a captured graph
-        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(s, &cap);
-        if (e != cudaSuccess) return cuda_status(e);
-        if (cap != cudaStreamCaptureStatusNone) return SV_ERR_UNSUPPORTED;
-        void *p = nullptr;
-        const size_t n = attend_counter_bytes(h->sms);
-        e = cudaMalloc(&p, n + attend_ws_bytes(h->sms));
-        if (e != cudaSuccess) return cuda_status(e);
-        e = cudaMemsetAsync(p, 0, n, s);
-        if (e != cudaSuccess) {
-            cudaFree(p);
-            return cuda_status(e);
-        }
-        h->kv_ws = (char *)p;
-    }
+    char *ws;
+    if (sv_status st = kv_workspace(h, s, &ws)) return st;
     AttendJob j = {(const uint16_t *)q, q_token_stride, q_head_stride,
                    {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
                    {k_scale, v_scale}, table, kv_len, cu_new, mask, B, T, Hq, H, Hq / H, D,
                    block, pages, cols, mask_words, scale, (uint16_t *)out, lse,
-                   (float *)(h->kv_ws + attend_counter_bytes(h->sms)), (unsigned *)h->kv_ws,
-                   h->d_err};
+                   (float *)(ws + attend_counter_bytes(h->sms)), (unsigned *)ws, h->d_err};
     return cuda_status(attend_launch(j, h->sms, s));
 }
 

@@ -455,8 +455,13 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  *     token sees nothing.  Softmax and sums are fp32.
  *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
  *     where a token sees nothing.
- * The handle's first call allocates its workspace (20 MB, of fixed size): make
- * it before any stream capture (SV_ERR_UNSUPPORTED inside one).
+ * The handle keeps a workspace of 20 MB for each stream that makes this call, so
+ * that calls on different streams may overlap, and one more for captured calls.
+ * They are allocated by a stream's first call; the handle's first call waits
+ * for its stream once.  Make it before any stream capture (SV_ERR_UNSUPPORTED
+ * inside one).  Captured calls share one workspace: graphs that hold this call,
+ * and branches of one, must not run at the same time.  From the 17th stream on,
+ * a stream's first call waits for the device and takes over another one's.
  * Rows from cu_new[B] on are not written.  Bytes past kv_len may hold
  * anything; those of visible tokens are finite, with scales in [2^-40, 2^40].
  * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D); latched
