@@ -677,7 +677,9 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             sh->sum[par][quarter][r0 + n] = l[i];
         }
     }
-    if (quarter == 0 && lane < R) sh->top[par][r0 + lane] = mu[lane];
+    // (a row that saw nothing here has no maximum: one of 0 would flush the
+    // sums that it has elsewhere against scores far below it)
+    if (quarter == 0 && lane < R) sh->top[par][r0 + lane] = none ? kNone : mu[lane];
     if (bar_or(5, kSoftWarps * 32, !ok)) return false;
     tc_fence_after();
 
