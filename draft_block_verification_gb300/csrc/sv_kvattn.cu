@@ -716,14 +716,15 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             s = fmaf(f1, (sh->sum[1][0][n] + sh->sum[1][1][n]) +
                              (sh->sum[1][2][n] + sh->sum[1][3][n]), s);
         }
-        const float inv = !whole ? 1.f : s > 0.f ? 1.f / s : 0.f;
+        // (a sum of NaN is no sum of nothing: it goes into the output)
+        const float inv = !whole ? 1.f : s == 0.f ? 0.f : 1.f / s;
         sh->out_f[0][n] = f0 * inv;
         sh->out_f[1][n] = f1 * inv;
         if (n < pc.rows) {
             if (whole) {
                 if (j.lse)
                     j.lse[sh->at[n]] =
-                        s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+                        s == 0.f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
             } else {
                 part[(size_t)kRowsMax * D + n] = m;
                 part[(size_t)kRowsMax * (D + 1) + n] = s;
@@ -795,9 +796,9 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             m = top;
         }
         const int64_t at = sh->at[n];
-        j.out[at * D + e] = __bfloat16_as_ushort(__float2bfloat16_rn(s > 0.f ? o / s : 0.f));
+        j.out[at * D + e] = __bfloat16_as_ushort(__float2bfloat16_rn(s == 0.f ? 0.f : o / s));
         if (e == 0 && j.lse)
-            j.lse[at] = s > 0.f ? (m + log2f(s)) * 0.6931471805599453f : -INFINITY;
+            j.lse[at] = s == 0.f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
     }
     bar_or(5, kSoftWarps * 32, false);  // the next piece's rows go where these are read from
     return true;
@@ -842,8 +843,11 @@ __device__ __forceinline__ void load_queries(const AttendJob &j, AttnShared *sh,
             // 2^e brings the largest element to [128, 256)
             const int e = amax > 0.f ? min(134 - (int)(__float_as_uint(amax) >> 23), 126) : 0;
             const float up = __int_as_float((127 + e) << 23);
+            // (an infinity would saturate as if it were a number)
             if (lane == 0)
-                sh->c[n] = n < pc.rows ? j.softmax_scale * 1.4426950408889634f / up : 0.f;
+                sh->c[n] = n >= pc.rows      ? 0.f
+                           : amax < INFINITY ? j.softmax_scale * 1.4426950408889634f / up
+                                             : __int_as_float(0x7FC00000);
             uint32_t hi = 0, lo = 0;
 #pragma unroll
             for (int i = 0; i < E; i += 2) {

@@ -455,6 +455,7 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  *     token sees nothing.  Softmax and sums are fp32.
  *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
  *     where a token sees nothing.
+ *   A row whose query holds NaN or an infinity is NaN (out and lse).
  * The handle keeps a workspace of 20 MB for each stream that makes this call, so
  * that calls on different streams may overlap, and one more for captured calls.
  * They are allocated by a stream's first call; the handle's first call waits

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv_units import call, case, check, tiles
+from test_gpu_kv_units import call, case, check, reference, tiles
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,37 @@ def test_low_scores_beside_tiles_that_a_row_does_not_see(dbv, B, new, G, H):
         out = call(dbv, c, scale=f)
         check(c, out, f)
         assert torch.isfinite(out["lse"]).all()
+
+
+def check_rows(c, out, lost):
+    """Rows of `lost` [T, Hq] are NaN, the others as the reference has them."""
+    for b in range(len(c["kv"])):
+        lo, hi = int(c["cu"][b]), int(c["cu"][b + 1])
+        want, lse, tol, rel = reference(c, b)
+        got, gl, bad = out["out"][lo:hi].double(), out["lse"][lo:hi].double(), lost[lo:hi]
+        assert torch.isnan(got[bad]).all() and torch.isnan(gl[bad]).all(), b
+        ok = ~bad
+        assert ((got - want).abs() <= tol)[ok].all(), b
+        assert torch.equal(torch.isinf(gl[ok]), torch.isinf(lse[ok])), b
+        ok &= torch.isfinite(lse)
+        assert ((gl - lse).abs() <= rel)[ok].all(), b
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,G,lens", [(1, 4, [300, 40000]), (5, 4, [1000] * 60), (9, 8, [700]),
+                                        (33, 4, [2000, 90])])
+def test_queries_that_are_not_finite(dbv, new, G, lens, D):
+    """A row whose query holds NaN or an infinity is NaN, in units of one CTA and
+    in shared ones, and no other row is."""
+    B, H = len(lens), 2
+    c = case(new, lens, [new] * B, H, G, D, 32)
+    clean = dict(c, q=c["q"].clone())
+    r = np.random.RandomState(D)
+    lost = torch.zeros(c["q"].shape[:2], dtype=torch.bool, device="cuda")
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"))):
+        for _ in range(max(1, B // 4)):
+            t, h, d = r.randint(c["q"].shape[0]), r.randint(H * G), r.randint(D)
+            c["q"][t, h, d] = bad
+            lost[t, h] = True
+    check_rows(clean, call(dbv, c), lost)
+    dbv.default_handle(c["q"].device).sync_status()
