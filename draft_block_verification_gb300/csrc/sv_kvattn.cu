@@ -71,12 +71,17 @@ constexpr uint32_t kAtSpin = 1u << 20; // tries of a wait (a tile takes microsec
 struct AttnShared {
     uint64_t full_k[kAtStages], full_v[kAtStages], empty_k[kAtStages], empty_v[kAtStages];
     uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2], q_full, drained[2];
+    // values of a tile with new tokens have been looked over: a pair's tile, or an
+    // even or odd one of all four warpgroups
+    uint64_t clean[4];
     uint32_t tmem;
     int abort;
     int last;                          // this CTA joins the unit's parts
     int first_b;
     long long first_x, total;          // where the span starts in sequence first_b; the call's cost
     float ks[kAtStages][8], vs[kAtStages][8];  // scales of the tile's pages
+    uint32_t looks[kSoftWarps];        // parities of `clean`, a copy per warp
+    uint32_t lost[2][4];               // tokens of the tile with NaN in their value, a bit each
     int at[kRowsMax];                  // output row (token * Hq + head), per row
     alignas(16) float c[kRowsMax];     // factor from S to log2 units, per row
     float wmax[kSoftWarps][32];        // tile maxima per warp and row
@@ -182,6 +187,12 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead, uint32
 __device__ __forceinline__ void fence_async()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Whether one of four e4m3 bytes is NaN (all magnitude bits set).
+__device__ __forceinline__ bool has_nan(uint32_t w)
+{
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
 // Barrier over `n` threads with an or over a flag.
@@ -479,6 +490,13 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));
         uint32_t sees = ~0u;  // which rows see this token
         if (edge) {
+            const int c = turns ? par : 2 + (int)sb;
+            const uint32_t looks = sh->looks[warp];
+            ok = ok && at_wait(sh, j.err, &sh->clean[c], (looks >> c) & 1);
+            __syncwarp();
+            sh->looks[warp] = looks ^ 1u << c;
+            // (its value is cleared: its weight brings NaN to the rows that see it)
+            if ((sh->lost[sb][quarter] >> lane) & 1) vl = __int_as_float(0x7FC00000);
             sees = 0;
             if (pos < pc.L) {
                 if (pos < ctx) {
@@ -906,6 +924,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
             mbar_init(&sh->p_full[i], kSoftWarps);
             mbar_init(&sh->pv_done[i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&sh->clean[i], 1);
         mbar_init(&sh->q_full, kSoftWarps);
         mbar_init(&sh->drained[0], 1);
         mbar_init(&sh->drained[1], 1);
@@ -972,6 +991,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
     if (warp < kSoftWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         bool ok = true;
+        sh->looks[warp] = 0;
         while (ok && walk.next(j, pc)) {
             const int N = round_rows(pc.rows);
             load_queries<D>(j, sh, s_q, pc, N);
@@ -1068,7 +1088,7 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 mbar_wait_n(&sh->full_k[i], (it / kAtStages) & 1, 1u << 12);
                 mbar_wait_n(&sh->full_v[i], (it / kAtStages) & 1, 1u << 12);
             }
-    } else if (warp == kSoftWarps + 1 && lane == 0) {
+    } else if (warp == kSoftWarps + 1) {
         // ---- issuer of the scores.  (One thread for both products would wait
         // with each for the other's inputs; issuing a product takes it some
         // seventy cycles, a commit almost as many.)
@@ -1085,9 +1105,11 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
             const uint64_t dlo = dq + (uint32_t)(N * D >> 4);
             ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
             ++pieces;
-            auto tiles = [&](auto is_one) {
+            const int ctx = pc.L - pc.n;
+            const int reach = min(max(ctx >> 7, pc.t0), pc.t1);  // first tile of new tokens
+            auto tiles = [&](auto is_one, int from, int to) {
 #pragma unroll 1
-                for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+                for (int t = from; t < to; ++t, ++it) {
                     const uint32_t st = it % kAtStages, sb = it & 1;
                     ok = ok && at_wait(sh, j.err, &sh->full_k[st], (it / kAtStages) & 1);
                     ok = ok && at_wait(sh, j.err, &sh->s_empty[sb], ((it >> 1) & 1) ^ 1);
@@ -1105,13 +1127,56 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                     tc_commit(&sh->empty_k[st]);
                 }
             };
-            if (one)
-                tiles(std::true_type{});
-            else
-                tiles(std::false_type{});
+            // (up to the new tokens without a stop; then a tile at a time)
+#pragma unroll 1
+            for (int t = pc.t0; t < pc.t1;) {
+                const int to = t < reach ? reach : t + 1;
+                if (lane == 0) {
+                    if (one)
+                        tiles(std::true_type{}, t, to);
+                    else
+                        tiles(std::false_type{}, t, to);
+                }
+                const bool look = t >= reach;
+                t = to;
+                it = __shfl_sync(0xFFFFFFFFu, it, 0);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (!look) continue;
+                // A new token's value may hold NaN, which a row that does not see it
+                // would get all the same (NaN times 0): the warp looks them over, 512
+                // bytes at a time, and clears such tokens' values.
+                const uint32_t st = (it - 1) % kAtStages, sb = (it - 1) & 1;
+                ok = at_wait(sh, j.err, &sh->full_v[st], ((it - 1) / kAtStages) & 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                constexpr int kParts = D / 16, kRows = 32 / kParts;
+                const int p0 = (t - 1) * kTile, end = min(pc.L - p0, kTile);
+                if (lane < 4) sh->lost[sb][lane] = 0;
+                __syncwarp();
+#pragma unroll 1
+                for (int r0 = max(ctx - p0, 0); r0 < end; r0 += kRows) {
+                    const int r = r0 + lane / kParts;
+                    uint4 *at = reinterpret_cast<uint4 *>(s_v + (size_t)st * 2 * kSide + r0 * D) +
+                                lane;
+                    bool nan = false;
+                    if (r < end) {
+                        const uint4 x = *at;
+                        nan = has_nan(x.x) | has_nan(x.y) | has_nan(x.z) | has_nan(x.w);
+                    }
+                    const uint32_t m = __ballot_sync(0xFFFFFFFFu, nan);
+                    if ((m >> (lane & ~(kParts - 1))) & ((1u << kParts) - 1)) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                        if (lane % kParts == 0) atomicOr(&sh->lost[sb][r >> 5], 1u << (r & 31));
+                    }
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->clean[N <= 64 ? sb : 2 + sb]);
+            }
         }
         // after a wait that ran out: products still in flight end before the exit
-        if (!ok) {
+        if (!ok && lane == 0) {
             tc_commit(&sh->drained[0]);
             mbar_wait_n(&sh->drained[0], 0, 1u << 12);
         }

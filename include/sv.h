@@ -464,7 +464,8 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  * and branches of one, must not run at the same time.  From the 17th stream on,
  * a stream's first call waits for the device and takes over another one's.
  * Rows from cu_new[B] on are not written.  Bytes past kv_len may hold
- * anything; those of visible tokens are finite, with scales in [2^-40, 2^40].
+ * anything; those of the tokens before the new ones are finite, and scales lie
+ * in [2^-40, 2^40].  A new token may be NaN: rows that see it are NaN, no others.
  * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D); latched
  * SV_ERR_DEVICE_BOUNDS for lengths or pages out of range (the sequence's
  * output is then not meaningful).

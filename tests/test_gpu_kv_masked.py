@@ -72,3 +72,35 @@ def test_queries_that_are_not_finite(dbv, new, G, lens, D):
             lost[t, h] = True
     check_rows(clean, call(dbv, c), lost)
     dbv.default_handle(c["q"].device).sync_status()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,G,lens", [(4, 4, [300, 128, 0]), (20, 1, [100, 250] * 100),
+                                        (33, 2, [2000, 90]), (60, 2, [200, 77]),
+                                        (150, 1, [60, 0])])
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("tree", [False, True])
+def test_new_tokens_that_are_nan(dbv, tree, side, new, G, lens, D):
+    """NaN in the key or value of some new tokens: rows that see one are NaN, the
+    rows that do not are as if its bytes were zero."""
+    B, H, block = len(lens), 2, 32
+    c = case(new, lens, [new] * B, H, G, D, block, tree=tree)
+    r = np.random.RandomState(D + new)
+    clean = dict(c, cache=[x.clone() for x in c["cache"]])
+    lost = torch.zeros(c["q"].shape[:2], dtype=torch.bool, device="cuda")
+    for b in range(0, B, 1 if B < 10 else 3):
+        for j in (new - 1, new // 2 + r.randint(new // 2)):
+            if tree and j == new - 1:  # one that no row sees
+                c["mask"][c["cu"][b]:c["cu"][b + 1], j // 32] &= ~np.uint32(1 << (j % 32))
+            p, h, d = lens[b] + j, r.randint(H), r.randint(D)
+            page = int(c["table"][b, p // block])
+            c["cache"][side][page, h, p % block, d] = r.choice([0x7F, 0xFF])
+            clean["cache"][side][page, h, p % block] = 0
+            for i in range(new):
+                t = int(c["cu"][b]) + i
+                sees = (c["mask"][t, j // 32] >> (j % 32)) & 1 if tree else j <= i
+                if sees:
+                    lost[t, h * G:(h + 1) * G] = True
+    assert lost.any() and not lost.all()
+    check_rows(clean, call(dbv, c), lost)
+    dbv.default_handle(c["q"].device).sync_status()
