@@ -31,6 +31,16 @@
 //   w'_p = 2^(z_p log2 e + log2 s^v_p - M),  M = max over the same sum,
 // so that O needs no scale; the sum of weights takes w'_p / s^v_p.
 //
+// That makes a weight's step one of the largest w', so a page of a large scale
+// would take the others' bits: 2^12 apart cost 1.6% of an output that came from
+// the small one, 2^18 all of it.  A piece of work whose pages' value scales lie
+// 2^6 apart or more is therefore taken in rounds, one for each class of scales
+// (six exponents), with weights and a running maximum of its own, added up in
+// fp32.  A CTA begins with loops that know no rounds and goes over to ones that
+// do at the first piece that needs them.  (One set of loops for both took 7% to
+// 13% longer on calls without rounds: what they keep takes registers from the
+// loops over tiles.)
+//
 // Split.  The tiles (128 tokens of one unit: sequence, head, row block) of the
 // whole call, laid end to end by their cost, are cut into equal spans, one per
 // CTA of one wave.  A unit that several CTAs share leaves partial sums in the
@@ -66,7 +76,144 @@ constexpr int kAtThreads = kSoftWarps * 32 + 128;
 constexpr int kAtRegs = 96, kSideRegs = 56, kSoftRegs = 104;
 static_assert(128 * kSideRegs + kSoftWarps * 32 * kSoftRegs <= kAtThreads * kAtRegs, "registers");
 constexpr float kNone = -1e30f;        // running maximum before any token
+constexpr int kClass = 6;              // value scales of a class: less than 2^6 apart
+// Rounds that the producer may be ahead of a reader of `more`: a tile each, at
+// most those in flight and one.
+constexpr int kRounds = 8;
+static_assert(kRounds > kAtStages + 1, "rounds");
+constexpr int kGaveUp = 2;             // AttnShared::abort: roles without rounds end
 constexpr uint32_t kAtSpin = 1u << 20; // tries of a wait (a tile takes microseconds)
+
+// ---------------------------------------------------------------------------
+// The units of a call.
+// ---------------------------------------------------------------------------
+// Quotient of non-negative numbers; 64-bit division costs thousands of cycles.
+__device__ __forceinline__ long long div_pos(long long a, long long b)
+{
+    if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
+struct SeqWork {
+    int n, L, first;         // new tokens, tokens, first row of q
+    int tiles, blocks, rows; // tiles of a unit, row blocks, rows of a block
+    int cost;                // of a tile
+    long long work;          // cost of the sequence
+    bool bad;
+};
+// Rows of the products for this many query rows: the two (up to 64) or four
+// warpgroups of a tile have 8 rows each, or 16, 24, 32.
+__device__ __forceinline__ int round_rows(int rows)
+{
+    return rows <= 64 ? (rows + 15) & ~15 : (rows + 31) & ~31;
+}
+// Time of a tile by its rows, as measured: even spans of it are even in time.
+__device__ __forceinline__ int tile_cost(int N)
+{
+    // in units of 0.04 us (152 units of 4,096 and 16,384 tokens, D = 128)
+    return N <= 32 ? 18 : N <= 48 ? 20 : N <= 64 ? 22 : N <= 96 ? 34 : 42;
+}
+
+__device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
+{
+    SeqWork s;
+    s.first = j.cu[b];
+    const int end = j.cu[b + 1];
+    s.L = j.kv_len[b];
+    s.n = end - s.first;
+    s.bad = s.first < 0 || end > j.T || s.n < 0 || s.L < s.n ||
+            ((s.L + (long long)j.block - 1) >> (31 - __clz(j.block))) > j.cols;
+    if (s.bad) s.n = 0;
+    const long long all = (long long)s.n * j.G;
+    s.tiles = (int)(((long long)s.L + kTile - 1) >> 7);
+    s.blocks = (int)((all + kRowsMax - 1) >> 7);
+    s.rows = s.blocks <= 1 ? (int)all : (int)div_pos(all + s.blocks - 1, s.blocks);
+    s.cost = tile_cost(round_rows(s.rows));
+    s.work = (long long)s.tiles * s.blocks * j.H * s.cost;
+    return s;
+}
+
+// A CTA's share of one unit, walked alike by every role.  Costs of tiles, laid
+// end to end, are cut into equal spans; a tile belongs to the span that its
+// first unit of cost lies in.
+struct Piece {
+    int b, h, row0, rows;    // sequence, cache head, first row (of n G) and rows
+    int t0, t1, tiles;       // tiles [t0, t1) of the unit's
+    int cost;                // of a tile
+    long long unit0;         // where the unit starts in the call's cost
+    int L, n, first;
+};
+struct PieceWalk {
+    long long pos, end;      // the next tile's start, the span's end
+    int b, h, block, tile;   // the next tile
+    SeqWork s;
+    // first, x: the sequence that `from` lies in, and where
+    __device__ __forceinline__ void start(const AttendJob &j, int first, long long x,
+                                          long long from, long long to)
+    {
+        pos = from;
+        end = to;
+        b = first;
+        h = block = tile = 0;
+        if (pos < end) {
+            s = seq_work(j, b);
+            // on to the first tile that starts within the span
+            long long t = div_pos(x + s.cost - 1, s.cost);
+            pos += t * s.cost - x;
+            const long long u = div_pos(t, s.tiles);
+            tile = (int)(t - u * s.tiles);
+            h = (int)div_pos(u, s.blocks);
+            block = (int)(u - (long long)h * s.blocks);
+        }
+    }
+    __device__ __forceinline__ bool next(const AttendJob &j, Piece &p)
+    {
+        if (pos >= end) return false;
+        while (h >= j.H || s.work == 0) {
+            s = seq_work(j, ++b);
+            h = 0;
+        }
+        const long long left = end - pos, all = (long long)(s.tiles - tile) * s.cost;
+        const int n = left >= all ? s.tiles - tile : (int)div_pos(left + s.cost - 1, s.cost);
+        p.t0 = tile;
+        p.t1 = tile + n;
+        p.b = b;
+        p.h = h;
+        p.row0 = block * s.rows;
+        p.rows = min(s.rows, s.n * j.G - p.row0);
+        p.tiles = s.tiles;
+        p.cost = s.cost;
+        p.unit0 = pos - (long long)tile * s.cost;
+        p.L = s.L;
+        p.n = s.n;
+        p.first = s.first;
+        pos += (long long)n * s.cost;
+        tile += n;
+        if (tile == s.tiles) {
+            tile = 0;
+            if (++block == s.blocks) {
+                block = 0;
+                ++h;
+            }
+        }
+        return true;
+    }
+};
+
+// For value scales that lie far apart (a round is a class of them, below).
+struct AttnRounds {
+    Piece piece;                       // the softmax warps', for its further rounds
+    // where the roles without rounds give up: the tiles so far (0 where they do
+    // not), the pieces so far, and the piece's start
+    uint32_t it, pieces;
+    int b;
+    long long x, pos;
+    uint32_t classes[4];               // exponents of the piece's value scales: of rounds to come
+    int more[kRounds];                 // the round's piece needs another one after it
+    uint64_t told[kRounds];            // that is known
+    uint32_t round[kSoftWarps];        // twice the round, and 1 after a piece's first, per warp
+    float old_f[kRowsMax];             // factors of the sums of the rounds before
+};
 
 struct AttnShared {
     uint64_t full_k[kAtStages], full_v[kAtStages], empty_k[kAtStages], empty_v[kAtStages];
@@ -92,6 +239,7 @@ struct AttnShared {
     float out_f[2][kRowsMax];          // factors of the output's sums
     short owner[256];                  // CTAs of a shared unit's tiles (spans below a tile)
     long long scan[kAtThreads / 32];
+    AttnRounds far;
 };
 
 // Product of packed fp32 pairs.
@@ -230,122 +378,6 @@ __device__ __forceinline__ bool at_wait(AttnShared *sh, int *err, uint64_t *bar,
     return at_wait_on(sh, err, bar, parity);
 }
 
-// ---------------------------------------------------------------------------
-// The units of a call.
-// ---------------------------------------------------------------------------
-// Quotient of non-negative numbers; 64-bit division costs thousands of cycles.
-__device__ __forceinline__ long long div_pos(long long a, long long b)
-{
-    if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
-}
-
-struct SeqWork {
-    int n, L, first;         // new tokens, tokens, first row of q
-    int tiles, blocks, rows; // tiles of a unit, row blocks, rows of a block
-    int cost;                // of a tile
-    long long work;          // cost of the sequence
-    bool bad;
-};
-// Rows of the products for this many query rows: the two (up to 64) or four
-// warpgroups of a tile have 8 rows each, or 16, 24, 32.
-__device__ __forceinline__ int round_rows(int rows)
-{
-    return rows <= 64 ? (rows + 15) & ~15 : (rows + 31) & ~31;
-}
-// Time of a tile by its rows, as measured: even spans of it are even in time.
-__device__ __forceinline__ int tile_cost(int N)
-{
-    // in units of 0.04 us (152 units of 4,096 and 16,384 tokens, D = 128)
-    return N <= 32 ? 18 : N <= 48 ? 20 : N <= 64 ? 22 : N <= 96 ? 34 : 42;
-}
-
-__device__ __forceinline__ SeqWork seq_work(const AttendJob &j, int b)
-{
-    SeqWork s;
-    s.first = j.cu[b];
-    const int end = j.cu[b + 1];
-    s.L = j.kv_len[b];
-    s.n = end - s.first;
-    s.bad = s.first < 0 || end > j.T || s.n < 0 || s.L < s.n ||
-            ((s.L + (long long)j.block - 1) >> (31 - __clz(j.block))) > j.cols;
-    if (s.bad) s.n = 0;
-    const long long all = (long long)s.n * j.G;
-    s.tiles = (int)(((long long)s.L + kTile - 1) >> 7);
-    s.blocks = (int)((all + kRowsMax - 1) >> 7);
-    s.rows = s.blocks <= 1 ? (int)all : (int)div_pos(all + s.blocks - 1, s.blocks);
-    s.cost = tile_cost(round_rows(s.rows));
-    s.work = (long long)s.tiles * s.blocks * j.H * s.cost;
-    return s;
-}
-
-// A CTA's share of one unit, walked alike by every role.  Costs of tiles, laid
-// end to end, are cut into equal spans; a tile belongs to the span that its
-// first unit of cost lies in.
-struct Piece {
-    int b, h, row0, rows;    // sequence, cache head, first row (of n G) and rows
-    int t0, t1, tiles;       // tiles [t0, t1) of the unit's
-    int cost;                // of a tile
-    long long unit0;         // where the unit starts in the call's cost
-    int L, n, first;
-};
-struct PieceWalk {
-    long long pos, end;      // the next tile's start, the span's end
-    int b, h, block, tile;   // the next tile
-    SeqWork s;
-    __device__ __forceinline__ void start(const AttendJob &j, const AttnShared *sh,
-                                          long long from, long long to)
-    {
-        pos = from;
-        end = to;
-        b = sh->first_b;
-        h = block = tile = 0;
-        if (pos < end) {
-            s = seq_work(j, b);
-            // on to the first tile that starts within the span
-            const long long x = sh->first_x;
-            long long t = div_pos(x + s.cost - 1, s.cost);
-            pos += t * s.cost - x;
-            const long long u = div_pos(t, s.tiles);
-            tile = (int)(t - u * s.tiles);
-            h = (int)div_pos(u, s.blocks);
-            block = (int)(u - (long long)h * s.blocks);
-        }
-    }
-    __device__ __forceinline__ bool next(const AttendJob &j, Piece &p)
-    {
-        if (pos >= end) return false;
-        while (h >= j.H || s.work == 0) {
-            s = seq_work(j, ++b);
-            h = 0;
-        }
-        const long long left = end - pos, all = (long long)(s.tiles - tile) * s.cost;
-        const int n = left >= all ? s.tiles - tile : (int)div_pos(left + s.cost - 1, s.cost);
-        p.t0 = tile;
-        p.t1 = tile + n;
-        p.b = b;
-        p.h = h;
-        p.row0 = block * s.rows;
-        p.rows = min(s.rows, s.n * j.G - p.row0);
-        p.tiles = s.tiles;
-        p.cost = s.cost;
-        p.unit0 = pos - (long long)tile * s.cost;
-        p.L = s.L;
-        p.n = s.n;
-        p.first = s.first;
-        pos += (long long)n * s.cost;
-        tile += n;
-        if (tile == s.tiles) {
-            tile = 0;
-            if (++block == s.blocks) {
-                block = 0;
-                ++h;
-            }
-        }
-        return true;
-    }
-};
-
 // Span of CTA i of `ctas` over `total` tiles, and the CTA that owns a tile.
 __device__ __forceinline__ long long span_at(long long total, int ctas, int i)
 {
@@ -440,7 +472,7 @@ __device__ __forceinline__ void load_scores(float (&y)[C8 * 8], uint32_t col)
     }
 }
 
-template <int D, int C8>
+template <int D, int C8, bool ROUNDS>
 __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, char *smem_v,
                                            char *smem_p, const Piece &pc, uint32_t &it,
                                            int stage_bytes, int ctas, bool turns, bool ok)
@@ -483,11 +515,10 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         ok = ok && at_wait(sh, j.err, &sh->s_full[sb], (it >> 1) & 1);
         tc_fence_after();
         const int p0 = t * kTile, pos = p0 + tk;
-        const float ks = sh->ks[st][page_in];
-        const float vs = fminf(fmaxf(sh->vs[st][page_in], 0x1p-60f), 0x1p60f);
+        const float ks = sh->ks[st][page_in], vs = sh->vs[st][page_in];
         float vl, ivs;
-        asm("lg2.approx.f32 %0, %1;" : "=f"(vl) : "f"(vs));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));
+        asm("lg2.approx.f32 %0, %1;" : "=f"(vl) : "f"(vs));  // (-inf: another round's)
+        asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(ROUNDS ? fmaxf(vs, 0x1p-60f) : vs));
         uint32_t sees = ~0u;  // which rows see this token
         if (edge) {
             const int c = turns ? par : 2 + (int)sb;
@@ -685,6 +716,11 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         const uint32_t last = turns && ((it - 1) & 1) != (uint32_t)par ? it - 2 : it - 1;
         ok = at_wait(sh, j.err, &sh->pv_done[last & 1], (last >> 1) & 1);
     }
+    const uint32_t r2 = ROUNDS ? sh->far.round[warp] : 0, round = r2 >> 1;
+    if (ROUNDS)
+        ok = ok && at_wait(sh, j.err, &sh->far.told[round % kRounds], round / kRounds & 1);
+    else
+        ok = ok && sh->far.it != it;            // (a piece that needs rounds is given up)
     warp_sum_rows(l, lane);
     if ((lane & 3) == 0) {
 #pragma unroll
@@ -701,7 +737,12 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     if (bar_or(5, kSoftWarps * 32, !ok)) return false;
     tc_fence_after();
 
+    // Rounds of a piece after its first add to the sums that these left in the
+    // workspace (of a whole unit in the part of the CTA's last unit, which comes
+    // after it); a thread reads what it wrote itself.
+    const bool first = !ROUNDS || !(r2 & 1), more = ROUNDS && sh->far.more[round % kRounds];
     const bool whole = pc.t0 == 0 && pc.t1 == pc.tiles;
+    const bool ends = whole && !more;           // the output follows
     int c0 = 0, c1 = 0, owners = 0;  // the CTAs that share the unit
     bool each = false;
     float *part = nullptr;
@@ -714,6 +755,8 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         owners = each ? pc.tiles : c1 - c0 + 1;
         // a unit that starts before this CTA's span is its first, else its last
         part = j.part + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * part_floats(D);
+    } else if (more || !first) {
+        part = j.part + ((size_t)blockIdx.x * 2 + 1) * part_floats(D);
     }
     const int d = tk;  // head element of this lane (D = 64: lanes 64.. hold copies)
     // (a pair that had no tile has no sums)
@@ -723,7 +766,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
     // a thread for each row: the factors that its sums of the two pairs get
     if (tid < (turns ? 2 : 4) * R) {
         const int n = tid;
-        const float m = turns ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
+        float m = turns ? fmaxf(sh->top[0][n], sh->top[1][n]) : sh->top[0][n];
         float f0 = 0.f, f1 = 0.f, s = 0.f;
         if (has0) {
             f0 = turns ? ex2f(sh->top[0][n] - m) : 1.f;
@@ -734,12 +777,24 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
             s = fmaf(f1, (sh->sum[1][0][n] + sh->sum[1][1][n]) +
                              (sh->sum[1][2][n] + sh->sum[1][3][n]), s);
         }
+        float fo = 0.f;
+        if (!first && n < pc.rows) {
+            const float mo = part[(size_t)kRowsMax * D + n];
+            const float so = part[(size_t)kRowsMax * (D + 1) + n];
+            const float top = fmaxf(m, mo), fn = ex2f(m - top);
+            fo = ex2f(mo - top);
+            s = fmaf(so, fo, s * fn);
+            f0 *= fn;
+            f1 *= fn;
+            m = top;
+        }
         // (a sum of NaN is no sum of nothing: it goes into the output)
-        const float inv = !whole ? 1.f : s == 0.f ? 0.f : 1.f / s;
+        const float inv = !ends ? 1.f : s == 0.f ? 0.f : 1.f / s;
         sh->out_f[0][n] = f0 * inv;
         sh->out_f[1][n] = f1 * inv;
+        if (ROUNDS) sh->far.old_f[n] = fo * inv;
         if (n < pc.rows) {
-            if (whole) {
+            if (ends) {
                 if (j.lse)
                     j.lse[sh->at[n]] =
                         s == 0.f ? -INFINITY : (m + log2f(s)) * 0.6931471805599453f;
@@ -771,7 +826,9 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (w + i >= pc.rows) break;
-                if (whole)
+                if (!first)
+                    o[i] = fmaf(sh->far.old_f[w + i], part[(size_t)(w + i) * D + d], o[i]);
+                if (ends)
                     j.out[(int64_t)sh->at[w + i] * D + d] =
                         __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
                 else
@@ -780,7 +837,7 @@ __device__ __forceinline__ bool soft_piece(const AttendJob &j, AttnShared *sh, c
         }
     }
     tc_fence_before();
-    if (whole) {
+    if (whole || more) {
         bar_or(5, kSoftWarps * 32, false);  // sum and top are free again
         return true;
     }
@@ -895,129 +952,74 @@ __device__ __forceinline__ void load_queries(const AttendJob &j, AttnShared *sh,
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAtThreads, 1)
-attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUtensorMap map_k,
-              const __grid_constant__ CUtensorMap map_v)
+// The roles' loops over the pieces of a span: without rounds (up to a piece that
+// needs them) or with them (from that piece on).
+template <int D, bool ROUNDS>
+__device__ __forceinline__ void attend_roles(const AttendJob &j, const CUtensorMap &map_k,
+                                             const CUtensorMap &map_v, AttnShared *sh, char *base,
+                                             int first, long long x, long long from, long long to,
+                                             uint32_t pieces)
 {
-    extern __shared__ char attn_raw[];
-    __shared__ AttnShared shared;
-    AttnShared *sh = &shared;
     constexpr int kSide = kTile * D;            // bytes of a tile's keys (or values)
     constexpr uint32_t kSwz = D == 128 ? 2 : 4;
-    char *base = attn_raw + ((1024 - (smem_u32(attn_raw) & 1023)) & 1023);
     char *s_k = base, *s_v = base + kSide, *s_q = base + 2 * kAtStages * kSide;
     char *s_p = s_q + 2 * kRowsMax * D;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-    if (tid == 0) {
-        for (int i = 0; i < kAtStages; ++i) {
-            mbar_init(&sh->full_k[i], 1);
-            mbar_init(&sh->full_v[i], 1);
-            mbar_init(&sh->empty_k[i], 1);
-            mbar_init(&sh->empty_v[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh->s_full[i], 1);
-            // (a warp arrives twice where two warpgroups have a tile)
-            mbar_init(&sh->s_empty[i], kSoftWarps);
-            mbar_init(&sh->p_full[i], kSoftWarps);
-            mbar_init(&sh->pv_done[i], 1);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(&sh->clean[i], 1);
-        mbar_init(&sh->q_full, kSoftWarps);
-        mbar_init(&sh->drained[0], 1);
-        mbar_init(&sh->drained[1], 1);
-        mbar_fence_init();
-        sh->abort = 0;
-        sh->first_b = 0;
-        sh->first_x = 0;
-    }
-    if (warp == kSoftWarps) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                         smem_u32(&sh->tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    pdl_wait();
-    pdl_trigger();
-
-    // ---- this CTA's span: each thread sums a run of sequences
-    const int per = (j.B + kAtThreads - 1) / kAtThreads;
-    const int b0 = min(tid * per, j.B), b1 = min(b0 + per, j.B);
-    long long own = 0;
-    for (int b = b0; b < b1; ++b) {
-        const SeqWork s = seq_work(j, b);
-        own += s.work;
-        if (s.bad && blockIdx.x == 0) latch(j.err, SV_ERR_DEVICE_BOUNDS);
-    }
-    long long run = own;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const long long a = __shfl_up_sync(0xFFFFFFFFu, run, k);
-        if (lane >= k) run += a;
-    }
-    if (lane == 31) sh->scan[warp] = run;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kAtThreads / 32; ++w) {
-        if (w < warp) run += sh->scan[w];
-        total += sh->scan[w];
-    }
     const int ctas = gridDim.x;
-    const int me = blockIdx.x;
-    const long long from = span_at(total, ctas, me), to = span_at(total, ctas, me + 1);
-    if (from < to && run > from && run - own <= from) {
-        long long x = from - (run - own);
-        int b = b0;
-        for (;; ++b) {
-            const long long w = seq_work(j, b).work;
-            if (x < w) break;
-            x -= w;
-        }
-        sh->first_b = b;
-        sh->first_x = x;
-    }
-    if (tid == 0) sh->total = total;
-    __syncthreads();
-
     PieceWalk walk;
     Piece pc;
-    walk.start(j, sh, from, to);
-    uint32_t it = 0;
+    uint32_t it = ROUNDS ? sh->far.it : 0, round = 0;
+    walk.start(j, first, x, from, to);
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        if (!ROUNDS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         bool ok = true;
-        sh->looks[warp] = 0;
-        while (ok && walk.next(j, pc)) {
+        if (ROUNDS)
+            sh->far.round[warp] = 0;
+        else
+            sh->looks[warp] = 0;
+        bool more = false;  // the piece has another round
+        while (ok) {
+            if (ROUNDS && more) {
+                pc = sh->far.piece;
+            } else {
+                if (!walk.next(j, pc)) break;
+                if (tid == 0) ++sh->far.pieces;
+                if (ROUNDS && tid == 0) sh->far.piece = pc;
+                load_queries<D>(j, sh, s_q, pc, round_rows(pc.rows));
+                fence_async();
+                bar_or(5, kSoftWarps * 32, false);  // the rows' factors are there
+                if (lane == 0) mbar_arrive(&sh->q_full);
+            }
             const int N = round_rows(pc.rows);
-            load_queries<D>(j, sh, s_q, pc, N);
-            fence_async();
-            bar_or(5, kSoftWarps * 32, false);  // the rows' factors are there
-            if (lane == 0) mbar_arrive(&sh->q_full);
             const bool turns = N <= 64;
 #define SV_SOFT(C)                                                                              \
     case C:                                                                                     \
-        ok = soft_piece<D, C>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, turns, ok);             \
+        ok = soft_piece<D, C, ROUNDS>(j, sh, s_v, s_p, pc, it, 2 * kSide, ctas, turns, ok);      \
         break;
             switch (N / (turns ? 16 : 32)) {
                 SV_SOFT(1) SV_SOFT(2) SV_SOFT(3) SV_SOFT(4)
             }
 #undef SV_SOFT
+            if (ROUNDS) {
+                const uint32_t r = sh->far.round[warp] >> 1;
+                more = sh->far.more[r % kRounds] != 0;
+                __syncwarp();
+                sh->far.round[warp] = (r + 1) * 2 + more;
+                __syncwarp();
+            }
         }
+        // (the issuers are waiting for the next piece)
+        if (!ROUNDS && !ok && tid == 0 && sh->abort == 0) *(volatile int *)&sh->abort = kGaveUp;
     } else if (warp >= kSoftWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+        if (!ROUNDS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
     }
     if (warp == kSoftWarps) {
         // ---- producer: the pages of each tile, looked up 32 at a time
-            const int per_tile = kTile >> (31 - __clz(j.block));
+        const int shift = 31 - __clz(j.block), per_tile = kTile >> shift;
         const int inner = lane & (per_tile - 1);
-        bool ok = true;
+        bool ok = true, more = false;
         while (ok && walk.next(j, pc)) {
-                const int last = (int)((pc.L + (long long)j.block - 1) >> (31 - __clz(j.block)));  // pages of the sequence
+            const int last = (int)((pc.L + (long long)j.block - 1) >> shift);  // pages of the sequence
             const int32_t *tab = j.table + (int64_t)pc.b * j.cols;
             auto window = [&](int w0, int &page, float &ks, float &vs) {
                 page = w0 + lane < last ? tab[w0 + lane] : -1;
@@ -1029,58 +1031,126 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 if (page >= 0) {
                     const int64_t ph = (int64_t)page * j.H + pc.h;
                     ks = j.scale[0][ph];
-                    vs = j.scale[1][ph];
+                    vs = fminf(fmaxf(j.scale[1][ph], 0x1p-60f), 0x1p60f);
                 }
             };
-            int w0 = (pc.t0 * per_tile) & ~31, page, npage;
-            float ks, vs, nks, nvs;
-            window(w0, page, ks, vs);
-            window(w0 + 32, npage, nks, nvs);
-            for (int t = pc.t0; t < pc.t1; ++t, ++it) {
-                const int st = it % kAtStages;
-                const uint32_t ph = ((it / kAtStages) & 1) ^ 1;
-                const int p0 = t * per_tile;
-                if (p0 >= w0 + 32) {
-                    w0 += 32;
-                    page = npage;
-                    ks = nks;
-                    vs = nvs;
-                    window(w0 + 32, npage, nks, nvs);
+            const int first_p = pc.t0 * per_tile, end_p = min(pc.t1 * per_tile, last);
+            auto exponent = [](float vs) { return (int)(__float_as_uint(vs) >> 23) - 64; };
+            if (ROUNDS && lane < 4) sh->far.classes[lane] = 0;
+            // without rounds: the lane's extreme exponents; with them: those of the
+            // round's class, and the last of the first round's
+            int top = 0, bottom = 127, top0 = 0;
+            auto own = [&](int w0) { return w0 + lane >= first_p && w0 + lane < end_p; };
+            auto note = [&](int w0, float vs) {
+                top = max(top, own(w0) ? exponent(vs) : 0);
+                bottom = min(bottom, own(w0) ? exponent(vs) : 127);
+            };
+            more = false;
+            do {
+                int w0 = first_p & ~31, page, npage;
+                float ks, vs, nks, nvs;
+                window(w0, page, ks, vs);
+                window(w0 + 32, npage, nks, nvs);
+                bool fresh = true;  // the window's value scales have not been looked at
+                if (more) {
+                    const uint32_t w = sh->far.classes[lane & 3];
+                    top = __reduce_max_sync(0xFFFFFFFFu, w ? (lane & 3) * 32 + 31 - __clz(w) : 0);
+                    bottom = top > top0 ? max(top - kClass, top0) + 1 : top - kClass + 1;
                 }
-                const bool mine = lane - (p0 - w0) >= 0 && lane - (p0 - w0) < per_tile;
-                const bool copy = mine && page >= 0;
-                const uint32_t bytes =
-                    (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copy)) * j.block * D;
-                ok = at_wait(sh, j.err, &sh->empty_k[st], ph);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_tx(&sh->full_k[st], bytes);
-                __syncwarp();
-                const int64_t row = (int64_t)page * j.H + pc.h;
-                auto fetch = [&](const CUtensorMap *map, char *dst, uint64_t *bar) {
-                    asm volatile(
-                        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
-                        "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-                        "l"(map), "r"(0), "r"(0), "r"((int)row), "r"(smem_u32(bar))
-                        : "memory");
-                };
-                if (copy)
-                    fetch(&map_k, s_k + (size_t)st * 2 * kSide + inner * j.block * D,
-                          &sh->full_k[st]);
-                ok = at_wait(sh, j.err, &sh->empty_v[st], ph);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                if (mine) {
-                    sh->ks[st][inner] = ks;
-                    sh->vs[st][inner] = vs;
+                for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+                    const int st = it % kAtStages;
+                    const uint32_t ph = ((it / kAtStages) & 1) ^ 1;
+                    const int p0 = t * per_tile;
+                    if (p0 >= w0 + 32) {
+                        if (!ROUNDS) note(w0, vs);
+                        w0 += 32;
+                        page = npage;
+                        ks = nks;
+                        vs = nvs;
+                        window(w0 + 32, npage, nks, nvs);
+                        fresh = true;
+                    }
+                    const bool mine = lane - (p0 - w0) >= 0 && lane - (p0 - w0) < per_tile;
+                    const bool copy = mine && page >= 0;
+                    const uint32_t bytes =
+                        (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copy)) * j.block * D;
+                    ok = at_wait(sh, j.err, &sh->empty_k[st], ph);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_tx(&sh->full_k[st], bytes);
+                    __syncwarp();
+                    const int64_t row = (int64_t)page * j.H + pc.h;
+                    auto fetch = [&](const CUtensorMap *map, char *dst, uint64_t *bar) {
+                        asm volatile(
+                            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
+                            "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                            "l"(map), "r"(0), "r"(0), "r"((int)row), "r"(smem_u32(bar))
+                            : "memory");
+                    };
+                    if (copy)
+                        fetch(&map_k, s_k + (size_t)st * 2 * kSide + inner * j.block * D,
+                              &sh->full_k[st]);
+                    if (ROUNDS && fresh) {
+                        fresh = false;
+                        const int e = exponent(vs);
+                        if (!more && t == pc.t0) {
+                            // the first class ends at the largest scale of the pages looked
+                            // up, or one above it where there are more
+                            const int f = w0 + 32 + lane < end_p ? exponent(nvs) : 0;
+                            top = top0 = __reduce_max_sync(0xFFFFFFFFu, max(own(w0) ? e : 0, f)) +
+                                         (w0 + 64 < end_p ? 1 : 0);
+                            bottom = top - kClass + 1;
+                        }
+                        if (!more && own(w0)) atomicOr(&sh->far.classes[e >> 5], 1u << (e & 31));
+                        if (e < bottom || e > top) vs = 0.f;
+                    }
+                    ok = at_wait(sh, j.err, &sh->empty_v[st], ph);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (!ROUNDS && t == pc.t1 - 1) {
+                        // (told before the last tile's values)
+                        note(w0, vs);
+                        more = __reduce_max_sync(0xFFFFFFFFu, top) -
+                                   __reduce_min_sync(0xFFFFFFFFu, bottom) >= kClass;
+                        if (more && lane == 0) {
+                            const SeqWork &s = walk.s;
+                            const long long unit = (long long)pc.h * s.blocks + pc.row0 / s.rows;
+                            sh->far.b = pc.b;
+                            sh->far.x = (unit * s.tiles + pc.t0) * s.cost;
+                            sh->far.pos = pc.unit0 + (long long)pc.t0 * pc.cost;
+                            sh->far.it = it + 1;
+                        }
+                    }
+                    if (mine) {
+                        sh->ks[st][inner] = ks;
+                        sh->vs[st][inner] = vs;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_tx(&sh->full_v[st], bytes);
+                    __syncwarp();
+                    if (copy)
+                        fetch(&map_v, s_v + (size_t)st * 2 * kSide + inner * j.block * D,
+                              &sh->full_v[st]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_tx(&sh->full_v[st], bytes);
-                __syncwarp();
-                if (copy)
-                    fetch(&map_v, s_v + (size_t)st * 2 * kSide + inner * j.block * D,
-                          &sh->full_v[st]);
-            }
+                if (ROUNDS) {
+                    // what the round leaves
+                    __syncwarp();
+                    const int base = (lane & 3) * 32;
+                    const int lo = max(bottom - base, 0), hi = min(top - base, 31);
+                    uint32_t w = sh->far.classes[lane & 3];
+                    if (lo <= hi) w &= ~((~0u << lo) & (~0u >> (31 - hi)));
+                    __syncwarp();
+                    if (lane < 4) sh->far.classes[lane] = w;
+                    more = __any_sync(0xFFFFFFFFu, w != 0);
+                    if (lane == 0) {
+                        sh->far.more[round % kRounds] = more;
+                        mbar_arrive(&sh->far.told[round % kRounds]);
+                    }
+                    ++round;
+                    __syncwarp();
+                }
+            } while (ROUNDS && ok && more);
+            if (!ROUNDS && more) break;
         }
         // after a wait that ran out: copies still in flight land before the exit
         if (!ok)
@@ -1097,14 +1167,16 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         const uint64_t dk0 = tc_desc(smem_u32(s_k), 16, 8 * D, kSwz);
         const uint64_t dq = tc_desc(smem_u32(s_q), 16, 8 * D, kSwz);
         bool ok = true;
-        uint32_t pieces = 0;
-        while (ok && walk.next(j, pc)) {
+        bool more = false;  // the piece has another round
+        while (ok && ((ROUNDS && more) || walk.next(j, pc))) {
             const int N = round_rows(pc.rows);
             const bool one = stacked(N);
             const uint32_t id_s = kKinds | ((uint32_t)((one ? 2 * N : N) >> 3) << 17);
             const uint64_t dlo = dq + (uint32_t)(N * D >> 4);
-            ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
-            ++pieces;
+            if (!ROUNDS || !more) {
+                ok = at_wait(sh, j.err, &sh->q_full, pieces & 1);
+                ++pieces;
+            }
             const int ctx = pc.L - pc.n;
             const int reach = min(max(ctx >> 7, pc.t0), pc.t1);  // first tile of new tokens
             auto tiles = [&](auto is_one, int from, int to) {
@@ -1174,6 +1246,11 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->clean[N <= 64 ? sb : 2 + sb]);
             }
+            if (ROUNDS) {
+                ok = ok && at_wait(sh, j.err, &sh->far.told[round % kRounds], round / kRounds & 1);
+                more = sh->far.more[round++ % kRounds] != 0;
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
         // after a wait that ran out: products still in flight end before the exit
         if (!ok && lane == 0) {
@@ -1187,8 +1264,8 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
         // D = 64: the second 64 rows read the same values again
         const uint64_t dv0 = tc_desc(smem_u32(s_v), 0, 8 * D, kSwz);
         const uint64_t dp0 = tc_desc(smem_u32(s_p), kTile * 128, 1024, 2);
-        bool ok = true;
-        while (ok && walk.next(j, pc)) {
+        bool ok = true, more = false;  // the piece has another round
+        while (ok && ((ROUNDS && more) || walk.next(j, pc))) {
             const int N = round_rows(pc.rows);
             const bool turns = N <= 64;
             const uint32_t id_o = kKinds | ((uint32_t)(2 * N >> 3) << 17);
@@ -1210,11 +1287,128 @@ attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUten
                 tc_commit(&sh->pv_done[sb]);
                 tc_commit(&sh->empty_v[st]);
             }
+            if (ROUNDS) {
+                ok = ok && at_wait(sh, j.err, &sh->far.told[round % kRounds], round / kRounds & 1);
+                more = sh->far.more[round++ % kRounds] != 0;
+            }
         }
         if (!ok) {
             tc_commit(&sh->drained[1]);
             mbar_wait_n(&sh->drained[1], 0, 1u << 12);
         }
+    }
+}
+
+// With rounds.  (A call, which has its own registers.)
+template <int D>
+__device__ __noinline__ void attend_rounds(const AttendJob *j, const CUtensorMap *map_k,
+                                           const CUtensorMap *map_v, AttnShared *sh, char *base,
+                                           long long to, uint32_t pieces)
+{
+    attend_roles<D, true>(*j, *map_k, *map_v, sh, base, sh->far.b, sh->far.x, sh->far.pos, to, pieces);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1)
+attend_kernel(const __grid_constant__ AttendJob j, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v)
+{
+    extern __shared__ char attn_raw[];
+    __shared__ AttnShared shared;
+    AttnShared *sh = &shared;
+    char *base = attn_raw + ((1024 - (smem_u32(attn_raw) & 1023)) & 1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < kAtStages; ++i) {
+            mbar_init(&sh->full_k[i], 1);
+            mbar_init(&sh->full_v[i], 1);
+            mbar_init(&sh->empty_k[i], 1);
+            mbar_init(&sh->empty_v[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->s_full[i], 1);
+            // (a warp arrives twice where two warpgroups have a tile)
+            mbar_init(&sh->s_empty[i], kSoftWarps);
+            mbar_init(&sh->p_full[i], kSoftWarps);
+            mbar_init(&sh->pv_done[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&sh->clean[i], 1);
+        for (int i = 0; i < kRounds; ++i) mbar_init(&sh->far.told[i], 1);
+        mbar_init(&sh->q_full, kSoftWarps);
+        mbar_init(&sh->drained[0], 1);
+        mbar_init(&sh->drained[1], 1);
+        mbar_fence_init();
+        sh->abort = 0;
+        sh->far.it = sh->far.pieces = 0;
+        sh->first_b = 0;
+        sh->first_x = 0;
+    }
+    if (warp == kSoftWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_u32(&sh->tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's span: each thread sums a run of sequences
+    const int per = (j.B + kAtThreads - 1) / kAtThreads;
+    const int b0 = min(tid * per, j.B), b1 = min(b0 + per, j.B);
+    long long own = 0;
+    for (int b = b0; b < b1; ++b) {
+        const SeqWork s = seq_work(j, b);
+        own += s.work;
+        if (s.bad && blockIdx.x == 0) latch(j.err, SV_ERR_DEVICE_BOUNDS);
+    }
+    long long run = own;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long a = __shfl_up_sync(0xFFFFFFFFu, run, k);
+        if (lane >= k) run += a;
+    }
+    if (lane == 31) sh->scan[warp] = run;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kAtThreads / 32; ++w) {
+        if (w < warp) run += sh->scan[w];
+        total += sh->scan[w];
+    }
+    const int ctas = gridDim.x;
+    const int me = blockIdx.x;
+    const long long from = span_at(total, ctas, me), to = span_at(total, ctas, me + 1);
+    if (from < to && run > from && run - own <= from) {
+        long long x = from - (run - own);
+        int b = b0;
+        for (;; ++b) {
+            const long long w = seq_work(j, b).work;
+            if (x < w) break;
+            x -= w;
+        }
+        sh->first_b = b;
+        sh->first_x = x;
+    }
+    if (tid == 0) sh->total = total;
+    __syncthreads();
+
+    attend_roles<D, false>(j, map_k, map_v, sh, base, sh->first_b, sh->first_x, from, to, 0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (__builtin_expect(sh->abort == kGaveUp, 0)) {
+        const uint32_t pieces = sh->far.pieces;
+        __syncthreads();
+        if (tid == 0) sh->abort = 0;
+        __syncthreads();
+        if (warp < kSoftWarps)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegs));
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtRegs));
+        attend_rounds<D>(&j, &map_k, &map_v, sh, base, to, pieces);
     }
     tc_fence_before();
     __syncthreads();

@@ -452,7 +452,11 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  *     j where bit j % 32 of word j / 32 of its row is set (draft trees; a
  *     token's own bit counts like any other).
  *   out [T, Hq, D] bf16 (16-byte aligned) = softmax(scale q.k) v; 0 where a
- *     token sees nothing.  Softmax and sums are fp32.
+ *     token sees nothing.  Scores, maxima and sums are fp32.  For the products a
+ *     query is held exactly down to 2^-17 of its largest element, and a weight to
+ *     2^-8 of itself, down to 2^-17.5 of the row's largest product of a weight and
+ *     a value scale, among pages whose value scales are less than 2^6 apart.
+ *     (Pages of scales further apart are taken apart; that takes longer.)
  *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
  *     where a token sees nothing.
  *   A row whose query holds NaN or an infinity is NaN (out and lse).
