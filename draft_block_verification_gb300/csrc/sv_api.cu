@@ -958,10 +958,13 @@ sv_status sv_kv_plan(sv_handle *h, int B, int block, int cols, int ring, int max
         (B > 0 && (!cached_len || !new_len || !held || !table || !kv_len || !held_out)) ||
         (max_tokens > 0 && (!slot || !pos)))
         return SV_ERR_INVALID_ARG;
-    // these are read by every CTA while others write the outputs
-    if (free_pos_out == free_pos || (B > 0 && (held_out == held || kv_len == cached_len)))
-        return SV_ERR_INVALID_ARG;
     if (B > kPlanMaxB) return SV_ERR_UNSUPPORTED;
+    // every CTA reads the inputs while others write the outputs
+    const void *const in[] = {cached_len, new_len, held, free_pos, free_ids, table};
+    const void *const out[] = {kv_len, cu_new, held_out, free_pos_out, slot, pos};
+    for (const void *o : out)
+        for (const void *i : in)
+            if (o && o == i) return SV_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_plan")) return fi;
     PlanJob j = {B, block, cols, ring, max_tokens, cached_len, new_len, held, free_pos, free_ids,

@@ -407,8 +407,8 @@ sv_status sv_packed_anyorder_step(sv_handle *h, const void *logits, sv_dtype dty
  *   b, then position; -1 beyond cu_new[B].
  *   table (in place): entries [held, w) are written; those from w on are dead.
  *   free_ids (in place): written only outside the queue.
- * held_out, free_pos_out and kv_len must not be held, free_pos and cached_len
- * themselves.  So a call whose outputs were dropped may be repeated.
+ * None of kv_len to pos may be an input's address, table and free_ids among them
+ * (SV_ERR_INVALID_ARG).  So a call whose outputs were dropped may be repeated.
  * A call that cannot be served changes nothing (outputs: kv_len = cached_len,
  * held_out = held, free_pos_out = free_pos, cu_new = 0, slot = pos = -1) and
  * latches SV_ERR_OOM (too few free pages) or SV_ERR_DEVICE_BOUNDS (a negative
