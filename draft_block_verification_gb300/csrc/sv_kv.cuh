@@ -13,7 +13,7 @@
 
 namespace sv {
 
-constexpr int kPlanMaxB = 16384;  // sequences of one plan (two shared words each)
+constexpr int kPlanMaxB = 16384;  // sequences of one plan (three shared words each)
 
 struct PlanJob {
     int B, block, cols, ring, cap;

@@ -20,8 +20,9 @@
 // The cache's bytes go from TMA to the tensor cores untouched (e4m3); so the
 // other operand is e4m3 as well, in two parts.  A bf16 query (8 significant
 // bits, scaled by a power of two per row) is the sum of two e4m3 values (4 bits
-// each): q = hi + lo exactly, up to 2^-19 of the row's largest element.  A
-// weight p is rounded to hi + lo with a relative error of 2^-8 at most (2^-10.5
+// each): q = hi + lo exactly, up to 2^-17 of the row's largest element (which is
+// brought to [128, 256); the least step of e4m3 is 2^-9).  A weight p is rounded
+// to hi + lo with a relative error of 2^-8 and the 2^-11 of fp16 at most (2^-10.5
 // in the mean square, under the output's own rounding to bf16), down to a step
 // of 2^-16.5 of the weight at the running maximum; lo carries a scale of its own
 // and accumulates apart.  Sums, maxima and the rescaling are fp32.
@@ -47,12 +48,13 @@
 // workspace; the last of them to finish joins them in the order of the CTAs, so
 // the result does not depend on who that is.
 //
-// Measured at D = 128, 8 cache heads, 4 query heads each: a tile of 32 KB takes
-// 0.70 us on an SM for up to 32 rows (7.1 TB/s over all, the copy rate), 0.80
-// for 48, 0.87 for 64, 1.33 for 96, 1.65 for 128, where the softmax warps bound
-// it; a unit some 7 us more (queries, the first tiles' maxima, the output).
-// 128 single tokens over 4,096 to 8,192 take 300 us (5.4 TB/s, 80% of the copy
-// rate), 64 draft blocks of 9 to 17 over 2,048 to 4,096 195 us.
+// Measured at D = 128, 8 cache heads, 4 query heads each, equal lengths: a tile
+// of 32 KB takes 0.76 us on an SM for up to 32 rows (6.5 TB/s over all), 0.85 for
+// 48, 0.90 for 64, 1.31 for 96, 1.65 for 128, where the softmax warps bound it; a
+// unit 7 to 10 us more up to 32 rows, 12 to 20 above (queries, the first tiles'
+// maxima, new tokens, the output), and a call some 12.  128 single tokens over
+// 4,096 to 8,192 take 314 us (5.2 TB/s, 76% of the copy rate), 64 draft blocks of
+// 9 to 17 over 2,048 to 4,096 208 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -110,7 +112,8 @@ __device__ __forceinline__ int round_rows(int rows)
 // Time of a tile by its rows, as measured: even spans of it are even in time.
 __device__ __forceinline__ int tile_cost(int N)
 {
-    // in units of 0.04 us (152 units of 4,096 and 16,384 tokens, D = 128)
+    // in units of 0.04 us (152 units of 4,096 and 16,384 tokens, D = 128; a unit's
+    // start and end, 7 to 20 us, are not in it)
     return N <= 32 ? 18 : N <= 48 ? 20 : N <= 64 ? 22 : N <= 96 ? 34 : 42;
 }
 
@@ -299,7 +302,6 @@ __device__ __forceinline__ void tc_st8(uint32_t addr, const float *v)
                  "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
                  : "memory");
 }
-// The registers of the loads before it may be read after it: they pass through.
 __device__ __forceinline__ void tc_ld4(uint32_t addr, float *v)
 {
     uint32_t r[4];
@@ -309,6 +311,7 @@ __device__ __forceinline__ void tc_ld4(uint32_t addr, float *v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
+// The registers of the loads before it may be read after it: they pass through.
 template <int N>
 __device__ __forceinline__ void tc_wait_ld(float (&v)[N])
 {

@@ -182,7 +182,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanJob j)
     }
 }
 
-static size_t plan_smem(int B) { return (size_t)B * 3 * sizeof(int32_t); }
+constexpr size_t plan_smem(int B) { return (size_t)B * 3 * sizeof(int32_t); }
+static_assert(plan_smem(kPlanMaxB) + sizeof(PlanSums) * (kPlanThreads / 32) <= 227 * 1024,
+              "a plan's sums fit the shared memory");
 
 cudaError_t plan_setup()
 {

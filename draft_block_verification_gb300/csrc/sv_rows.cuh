@@ -6,7 +6,7 @@
 
 namespace sv {
 
-constexpr int kRowsMaxV = 1 << 20;  // ids of a row (4096 blocks of 256 in shared memory)
+constexpr int kRowsMaxV = 1 << 20;  // ids of a row (1,024 blocks of 1,024 in shared memory)
 
 struct RowsJob {
     const char *x;             // logits, rs bytes from row to row

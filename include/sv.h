@@ -454,7 +454,7 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  *   out [T, Hq, D] bf16 (16-byte aligned) = softmax(scale q.k) v; 0 where a
  *     token sees nothing.  Scores, maxima and sums are fp32.  For the products a
  *     query is held exactly down to 2^-17 of its largest element, and a weight to
- *     2^-8 of itself, down to 2^-17.5 of the row's largest product of a weight and
+ *     2^-8 + 2^-11 of itself, down to 2^-17.5 of the row's largest product of a weight and
  *     a value scale, among pages whose value scales are less than 2^6 apart.
  *     (Pages of scales further apart are taken apart; that takes longer.)
  *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
