@@ -456,7 +456,8 @@ sv_status sv_kv_append(sv_handle *h, const void *k, const void *v, sv_dtype dtyp
  *     query is held exactly down to 2^-17 of its largest element, and a weight to
  *     2^-8 + 2^-11 of itself, down to 2^-17.5 of the row's largest product of a weight and
  *     a value scale, among pages whose value scales are less than 2^6 apart.
- *     (Pages of scales further apart are taken apart; that takes longer.)
+ *     (Pages of scales further apart are taken apart; that takes longer.  Products
+ *     below 2^-126 of the row's largest count as 0.)
  *   lse [T, Hq] fp32 or NULL: natural log of the sum of exponentials, -inf
  *     where a token sees nothing.
  *   A row whose query holds NaN or an infinity is NaN (out and lse).
