@@ -88,6 +88,18 @@ def lib():
         L.sv_kv_attention.restype = i32
         L.sv_kv_attention.argtypes = ([vp] * 2 + [i64] * 2 + [i32] * 4 + [vp] * 4 + [i32] * 2 +
                                       [vp, i32] + [vp] * 2 + [i32, vp, i32, f32] + [vp] * 3)
+        L.sv_kv_prefix_work_bytes.restype = C.c_size_t
+        L.sv_kv_prefix_work_bytes.argtypes = [vp] + [i32] * 6
+        L.sv_kv_prefix_attention.restype = i32
+        L.sv_kv_prefix_attention.argtypes = (
+            [vp] * 2 + [i64] * 2 + [i32] * 4 + [vp] * 4 + [i32] * 2 + [vp, i32] + [vp] * 2 +
+            [i32] + [vp] * 2 + [i32, vp, i32, f32] + [vp] * 3 + [C.c_size_t, vp])
+        L.sv_kv_read.restype = i32
+        L.sv_kv_read.argtypes = ([vp] * 5 + [i32] * 4 + [vp, i32] + [vp] * 2 + [i32] * 2 +
+                                 [vp] * 2 + [i32] + [i64] * 4 + [vp])
+        L.sv_qk_norm_rope.restype = i32
+        L.sv_qk_norm_rope.argtypes = ([vp] * 3 + [i32] + [i64] * 4 + [i32] * 4 + [vp] * 2 +
+                                      [f32, vp] + [i32] * 2 + [vp] * 3 + [i32] + [i64] * 4 + [vp])
         L.sv_sample_rows.restype = i32
         L.sv_sample_rows.argtypes = [vp, vp, i32, i64, i32, i32] + [vp] * 9
         _lib = L
@@ -581,6 +593,147 @@ def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new
         out["lse"].data_ptr() if want_lse else None, raw),
         "sv_kv_attention")
     return out
+
+
+def sv_kv_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new,
+                           prefix_len=None, *, cu_group=None, scale=None, mask=None,
+                           want_lse=False, handle=None, stream=None):
+    """sv_kv_attention for sequences that share a prefix, whose pages are read
+    once for all (see sv.h): sequences cu_group[g] .. cu_group[g + 1] - 1
+    ([groups + 1] int32; None: all) share at most their first prefix_len[g]
+    tokens ([groups] int32; None: as far as their tables agree).  Returns a
+    dict (out, and lse)."""
+    dev = _cuda(q, "q")
+    (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+        raise ValueError("q must be a bfloat16 [T, Hq, D] tensor with the cache's D, contiguous "
+                         "in its last dimension")
+    if table.dim() != 2:
+        raise ValueError("table must be [B, cols]")
+    T, Hq, _ = q.shape
+    B, cols = kv_len.shape[0], table.shape[1]
+    i32 = torch.int32
+    if cu_group is not None and (cu_group.dim() != 1 or cu_group.shape[0] < 2):
+        raise ValueError("cu_group must be [groups + 1]")
+    groups = 1 if cu_group is None else cu_group.shape[0] - 1
+    words = 0
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError("mask must be [T, words]")
+        words = mask.shape[1]
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
+    ptr, raw = _call_on(handle, stream, dev)
+    L = lib()
+    size = L.sv_kv_prefix_work_bytes(ptr, T, Hq, H, D, B, groups)
+    out = {"out": torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)}
+    if want_lse:
+        out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    work = torch.empty(size, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        work.record_stream(stream)
+    _check(L.sv_kv_prefix_attention(
+        ptr, q.data_ptr(), q.stride(0), q.stride(1), T, Hq, H, D, *cache, block, pages,
+        _dense(table, i32, (B, cols), "table", dev), cols,
+        _dense(kv_len, i32, (B,), "kv_len", dev), _dense(cu_new, i32, (B + 1,), "cu_new", dev), B,
+        None if prefix_len is None else _dense(prefix_len, i32, (groups,), "prefix_len", dev),
+        None if cu_group is None else _dense(cu_group, i32, (groups + 1,), "cu_group", dev),
+        groups, None if mask is None else _dense(mask, i32, (T, words), "mask", dev), words,
+        float(D ** -0.5 if scale is None else scale), out["out"].data_ptr(),
+        out["lse"].data_ptr() if want_lse else None, work.data_ptr(), size, raw),
+        "sv_kv_prefix_attention")
+    return out
+
+
+_CODE = {torch.bfloat16: SV_BF16, torch.float32: SV_F32}
+
+
+def _rows_out(t, shape, dtype, dev, name):
+    """A given output of this shape (last dimension contiguous), or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or t.stride(2) != 1:
+        raise ValueError("%s must be a %s tensor of shape %s on %s, contiguous in its last "
+                         "dimension" % (name, dtype, tuple(shape), dev))
+    return t
+
+
+def sv_kv_read(k_cache, v_cache, k_scale, v_scale, table, cu, rows, *, first=None,
+               dtype=torch.bfloat16, out=None, handle=None, stream=None):
+    """Tokens read back from the paged cache (see sv.h): rows cu[b] .. cu[b + 1]
+    - 1 ([B + 1] int32) are positions first[b] on of sequence b (None: 0), in
+    bfloat16 or float32.  rows: the outputs' rows; out: (k, v) [rows, Hkv, D] to
+    write to.  Returns a dict (k, v); rows from cu[B] on are not written."""
+    dev = _cuda(k_cache, "k_cache")
+    (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, cols]")
+    if dtype not in _CODE:
+        raise ValueError("dtype must be bfloat16 or float32")
+    B, cols = table.shape
+    T, i32 = int(rows), torch.int32
+    if T < 0:
+        raise ValueError("rows must not be negative")
+    k, v = (None, None) if out is None else out
+    k = _rows_out(k, (T, H, D), dtype, dev, "k")
+    v = _rows_out(v, (T, H, D), dtype, dev, "v")
+    ptr, raw = _call_on(handle, stream, dev)
+    _check(lib().sv_kv_read(
+        ptr, *cache, H, D, block, pages, _dense(table, i32, (B, cols), "table", dev), cols,
+        None if first is None else _dense(first, i32, (B,), "first", dev),
+        _dense(cu, i32, (B + 1,), "cu", dev), B, T, k.data_ptr(), v.data_ptr(), _CODE[dtype],
+        k.stride(0), k.stride(1), v.stride(0), v.stride(1), raw), "sv_kv_read")
+    return {"k": k, "v": v}
+
+
+def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
+                    interleaved=False, dtype=None, out=None, handle=None, stream=None):
+    """Norms of queries and keys for each head, and the rotation by position, in
+    one pass (see sv.h): q [T, Hq, D] and k [T, Hkv, D] (bfloat16 or float32, one
+    of them may be None), pos [T] int32 (negative: the row is skipped), inv_freq
+    [rot / 2] float32 (None: no rotation), weights [D] float32 (None: no norm).
+    dtype: of the outputs (None: the inputs'); out: (q, k) to write to, which may
+    be the inputs.  Returns a dict (q, k)."""
+    x = k if q is None else q
+    dev = _cuda(x, "k" if q is None else "q")
+    if x.dim() != 3 or x.dtype not in _CODE:
+        raise ValueError("q and k must be bfloat16 or float32 tensors [T, heads, D]")
+    T, _, D = x.shape
+    if dtype is None:
+        dtype = x.dtype
+    elif dtype not in _CODE:
+        raise ValueError("dtype must be bfloat16 or float32")
+    o = (None, None) if out is None else out
+    heads, src, dst, ins, outs = [], [], [], [], []
+    res = {}
+    for t, to, name in ((q, o[0], "q"), (k, o[1], "k")):
+        if t is None:
+            heads.append(0), src.append(None), dst.append(None)
+            ins += (0, 0)
+            outs += (0, 0)
+            res[name] = None
+            continue
+        if t is not x and (t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or
+                           t.dtype is not x.dtype or t.device != dev):
+            raise ValueError("q and k must have one T, D, type and device")
+        if t.stride(2) != 1:
+            raise ValueError("%s: the last dimension must be contiguous" % name)
+        y = res[name] = _rows_out(to, t.shape, dtype, dev, name + " of out")
+        heads.append(t.shape[1]), src.append(t.data_ptr()), dst.append(y.data_ptr())
+        ins += (t.stride(0), t.stride(1))
+        outs += (y.stride(0), y.stride(1))
+    f32, rot = torch.float32, 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.shape[0]
+        inv_freq = _dense(inv_freq, f32, (rot // 2,), "inv_freq", dev)
+    w = [None if t is None else _dense(t, f32, (D,), n, dev)
+         for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    ptr, raw = _call_on(handle, stream, dev)
+    _check(lib().sv_qk_norm_rope(
+        ptr, *src, _CODE[x.dtype], *ins, T, *heads, D, *w, float(eps), inv_freq, rot,
+        1 if interleaved else 0, _dense(pos, torch.int32, (T,), "pos", dev), *dst, _CODE[dtype],
+        *outs, raw), "sv_qk_norm_rope")
+    return res
 
 
 def sv_sample_rows(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -324,6 +324,26 @@ bool kv_cache_ok(const void *cache, const float *scale)
     return cache && scale && aligned16(cache);
 }
 
+// sv_kv_prefix_attention's workspace: byte offsets, and its size.
+struct PrefixSpace {
+    size_t counters, attend, skip, group, far_ms, far_o, part, bytes;
+    int64_t units;  // at most
+    PrefixSpace(int sms, int T, int Hq, int H, int D, int B, int groups)
+    {
+        auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+        const int64_t rows = (int64_t)T * (Hq / H);
+        units = H * (rows / kPrefixRows + std::min<int64_t>(groups, std::min(B, T)));
+        counters = 0;
+        attend = counters + up(attend_counter_bytes(sms));
+        skip = attend + up(attend_ws_bytes(sms));
+        group = skip + up((size_t)B * sizeof(int32_t));
+        far_ms = group + up(((size_t)groups + 1) * sizeof(PrefixGroup));
+        far_o = far_ms + up((size_t)T * Hq * sizeof(float2));
+        part = far_o + up((size_t)T * Hq * D * sizeof(float));
+        bytes = part + prefix_part_bytes(sms, units, D);
+    }
+};
+
 void fill_common(Job &j, sv_handle *h, const void *src0, sv_dtype dt, int64_t rs, int V)
 {
     memset(&j, 0, sizeof j);
@@ -478,6 +498,8 @@ sv_status sv_create(sv_handle **out)
     if (e == cudaSuccess) e = plan_setup();
     if (e == cudaSuccess) e = rows_setup();
     if (e == cudaSuccess) e = attend_setup();
+    if (e == cudaSuccess) e = attend_far_setup();
+    if (e == cudaSuccess) e = prefix_setup();
     if (e == cudaSuccess) e = cudaMalloc(&h->d_err, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_ctl, C_NCTL * sizeof(unsigned));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_gtab, kGTab * sizeof(float));
@@ -1032,8 +1054,147 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
                    {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
                    {k_scale, v_scale}, table, kv_len, cu_new, mask, B, T, Hq, H, Hq / H, D,
                    block, pages, cols, mask_words, scale, (uint16_t *)out, lse,
-                   (float *)(ws + attend_counter_bytes(h->sms)), (unsigned *)ws, h->d_err};
+                   nullptr, nullptr, nullptr, (float *)(ws + attend_counter_bytes(h->sms)), (unsigned *)ws, h->d_err};
     return cuda_status(attend_launch(j, h->sms, s));
+}
+
+size_t sv_kv_prefix_work_bytes(const sv_handle *h, int T, int Hq, int H, int D, int B, int groups)
+{
+    if (!h || T < 0 || B < 0 || Hq < 1 || H < 1 || Hq % H || groups < 1 || (D != 64 && D != 128))
+        return 0;
+    return PrefixSpace(h->sms, T, Hq, H, D, B, groups).bytes;
+}
+
+sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_stride,
+                                 int64_t q_head_stride, int T, int Hq, int H, int D,
+                                 const void *k_cache, const void *v_cache, const float *k_scale,
+                                 const float *v_scale, int block, int pages,
+                                 const int32_t *table, int cols, const int32_t *kv_len,
+                                 const int32_t *cu_new, int B, const int32_t *prefix_len,
+                                 const int32_t *cu_group, int groups, const uint32_t *mask,
+                                 int mask_words, float scale, void *out, float *lse, void *work,
+                                 size_t work_bytes, void *stream)
+{
+    if (!h || T < 0 || B < 0 || Hq < 1 || H < 1 || Hq % H || pages < 1 || cols < 1 ||
+        !kv_block_ok(block) || groups < 1 || (!cu_group && groups != 1))
+        return SV_ERR_INVALID_ARG;
+    if (!isfinite(scale) || q_token_stride < 0 || q_head_stride < 0 ||
+        (mask && mask_words < 1))
+        return SV_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SV_ERR_UNSUPPORTED;
+    if ((int64_t)T * Hq > 0x7FFFFFFF || (int64_t)pages * block > 0x7FFFFFFF ||
+        (int64_t)cols * block > 0x7FFFFFFF || (int64_t)pages * H > 0x7FFFFFFF)
+        return SV_ERR_UNSUPPORTED;
+    if (!kv_cache_ok(k_cache, k_scale) || !kv_cache_ok(v_cache, v_scale))
+        return SV_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return SV_OK;
+    if (!q || !table || !kv_len || !cu_new || !out || (uintptr_t)q % 2 || !aligned16(out) ||
+        !work || !aligned16(work))
+        return SV_ERR_INVALID_ARG;
+    const PrefixSpace w(h->sms, T, Hq, H, D, B, groups);
+    if (w.units > kPrefixMaxUnits) return SV_ERR_UNSUPPORTED;
+    if (work_bytes < w.bytes) return SV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_kv_prefix_attention")) return fi;
+    cudaStream_t s = (cudaStream_t)stream;
+    char *ws = (char *)work;
+    PrefixJob p = {(const uint16_t *)q, q_token_stride, q_head_stride,
+                   {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
+                   {k_scale, v_scale}, table, kv_len, cu_new, prefix_len, cu_group, B, T, Hq, H,
+                   Hq / H, D, block, pages, cols, groups, scale, (uint16_t *)out, lse,
+                   (int32_t *)(ws + w.skip), (PrefixGroup *)(ws + w.group),
+                   (const float *)(ws + w.far_o), (const float2 *)(ws + w.far_ms),
+                   (float *)(ws + w.part), h->d_err};
+    AttendJob j = {p.q, p.qts, p.qhs, {p.cache[0], p.cache[1]}, {k_scale, v_scale}, table, kv_len,
+                   cu_new, mask, B, T, Hq, H, Hq / H, D, block, pages, cols, mask_words, scale,
+                   p.out, lse, p.skip, (float *)(ws + w.far_o), (float2 *)(ws + w.far_ms),
+                   (float *)(ws + w.attend), (unsigned *)(ws + w.counters), h->d_err};
+    cudaError_t e = prefix_prep_launch(p, j.arrived,
+                                       (int)(attend_counter_bytes(h->sms) / sizeof(unsigned)), s);
+    if (e == cudaSuccess) e = attend_far_launch(j, h->sms, s);
+    if (e == cudaSuccess) e = prefix_launch(p, h->sms, w.units, s);
+    return cuda_status(e);
+}
+
+sv_status sv_kv_read(sv_handle *h, const void *k_cache, const void *v_cache,
+                     const float *k_scale, const float *v_scale, int H, int D, int block,
+                     int pages, const int32_t *table, int cols, const int32_t *first,
+                     const int32_t *cu, int B, int T, void *k, void *v, sv_dtype dtype,
+                     int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                     int64_t v_head_stride, void *stream)
+{
+    if (!h || T < 0 || B < 0 || H < 1 || pages < 1 || cols < 1 || !kv_block_ok(block))
+        return SV_ERR_INVALID_ARG;
+    if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return SV_ERR_UNSUPPORTED;
+    if (H > 32767 || (int64_t)pages * block > 0x7FFFFFFF || (int64_t)cols * block > 0x7FFFFFFF)
+        return SV_ERR_UNSUPPORTED;
+    if (!kv_cache_ok(k_cache, k_scale) || !kv_cache_ok(v_cache, v_scale))
+        return SV_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return SV_OK;
+    const int esz = dtype == SV_BF16 ? 2 : 4;
+    if (!table || !cu || !k || !v || (uintptr_t)k % esz || (uintptr_t)v % esz ||
+        k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+        return SV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_kv_read")) return fi;
+    ReadJob j = {{(const uint8_t *)k_cache, (const uint8_t *)v_cache},
+                 {k_scale, v_scale}, table, first, cu, B, T, H, D, block, pages, cols, dtype,
+                 {(char *)k, (char *)v},
+                 {k_token_stride * esz, v_token_stride * esz},
+                 {k_head_stride * esz, v_head_stride * esz}, h->d_err};
+    return cuda_status(read_launch(j, h->sms, (cudaStream_t)stream));
+}
+
+sv_status sv_qk_norm_rope(sv_handle *h, const void *q, const void *k, sv_dtype dtype,
+                          int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                          int64_t k_head_stride, int T, int Hq, int H, int D,
+                          const float *q_weight, const float *k_weight, float eps,
+                          const float *inv_freq, int rot, int interleaved, const int32_t *pos,
+                          void *q_out, void *k_out, sv_dtype out_dtype,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride,
+                          int64_t k_out_token_stride, int64_t k_out_head_stride, void *stream)
+{
+    if (!h || T < 0 || Hq < 0 || H < 0 || D < 2 || D % 2 || rot < 0 || rot % 2 || rot > D)
+        return SV_ERR_INVALID_ARG;
+    if ((dtype != SV_F32 && dtype != SV_BF16) || (out_dtype != SV_F32 && out_dtype != SV_BF16) ||
+        !(eps >= 0.f) || !isfinite(eps))
+        return SV_ERR_INVALID_ARG;
+    if (D > kRopeMaxD || Hq > (1 << 20) || H > (1 << 20) ||
+        (int64_t)T * ((int64_t)Hq + H) > 0x7FFFFFFF)
+        return SV_ERR_UNSUPPORTED;
+    if (T == 0 || (Hq == 0 && H == 0)) return SV_OK;
+    if (!pos || (rot > 0 && !inv_freq)) return SV_ERR_INVALID_ARG;
+    const int is = dtype == SV_BF16 ? 2 : 4, os = out_dtype == SV_BF16 ? 2 : 4;
+    const struct {
+        int heads;
+        const void *in;
+        void *out;
+        int64_t ts, hs, ots, ohs;
+    } side[2] = {{Hq, q, q_out, q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride},
+                 {H, k, k_out, k_token_stride, k_head_stride, k_out_token_stride, k_out_head_stride}};
+    for (const auto &x : side) {
+        if (!x.heads) continue;
+        if (!x.in || !x.out || (uintptr_t)x.in % is || (uintptr_t)x.out % os || x.ts < 0 ||
+            x.hs < 0 || x.ots < 0 || x.ohs < 0)
+            return SV_ERR_INVALID_ARG;
+        // rows that several outputs share
+        if ((T > 1 && x.ots == 0) || (x.heads > 1 && x.ohs == 0)) return SV_ERR_INVALID_ARG;
+        // in place: row by row
+        if (x.in == x.out && (is != os || x.ts != x.ots || x.hs != x.ohs)) return SV_ERR_INVALID_ARG;
+    }
+    if (Hq && H && (q_out == k_out || q_out == k || k_out == q)) return SV_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(h->mu);
+    if (sv_status fi = fault_injected("sv_qk_norm_rope")) return fi;
+    RopeJob j = {{(const char *)q, (const char *)k},
+                 {(char *)q_out, (char *)k_out},
+                 {q_token_stride * is, k_token_stride * is},
+                 {q_head_stride * is, k_head_stride * is},
+                 {q_out_token_stride * os, k_out_token_stride * os},
+                 {q_out_head_stride * os, k_out_head_stride * os},
+                 dtype, out_dtype, T, Hq, H, D, rot, interleaved != 0, {q_weight, k_weight},
+                 inv_freq, eps, pos};
+    return cuda_status(rope_launch(j, (cudaStream_t)stream));
 }
 
 sv_status sv_sample_rows(sv_handle *h, const void *logits, sv_dtype dtype, int64_t row_stride,

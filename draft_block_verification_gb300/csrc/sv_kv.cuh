@@ -1,6 +1,7 @@
 // sv_kv.cuh -- jobs of the paged 8-bit key/value cache: the plan that gives
-// new tokens their places, the append that writes them, and the attention
-// that reads the cache.
+// new tokens their places, the append that writes them, the attention that
+// reads the cache, alone or for a batch that shares a prefix, and reading it
+// back; and of the norms and rotation of queries and keys before them.
 //
 // The cache.  Keys and values are held apart, each as [pages, Hkv, block, D]
 // bytes (e4m3) with one fp32 scale for each page and head, [pages, Hkv]: the
@@ -51,6 +52,12 @@ struct AttendJob {
     float softmax_scale;
     uint16_t *out;             // [T, Hq, D]
     float *lse;                // [T, Hq] or null
+    // attend_far: for each sequence the pages at its front that another kernel
+    // reads; rows of such sequences leave their sums (before the division) and the
+    // maximum and sum of weights here, in place of out and lse
+    const int32_t *skip;
+    float *far_o;              // [T, Hq, D]
+    float2 *far_ms;            // [T, Hq]
     float *part;               // partial sums of shared units (workspace)
     unsigned *arrived;         // a counter a CTA, zero between calls
     int *err;
@@ -59,5 +66,65 @@ size_t attend_ws_bytes(int sms);       // partial sums
 size_t attend_counter_bytes(int sms);  // counters, before them
 cudaError_t attend_setup();
 cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s);
+cudaError_t attend_far_setup();
+cudaError_t attend_far_launch(const AttendJob &j, int sms, cudaStream_t s);
+
+// A group's shared pages and where its work starts (sv_kvprefix.cu); an entry more
+// than there are groups, with the totals.
+struct PrefixGroup {
+    int first, rows;           // first row of q, query rows a cache head
+    int pages, lead;           // shared, as the table row of this sequence has them
+    long long start;           // in tiles of slots
+    int unit0, pad;
+};
+struct PrefixJob {
+    const uint16_t *q;         // [T, Hq, D] bf16
+    int64_t qts, qhs;          // strides, elements
+    const uint8_t *cache[2];
+    const float *scale[2];
+    const int32_t *table, *kv_len, *cu;
+    const int32_t *prefix_len; // [groups] or null
+    const int32_t *cu_group;   // [groups + 1], or null: one group
+    int B, T, Hq, H, G, D, block, pages, cols, groups;
+    float softmax_scale;
+    uint16_t *out;             // [T, Hq, D]
+    float *lse;                // [T, Hq] or null
+    int32_t *skip;             // [B] shared pages
+    PrefixGroup *group;        // [groups + 1]
+    const float *far_o;        // what attend left
+    const float2 *far_ms;
+    float *part;               // pieces' sums
+    int *err;
+};
+constexpr int kPrefixRows = 256;                             // query rows of a unit
+constexpr int64_t kPrefixMaxUnits = 1 << 24;
+size_t prefix_part_bytes(int sms, int64_t units, int D);
+cudaError_t prefix_setup();
+cudaError_t prefix_prep_launch(const PrefixJob &j, unsigned *counters, int n, cudaStream_t s);
+cudaError_t prefix_launch(const PrefixJob &j, int sms, int64_t units, cudaStream_t s);
+
+struct RopeJob {
+    const char *src[2];        // queries [T, Hq, D], keys [T, H, D]
+    char *dst[2];
+    int64_t ts[2], hs[2], ots[2], ohs[2];  // token and head strides, bytes
+    int dtype, odtype, T, Hq, H, D, rot, inter;
+    const float *weight[2];    // [D] or null
+    const float *inv_freq;     // [rot / 2]
+    float eps;
+    const int32_t *pos;        // [T], negative: skipped
+};
+constexpr int kRopeMaxD = 512;
+cudaError_t rope_launch(const RopeJob &j, cudaStream_t s);
+
+struct ReadJob {
+    const uint8_t *cache[2];
+    const float *scale[2];
+    const int32_t *table, *first, *cu;  // first: null for 0
+    int B, T, H, D, block, pages, cols, dtype;
+    char *dst[2];              // [T, H, D]
+    int64_t ts[2], hs[2];      // strides, bytes
+    int *err;
+};
+cudaError_t read_launch(const ReadJob &j, int sms, cudaStream_t s);
 
 }  // namespace sv

@@ -50,7 +50,8 @@
  *   sv_verify_greedy_static, sv_verify_sample, sv_verify_tree,
  *   sv_verify_spot, sv_packed_step, sv_packed_topk_step,
  *   sv_packed_anyorder_step, sv_kv_plan, sv_kv_append, sv_kv_attention,
- *   sv_sample_rows) return the
+ *   sv_kv_prefix_attention, sv_kv_read, sv_qk_norm_rope, sv_sample_rows)
+ *   return the
  *   status `code` (1..6) at its launch point,
  *   after its argument checks and before anything is enqueued.  It is read
  *   at every call; unset, nothing is injected.
@@ -58,6 +59,7 @@
 #ifndef SV_H
 #define SV_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -482,6 +484,87 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
                           int cols, const int32_t *kv_len, const int32_t *cu_new, int B,
                           const uint32_t *mask, int mask_words, float scale, void *out,
                           float *lse, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_kv_prefix_attention.  sv_kv_attention for sequences that share a prefix
+ * (one prompt before all of them, say): the shared pages are read once for the
+ * queries of all.  Arguments, out and lse as there; and
+ *   cu_group [groups + 1]: sequences cu_group[g] .. cu_group[g + 1] - 1 are a
+ *     group (in order, each in one group at most), or NULL (groups = 1): all.
+ *   prefix_len [groups]: a group shares its first prefix_len[g] tokens at most,
+ *     or NULL: no bound.
+ *   Shared are the leading pages that the table has alike for all sequences of
+ *   the group with new tokens, wholly within prefix_len[g] and within the tokens
+ *   before each sequence's new ones.  So the result does not depend on cu_group
+ *   and prefix_len; they say where to look.  Groups that share nothing, and
+ *   sequences of no group, go the way of sv_kv_attention.
+ *   Precision: as sv_kv_attention; on the shared pages a weight is held to 2^-8
+ *   of itself and scales may lie any distance apart.
+ *   work: device memory of the caller, 16-byte aligned, of the size that
+ *     sv_kv_prefix_work_bytes tells for these sizes (0 for sizes that the call
+ *     refuses).  Its content is of no consequence before and after; calls that
+ *     may run at the same time, captured ones among them, need one each.
+ * Errors: SV_ERR_INVALID_ARG (too small a workspace among them);
+ * SV_ERR_UNSUPPORTED (D; sizes beyond 32 bits); latched SV_ERR_DEVICE_BOUNDS as
+ * sv_kv_attention, and for groups out of order or range (nothing is shared
+ * then).
+ * ------------------------------------------------------------------------- */
+size_t sv_kv_prefix_work_bytes(const sv_handle *h, int T, int Hq, int H, int D, int B,
+                               int groups);
+sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_stride,
+                                 int64_t q_head_stride, int T, int Hq, int H, int D,
+                                 const void *k_cache, const void *v_cache, const float *k_scale,
+                                 const float *v_scale, int block, int pages,
+                                 const int32_t *table, int cols, const int32_t *kv_len,
+                                 const int32_t *cu_new, int B, const int32_t *prefix_len,
+                                 const int32_t *cu_group, int groups, const uint32_t *mask,
+                                 int mask_words, float scale, void *out, float *lse, void *work,
+                                 size_t work_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_kv_read.  Tokens read back from the cache: rows cu[b] .. cu[b + 1] - 1 of
+ * k, v [T, H, D] (fp32 or bf16, strides in elements, D contiguous) become
+ * positions first[b] .. of sequence b (first NULL: 0): each byte's e4m3 value
+ * times its page's and head's scale, rounded once (exact in bf16 where the scale
+ * is a power of two).  NaN stays NaN.  Rows from cu[B] on are not written.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D, H > 32767); rows whose
+ * position or page is out of range latch SV_ERR_DEVICE_BOUNDS and are not
+ * written.
+ * ------------------------------------------------------------------------- */
+sv_status sv_kv_read(sv_handle *h, const void *k_cache, const void *v_cache,
+                     const float *k_scale, const float *v_scale, int H, int D, int block,
+                     int pages, const int32_t *table, int cols, const int32_t *first,
+                     const int32_t *cu, int B, int T, void *k, void *v, sv_dtype dtype,
+                     int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                     int64_t v_head_stride, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * sv_qk_norm_rope.  What comes between a projection and the cache: norms of
+ * queries and keys for each head, and the rotation by position.  q [T, Hq, D],
+ * k [T, H, D] (fp32 or bf16, strides in elements, D contiguous and even, at most
+ * 512; Hq or H may be 0), outputs alike (of out_dtype).  Of each head x:
+ *   x'_d = x_d w_d / sqrt(mean(x^2) + eps), w = q_weight or k_weight [D] (NULL:
+ *     x' = x);
+ *   pairs (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) with `interleaved`,
+ *     i < rot / 2, are turned by t = pos[token] inv_freq[i]:
+ *     y_a = x'_a cos t - x'_b sin t,  y_b = x'_b cos t + x'_a sin t;
+ *   elements from rot on (rot even, 0 to D) are x'.
+ * In fp32, rounded once to the outputs' type; an angle is right to 2^-32 of a
+ * turn for |inv_freq| < 2 at any position.  (Squares are summed in fp32: heads
+ * beyond 2^60 need no norm.)
+ * A token with a negative position is skipped (sv_kv_plan's padding).  An output
+ * may be its input, with the same type and strides; other overlaps may not be.
+ * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D > 512, T (Hq + H) beyond
+ * 2^31 - 1).
+ * ------------------------------------------------------------------------- */
+sv_status sv_qk_norm_rope(sv_handle *h, const void *q, const void *k, sv_dtype dtype,
+                          int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                          int64_t k_head_stride, int T, int Hq, int H, int D,
+                          const float *q_weight, const float *k_weight, float eps,
+                          const float *inv_freq, int rot, int interleaved, const int32_t *pos,
+                          void *q_out, void *k_out, sv_dtype out_dtype,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride,
+                          int64_t k_out_token_stride, int64_t k_out_head_stride, void *stream);
 
 /* ---------------------------------------------------------------------------
  * sv_sample_rows.  One draw from each of R logit rows (any V <= 2^20, any row
