@@ -14,8 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(HERE, "_lib")
 LIBPATH = os.path.join(LIBDIR, "libsv.so")
 SOURCES = ["sv_pass.cu", "sv_post.cu", "sv_api.cu", "sv_selftest.cu", "sv_static.cu",
-           "sv_topk.cu", "sv_kvplan.cu", "sv_kvattn.cu", "sv_rows.cu", "sv_kvfar.cu",
-           "sv_kvprefix.cu", "sv_kvread.cu", "sv_rope.cu"]
+           "sv_topk.cu", "sv_kvplan.cu", "sv_kvattn.cu", "sv_rows.cu", "sv_kvprefix.cu",
+           "sv_kvtail.cu", "sv_kvread.cu", "sv_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

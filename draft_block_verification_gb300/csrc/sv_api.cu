@@ -326,21 +326,22 @@ bool kv_cache_ok(const void *cache, const float *scale)
 
 // sv_kv_prefix_attention's workspace: byte offsets, and its size.
 struct PrefixSpace {
-    size_t counters, attend, skip, group, far_ms, far_o, part, bytes;
+    size_t seq, group, arrived, unit_ctas, part_unit, part, tail, bytes;
     int64_t units;  // at most
     PrefixSpace(int sms, int T, int Hq, int H, int D, int B, int groups)
     {
         auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
         const int64_t rows = (int64_t)T * (Hq / H);
         units = H * (rows / kPrefixRows + std::min<int64_t>(groups, std::min(B, T)));
-        counters = 0;
-        attend = counters + up(attend_counter_bytes(sms));
-        skip = attend + up(attend_ws_bytes(sms));
-        group = skip + up((size_t)B * sizeof(int32_t));
-        far_ms = group + up(((size_t)groups + 1) * sizeof(PrefixGroup));
-        far_o = far_ms + up((size_t)T * Hq * sizeof(float2));
-        part = far_o + up((size_t)T * Hq * D * sizeof(float));
-        bytes = part + prefix_part_bytes(sms, units, D);
+        units = std::max(units, std::min<int64_t>(2 * units, sms / 2));  // (of half the rows)
+        seq = 0;  // skip, seq_group, part0 [B], unit0 [B + 1], tail_stages
+        group = seq + up(((size_t)4 * B + 2) * sizeof(int32_t));
+        arrived = group + up(((size_t)groups + 1) * sizeof(PrefixGroup));
+        unit_ctas = arrived + up((size_t)kTailParts * tail_warps(sms) * sizeof(unsigned));
+        part_unit = unit_ctas + up((size_t)units * sizeof(int2));
+        part = part_unit + up((size_t)2 * sms * sizeof(int32_t));
+        tail = part + up(prefix_part_bytes(sms, units, D));
+        bytes = tail + tail_part_bytes(sms, D);
     }
 };
 
@@ -498,8 +499,8 @@ sv_status sv_create(sv_handle **out)
     if (e == cudaSuccess) e = plan_setup();
     if (e == cudaSuccess) e = rows_setup();
     if (e == cudaSuccess) e = attend_setup();
-    if (e == cudaSuccess) e = attend_far_setup();
     if (e == cudaSuccess) e = prefix_setup();
+    if (e == cudaSuccess) e = tail_setup();
     if (e == cudaSuccess) e = cudaMalloc(&h->d_err, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_ctl, C_NCTL * sizeof(unsigned));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_gtab, kGTab * sizeof(float));
@@ -1054,7 +1055,7 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
                    {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
                    {k_scale, v_scale}, table, kv_len, cu_new, mask, B, T, Hq, H, Hq / H, D,
                    block, pages, cols, mask_words, scale, (uint16_t *)out, lse,
-                   nullptr, nullptr, nullptr, (float *)(ws + attend_counter_bytes(h->sms)), (unsigned *)ws, h->d_err};
+                   (float *)(ws + attend_counter_bytes(h->sms)), (unsigned *)ws, h->d_err};
     return cuda_status(attend_launch(j, h->sms, s));
 }
 
@@ -1098,21 +1099,19 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
     if (sv_status fi = fault_injected("sv_kv_prefix_attention")) return fi;
     cudaStream_t s = (cudaStream_t)stream;
     char *ws = (char *)work;
+    int32_t *seq = (int32_t *)(ws + w.seq);
     PrefixJob p = {(const uint16_t *)q, q_token_stride, q_head_stride,
                    {(const uint8_t *)k_cache, (const uint8_t *)v_cache},
-                   {k_scale, v_scale}, table, kv_len, cu_new, prefix_len, cu_group, B, T, Hq, H,
-                   Hq / H, D, block, pages, cols, groups, scale, (uint16_t *)out, lse,
-                   (int32_t *)(ws + w.skip), (PrefixGroup *)(ws + w.group),
-                   (const float *)(ws + w.far_o), (const float2 *)(ws + w.far_ms),
-                   (float *)(ws + w.part), h->d_err};
-    AttendJob j = {p.q, p.qts, p.qhs, {p.cache[0], p.cache[1]}, {k_scale, v_scale}, table, kv_len,
-                   cu_new, mask, B, T, Hq, H, Hq / H, D, block, pages, cols, mask_words, scale,
-                   p.out, lse, p.skip, (float *)(ws + w.far_o), (float2 *)(ws + w.far_ms),
-                   (float *)(ws + w.attend), (unsigned *)(ws + w.counters), h->d_err};
-    cudaError_t e = prefix_prep_launch(p, j.arrived,
-                                       (int)(attend_counter_bytes(h->sms) / sizeof(unsigned)), s);
-    if (e == cudaSuccess) e = attend_far_launch(j, h->sms, s);
-    if (e == cudaSuccess) e = prefix_launch(p, h->sms, w.units, s);
+                   {k_scale, v_scale}, table, kv_len, cu_new, prefix_len, cu_group, mask, B, T,
+                   Hq, H, Hq / H, D, block, pages, cols, groups, mask_words, scale,
+                   (uint16_t *)out, lse, seq, seq + B, seq + (size_t)3 * B, seq + (size_t)2 * B,
+                   seq + (size_t)4 * B + 1, (PrefixGroup *)(ws + w.group),
+                   (unsigned *)(ws + w.arrived), h->sms, (int2 *)(ws + w.unit_ctas),
+                   (int32_t *)(ws + w.part_unit), (float *)(ws + w.part),
+                   (float *)(ws + w.tail), h->d_err};
+    cudaError_t e = prefix_prep_launch(p, h->sms, s);
+    if (e == cudaSuccess) e = prefix_launch(p, h->sms, s);
+    if (e == cudaSuccess) e = tail_launch(p, h->sms, s);
     return cuda_status(e);
 }
 

@@ -52,12 +52,6 @@ struct AttendJob {
     float softmax_scale;
     uint16_t *out;             // [T, Hq, D]
     float *lse;                // [T, Hq] or null
-    // attend_far: for each sequence the pages at its front that another kernel
-    // reads; rows of such sequences leave their sums (before the division) and the
-    // maximum and sum of weights here, in place of out and lse
-    const int32_t *skip;
-    float *far_o;              // [T, Hq, D]
-    float2 *far_ms;            // [T, Hq]
     float *part;               // partial sums of shared units (workspace)
     unsigned *arrived;         // a counter a CTA, zero between calls
     int *err;
@@ -66,16 +60,16 @@ size_t attend_ws_bytes(int sms);       // partial sums
 size_t attend_counter_bytes(int sms);  // counters, before them
 cudaError_t attend_setup();
 cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s);
-cudaError_t attend_far_setup();
-cudaError_t attend_far_launch(const AttendJob &j, int sms, cudaStream_t s);
 
-// A group's shared pages and where its work starts (sv_kvprefix.cu); an entry more
-// than there are groups, with the totals.
+// Attention over a shared prefix: prep finds what is shared and cuts the work, the
+// prefix kernel reads the shared pages, the tail kernel the rest, and joins.
+// A group's shared pages and where its work starts; an entry more than there are
+// groups, with the totals.
 struct PrefixGroup {
     int first, rows;           // first row of q, query rows a cache head
     int pages, lead;           // shared, as the table row of this sequence has them
     long long start;           // in tiles of slots
-    int unit0, pad;
+    int unit0, block;          // rows of a unit
 };
 struct PrefixJob {
     const uint16_t *q;         // [T, Hq, D] bf16
@@ -85,23 +79,50 @@ struct PrefixJob {
     const int32_t *table, *kv_len, *cu;
     const int32_t *prefix_len; // [groups] or null
     const int32_t *cu_group;   // [groups + 1], or null: one group
-    int B, T, Hq, H, G, D, block, pages, cols, groups;
+    const uint32_t *mask;      // [T, words] or null
+    int B, T, Hq, H, G, D, block, pages, cols, groups, words;
     float softmax_scale;
     uint16_t *out;             // [T, Hq, D]
     float *lse;                // [T, Hq] or null
-    int32_t *skip;             // [B] shared pages
+    // from prep
+    int32_t *skip, *seq_group; // [B] shared pages, and of which group
+    int32_t *unit0;            // [B + 1] the tail's tasks of the sequences before
+    int32_t *part0;            // [B] its parts
+    int32_t *tail_stages;      // of a task, at most
     PrefixGroup *group;        // [groups + 1]
-    const float *far_o;        // what attend left
-    const float2 *far_ms;
+    unsigned *tail_arrived;    // a counter a part
+    // from the prefix kernel
+    int prefix_ctas;
+    int2 *unit_ctas;           // the first and the last CTA with a piece of a unit
+    int32_t *part_unit;        // [2 CTAs] the unit of a part
     float *part;               // pieces' sums
+    float *tail_part;          // sums of ranges
     int *err;
 };
 constexpr int kPrefixRows = 256;                             // query rows of a unit
 constexpr int64_t kPrefixMaxUnits = 1 << 24;
 size_t prefix_part_bytes(int sms, int64_t units, int D);
 cudaError_t prefix_setup();
-cudaError_t prefix_prep_launch(const PrefixJob &j, unsigned *counters, int n, cudaStream_t s);
-cudaError_t prefix_launch(const PrefixJob &j, int sms, int64_t units, cudaStream_t s);
+cudaError_t prefix_prep_launch(const PrefixJob &j, int sms, cudaStream_t s);
+cudaError_t prefix_launch(const PrefixJob &j, int sms, cudaStream_t s);
+constexpr int kTailTiles = 2;                                // eights of rows of a task
+constexpr int kTailTile = 32;                                // tokens of a stage
+constexpr int kTailParts = 2;                                // ranges that join, a warp
+inline __host__ __device__ int tail_warps(int sms) { return 12 * sms; }
+// A sequence's rows of a cache head, cut evenly into blocks of eights.
+struct TailBlocks {
+    int blocks, rows;
+    __host__ __device__ explicit TailBlocks(int all)
+    {
+        const int eights = (all + 7) / 8;
+        blocks = (eights + kTailTiles - 1) / kTailTiles;
+        rows = blocks ? (eights + blocks - 1) / blocks * 8 : 0;
+        blocks = rows ? (all + rows - 1) / rows : 0;
+    }
+};
+size_t tail_part_bytes(int sms, int D);
+cudaError_t tail_setup();
+cudaError_t tail_launch(const PrefixJob &j, int sms, cudaStream_t s);
 
 struct RopeJob {
     const char *src[2];        // queries [T, Hq, D], keys [T, H, D]

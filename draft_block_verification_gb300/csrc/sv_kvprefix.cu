@@ -3,19 +3,18 @@
 // read once, for the query rows of the whole group.
 //
 // The result is that of the attention over each sequence by itself (z, w, o as
-// in sv_attend.cuh).  A row's positions are cut in two, the shared pages and the
+// in sv_kvattn.cu).  A row's positions are cut in two, the shared pages and the
 // rest; each part leaves its maximum m, its sum of weights l = sum 2^(y - m) and
 // its sum of weighted values o = sum 2^(y - m) v, and
 //   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
 //
-// Four kernels:
+// Three kernels:
 //   prep     which pages are shared: the leading entries of the group's table
 //            rows that are equal, no further than the caller's bound and the
 //            tokens before each sequence's new ones.  So a bound that is too
-//            large changes nothing.
-//   attend   (sv_kvfar.cu) the rest of each sequence.
+//            large changes nothing.  And how the work is cut.
 //   prefix   the shared pages, below.
-//   combine  the join.
+//   tail     (sv_kvtail.cu) the rest of each sequence, and the join.
 //
 // Shape of the prefix.  All rows see all of it, so there is nothing to mask but
 // the end of the last tile.  A unit is a cache head's block of up to 256 query
@@ -23,7 +22,7 @@
 // of the products, a row's scores lie in one thread's registers, and maxima and
 // sums need no exchange:
 //   S [128 rows x 128 tokens] = Q K^T    in 8 bits: the cache's bytes as they
-//       lie, the query exactly in two e4m3 parts (as in sv_attend.cuh), added up
+//       lie, the query exactly in two e4m3 parts (as in sv_kvattn.cu), added up
 //   O [128 rows x D]         += P V      in bf16: P from tensor memory, V's bytes
 //       brought to bf16 in shared memory
 // A weight is rounded to bf16, within 2^-8 of itself at any size, and a value
@@ -43,7 +42,7 @@
 //
 // Split.  Tiles of all units laid end to end are cut into equal spans, one a
 // CTA.  A unit's piece leaves its sums in the workspace, [D][256] fp32 with rows
-// contiguous; the combine kernel adds a unit's pieces in the order of the CTAs.
+// contiguous; the tail kernel adds a unit's pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,12 +57,13 @@ constexpr int kPxRows = kPrefixRows;   // query rows of a unit, two slots of 128
 constexpr int kPxK = 3, kPxV = 2;      // tiles of keys and of values in flight
 constexpr int kPxRing = 8;             // tiles whose scales are kept
 constexpr int kPxSoft = 8;             // softmax warps, four a slot
-constexpr int kPxThreads = 512;        // + 4 converting warps, producer, issuer, 2 idle
+constexpr int kPxThreads = 512;        // + 4 converting warps, producer, 2 issuers, 1 idle
 // Registers: 128 a thread at launch; the softmax warps, which hold a row's 128
 // scores, take what the others leave (256 * 184 + 256 * 72 = 512 * 128).
 constexpr int kPxRegs = 128, kPxSoftRegs = 184, kPxSideRegs = 72;
 static_assert(256 * kPxSoftRegs + 256 * kPxSideRegs <= kPxThreads * kPxRegs, "registers");
 constexpr float kPxLazy = 8.f;         // log2 of how far a weight may pass 1
+constexpr uint32_t kPxTries = 1u << 16; // of a wait
 constexpr float kPxNone = -1e30f;      // maximum of no tokens
 
 // ---------------------------------------------------------------------------
@@ -72,22 +72,24 @@ constexpr float kPxNone = -1e30f;      // maximum of no tokens
 constexpr int kPrepCtas = 8, kPrepThreads = 512;
 
 struct RowBlocks {
-    int blocks, last;                  // row blocks of a head; the last one's cost
-    __device__ __forceinline__ explicit RowBlocks(int rows)
+    int blocks, full, last;            // row blocks of a head; cost of one and of the last
+    __device__ __forceinline__ RowBlocks(int rows, int block)
     {
-        blocks = (rows + kPxRows - 1) / kPxRows;
-        const int rest = rows - (blocks - 1) * kPxRows;
-        last = rest > 128 ? 2 : 1;     // one slot's tiles cost half
+        blocks = (rows + block - 1) / block;
+        full = block > 128 ? 2 : 1;    // one slot's tiles cost half
+        last = rows - (blocks - 1) * block > 128 ? 2 : 1;
     }
     // of all blocks, in slots' tiles a tile
-    __device__ __forceinline__ int cost() const { return 2 * (blocks - 1) + last; }
+    __device__ __forceinline__ int cost() const { return full * (blocks - 1) + last; }
 };
 
 // One cluster: its warps take the sequences, its first CTA's the groups.
 __global__ void __cluster_dims__(kPrepCtas, 1, 1) __launch_bounds__(kPrepThreads)
-prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
+prefix_prep_kernel(const PrefixJob j, int warps)
 {
     __shared__ int s_bad;
+    __shared__ longlong2 s_sum[kPrepThreads / 32];
+    __shared__ int2 s_scan[kPrepThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kPrepThreads / 32;
     const int shift = 31 - __clz(j.block);
@@ -95,7 +97,7 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
     pdl_trigger();
     if (tid == 0) s_bad = 0;
     if (blockIdx.x == 0)
-        for (int i = tid; i < n_counters; i += kPrepThreads) counters[i] = 0;
+        for (int i = tid; i < kTailParts * warps; i += kPrepThreads) j.tail_arrived[i] = 0;
     auto edge = [&](int g) { return j.cu_group ? j.cu_group[g] : g ? j.B : 0; };
     auto tokens = [&](int b, int &n, int &L) {  // false: lengths out of range
         const int first = j.cu[b], end = j.cu[b + 1];
@@ -156,6 +158,7 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
                 }
             }
         }
+        // (of no group: 0 already)
         if (lane == 0) j.skip[b] = same;
     }
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -168,9 +171,9 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
     const bool bad = s_bad;
     if (bad && tid == 0) latch(j.err, SV_ERR_DEVICE_BOUNDS);
     if (bad)
-        for (int b = tid; b < j.B; b += kPrepThreads) j.skip[b] = 0;
+        for (int b = tid; b < j.B; b += kPrepThreads) j.skip[b] = j.seq_group[b] = 0;
     for (int g = warp; g < j.groups; g += kWarps) {
-        PrefixGroup r = {0, 0, 0, 0, 0, 0, 0};
+        PrefixGroup r = {0, 0, 0, 0, 0, 0, kPxRows};
         if (!bad) {
             const int lo = edge(g), hi = edge(g + 1);
             int pages = 0x7FFFFFFF, lead = 0x7FFFFFFF, live = 0;
@@ -192,6 +195,7 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
             for (int b = lo + lane; b < hi; b += 32) {
                 int n, L;
                 j.skip[b] = tokens(b, n, L) && n > 0 ? pages : 0;
+                j.seq_group[b] = g;
             }
             if (rows > 0) {
                 r.first = first;
@@ -203,7 +207,92 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
         if (lane == 0) j.group[g] = r;
     }
     __syncthreads();
+    // the tail's tasks: what is left of each sequence, cut into ranges of `c` stages
+    auto left = [&](int b, long long &blocks, int &stages) {
+        int n, L;
+        const bool fine = tokens(b, n, L);
+        if (!fine) latch(j.err, SV_ERR_DEVICE_BOUNDS);
+        blocks = fine && n > 0 ? (long long)TailBlocks(n * j.G).blocks * j.H : 0;
+        stages = blocks ? (L - __ldcg(j.skip + b) * j.block + kTailTile - 1) / kTailTile : 0;
+    };
+    long long all = 0, many = 0;
+    for (int b = tid; b < j.B; b += kPrepThreads) {
+        long long blocks;
+        int stages;
+        left(b, blocks, stages);
+        all += blocks * stages;
+        many += blocks;
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) {
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, k);
+        many += __shfl_xor_sync(0xFFFFFFFFu, many, k);
+    }
+    if (lane == 0) s_sum[warp] = make_longlong2(all, many);
+    __syncthreads();
+    all = many = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        all += s_sum[w].x;
+        many += s_sum[w].y;
+    }
+    __syncthreads();
+    // a task a warp, of 256 tokens at least; where there are about as many as warps
+    // before any is cut, only those of twice the mean
+    const long long mean = (all + warps - 1) / warps;
+    const int c = (int)max(8LL, 2 * many >= warps ? 2 * mean : mean);
+    if (tid == 0) *j.tail_stages = c;
+    int units = 0, parts = 0;
+    for (int b0 = 0; b0 < j.B; b0 += kPrepThreads) {
+        const int b = b0 + tid;
+        int mine = 0, part = 0;
+        if (b < j.B) {
+            long long blocks;
+            int stages;
+            left(b, blocks, stages);
+            const int nz = (stages + c - 1) / c;
+            mine = (int)(blocks * nz);
+            part = nz > 1 ? mine : 0;
+        }
+        int ms = mine, ps = part;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, ms, k), y = __shfl_up_sync(0xFFFFFFFFu, ps, k);
+            if (lane >= k) {
+                ms += x;
+                ps += y;
+            }
+        }
+        if (lane == 31) s_scan[warp] = make_int2(ms, ps);
+        __syncthreads();
+        int um = 0, pm = 0, ua = 0, pa = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            const int2 x = s_scan[w];
+            if (w < warp) {
+                um += x.x;
+                pm += x.y;
+            }
+            ua += x.x;
+            pa += x.y;
+        }
+        if (b < j.B) {
+            j.unit0[b] = units + um + ms - mine;
+            j.part0[b] = parts + pm + ps - part;
+        }
+        units += ua;
+        parts += pa;
+        __syncthreads();
+    }
+    if (tid == 0) j.unit0[j.B] = units;
     if (warp != 0) return;
+    // Rows of a unit.  A piece's sums are as many as its rows, whatever its tokens; so
+    // where CTAs by far outnumber the units, units of half the rows halve what the
+    // tail has to read (with as many units as CTAs the halves would only have values
+    // brought to bf16 twice).
+    int big = 0;
+    for (int g = lane; g < j.groups; g += 32)
+        if (__ldcg(&j.group[g].pages)) big += RowBlocks(__ldcg(&j.group[g].rows), kPxRows).blocks * j.H;
+    big = __reduce_add_sync(0xFFFFFFFFu, big);
+    const int block = 4 * big < j.prefix_ctas ? 128 : kPxRows;
     // where each group's work and units start
     long long at = 0;
     int unit = 0;
@@ -215,7 +304,7 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
             const PrefixGroup *r = j.group + g;
             const int pages = __ldcg(&r->pages), rows = __ldcg(&r->rows);
             if (pages) {
-                const RowBlocks rb(rows);
+                const RowBlocks rb(rows, block);
                 const long long tiles = (((long long)pages << shift) + kPxTile - 1) / kPxTile;
                 w = tiles * rb.cost() * j.H;
                 u = rb.blocks * j.H;
@@ -235,12 +324,13 @@ prefix_prep_kernel(const PrefixJob j, unsigned *counters, int n_counters)
         if (g < j.groups) {
             j.group[g].start = at + ws - w;
             j.group[g].unit0 = unit + us - u;
+            j.group[g].block = block;
         }
         at += __shfl_sync(0xFFFFFFFFu, ws, 31);
         unit += __shfl_sync(0xFFFFFFFFu, us, 31);
     }
     if (lane == 0) {
-        PrefixGroup r = {0, 0, 0, 0, 0, 0, 0};
+        PrefixGroup r = {0, 0, 0, 0, 0, 0, kPxRows};
         r.start = at;
         r.unit0 = unit;
         j.group[j.groups] = r;
@@ -280,15 +370,15 @@ struct PxWalk {
             while (g < j.groups && j.group[g + 1].start <= pos) ++g;
             if (g >= j.groups) return false;
             const PrefixGroup r = j.group[g];
-            const RowBlocks rb(r.rows);
+            const RowBlocks rb(r.rows, r.block);
             const int tiles = (int)((((long long)r.pages * j.block) + kPxTile - 1) / kPxTile);
-            const long long head = (long long)tiles * rb.cost(), wide = (long long)tiles * 2;
+            const long long head = (long long)tiles * rb.cost(), wide = (long long)tiles * rb.full;
             long long x = pos - r.start;
             const int h = (int)div_pos(x, head);
             x -= h * head;
             const int block = min((int)div_pos(x, wide), rb.blocks - 1);
             x -= block * wide;
-            const int cost = block == rb.blocks - 1 ? rb.last : 2;
+            const int cost = block == rb.blocks - 1 ? rb.last : rb.full;
             const int t = (int)div_pos(x + cost - 1, cost);
             pos += (long long)t * cost - x;
             if (t >= tiles) continue;  // (the unit's last tile starts before the span)
@@ -297,8 +387,8 @@ struct PxWalk {
             pos += (long long)n * cost;
             p.g = g;
             p.h = h;
-            p.row0 = block * kPxRows;
-            p.rows = min(kPxRows, r.rows - p.row0);
+            p.row0 = block * r.block;
+            p.rows = min(r.block, r.rows - p.row0);
             p.t0 = t;
             p.t1 = t + n;
             p.tiles = tiles;
@@ -324,14 +414,13 @@ __device__ __forceinline__ float *px_part(const PrefixJob &j, int ctas, int cta,
 
 struct PxShared {
     uint64_t full_k[kPxK], empty_k[kPxK], full_v[kPxV], empty_v[kPxV], full_b[2], empty_b[2];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full, scales[kPxRing], drained;
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full, turn[2], scales[kPxRing], drained[2];
     uint32_t tmem;
     int abort;
     // for each 16 tokens: the key's scale, log2 of the value scale's fraction (1 to 2)
-    // and its inverse; the scale's power of two, as two factors after the bytes'
-    // exponents
+    // and its inverse; the scale's power of two, as two factors
     float4 sc[kPxRing][8];
-    uint32_t up[kPxRing][8];
+    uint32_t up[kPxRing][8], more[kPxRing][8];
     float c[kPxRows];                  // factor from S to log2 units, per row
     float m[2][128], l[2][128];        // of the two slots, where they share rows
 };
@@ -351,13 +440,17 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, float *v)
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tc_st8u(uint32_t addr, const uint32_t *v)
+__device__ __forceinline__ void tc_st32u(uint32_t addr, const uint32_t *v)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                     addr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                 "r"(v[7])
-                 : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
 }
 // A from tensor memory, 16-bit.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -369,10 +462,24 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Bytes of w by selector; a selector's bit 3 takes the byte's sign, eight times.
+__device__ __forceinline__ uint32_t sign_pairs(uint32_t w, uint32_t sel)
+{
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(d) : "r"(w), "r"(sel));
     return d;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
@@ -382,172 +489,241 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// Four e4m3 bytes to bf16 pairs.  The byte's exponent and fraction, moved to
-// bf16's places, are the value times 2^-120 (subnormals too: both formats count
-// the same steps); `up` holds 2^(60 + e) and 2^60 in its halves, e the exponent
-// of the scale: the factor is taken in two steps, which stay within the range.
+// Bounded wait that also ends when another role has given up.  A try lets the
+// warp sleep until the phase completes or some 10 us have passed: polling warps
+// would take a quarter of the instruction slots.
+__device__ __forceinline__ bool px_wait(PxShared *sh, int *err, uint64_t *bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < kPxTries; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(10000)
+            : "memory");
+        if (ok) return true;
+        if (*(volatile int *)&sh->abort) return false;
+    }
+    *(volatile int *)&sh->abort = 1;
+    latch(err, SV_ERR_TIMEOUT);
+    return false;
+}
+
+// Four e4m3 bytes to bf16 pairs.  A byte with its sign in the byte above it, moved
+// up by four bits, has sign, exponent and fraction in bf16's places (once the bits
+// between are cleared) and stands for its value times 2^-120: both formats count the
+// same steps, subnormals too.  up: 2^(120 + e), twice, e the scale's exponent, of
+// which more than 7 would leave the range (kPxTop).
+constexpr int kPxTop = 7;
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t w, uint32_t up, uint32_t &lo, uint32_t &hi)
 {
-    const uint32_t head = ((w >> 4) & 0x07070707u) | (w & 0x80808080u);
-    const uint32_t tail = (w << 4) & 0xF0F0F0F0u;
-    constexpr uint32_t k60 = 0x5D805D80u;       // 2^60, twice
-    lo = mul_bf16x2(mul_bf16x2(__byte_perm(tail, head, 0x5140), k60), up);
-    hi = mul_bf16x2(mul_bf16x2(__byte_perm(tail, head, 0x7362), k60), up);
+    constexpr uint32_t kKeep = 0x87F087F0u;
+    lo = mul_bf16x2((sign_pairs(w, 0x9180) << 4) & kKeep, up);
+    hi = mul_bf16x2((sign_pairs(w, 0xB3A2) << 4) & kKeep, up);
 }
 
 // The piece's queries: hi and lo parts to shared memory, rows of D bytes in the
-// swizzle of the keys; D / 8 lanes a row, eight rows or more a warp in flight.
+// swizzle of the keys; D / 16 lanes a row, kAhead rows a lane in flight.  (Kept
+// short: code that runs once a piece comes from far, some 300 cycles for every
+// eight instructions.)
 template <int D>
 __device__ __forceinline__ void px_queries(const PrefixJob &j, PxShared *sh, char *smem_q,
                                            const PxPiece &pc)
 {
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kAhead = 4;
+    constexpr int kStep = kPxSoft * kRows;      // rows of a load of all warps
     constexpr int kSide = 128 * D;              // bytes of a slot's part
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % kLanes, all = pc.wide() ? kPxRows : 128;
     const bool vec = (((uintptr_t)j.q | (uintptr_t)(j.qts * 2) | (uintptr_t)(j.qhs * 2)) & 15) == 0;
-    const bool minus = j.softmax_scale < 0.f;   // (maxima are taken of scores that grow)
-#pragma unroll 1
-    for (int n0 = warp * kRows * kBatch; n0 < all; n0 += kPxSoft * kRows * kBatch) {
-        uint4 raw[kBatch];
+    const float sign = j.softmax_scale < 0.f ? -1.f : 1.f;  // (maxima are of scores that grow)
+    const int mine = warp * kRows + lane / kLanes;
+    // the token and head of the next row to fetch
+    const int row0 = pc.row0 + mine, tok_step = kStep / j.G, head_step = kStep - tok_step * j.G;
+    int tok = row0 / j.G, head = row0 - tok * j.G, at = mine;
+    auto fetch = [&](uint4 (&v)[2]) {
+        v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < pc.rows) {
+            const uint16_t *q = j.q + (int64_t)(pc.first + tok) * j.qts +
+                                (int64_t)(pc.h * j.G + head) * j.qhs + l * 16;
+            if (vec) {
+                v[0] = reinterpret_cast<const uint4 *>(q)[0];
+                v[1] = reinterpret_cast<const uint4 *>(q)[1];
+            } else {
+                uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int n = n0 + k * kRows + lane / kLanes;
-            raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (n < pc.rows) {
-                const int row = pc.row0 + n, tok = row / j.G;
-                const uint16_t *q = j.q + (int64_t)(pc.first + tok) * j.qts +
-                                    (int64_t)(pc.h * j.G + row - tok * j.G) * j.qhs + l * 8;
-                if (vec) {
-                    raw[k] = *reinterpret_cast<const uint4 *>(q);
-                } else {
-                    raw[k].x = q[0] | (uint32_t)q[1] << 16;
-                    raw[k].y = q[2] | (uint32_t)q[3] << 16;
-                    raw[k].z = q[4] | (uint32_t)q[5] << 16;
-                    raw[k].w = q[6] | (uint32_t)q[7] << 16;
-                }
+                for (int i = 0; i < 8; ++i) w[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
+                v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                v[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
         }
+        at += kStep;
+        tok += tok_step;
+        head += head_step;
+        if (head >= j.G) {
+            head -= j.G;
+            ++tok;
+        }
+    };
+    uint4 raw[kAhead][2];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int n = n0 + k * kRows + lane / kLanes;
-            float x[8];
-            VecTraits<uint16_t>::unpack(raw[k], x);
-            float amax = 0.f;
-            bool odd = false;                   // NaN or an infinity
+    for (int k = 0; k < kAhead; ++k) fetch(raw[k]);
+#pragma unroll 1
+    for (int n = mine; n < all; n += kStep) {
+        float x[16];
+        {
+            float a[8], b[8];
+            VecTraits<uint16_t>::unpack(raw[0][0], a);
+            VecTraits<uint16_t>::unpack(raw[0][1], b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                amax = fmaxf(amax, fabsf(x[i]));
-                odd |= !(fabsf(x[i]) < INFINITY);
-            }
-#pragma unroll
-            for (int i = kLanes / 2; i > 0; i >>= 1) {
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, i));
-                odd |= __shfl_xor_sync(0xFFFFFFFFu, (int)odd, i) != 0;
-            }
-            // 2^e brings the largest element to [128, 256)
-            const int e = amax > 0.f && !odd ? min(134 - (int)(__float_as_uint(amax) >> 23), 126) : 0;
-            const float up = __int_as_float((127 + e) << 23);
-            if (l == 0 && n < all)
-                sh->c[n] = n >= pc.rows ? 0.f
-                           : odd        ? __int_as_float(0x7FC00000)
-                                        : fabsf(j.softmax_scale) * 1.4426950408889634f / up;
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                uint16_t h8, l8;
-                const float a = minus ? -x[i] * up : x[i] * up;
-                const float b = minus ? -x[i + 1] * up : x[i + 1] * up;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(b), "f"(a));
-                uint32_t h16;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
-                const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&h16));
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-                    : "=h"(l8)
-                    : "f"(b - h.y), "f"(a - h.x));
-                if (i & 2) {
-                    hi[i >> 2] |= (uint32_t)h8 << 16;
-                    lo[i >> 2] |= (uint32_t)l8 << 16;
-                } else {
-                    hi[i >> 2] = h8;
-                    lo[i >> 2] = l8;
-                }
-            }
-            if (n < all) {
-                const int r = n & 127, sw = D == 128 ? r & 7 : (r >> 1) & 3;
-                char *at = smem_q + (n >> 7) * (2 * kSide) + r * D + (((l >> 1) ^ sw) << 4) + (l & 1) * 8;
-                *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(at + kSide) = make_uint2(lo[0], lo[1]);
+                x[i] = a[i];
+                x[8 + i] = b[i];
             }
         }
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) {
+            raw[k][0] = raw[k + 1][0];
+            raw[k][1] = raw[k + 1][1];
+        }
+        fetch(raw[kAhead - 1]);
+        // (as integers NaN is above infinity, and above the rest)
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int i = kLanes / 2; i > 0; i >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+        const bool odd = top >= 0x7F800000u;    // NaN or an infinity
+        // 2^e brings the largest element to [128, 256)
+        const int e = top > 0 && !odd ? min(134 - (int)(top >> 23), 126) : 0;
+        const float up = __int_as_float((127 + e) << 23);
+        if (l == 0)
+            sh->c[n] = n >= pc.rows ? 0.f
+                       : odd        ? __int_as_float(0x7FC00000)
+                                    : fabsf(j.softmax_scale) * 1.4426950408889634f / up;
+        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            uint16_t h8, l8;
+            const float a = x[i] * (sign * up), b = x[i + 1] * (sign * up);
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(b), "f"(a));
+            uint32_t h16;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
+            const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&h16));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l8) : "f"(b - h.y), "f"(a - h.x));
+            hi[i >> 2] |= (uint32_t)h8 << (8 * (i & 2));
+            lo[i >> 2] |= (uint32_t)l8 << (8 * (i & 2));
+        }
+        const int r = n & 127, sw = D == 128 ? r & 7 : (r >> 1) & 3;
+        char *to = smem_q + (n >> 7) * (2 * kSide) + r * D + ((l ^ sw) << 4);
+        *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(to + kSide) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
-// One tile of a softmax thread: a row's 128 scores to weights.
-// M, l: the row's running maximum and sum of weights.
+// One tile of a softmax thread: a row's 128 scores to weights, 64 at a time.
+// M (a whole number), l: the row's running maximum and sum of weights.  Weights are
+// taken against the maximum in use before it is known whether one passes it by too
+// much; where one does, M moves, and what there is of the row (sums, values, the
+// tile's first 64 weights) is scaled by the power of two.
+// same: pages of 64 tokens or more, one scale for the 64.
+// (The factors are taken before the scores, the weights stored after them: loads
+// and stores between would keep the scores' chains from overlapping.)
 template <int D>
 __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
-                                             uint64_t *pv_done, uint32_t count, bool first, int ring,
-                                             int chunks, float c, float &M, float &l)
+                                             uint64_t *pv_done, uint32_t count, bool first,
+                                             const float4 *sc, bool same, float c, float &M,
+                                             float &l)
 {
-    float s[128];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tc_ld32(s_at + i * 32, s + i * 32);
-    tc_wait_ld(s);
-    float m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (k >= chunks) break;
-        const float4 f = sh->sc[ring][k];
-        float a = s[16 * k], b = s[16 * k + 1];
-#pragma unroll
-        for (int i = 2; i < 16; i += 4) {
-            a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
-            if (i + 3 < 16) b = max3(b, s[16 * k + i + 2], s[16 * k + i + 3]);
-        }
-        m = fmaxf(m, fmaf(fmaxf(a, b), c * f.x, f.y));
-    }
     bool ok = true;
-    if (first) {
-        M = m > -INFINITY ? m : 0.f;
-        l = 0.f;
-    } else if (__any_sync(0xFFFFFFFFu, m > M + kPxLazy)) {
-        const float to = m > M + kPxLazy ? m : M, f = ex2f(M - to);
-        M = to;
-        l *= f;
-        ok = at_wait(&sh->abort, err, pv_done, (count - 1) & 1);
-        tc_fence_after();
 #pragma unroll 1
-        for (int i = 0; i < D; i += 8) {
-            float o[8];
-            tc_ld8(o_at + i, o);
-            tc_wait_ld(o);
+    for (int q = 0; q < 2; ++q) {
+        float s[64];
+        tc_ld32(s_at + q * 64, s);
+        tc_ld32(s_at + q * 64 + 32, s + 32);
+        float4 f[4];
+        f[0] = sc[4 * q];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] *= f;
-            tc_st8(o_at + i, o);
+        for (int k = 1; k < 4; ++k) {
+            f[k] = f[0];
+            if (!same) f[k] = sc[4 * q + k];
         }
-        tc_wait_st();
-    }
+        tc_wait_ld(s);
+        uint32_t p[32];
+        float add;
+#pragma unroll 1
+        for (;;) {
+            float top = -INFINITY;
+            add = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        uint32_t p[8];
-        if (k < chunks) {
-            const float4 f = sh->sc[ring][k];
-            const float2 u = make_float2(c * f.x, c * f.x), v = make_float2(f.y - M, f.y - M);
-            float2 sum = make_float2(0.f, 0.f);
+            for (int k = 0; k < 4; ++k) {
+                const float2 u = make_float2(c * f[k].x, c * f[k].x);
+                const float2 v = make_float2(f[k].y - M, f[k].y - M);
+                float2 sum;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 y = fma2(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), u, v);
-                const float2 w = make_float2(ex2f(y.x), ex2f(y.y));
-                sum = add2(sum, w);
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[i]) : "f"(w.y), "f"(w.x));
+                for (int i = 0; i < 8; ++i) {
+                    const float2 y = fma2(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), u, v);
+                    top = max3(top, y.x, y.y);
+                    const float2 w = make_float2(ex2f(y.x), ex2f(y.y));
+                    sum = i ? add2(sum, w) : w;
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[8 * k + i]) : "f"(w.y), "f"(w.x));
+                }
+                add = fmaf(sum.x + sum.y, f[k].z, add);
             }
-            l = fmaf(sum.x + sum.y, f.z, l);
-        } else {
+            // (M is unset, at kPxNone, before a row's first tile)
+            if (!__any_sync(0xFFFFFFFFu, top > kPxLazy)) break;
+            float to = top > kPxLazy ? M + ceilf(top) : M;
+            if (M == kPxNone) {
+                // no sum was taken against it: from the scores themselves
+                to = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = 0u;
+                for (int k = 0; k < 4; ++k) {
+                    float a = s[16 * k], b = s[16 * k + 1];
+#pragma unroll
+                    for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
+                    to = fmaxf(to, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
+                }
+                to = to > -INFINITY ? ceilf(to) : 0.f;
+                M = to;
+                continue;
+            }
+            const float scale = pow2_int(M - to);
+            M = to;
+            l *= scale;
+            if (!first) {
+                ok = ok && px_wait(sh, err, pv_done, (count - 1) & 1);
+                tc_fence_after();
+#pragma unroll 1
+                for (int i = 0; i < D; i += 8) {
+                    float o[8];
+                    tc_ld8(o_at + i, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) o[n] *= scale;
+                    tc_st8(o_at + i, o);
+                }
+            }
+            if (q) {
+                tc_wait_st();
+                uint32_t two;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(two) : "f"(scale));
+#pragma unroll 1
+                for (int i = 0; i < 32; i += 8) {
+                    float o[8];
+                    tc_ld8(s_at + i, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+                        o[n] = __uint_as_float(mul_bf16x2(__float_as_uint(o[n]), two));
+                    tc_st8(s_at + i, o);
+                }
+            }
+            tc_wait_st();
         }
-        tc_st8u(s_at + k * 8, p);
+        l += add;
+        // (over scores that have been taken)
+        tc_st32u(s_at + q * 32, p);
     }
     tc_wait_st();
     return ok;
@@ -571,7 +747,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
     if (tid == 0) {
         for (int i = 0; i < kPxK; ++i) {
             mbar_init(&sh->full_k[i], 1);
-            mbar_init(&sh->empty_k[i], 1);
+            mbar_init(&sh->empty_k[i], 2);
         }
         for (int i = 0; i < kPxV; ++i) {
             mbar_init(&sh->full_v[i], 1);
@@ -579,14 +755,15 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->full_b[i], 4);
-            mbar_init(&sh->empty_b[i], 1);
+            mbar_init(&sh->empty_b[i], 2);
+            mbar_init(&sh->drained[i], 1);
+            mbar_init(&sh->turn[i], 1);
             mbar_init(&sh->s_full[i], 1);
             mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->pv_done[i], 1);
         }
         for (int i = 0; i < kPxRing; ++i) mbar_init(&sh->scales[i], 1);
         mbar_init(&sh->q_full, kPxSoft);
-        mbar_init(&sh->drained, 1);
         mbar_fence_init();
         sh->abort = 0;
     }
@@ -616,6 +793,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_at = lanes + slot * 128, o_at = lanes + 256 + slot * 128;
         uint32_t count = 0;                     // this slot's tiles so far
+        if (tid == 0) j.part_unit[2 * blockIdx.x] = j.part_unit[2 * blockIdx.x + 1] = -1;
         while (ok && walk.next(j, pc)) {
             const bool wide = pc.wide();
             px_queries<D>(j, sh, s_q, pc);
@@ -627,22 +805,20 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             float M = kPxNone, l = 0.f;
             for (int i = from; i < n && ok; i += step, ++count) {
                 const int ring = (int)((it + i) % kPxRing);
-                ok = at_wait(&sh->abort, j.err, &sh->scales[ring], ((it + i) / kPxRing) & 1);
-                ok = ok && at_wait(&sh->abort, j.err, &sh->s_full[slot], count & 1);
+                ok = px_wait(sh, j.err, &sh->scales[ring], ((it + i) / kPxRing) & 1);
+                ok = ok && px_wait(sh, j.err, &sh->s_full[slot], count & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const long long left = (long long)pc.pages * j.block - (long long)(pc.t0 + i) * kPxTile;
-                const int chunks = left >= kPxTile ? 8 : (int)(left >> 4);
                 ok = px_soft_tile<D>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
-                                     ring, chunks, c, M, l);
+                                     sh->sc[ring], j.block >= 64, c, M, l);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full[slot]);
             }
             const bool had = from < n;
-            if (had && ok) ok = at_wait(&sh->abort, j.err, &sh->pv_done[slot], (count - 1) & 1);
+            if (had && ok) ok = px_wait(sh, j.err, &sh->pv_done[slot], (count - 1) & 1);
             if (!wide) {
                 sh->m[slot][r] = M;
                 sh->l[slot][r] = l;
@@ -653,6 +829,11 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             }
             tc_fence_after();
             // ---- the piece's sums
+            if (tid == 0) {
+                if (pc.t0 == 0) j.unit_ctas[pc.unit].x = blockIdx.x;
+                if (pc.t1 == pc.tiles) j.unit_ctas[pc.unit].y = blockIdx.x;
+                if (!pc.whole()) j.part_unit[2 * blockIdx.x + (pc.t0 == 0 ? 1 : 0)] = pc.unit;
+            }
             float *part = px_part(j, ctas, blockIdx.x, pc.t0, pc.whole(), pc.unit);
             if (wide) {
                 float *at = part + slot * 128 + r;
@@ -703,25 +884,30 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             while (ok && walk.next(j, pc)) {
                 for (int t = pc.t0; t < pc.t1; ++t, ++it) {
                     const int st = it % kPxV, sb = it & 1, ring = it % kPxRing;
-                    ok = at_wait(&sh->abort, j.err, &sh->scales[ring], (it / kPxRing) & 1);
-                    ok = ok && at_wait(&sh->abort, j.err, &sh->full_v[st], (it / kPxV) & 1);
-                    ok = ok && at_wait(&sh->abort, j.err, &sh->empty_b[sb], ((it >> 1) & 1) ^ 1);
+                    ok = px_wait(sh, j.err, &sh->scales[ring], (it / kPxRing) & 1);
+                    ok = ok && px_wait(sh, j.err, &sh->full_v[st], (it / kPxV) & 1);
+                    ok = ok && px_wait(sh, j.err, &sh->empty_b[sb], ((it >> 1) & 1) ^ 1);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const bool live = (long long)t * kPxTile + tk < (long long)pc.pages * j.block;
-                    const uint32_t up = sh->up[ring][tk >> 4];
+                    const uint32_t up = sh->up[ring][tk >> 4], more = sh->more[ring][tk >> 4];
+                    constexpr uint32_t kOne = 0x3F803F80u;
                     const char *src = s_v + st * kSide + tk * D;
                     char *dst = s_b + sb * kWideV + tk * 128;
                     const int sw = D == 128 ? tk & 7 : (tk >> 1) & 3;
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < D / 16; ++i) {
-                        uint4 w = *reinterpret_cast<const uint4 *>(src + ((i ^ sw) << 4));
-                        if (!live) w = make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + ((i ^ sw) << 4));
                         uint4 a, b;
                         e4m3_to_bf16(w.x, up, a.x, a.y);
                         e4m3_to_bf16(w.y, up, a.z, a.w);
                         e4m3_to_bf16(w.z, up, b.x, b.y);
                         e4m3_to_bf16(w.w, up, b.z, b.w);
+                        if (more != kOne) {     // a scale of 256 or more
+                            a.x = mul_bf16x2(a.x, more); a.y = mul_bf16x2(a.y, more);
+                            a.z = mul_bf16x2(a.z, more); a.w = mul_bf16x2(a.w, more);
+                            b.x = mul_bf16x2(b.x, more); b.y = mul_bf16x2(b.y, more);
+                            b.z = mul_bf16x2(b.z, more); b.w = mul_bf16x2(b.w, more);
+                        }
                         char *at = dst + (i >> 2) * (kPxTile * 128);
                         const int q = (i & 3) * 2;
                         *reinterpret_cast<uint4 *>(at + ((q ^ (tk & 7)) << 4)) = a;
@@ -768,45 +954,49 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         window(w0 + 32, npage, nks, nvs);
                     }
                     const bool mine = lane - (p0 - w0) >= 0 && lane - (p0 - w0) < per_tile;
-                    const bool copy = mine && page >= 0;
-                    const uint32_t bytes =
-                        (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, copy)) * j.block * D;
-                    const int64_t row = (int64_t)page * j.H + pc.h;
+                    const bool live = w0 + lane < pc.pages;
+                    // (behind the last page the tile's first one once more: tokens
+                    // of weight 0, but no NaN)
+                    const int begin = __shfl_sync(0xFFFFFFFFu, page, p0 - w0);
+                    const int row = max(live ? page : begin, 0) * j.H + pc.h;
                     auto fetch = [&](const CUtensorMap *map, char *dst, uint64_t *bar) {
                         asm volatile(
                             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::"
                             "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-                            "l"(map), "r"(0), "r"(0), "r"((int)row), "r"(smem_u32(bar))
+                            "l"(map), "r"(0), "r"(0), "r"(row), "r"(smem_u32(bar))
                             : "memory");
                     };
                     const int sk = it % kPxK, sv = it % kPxV, ring = it % kPxRing;
-                    ok = at_wait(&sh->abort, j.err, &sh->empty_k[sk], ((it / kPxK) & 1) ^ 1);
+                    ok = px_wait(sh, j.err, &sh->empty_k[sk], ((it / kPxK) & 1) ^ 1);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_tx(&sh->full_k[sk], bytes);
+                    if (lane == 0) mbar_arrive_tx(&sh->full_k[sk], kSide);
                     __syncwarp();
-                    if (copy) fetch(&map_k, s_k + sk * kSide + inner * j.block * D, &sh->full_k[sk]);
+                    if (mine) fetch(&map_k, s_k + sk * kSide + inner * j.block * D, &sh->full_k[sk]);
                     // (the tile that had these places is behind the scores of all
                     // but the last tiles)
                     if (mine) {
                         const uint32_t u = __float_as_uint(vs);
                         const int e = (int)(u >> 23) - 127;
                         const float f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
-                        const float4 sc = make_float4(ks, f == 1.f ? 0.f : log2f(f), 1.f / f, 0.f);
-                        const uint32_t up = (uint32_t)(127 + 60 + e) << 7;  // bf16
+                        const float4 sc = live ? make_float4(ks, f == 1.f ? 0.f : log2f(f), 1.f / f, 0.f)
+                                               : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                        const uint32_t up = (uint32_t)(127 + 120 + min(e, kPxTop)) << 7;  // bf16
+                        const uint32_t more = (uint32_t)(127 + max(e - kPxTop, 0)) << 7;
                         for (int i = 0; i < j.block >> 4; ++i) {
                             sh->sc[ring][inner * (j.block >> 4) + i] = sc;
                             sh->up[ring][inner * (j.block >> 4) + i] = up | up << 16;
+                            sh->more[ring][inner * (j.block >> 4) + i] = more | more << 16;
                         }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->scales[ring]);
-                    ok = at_wait(&sh->abort, j.err, &sh->empty_v[sv], ((it / kPxV) & 1) ^ 1);
+                    ok = px_wait(sh, j.err, &sh->empty_v[sv], ((it / kPxV) & 1) ^ 1);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_tx(&sh->full_v[sv], bytes);
+                    if (lane == 0) mbar_arrive_tx(&sh->full_v[sv], kSide);
                     __syncwarp();
-                    if (copy) fetch(&map_v, s_v + sv * kSide + inner * j.block * D, &sh->full_v[sv]);
+                    if (mine) fetch(&map_v, s_v + sv * kSide + inner * j.block * D, &sh->full_v[sv]);
                 }
             }
             // after a wait that ran out: copies still in flight land before the exit
@@ -814,82 +1004,82 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 for (int i = 0; i < kPxK; ++i) mbar_wait_n(&sh->full_k[i], (it / kPxK) & 1, 1u << 12);
                 for (int i = 0; i < kPxV; ++i) mbar_wait_n(&sh->full_v[i], (it / kPxV) & 1, 1u << 12);
             }
-        } else if (warp == 13 && lane == 0) {
-            // ---- issuer of the products
+        } else if (warp < 15) {
+            // ---- issuers of the products, one a slot.  A step: the product of the slot's
+            // weights with the tile's values, then the scores of its next tile, whose
+            // place the weights have held.  (The whole warp walks along, so that
+            // descriptors lie in uniform registers; one thread issues.)
             constexpr uint32_t kSums = 1u << 4, kM = 128u >> 4 << 24;  // fp32 sums, M = 128
             constexpr uint32_t kIdS = kSums | (128u >> 3 << 17) | kM;
             // bf16 both; B with its rows (tokens) as the products' dimension
             constexpr uint32_t kIdO = kSums | 1u << 7 | 1u << 10 | 1u << 16 | ((uint32_t)D >> 3 << 17) | kM;
+            const int slot = __shfl_sync(0xFFFFFFFFu, warp - 13, 0);
+            const uint32_t col = tmem + slot * 128;
             const uint64_t dk0 = tc_desc(smem_u32(s_k), 16, 8 * D, kSwz);
             const uint64_t dq0 = tc_desc(smem_u32(s_q), 16, 8 * D, kSwz);
             const uint64_t db0 = tc_desc(smem_u32(s_b), kPxTile * 128, 1024, 2);
-            uint32_t count[2] = {0, 0}, pieces = 0;
-            auto scores = [&](int slot, bool wide, uint32_t i) {
-                const int st = i % kPxK;
-                ok = ok && at_wait(&sh->abort, j.err, &sh->full_k[st], (i / kPxK) & 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t dk = dk0 + st * (kSide >> 4);
-                const uint64_t dq = dq0 + (wide ? slot : 0) * (2 * kSide >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    tc_mma(tmem + slot * 128, dq + 2 * k, dk + 2 * k, kIdS, k);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    tc_mma(tmem + slot * 128, dq + (kSide >> 4) + 2 * k, dk + 2 * k, kIdS, 1);
-                tc_commit(&sh->s_full[slot]);
-            };
-            auto values = [&](int slot, uint32_t i, bool add) {
-                const int sb = i & 1;
-                ok = ok && at_wait(&sh->abort, j.err, &sh->full_b[sb], (i >> 1) & 1);
-                ok = ok && at_wait(&sh->abort, j.err, &sh->p_full[slot], count[slot]++ & 1);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t db = db0 + sb * (kWideV >> 4);
-#pragma unroll
-                for (int k = 0; k < kPxTile / 16; ++k)
-                    tc_mma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + 8 * k, db + 128 * k, kIdO,
-                              add || k);
-                tc_commit(&sh->pv_done[slot]);
-            };
+            const bool one = elect_one();
+            uint32_t count = 0, pieces = 0, wides = 0;
             while (ok && walk.next(j, pc)) {
                 const bool wide = pc.wide();
-                const int n = pc.t1 - pc.t0;
-                ok = at_wait(&sh->abort, j.err, &sh->q_full, pieces++ & 1);
-                tc_fence_after();
-                if (wide) {
-                    scores(0, true, it);
-                    scores(1, true, it);
-                    if (ok) tc_commit(&sh->empty_k[it % kPxK]);
-                    for (int i = 0; i < n && ok; ++i, ++it) {
-                        values(0, it, i > 0);
-                        if (i + 1 < n) scores(0, true, it + 1);
-                        values(1, it, i > 0);
-                        if (ok) tc_commit(&sh->empty_b[it & 1]);
-                        if (i + 1 < n) {
-                            scores(1, true, it + 1);
-                            if (ok) tc_commit(&sh->empty_k[(it + 1) % kPxK]);
-                        }
+                const int n = pc.t1 - pc.t0, step = wide ? 1 : 2;
+                const uint64_t dq = dq0 + (wide ? slot : 0) * (2 * kSide >> 4);
+                ok = px_wait(sh, j.err, &sh->q_full, pieces++ & 1);
+                // tiles of this slot, its own first one ahead
+#pragma unroll 1
+                for (int i = (wide ? 0 : slot) - step; i < n && ok; i += step) {
+                    const bool now = i >= 0, next = i + step < n;
+                    const uint32_t t = it + i, sb = t & 1;
+                    const uint32_t tn = t + step, st = tn % kPxK;
+                    // (the weights last: from then on nothing is in the way)
+                    if (next) ok = px_wait(sh, j.err, &sh->full_k[st], (tn / kPxK) & 1);
+                    if (now) {
+                        ok = ok && px_wait(sh, j.err, &sh->full_b[sb], (t >> 1) & 1);
+                        // the slots take turns: one's softmax runs under the other's
+                        // products (side by side, both wait for the products, then the
+                        // products for both; free to run, one gets a tile ahead and
+                        // waits for values that the other holds)
+                        if (wide && (slot || wides))
+                            ok = ok && px_wait(sh, j.err, &sh->turn[slot ^ 1], (wides + slot + 1) & 1);
+                        ok = ok && px_wait(sh, j.err, &sh->p_full[slot], count++ & 1);
                     }
-                } else {
-                    for (int i = 0; i < 2 && i < n; ++i) {
-                        scores(i, false, it + i);
-                        if (ok) tc_commit(&sh->empty_k[(it + i) % kPxK]);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (now && one) {
+                        const uint64_t db = db0 + sb * (kWideV >> 4);
+#pragma unroll
+                        for (int k = 0; k < kPxTile / 16; ++k)
+                            tc_mma_ts(col + 256, col + 8 * k, db + 128 * k, kIdO, k || i >= step);
+                        tc_commit(&sh->pv_done[slot]);
+                        // (both slots release a tile)
+                        tc_commit(&sh->empty_b[sb]);
+                        if (!wide) tc_commit(&sh->empty_b[sb]);
                     }
-                    for (int i = 0; i < n && ok; ++i, ++it) {
-                        values(i & 1, it, i > 1);
-                        if (ok) tc_commit(&sh->empty_b[it & 1]);
-                        if (i + 2 < n) {
-                            scores(i & 1, false, it + 2);
-                            if (ok) tc_commit(&sh->empty_k[(it + 2) % kPxK]);
-                        }
+                    if (next && one) {
+                        const uint64_t dk = dk0 + st * (kSide >> 4);
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            tc_mma(col, dq + 2 * k, dk + 2 * k, kIdS, k);
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k)
+                            tc_mma(col, dq + (kSide >> 4) + 2 * k, dk + 2 * k, kIdS, 1);
+                        tc_commit(&sh->s_full[slot]);
+                        tc_commit(&sh->empty_k[st]);
+                        if (!wide) tc_commit(&sh->empty_k[st]);
                     }
+                    if (now && wide) {
+                        ++wides;
+                        if (one) mbar_arrive(&sh->turn[slot]);
+                    }
+                    __syncwarp();
                 }
+                it += n;
             }
             // after a wait that ran out: products still in flight end before the exit
-            if (!ok) {
-                tc_commit(&sh->drained);
-                mbar_wait_n(&sh->drained, 0, 1u << 12);
+            if (!ok && one) {
+                tc_commit(&sh->drained[slot]);
+                mbar_wait_n(&sh->drained[slot], 0, 1u << 12);
             }
         }
     }
@@ -899,105 +1089,6 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
-}
-
-// ---------------------------------------------------------------------------
-// The join: a unit's pieces and what attend left of its rows.  A CTA has 32
-// rows (lanes) and 32 elements of them: two warps with 16 each, times four that
-// share the pieces.
-// ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 256, kJoinWays = 4;
-
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixJob j, int ctas)
-{
-    __shared__ float s_sum[kJoinWays][2][16][32], s_m[kJoinWays][2][32], s_l[kJoinWays][2][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp >> 1, half = warp & 1;
-    pdl_wait();
-    pdl_trigger();
-    const int unit = blockIdx.x >> 3, n = (blockIdx.x & 7) * 32 + lane;
-    if (unit >= j.group[j.groups].unit0) return;
-    int lo = 0, hi = j.groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (j.group[mid].unit0 <= unit) lo = mid; else hi = mid;
-    }
-    while (j.group[lo + 1].unit0 <= unit) ++lo;   // (groups without units)
-    const PrefixGroup r = j.group[lo];
-    const RowBlocks rb(r.rows);
-    const int u = unit - r.unit0, h = u / rb.blocks, block = u - h * rb.blocks;
-    const int rows = min(kPxRows, r.rows - block * kPxRows);
-    if ((int)(blockIdx.x & 7) * 32 >= rows) return;
-    const int tiles = (int)((((long long)r.pages * j.block) + kPxTile - 1) / kPxTile);
-    const int cost = block == rb.blocks - 1 ? rb.last : 2;
-    const long long total = j.group[j.groups].start;
-    const long long at = r.start + (long long)tiles * ((long long)h * rb.cost() + 2LL * block);
-    const int c0 = span_owner(total, ctas, at);
-    const int c1 = span_owner(total, ctas, at + (long long)(tiles - 1) * cost);
-    const int e0 = blockIdx.y * 32 + half * 16;
-    float m = kPxNone, l = 0.f, o[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-    for (int c = c0 + way; c <= c1; c += kJoinWays) {
-        // the CTA's first tile of the unit, if it has one
-        const long long from = span_at(total, ctas, c), to = span_at(total, ctas, c + 1);
-        const int t = from > at ? (int)div_pos(from - at + cost - 1, cost) : 0;
-        if (t >= tiles || at + (long long)t * cost >= to) continue;
-        const float *p = px_part(j, ctas, c, t, c0 == c1, unit) + n;
-        const float mc = __ldcg(p + (size_t)j.D * kPxRows);
-        const float lc = __ldcg(p + (size_t)(j.D + 1) * kPxRows);
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __ldcg(p + (size_t)(e0 + i) * kPxRows);
-        const float top = fmaxf(m, mc), f = ex2f(m - top), g = ex2f(mc - top);
-        m = top;
-        l = fmaf(l, f, lc * g);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fmaf(o[i], f, x[i] * g);
-    }
-    const int row = block * kPxRows + n, tok = row / j.G;
-    const int64_t to = (int64_t)(r.first + tok) * j.Hq + h * j.G + (row - tok * j.G);
-    if (way == 1 && n < rows) {
-        // what attend left
-        const float2 ms = __ldcg(j.far_ms + to);
-        const float4 *p = reinterpret_cast<const float4 *>(j.far_o + to * j.D + e0);
-        const float top = fmaxf(m, ms.x), f = ex2f(m - top), g = ex2f(ms.x - top);
-        m = top;
-        l = fmaf(l, f, ms.y * g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 x = __ldcg(p + i);
-            o[4 * i] = fmaf(o[4 * i], f, x.x * g);
-            o[4 * i + 1] = fmaf(o[4 * i + 1], f, x.y * g);
-            o[4 * i + 2] = fmaf(o[4 * i + 2], f, x.z * g);
-            o[4 * i + 3] = fmaf(o[4 * i + 3], f, x.w * g);
-        }
-    }
-    if (way > 0) {
-        s_m[way][half][lane] = m;
-        s_l[way][half][lane] = l;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s_sum[way][half][i][lane] = o[i];
-    }
-    __syncthreads();
-    if (way > 0 || n >= rows) return;
-#pragma unroll
-    for (int w = 1; w < kJoinWays; ++w) {
-        const float mc = s_m[w][half][lane], top = fmaxf(m, mc), f = ex2f(m - top), g = ex2f(mc - top);
-        m = top;
-        l = fmaf(l, f, s_l[w][half][lane] * g);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fmaf(o[i], f, s_sum[w][half][i][lane] * g);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-            : "=r"(w[i]) : "f"(o[2 * i + 1] * inv), "f"(o[2 * i] * inv));
-    uint4 *dst = reinterpret_cast<uint4 *>(j.out + to * j.D + e0);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (j.lse && e0 == 0) j.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 constexpr size_t prefix_smem(int D)
@@ -1027,29 +1118,26 @@ cudaError_t prefix_setup()
     return e;
 }
 
-cudaError_t prefix_prep_launch(const PrefixJob &j, unsigned *counters, int n, cudaStream_t s)
+cudaError_t prefix_prep_launch(const PrefixJob &j, int sms, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     pdl_config(cfg, at, dim3(kPrepCtas), dim3(kPrepThreads), 0, s);
-    return cudaLaunchKernelEx(&cfg, prefix_prep_kernel, j, counters, n);
+    return cudaLaunchKernelEx(&cfg, prefix_prep_kernel, j, tail_warps(sms));
 }
 
-cudaError_t prefix_launch(const PrefixJob &j, int sms, int64_t units, cudaStream_t s)
+cudaError_t prefix_launch(const PrefixJob &j, int sms, cudaStream_t s)
 {
     CUtensorMap mk, mv;
-    if (!cache_map(&mk, j.cache[0], j.D, j.block, j.pages, j.H) ||
-        !cache_map(&mv, j.cache[1], j.D, j.block, j.pages, j.H))
+    if (!cache_map(&mk, j.cache[0], j.D, j.block, j.block, j.pages, j.H) ||
+        !cache_map(&mv, j.cache[1], j.D, j.block, j.block, j.pages, j.H))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     // (one CTA an SM, also at D = 64: each holds all of the SM's tensor memory)
     pdl_config(cfg, at, dim3(sms), dim3(kPxThreads), prefix_smem(128), s);
-    cudaError_t e = j.D == 64 ? cudaLaunchKernelEx(&cfg, prefix_kernel<64>, j, mk, mv)
-                              : cudaLaunchKernelEx(&cfg, prefix_kernel<128>, j, mk, mv);
-    if (e != cudaSuccess) return e;
-    pdl_config(cfg, at, dim3((unsigned)(units * 8), j.D / 32), dim3(kJoinThreads), 0, s);
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel, j, sms);
+    return j.D == 64 ? cudaLaunchKernelEx(&cfg, prefix_kernel<64>, j, mk, mv)
+                     : cudaLaunchKernelEx(&cfg, prefix_kernel<128>, j, mk, mv);
 }
 
 }  // namespace sv

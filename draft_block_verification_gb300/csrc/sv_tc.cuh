@@ -168,8 +168,8 @@ __device__ __forceinline__ bool at_wait(int *abort, int *err, uint64_t *bar, uin
     return at_wait_on(abort, err, bar, parity);
 }
 
-// Map of one side of the cache: [pages * H][block][D] bytes, a page's head at a
-// time, in the swizzle that the products read.
-bool cache_map(CUtensorMap *m, const uint8_t *cache, int D, int block, int pages, int H);
+// Map of one side of the cache: [pages * H][block][D] bytes, `rows` rows of a
+// page's head at a time, in the swizzle that the products read.
+bool cache_map(CUtensorMap *m, const uint8_t *cache, int D, int block, int rows, int pages, int H);
 
 }  // namespace sv
