@@ -326,17 +326,19 @@ bool kv_cache_ok(const void *cache, const float *scale)
 
 // sv_kv_prefix_attention's workspace: byte offsets, and its size.
 struct PrefixSpace {
-    size_t seq, group, arrived, unit_ctas, part_unit, part, tail, bytes;
+    size_t seq, span, arrived, unit_ctas, part_unit, part, tail, bytes;
     int64_t units;  // at most
     PrefixSpace(int sms, int T, int Hq, int H, int D, int B, int groups)
     {
         auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
         const int64_t rows = (int64_t)T * (Hq / H);
-        units = H * (rows / kPrefixRows + std::min<int64_t>(groups, std::min(B, T)));
+        // of groups, and of sequences with rows enough
+        units = H * (2 * rows / kPrefixRows + std::min<int64_t>(groups, std::min(B, T)) +
+                     std::min<int64_t>(B, rows / kTailMax));
         units = std::max(units, std::min<int64_t>(2 * units, sms / 2));  // (of half the rows)
         seq = 0;  // skip, seq_group, part0 [B], unit0 [B + 1], tail_stages
-        group = seq + up(((size_t)4 * B + 2) * sizeof(int32_t));
-        arrived = group + up(((size_t)groups + 1) * sizeof(PrefixGroup));
+        span = seq + up(((size_t)4 * B + 2) * sizeof(int32_t));
+        arrived = span + up(((size_t)groups + B + 1) * sizeof(PrefixSpan));
         unit_ctas = arrived + up((size_t)kTailParts * tail_warps(sms) * sizeof(unsigned));
         part_unit = unit_ctas + up((size_t)units * sizeof(int2));
         part = part_unit + up((size_t)2 * sms * sizeof(int32_t));
@@ -1105,7 +1107,7 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
                    {k_scale, v_scale}, table, kv_len, cu_new, prefix_len, cu_group, mask, B, T,
                    Hq, H, Hq / H, D, block, pages, cols, groups, mask_words, scale,
                    (uint16_t *)out, lse, seq, seq + B, seq + (size_t)3 * B, seq + (size_t)2 * B,
-                   seq + (size_t)4 * B + 1, (PrefixGroup *)(ws + w.group),
+                   seq + (size_t)4 * B + 1, (PrefixSpan *)(ws + w.span),
                    (unsigned *)(ws + w.arrived), h->sms, (int2 *)(ws + w.unit_ctas),
                    (int32_t *)(ws + w.part_unit), (float *)(ws + w.part),
                    (float *)(ws + w.tail), h->d_err};

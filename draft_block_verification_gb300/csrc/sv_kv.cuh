@@ -63,13 +63,14 @@ cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s);
 
 // Attention over a shared prefix: prep finds what is shared and cuts the work, the
 // prefix kernel reads the shared pages, the tail kernel the rest, and joins.
-// A group's shared pages and where its work starts; an entry more than there are
-// groups, with the totals.
-struct PrefixGroup {
-    int first, rows;           // first row of q, query rows a cache head
-    int pages, lead;           // shared, as the table row of this sequence has them
-    long long start;           // in tiles of slots
-    int unit0, block;          // rows of a unit
+// A span: pages that query rows read, a group's shared ones or a sequence's own.
+// First the groups', then the sequences', then an entry with the totals.
+struct PrefixSpan {
+    int first, rows;           // first row of q, query rows a cache head (0: no work)
+    int lead, page0;           // the table row, and its first page
+    int end, ctx;              // tokens from there on, and those that every row sees
+    long long start;           // where its work starts, in tiles of slots
+    int unit0, block;          // its first unit, rows of a unit
 };
 struct PrefixJob {
     const uint16_t *q;         // [T, Hq, D] bf16
@@ -89,7 +90,7 @@ struct PrefixJob {
     int32_t *unit0;            // [B + 1] the tail's tasks of the sequences before
     int32_t *part0;            // [B] its parts
     int32_t *tail_stages;      // of a task, at most
-    PrefixGroup *group;        // [groups + 1]
+    PrefixSpan *span;          // [groups + B + 1]
     unsigned *tail_arrived;    // a counter a part
     // from the prefix kernel
     int prefix_ctas;
@@ -105,6 +106,7 @@ size_t prefix_part_bytes(int sms, int64_t units, int D);
 cudaError_t prefix_setup();
 cudaError_t prefix_prep_launch(const PrefixJob &j, int sms, cudaStream_t s);
 cudaError_t prefix_launch(const PrefixJob &j, int sms, cudaStream_t s);
+constexpr int kTailMax = 32;                                 // rows a cache head that the tail reads for
 constexpr int kTailTiles = 2;                                // eights of rows of a task
 constexpr int kTailTile = 32;                                // tokens of a stage
 constexpr int kTailParts = 2;                                // ranges that join, a warp

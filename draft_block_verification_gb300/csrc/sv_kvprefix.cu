@@ -13,12 +13,14 @@
 //            rows that are equal, no further than the caller's bound and the
 //            tokens before each sequence's new ones.  So a bound that is too
 //            large changes nothing.  And how the work is cut.
-//   prefix   the shared pages, below.
-//   tail     (sv_kvtail.cu) the rest of each sequence, and the join.
+//   prefix   below: the shared pages, and what sequences of many rows have of
+//            their own.
+//   tail     (sv_kvtail.cu) what sequences of few rows have, and the join.
 //
-// Shape of the prefix.  All rows see all of it, so there is nothing to mask but
-// the end of the last tile.  A unit is a cache head's block of up to 256 query
-// rows, two times 128 (slots); a tile is 128 tokens.  Queries are the 128 rows
+// Shape of the prefix kernel.  A span is a run of pages that a run of query rows reads:
+// a group's shared pages, which all of its rows see whole, or a sequence's own ones,
+// where the new tokens are masked.  A unit is a cache head's block of up to 256 rows
+// of a span, two times 128 (slots); a tile is 128 tokens.  Queries are the 128 rows
 // of the products, a row's scores lie in one thread's registers, and maxima and
 // sums need no exchange:
 //   S [128 rows x 128 tokens] = Q K^T    in 8 bits: the cache's bytes as they
@@ -41,8 +43,8 @@
 // 2^8 are a row's sums rescaled.
 //
 // Split.  Tiles of all units laid end to end are cut into equal spans, one a
-// CTA.  A unit's piece leaves its sums in the workspace, [D][256] fp32 with rows
-// contiguous; the tail kernel adds a unit's pieces.
+// CTA.  A unit's piece leaves its sums in the workspace, fp32, four elements of 256
+// rows after the other; the tail kernel adds a unit's pieces.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,6 +57,8 @@ namespace sv {
 constexpr int kPxTile = 128;           // tokens of a tile
 constexpr int kPxRows = kPrefixRows;   // query rows of a unit, two slots of 128
 constexpr int kPxK = 3, kPxV = 2;      // tiles of keys and of values in flight
+constexpr int kPxPieces = 4;           // pieces known ahead
+constexpr int kPxReaders = 14;         // warps that read them
 constexpr int kPxRing = 8;             // tiles whose scales are kept
 constexpr int kPxSoft = 8;             // softmax warps, four a slot
 constexpr int kPxThreads = 512;        // + 4 converting warps, producer, 2 issuers, 1 idle
@@ -71,17 +75,27 @@ constexpr float kPxNone = -1e30f;      // maximum of no tokens
 // ---------------------------------------------------------------------------
 constexpr int kPrepCtas = 8, kPrepThreads = 512;
 
+// Row blocks of a head, and costs, in tiles of a slot (1,750 cycles).  What a piece's
+// start and end take (queries, first scores, sums) is counted at the front of a unit.
+constexpr int kPxUnitCost = 6;
 struct RowBlocks {
-    int blocks, full, last;            // row blocks of a head; cost of one and of the last
+    int blocks, full, last;            // blocks; a tile's cost, in all blocks and in the last
     __device__ __forceinline__ RowBlocks(int rows, int block)
     {
         blocks = (rows + block - 1) / block;
         full = block > 128 ? 2 : 1;    // one slot's tiles cost half
         last = rows - (blocks - 1) * block > 128 ? 2 : 1;
     }
-    // of all blocks, in slots' tiles a tile
-    __device__ __forceinline__ int cost() const { return full * (blocks - 1) + last; }
+    __device__ __forceinline__ long long unit(int tiles) const
+    {
+        return kPxUnitCost + (long long)tiles * full;
+    }
+    __device__ __forceinline__ long long head(int tiles) const
+    {
+        return (blocks - 1) * unit(tiles) + kPxUnitCost + (long long)tiles * last;
+    }
 };
+__device__ __forceinline__ int px_tiles(int end) { return (int)(((long long)end + kPxTile - 1) / kPxTile); }
 
 // One cluster: its warps take the sequences, its first CTA's the groups.
 __global__ void __cluster_dims__(kPrepCtas, 1, 1) __launch_bounds__(kPrepThreads)
@@ -173,7 +187,7 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     if (bad)
         for (int b = tid; b < j.B; b += kPrepThreads) j.skip[b] = j.seq_group[b] = 0;
     for (int g = warp; g < j.groups; g += kWarps) {
-        PrefixGroup r = {0, 0, 0, 0, 0, 0, kPxRows};
+        PrefixSpan r = {};
         if (!bad) {
             const int lo = edge(g), hi = edge(g + 1);
             int pages = 0x7FFFFFFF, lead = 0x7FFFFFFF, live = 0;
@@ -200,11 +214,11 @@ prefix_prep_kernel(const PrefixJob j, int warps)
             if (rows > 0) {
                 r.first = first;
                 r.rows = (int)rows;
-                r.pages = pages;
                 r.lead = lead;
+                r.end = r.ctx = pages << shift;
             }
         }
-        if (lane == 0) j.group[g] = r;
+        if (lane == 0) j.span[g] = r;
     }
     __syncthreads();
     // the tail's tasks: what is left of each sequence, cut into ranges of `c` stages
@@ -213,8 +227,24 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         const bool fine = tokens(b, n, L);
         if (!fine) latch(j.err, SV_ERR_DEVICE_BOUNDS);
         blocks = fine && n > 0 ? (long long)TailBlocks(n * j.G).blocks * j.H : 0;
-        stages = blocks ? (L - __ldcg(j.skip + b) * j.block + kTailTile - 1) / kTailTile : 0;
+        const int own = L - __ldcg(j.skip + b) * j.block;
+        // (rows that the prefix kernel takes are only joined)
+        stages = !blocks ? 0 : n * j.G > kTailMax ? 1 : (own + kTailTile - 1) / kTailTile;
     };
+    for (int b = tid; b < j.B; b += kPrepThreads) {
+        int n, L;
+        PrefixSpan r = {};
+        if (tokens(b, n, L) && n * j.G > kTailMax) {
+            const int skip = __ldcg(j.skip + b);
+            r.first = j.cu[b];
+            r.rows = n * j.G;
+            r.lead = b;
+            r.page0 = skip;
+            r.end = L - (skip << shift);
+            r.ctx = r.end - n;
+        }
+        j.span[j.groups + b] = r;
+    }
     long long all = 0, many = 0;
     for (int b = tid; b < j.B; b += kPrepThreads) {
         long long blocks;
@@ -288,25 +318,26 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     // where CTAs by far outnumber the units, units of half the rows halve what the
     // tail has to read (with as many units as CTAs the halves would only have values
     // brought to bf16 twice).
+    const int spans = j.groups + j.B;
     int big = 0;
-    for (int g = lane; g < j.groups; g += 32)
-        if (__ldcg(&j.group[g].pages)) big += RowBlocks(__ldcg(&j.group[g].rows), kPxRows).blocks * j.H;
+    for (int g = lane; g < spans; g += 32) {
+        const int rows = __ldcg(&j.span[g].rows);
+        if (rows) big += RowBlocks(rows, kPxRows).blocks * j.H;
+    }
     big = __reduce_add_sync(0xFFFFFFFFu, big);
     const int block = 4 * big < j.prefix_ctas ? 128 : kPxRows;
-    // where each group's work and units start
+    // where each span's work and units start
     long long at = 0;
     int unit = 0;
-    for (int g0 = 0; g0 < j.groups; g0 += 32) {
+    for (int g0 = 0; g0 < spans; g0 += 32) {
         const int g = g0 + lane;
         long long w = 0;
         int u = 0;
-        if (g < j.groups) {
-            const PrefixGroup *r = j.group + g;
-            const int pages = __ldcg(&r->pages), rows = __ldcg(&r->rows);
-            if (pages) {
+        if (g < spans) {
+            const int rows = __ldcg(&j.span[g].rows);
+            if (rows) {
                 const RowBlocks rb(rows, block);
-                const long long tiles = (((long long)pages << shift) + kPxTile - 1) / kPxTile;
-                w = tiles * rb.cost() * j.H;
+                w = rb.head(px_tiles(__ldcg(&j.span[g].end))) * j.H;
                 u = rb.blocks * j.H;
             }
         }
@@ -321,19 +352,19 @@ prefix_prep_kernel(const PrefixJob j, int warps)
                 us += c;
             }
         }
-        if (g < j.groups) {
-            j.group[g].start = at + ws - w;
-            j.group[g].unit0 = unit + us - u;
-            j.group[g].block = block;
+        if (g < spans) {
+            j.span[g].start = at + ws - w;
+            j.span[g].unit0 = unit + us - u;
+            j.span[g].block = block;
         }
         at += __shfl_sync(0xFFFFFFFFu, ws, 31);
         unit += __shfl_sync(0xFFFFFFFFu, us, 31);
     }
     if (lane == 0) {
-        PrefixGroup r = {0, 0, 0, 0, 0, 0, kPxRows};
+        PrefixSpan r = {};
         r.start = at;
         r.unit0 = unit;
-        j.group[j.groups] = r;
+        j.span[spans] = r;
     }
 }
 
@@ -341,67 +372,66 @@ prefix_prep_kernel(const PrefixJob j, int warps)
 // Units and pieces.
 // ---------------------------------------------------------------------------
 struct PxPiece {
-    int g, h, row0, rows;              // group, cache head, rows of the group
+    int h, row0, rows;                 // cache head, rows of the span (0: no more pieces)
     int t0, t1, tiles;                 // tiles [t0, t1) of the unit's
     int unit;                          // of the call
-    int first, lead, pages;
+    int first, lead, page0, end, ctx;  // of the span
     __device__ __forceinline__ bool wide() const { return rows > 128; }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
-// A tile belongs to the span that its first unit of cost lies in.
+// A CTA's pieces, found by its producer.  A tile belongs to the share that its first
+// unit of cost lies in.
 struct PxWalk {
     long long pos, end;
-    int g;
-    __device__ __forceinline__ void start(const PrefixJob &j, long long from, long long to)
-    {
-        pos = from;
-        end = to;
-        int lo = 0, hi = j.groups;     // the last group that starts at pos or before
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (j.group[mid].start <= pos) lo = mid; else hi = mid;
-        }
-        g = lo;
-    }
-    __device__ __forceinline__ bool next(const PrefixJob &j, PxPiece &p)
+    __device__ __forceinline__ bool next(const PrefixJob &j, PxPiece &p, int lane)
     {
         for (;;) {
             if (pos >= end) return false;
-            while (g < j.groups && j.group[g + 1].start <= pos) ++g;
-            if (g >= j.groups) return false;
-            const PrefixGroup r = j.group[g];
+            // the last span that starts at pos or before
+            int lo = 0, n = j.groups + j.B;
+            while (n > 1) {
+                const int step = (n + 31) >> 5, at = lo + lane * step;
+                const bool on = at < lo + n && j.span[at].start <= pos;
+                const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, on));  // (lane 0 is on)
+                n = min(step, n - k * step);
+                lo += k * step;
+            }
+            const PrefixSpan r = j.span[lo];
             const RowBlocks rb(r.rows, r.block);
-            const int tiles = (int)((((long long)r.pages * j.block) + kPxTile - 1) / kPxTile);
-            const long long head = (long long)tiles * rb.cost(), wide = (long long)tiles * rb.full;
+            const int tiles = px_tiles(r.end);
+            const long long head = rb.head(tiles), unit = rb.unit(tiles);
             long long x = pos - r.start;
             const int h = (int)div_pos(x, head);
             x -= h * head;
-            const int block = min((int)div_pos(x, wide), rb.blocks - 1);
-            x -= block * wide;
+            const int block = min((int)div_pos(x, unit), rb.blocks - 1);
+            x -= block * unit;
             const int cost = block == rb.blocks - 1 ? rb.last : rb.full;
-            const int t = (int)div_pos(x + cost - 1, cost);
-            pos += (long long)t * cost - x;
-            if (t >= tiles) continue;  // (the unit's last tile starts before the span)
+            // a tile lies behind its unit's front
+            const long long front = pos - x + kPxUnitCost;
+            const int t = x <= kPxUnitCost ? 0 : (int)div_pos(x - kPxUnitCost + cost - 1, cost);
+            pos = front + (long long)min(t, tiles) * cost;
+            if (t >= tiles) continue;  // (the unit's last tile starts before the share)
             if (pos >= end) return false;
-            const int n = (int)min((long long)(tiles - t), div_pos(end - pos + cost - 1, cost));
-            pos += (long long)n * cost;
-            p.g = g;
+            const int m = (int)min((long long)(tiles - t), div_pos(end - pos + cost - 1, cost));
+            pos += (long long)m * cost;
             p.h = h;
             p.row0 = block * r.block;
             p.rows = min(r.block, r.rows - p.row0);
             p.t0 = t;
-            p.t1 = t + n;
+            p.t1 = t + m;
             p.tiles = tiles;
             p.unit = r.unit0 + h * rb.blocks + block;
             p.first = r.first;
             p.lead = r.lead;
-            p.pages = r.pages;
+            p.page0 = r.page0;
+            p.end = r.end;
+            p.ctx = r.ctx;
             return true;
         }
     }
 };
 
-// A piece's sums: [D][256] of values, then 256 maxima and 256 sums of weights.
+// A piece's sums: [D / 4][256][4] of values, then 256 maxima and 256 sums of weights.
 // CTA i has parts 2 i (its first unit, begun by another CTA) and 2 i + 1 (one that
 // another CTA goes on with); whole units come behind those.
 __host__ __device__ constexpr size_t px_part_floats(int D) { return (size_t)kPxRows * (D + 2); }
@@ -421,6 +451,9 @@ struct PxShared {
     // and its inverse; the scale's power of two, as two factors
     float4 sc[kPxRing][8];
     uint32_t up[kPxRing][8], more[kPxRing][8];
+    PxPiece piece[kPxPieces];          // handed from the producer to the other roles
+    uint64_t piece_full[kPxPieces], piece_empty[kPxPieces];
+    uint32_t lost[2][4];               // tokens of a tile with NaN in their value, a bit each
     float c[kPxRows];                  // factor from S to log2 units, per row
     float m[2][128], l[2][128];        // of the two slots, where they share rows
 };
@@ -571,17 +604,8 @@ __device__ __forceinline__ void px_queries(const PrefixJob &j, PxShared *sh, cha
     for (int k = 0; k < kAhead; ++k) fetch(raw[k]);
 #pragma unroll 1
     for (int n = mine; n < all; n += kStep) {
-        float x[16];
-        {
-            float a[8], b[8];
-            VecTraits<uint16_t>::unpack(raw[0][0], a);
-            VecTraits<uint16_t>::unpack(raw[0][1], b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = a[i];
-                x[8 + i] = b[i];
-            }
-        }
+        const uint32_t x[8] = {raw[0][0].x, raw[0][0].y, raw[0][0].z, raw[0][0].w,
+                               raw[0][1].x, raw[0][1].y, raw[0][1].z, raw[0][1].w};
 #pragma unroll
         for (int k = 0; k + 1 < kAhead; ++k) {
             raw[k][0] = raw[k + 1][0];
@@ -589,31 +613,41 @@ __device__ __forceinline__ void px_queries(const PrefixJob &j, PxShared *sh, cha
         }
         fetch(raw[kAhead - 1]);
         // (as integers NaN is above infinity, and above the rest)
-        uint32_t top = 0;
+        uint32_t two = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) two = __vmaxu2(two, x[i] & 0x7FFF7FFFu);
+        uint32_t top = max(two << 16, two & 0xFFFF0000u);
 #pragma unroll
         for (int i = kLanes / 2; i > 0; i >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
         const bool odd = top >= 0x7F800000u;    // NaN or an infinity
-        // 2^e brings the largest element to [128, 256)
+        // 2^e brings the largest element to [128, 256); fp16 holds the rest as it is, down
+        // to steps of 2^-24
         const int e = top > 0 && !odd ? min(134 - (int)(top >> 23), 126) : 0;
         const float up = __int_as_float((127 + e) << 23);
         if (l == 0)
             sh->c[n] = n >= pc.rows ? 0.f
                        : odd        ? __int_as_float(0x7FC00000)
                                     : fabsf(j.softmax_scale) * 1.4426950408889634f / up;
-        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+        uint32_t hi[4], lo[4];
+        const float by = sign * up;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            uint16_t h8, l8;
-            const float a = x[i] * (sign * up), b = x[i + 1] * (sign * up);
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h8) : "f"(b), "f"(a));
-            uint32_t h16;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h8));
-            const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&h16));
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l8) : "f"(b - h.y), "f"(a - h.x));
-            hi[i >> 2] |= (uint32_t)h8 << (8 * (i & 2));
-            lo[i >> 2] |= (uint32_t)l8 << (8 * (i & 2));
+        for (int i = 0; i < 4; ++i) {
+            uint16_t h8[2], l8[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w = x[2 * i + k];
+                uint32_t v, back;
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                    : "=r"(v)
+                    : "f"(__uint_as_float(w & 0xFFFF0000u) * by), "f"(__uint_as_float(w << 16) * by));
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h8[k]) : "r"(v));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h8[k]));
+                const __half2 d = __hsub2(*reinterpret_cast<__half2 *>(&v), *reinterpret_cast<__half2 *>(&back));
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+                    : "=h"(l8[k]) : "r"(*reinterpret_cast<const uint32_t *>(&d)));
+            }
+            hi[i] = h8[0] | (uint32_t)h8[1] << 16;
+            lo[i] = l8[0] | (uint32_t)l8[1] << 16;
         }
         const int r = n & 127, sw = D == 128 ? r & 7 : (r >> 1) & 3;
         char *to = smem_q + (n >> 7) * (2 * kSide) + r * D + ((l ^ sw) << 4);
@@ -622,19 +656,63 @@ __device__ __forceinline__ void px_queries(const PrefixJob &j, PxShared *sh, cha
     }
 }
 
+// The next piece, for a warp that is not the producer; false: no more.
+__device__ __forceinline__ bool px_next(PxShared *sh, int *err, uint32_t &pieces, PxPiece &p, int lane)
+{
+    const int i = pieces % kPxPieces;
+    bool ok = px_wait(sh, err, &sh->piece_full[i], pieces / kPxPieces & 1);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok) p = sh->piece[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->piece_empty[i]);
+    ++pieces;
+    return ok && p.rows > 0;
+}
+
+// Which of a tile's 128 tokens a row sees, a bit each: its token is new token i of the
+// sequence, `at` the tile's first token.
+struct PxSees {
+    uint32_t w[4];
+    __device__ __forceinline__ PxSees(const PrefixJob &j, const PxPiece &pc, int i, bool live, int at)
+    {
+        const uint32_t *m = j.mask && live ? j.mask + (int64_t)(pc.first + i) * j.words : nullptr;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int p = at + 32 * k, q = p - pc.ctx;  // of the word's first token
+            // tokens before the new ones, and before the end
+            auto first = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+            uint32_t see;
+            if (j.mask) {
+                see = first(-q);
+                if (m && q > -32) {
+                    // bits q to q + 31 of the row's mask
+                    const int a = q >> 5, s = q & 31;
+                    const uint32_t lo = a >= 0 && a < j.words ? m[a] : 0u;
+                    const uint32_t hi = a + 1 >= 0 && a + 1 < j.words ? m[a + 1] : 0u;
+                    see |= __funnelshift_r(lo, hi, s);
+                }
+            } else {
+                see = first(i + 1 - q);
+            }
+            w[k] = see & first(pc.end - p);
+        }
+    }
+};
+
 // One tile of a softmax thread: a row's 128 scores to weights, 64 at a time.
 // M (a whole number), l: the row's running maximum and sum of weights.  Weights are
 // taken against the maximum in use before it is known whether one passes it by too
 // much; where one does, M moves, and what there is of the row (sums, values, the
 // tile's first 64 weights) is scaled by the power of two.
-// same: pages of 64 tokens or more, one scale for the 64.
+// same: pages of 64 tokens or more, one scale for the 64.  EDGE: only the tokens of
+// `sees` count, and those of `lost` are NaN.
 // (The factors are taken before the scores, the weights stored after them: loads
 // and stores between would keep the scores' chains from overlapping.)
-template <int D>
+template <int D, bool EDGE>
 __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
                                              uint64_t *pv_done, uint32_t count, bool first,
                                              const float4 *sc, bool same, float c, float &M,
-                                             float &l)
+                                             float &l, const uint32_t *sees, const uint32_t *lost)
 {
     bool ok = true;
 #pragma unroll 1
@@ -650,6 +728,16 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
             if (!same) f[k] = sc[4 * q + k];
         }
         tc_wait_ld(s);
+        if (EDGE) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                const uint32_t see = sees[2 * q + (i >> 5)], gone = lost[2 * q + (i >> 5)];
+                if (!(see >> (i & 31) & 1))
+                    s[i] = -INFINITY;
+                else if (gone >> (i & 31) & 1)
+                    s[i] = __int_as_float(0x7FC00000);
+            }
+        }
         uint32_t p[32];
         float add;
 #pragma unroll 1
@@ -671,24 +759,24 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
                 }
                 add = fmaf(sum.x + sum.y, f[k].z, add);
             }
-            // (M is unset, at kPxNone, before a row's first tile)
+            // (M is unset, at kPxNone, before a row's first token)
             if (!__any_sync(0xFFFFFFFFu, top > kPxLazy)) break;
             float to = top > kPxLazy ? M + ceilf(top) : M;
+            float scale = pow2_int(M - to);
             if (M == kPxNone) {
-                // no sum was taken against it: from the scores themselves
-                to = -INFINITY;
+                // no sum was taken against it: from the scores themselves (it stays where
+                // there are none)
+                float m = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float a = s[16 * k], b = s[16 * k + 1];
 #pragma unroll
                     for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
-                    to = fmaxf(to, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
+                    m = fmaxf(m, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
                 }
-                to = to > -INFINITY ? ceilf(to) : 0.f;
-                M = to;
-                continue;
+                to = m > -INFINITY ? ceilf(m) : M;
+                scale = 1.f;
             }
-            const float scale = pow2_int(M - to);
             M = to;
             l *= scale;
             if (!first) {
@@ -763,6 +851,10 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             mbar_init(&sh->pv_done[i], 1);
         }
         for (int i = 0; i < kPxRing; ++i) mbar_init(&sh->scales[i], 1);
+        for (int i = 0; i < kPxPieces; ++i) {
+            mbar_init(&sh->piece_full[i], 1);
+            mbar_init(&sh->piece_empty[i], kPxReaders);
+        }
         mbar_init(&sh->q_full, kPxSoft);
         mbar_fence_init();
         sh->abort = 0;
@@ -780,11 +872,8 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const int ctas = gridDim.x;
-    const long long total = j.group[j.groups].start;
-    PxWalk walk;
-    walk.start(j, span_at(total, ctas, blockIdx.x), span_at(total, ctas, blockIdx.x + 1));
     PxPiece pc;
-    uint32_t it = 0;                            // tiles of this CTA so far
+    uint32_t it = 0, pieces = 0;                // tiles and pieces of this CTA so far
     bool ok = true;
 
     if (warp < kPxSoft) {
@@ -794,13 +883,17 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         const uint32_t s_at = lanes + slot * 128, o_at = lanes + 256 + slot * 128;
         uint32_t count = 0;                     // this slot's tiles so far
         if (tid == 0) j.part_unit[2 * blockIdx.x] = j.part_unit[2 * blockIdx.x + 1] = -1;
-        while (ok && walk.next(j, pc)) {
+        while (ok && px_next(sh, j.err, pieces, pc, lane)) {
             const bool wide = pc.wide();
             px_queries<D>(j, sh, s_q, pc);
             fence_async();
             bar_or(1, kPxSoft * 32, false);     // the rows' factors are there
             if (lane == 0) mbar_arrive(&sh->q_full);
-            const float c = sh->c[wide ? slot * 128 + r : r];
+            const int row = wide ? slot * 128 + r : r;
+            // (a score that is hidden, -inf, keeps its sign against a factor of 0)
+            float c = sh->c[row];
+            if (c == 0.f) c = 1e-38f;
+            const int token = (pc.row0 + row) / j.G;  // of the span's
             const int step = wide ? 1 : 2, from = wide ? 0 : slot, n = pc.t1 - pc.t0;
             float M = kPxNone, l = 0.f;
             for (int i = from; i < n && ok; i += step, ++count) {
@@ -810,8 +903,22 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                ok = px_soft_tile<D>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
-                                     sh->sc[ring], j.block >= 64, c, M, l);
+                const int at = (pc.t0 + i) * kPxTile;
+                if (__builtin_expect(at + kPxTile <= pc.ctx, 1)) {
+                    ok = px_soft_tile<D, false>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
+                                                sh->sc[ring], j.block >= 64, c, M, l, nullptr, nullptr);
+                } else {
+                    // (which tokens are lost is known once the values are converted)
+                    const uint32_t sb = (it + i) & 1;
+                    ok = px_wait(sh, j.err, &sh->full_b[sb], ((it + i) >> 1) & 1);
+                    const PxSees sees(j, pc, token, row < pc.rows, at);
+                    uint32_t lost[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) lost[k] = sh->lost[sb][k];
+                    ok = __all_sync(0xFFFFFFFFu, ok) &&
+                         px_soft_tile<D, true>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
+                                               sh->sc[ring], j.block >= 64, c, M, l, sees.w, lost);
+                }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 tc_fence_before();
                 __syncwarp();
@@ -835,41 +942,44 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 if (!pc.whole()) j.part_unit[2 * blockIdx.x + (pc.t0 == 0 ? 1 : 0)] = pc.unit;
             }
             float *part = px_part(j, ctas, blockIdx.x, pc.t0, pc.whole(), pc.unit);
+            float4 *to = reinterpret_cast<float4 *>(part) + row;
+            float *ml = part + (size_t)D * kPxRows + row;
             if (wide) {
-                float *at = part + slot * 128 + r;
 #pragma unroll 1
-                for (int i = 0; i < D; i += 16) {
-                    float o[16];
-                    tc_ld8(o_at + i, o);
-                    tc_ld8(o_at + i + 8, o + 8);
+                for (int i = 0; i < D; i += 32) {
+                    float o[32];
+                    tc_ld32(o_at + i, o);
                     tc_wait_ld(o);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) at[(size_t)(i + q) * kPxRows] = o[q];
+                    for (int q = 0; q < 8; ++q)
+                        to[(i / 4 + q) * kPxRows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
-                at[(size_t)D * kPxRows] = M;
-                at[(size_t)(D + 1) * kPxRows] = l;
+                ml[0] = M;
+                ml[kPxRows] = l;
             } else {
                 // both slots' sums of a row; half of its elements each
                 const float m0 = sh->m[0][r], m1 = n > 1 ? sh->m[1][r] : kPxNone;
                 const float m = fmaxf(m0, m1), f0 = ex2f(m0 - m), f1 = n > 1 ? ex2f(m1 - m) : 0.f;
-                float *at = part + r;
 #pragma unroll 1
-                for (int i = slot * (D / 2); i < (slot + 1) * (D / 2); i += 8) {
-                    float a[8], b[8];
+                for (int i = slot * (D / 2); i < (slot + 1) * (D / 2); i += 16) {
+                    float a[16], b[16];
                     tc_ld8(lanes + 256 + i, a);
-                    tc_wait_ld(a);
+                    tc_ld8(lanes + 256 + i + 8, a + 8);
                     if (n > 1) {
                         tc_ld8(lanes + 384 + i, b);
-                        tc_wait_ld(b);
+                        tc_ld8(lanes + 384 + i + 8, b + 8);
                     }
+                    tc_wait_ld(a);
+                    if (n > 1) tc_wait_ld(b);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        at[(size_t)(i + q) * kPxRows] = n > 1 ? fmaf(b[q], f1, a[q] * f0) : a[q];
+                    for (int q = 0; q < 16; ++q) a[q] = n > 1 ? fmaf(b[q], f1, a[q] * f0) : a[q];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        to[(i / 4 + q) * kPxRows] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
                 }
                 if (slot == 0) {
-                    at[(size_t)D * kPxRows] = m;
-                    at[(size_t)(D + 1) * kPxRows] = n > 1 ? fmaf(sh->l[1][r], f1, sh->l[0][r] * f0)
-                                                          : sh->l[0][r];
+                    ml[0] = m;
+                    ml[kPxRows] = n > 1 ? fmaf(sh->l[1][r], f1, sh->l[0][r] * f0) : sh->l[0][r];
                 }
             }
             tc_fence_before();
@@ -881,7 +991,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         if (warp < 12) {
             // ---- the values to bf16, a token a thread
             const int tk = tid - kPxSoft * 32;
-            while (ok && walk.next(j, pc)) {
+            while (ok && px_next(sh, j.err, pieces, pc, lane)) {
                 for (int t = pc.t0; t < pc.t1; ++t, ++it) {
                     const int st = it % kPxV, sb = it & 1, ring = it % kPxRing;
                     ok = px_wait(sh, j.err, &sh->scales[ring], (it / kPxRing) & 1);
@@ -894,6 +1004,17 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     const char *src = s_v + st * kSide + tk * D;
                     char *dst = s_b + sb * kWideV + tk * 128;
                     const int sw = D == 128 ? tk & 7 : (tk >> 1) & 3;
+                    // New tokens may be NaN, which would become numbers here.
+                    if (__builtin_expect((t + 1) * kPxTile > pc.ctx, 0)) {
+                        bool nan = false;
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src + (i << 4));
+                            nan |= has_nan(w.x) | has_nan(w.y) | has_nan(w.z) | has_nan(w.w);
+                        }
+                        const uint32_t m = __ballot_sync(0xFFFFFFFFu, nan);
+                        if (lane == 0) sh->lost[sb][warp - kPxSoft] = m;
+                    }
 #pragma unroll 2
                     for (int i = 0; i < D / 16; ++i) {
                         const uint4 w = *reinterpret_cast<const uint4 *>(src + ((i ^ sw) << 4));
@@ -922,14 +1043,28 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 }
             }
         } else if (warp == 12) {
-            // ---- producer: the pages of each tile, looked up 32 at a time
+            // ---- producer: the pieces, and the pages of each tile, looked up 32 at a time
             const int shift = 31 - __clz(j.block), per_tile = kPxTile >> shift;
             const int inner = lane & (per_tile - 1);
-            while (ok && walk.next(j, pc)) {
-                const int32_t *tab = j.table + (int64_t)pc.lead * j.cols;
+            const long long total = j.span[j.groups + j.B].start;
+            PxWalk walk = {span_at(total, ctas, blockIdx.x), span_at(total, ctas, blockIdx.x + 1)};
+            for (bool more = true; ok && more;) {
+                more = walk.next(j, pc, lane);
+                if (!more) pc.rows = 0;
+                const int slot = pieces % kPxPieces;
+                ok = px_wait(sh, j.err, &sh->piece_empty[slot], (pieces / kPxPieces & 1) ^ 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (lane == 0) {
+                    sh->piece[slot] = pc;
+                    mbar_arrive(&sh->piece_full[slot]);
+                }
+                ++pieces;
+                if (!ok || !more) break;
+                const int pages = (int)(((long long)pc.end + j.block - 1) >> shift);
+                const int32_t *tab = j.table + (int64_t)pc.lead * j.cols + pc.page0;
                 auto window = [&](int w0, int &page, float &ks, float &vs) {
-                    page = w0 + lane < pc.pages ? tab[w0 + lane] : -1;
-                    if (w0 + lane < pc.pages && (page < 0 || page >= j.pages)) {
+                    page = w0 + lane < pages ? tab[w0 + lane] : -1;
+                    if (w0 + lane < pages && (page < 0 || page >= j.pages)) {
                         latch(j.err, SV_ERR_DEVICE_BOUNDS);
                         page = -1;
                     }
@@ -954,7 +1089,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         window(w0 + 32, npage, nks, nvs);
                     }
                     const bool mine = lane - (p0 - w0) >= 0 && lane - (p0 - w0) < per_tile;
-                    const bool live = w0 + lane < pc.pages;
+                    const bool live = w0 + lane < pages;
                     // (behind the last page the tile's first one once more: tokens
                     // of weight 0, but no NaN)
                     const int begin = __shfl_sync(0xFFFFFFFFu, page, p0 - w0);
@@ -980,7 +1115,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         const int e = (int)(u >> 23) - 127;
                         const float f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
                         const float4 sc = live ? make_float4(ks, f == 1.f ? 0.f : log2f(f), 1.f / f, 0.f)
-                                               : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                                               : make_float4(1.f, -INFINITY, 0.f, 0.f);
                         const uint32_t up = (uint32_t)(127 + 120 + min(e, kPxTop)) << 7;  // bf16
                         const uint32_t more = (uint32_t)(127 + max(e - kPxTop, 0)) << 7;
                         for (int i = 0; i < j.block >> 4; ++i) {
@@ -1019,12 +1154,12 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             const uint64_t dq0 = tc_desc(smem_u32(s_q), 16, 8 * D, kSwz);
             const uint64_t db0 = tc_desc(smem_u32(s_b), kPxTile * 128, 1024, 2);
             const bool one = elect_one();
-            uint32_t count = 0, pieces = 0, wides = 0;
-            while (ok && walk.next(j, pc)) {
+            uint32_t count = 0, wides = 0;
+            while (ok && px_next(sh, j.err, pieces, pc, lane)) {
                 const bool wide = pc.wide();
                 const int n = pc.t1 - pc.t0, step = wide ? 1 : 2;
                 const uint64_t dq = dq0 + (wide ? slot : 0) * (2 * kSide >> 4);
-                ok = px_wait(sh, j.err, &sh->q_full, pieces++ & 1);
+                ok = px_wait(sh, j.err, &sh->q_full, (pieces - 1) & 1);
                 // tiles of this slot, its own first one ahead
 #pragma unroll 1
                 for (int i = (wide ? 0 : slot) - step; i < n && ok; i += step) {

@@ -56,6 +56,7 @@ struct TailWarp {
 // A task: sequence, cache head, rows, stages.
 struct TailTask {
     int b, h, row0, rows, first, n, L, skip, z, nz;
+    bool own;                          // the sequence's own tokens are read here
     int s0, s1;                        // stages of 32 tokens behind the skipped pages
     int part0;                         // counter and parts of its rows: their first
 };
@@ -84,7 +85,8 @@ __device__ __forceinline__ TailTask tail_task(const PrefixJob &j, int u, int lan
     t.skip = j.skip[t.b];
     const int c = *j.tail_stages, rows = t.n * j.G;
     const TailBlocks rb(rows);
-    const int own = t.L - t.skip * j.block, all = (own + kTlTile - 1) / kTlTile;
+    t.own = rows <= kTailMax;
+    const int own = t.L - t.skip * j.block, all = t.own ? (own + kTlTile - 1) / kTlTile : 1;
     t.nz = (all + c - 1) / c;
     const int i = u - j.unit0[t.b], q = i / t.nz;
     t.z = i - q * t.nz;
@@ -93,7 +95,7 @@ __device__ __forceinline__ TailTask tail_task(const PrefixJob &j, int u, int lan
     t.rows = min(rb.rows, rows - t.row0);
     // without a mask no row sees past its own token
     const int sees = j.mask ? own : own - t.n + (t.row0 + t.rows - 1) / j.G + 1;
-    const int seen = (sees + kTlTile - 1) / kTlTile;
+    const int seen = t.own ? (sees + kTlTile - 1) / kTlTile : 0;
     t.s0 = min(t.z * c, seen);
     t.s1 = min(t.s0 + c, seen);
     t.part0 = j.part0[t.b] + q * t.nz;
@@ -157,13 +159,12 @@ struct TailSums {
             o[n][i][3] *= b;
         }
     }
-    // another's sums of eight rows, its o by get(i) (a float4)
+    // another's sums of eight rows, its o by get(x)
     template <typename Get>
     __device__ __forceinline__ void add(int n, float m0, float m1, float l0, float l1, Get get)
     {
         float4 x[D / 16];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) x[i] = get(i);
+        get(x);
         const float t0 = fmaxf(m[n][0], m0), t1 = fmaxf(m[n][1], m1);
         const float f0 = ex2f(m[n][0] - t0), f1 = ex2f(m[n][1] - t1);
         const float g0 = ex2f(m0 - t0), g1 = ex2f(m1 - t1);
@@ -534,9 +535,12 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
     const float out = __int_as_float((127 + ref - (int)kTlUnit) << 23);
 #pragma unroll
     for (int n = 0; n < NT; ++n) s.scale(n, out, out);
-    // ---- what the prefix kernel left of these rows, its pieces dealt to the ranges
-    if (t.skip > 0) {
-        const PrefixGroup gr = j.group[j.seq_group[t.b]];
+    // ---- what the prefix kernel left of these rows, its pieces dealt to the ranges: of
+    // the group's span and of the sequence's
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        if (which ? t.own : t.skip == 0) continue;
+        const PrefixSpan gr = j.span[which ? j.groups + t.b : j.seq_group[t.b]];
         const int blocks = (gr.rows + gr.block - 1) / gr.block;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -563,18 +567,25 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
                     const int cta = min(cc[r].x + k, j.prefix_ctas - 1), slot = 2 * cta + (k == 0 ? 1 : 0);
                     const bool whole = cc[r].x == cc[r].y;
                     const size_t i = whole ? (size_t)2 * j.prefix_ctas + unit[r] : (size_t)slot;
-                    p[r] = j.part + i * ((size_t)kPrefixRows * (D + 2)) + ((at + r) & (gr.block - 1));
+                    const int in = (at + r) & (gr.block - 1);
+                    p[r] = j.part + i * ((size_t)kPrefixRows * (D + 2));
                     on[r] = (__ldcg(j.part_unit + slot) == unit[r] || whole) && cc[r].x + k <= cc[r].y;
-                    m1[r] = __ldcg(p[r] + (size_t)D * kPrefixRows);
-                    l1[r] = __ldcg(p[r] + (size_t)(D + 1) * kPrefixRows);
+                    m1[r] = __ldcg(p[r] + (size_t)D * kPrefixRows + in);
+                    l1[r] = __ldcg(p[r] + (size_t)(D + 1) * kPrefixRows + in);
+                    p[r] += 4 * in + (size_t)g * (D / 8) * kPrefixRows;
                 }
                 s.add(n, on[0] ? m1[0] : kTlNone, on[1] ? m1[1] : kTlNone, on[0] && g == 0 ? l1[0] : 0.f,
-                      on[1] && g == 0 ? l1[1] : 0.f, [&](int i) {
-                          const size_t d = (size_t)(g * (D / 8) + 2 * i) * kPrefixRows;
-                          const float a = __ldcg(p[0] + d), b = __ldcg(p[0] + d + kPrefixRows);
-                          const float e = __ldcg(p[1] + d), f = __ldcg(p[1] + d + kPrefixRows);
-                          return make_float4(on[0] ? a : 0.f, on[1] ? e : 0.f, on[0] ? b : 0.f,
-                                             on[1] ? f : 0.f);
+                      on[1] && g == 0 ? l1[1] : 0.f, [&](float4 (&x)[D / 16]) {
+#pragma unroll
+                          for (int i = 0; i < D / 32; ++i) {
+                              const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+                              float4 a = __ldcg(reinterpret_cast<const float4 *>(p[0]) + i * kPrefixRows);
+                              float4 b = __ldcg(reinterpret_cast<const float4 *>(p[1]) + i * kPrefixRows);
+                              if (!on[0]) a = zero;
+                              if (!on[1]) b = zero;
+                              x[2 * i] = make_float4(a.x, b.x, a.y, b.y);
+                              x[2 * i + 1] = make_float4(a.z, b.z, a.w, b.w);
+                          }
                       });
             }
             __syncwarp();
@@ -607,7 +618,10 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
             for (int n = 0; n < NT; ++n) {
                 const float4 *from = part + (size_t)z * (kTailTiles * kStride) + n * kStride;
                 const float4 x = __ldcg(from + D / 16 * 32);
-                s.add(n, x.x, x.y, x.z, x.w, [&](int i) { return __ldcg(from + i * 32); });
+                s.add(n, x.x, x.y, x.z, x.w, [&](float4 (&o)[D / 16]) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) o[i] = __ldcg(from + i * 32);
+                });
             }
     }
 #pragma unroll
