@@ -649,9 +649,7 @@ _CODE = {torch.bfloat16: SV_BF16, torch.float32: SV_F32}
 
 
 def _rows_out(t, shape, dtype, dev, name):
-    """A given output of this shape (last dimension contiguous), or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+    """Checks a given output: this shape, its last dimension contiguous."""
     if t.shape != shape or t.dtype is not dtype or t.device != dev or t.stride(2) != 1:
         raise ValueError("%s must be a %s tensor of shape %s on %s, contiguous in its last "
                          "dimension" % (name, dtype, tuple(shape), dev))
@@ -674,15 +672,20 @@ def sv_kv_read(k_cache, v_cache, k_scale, v_scale, table, cu, rows, *, first=Non
     T, i32 = int(rows), torch.int32
     if T < 0:
         raise ValueError("rows must not be negative")
-    k, v = (None, None) if out is None else out
-    k = _rows_out(k, (T, H, D), dtype, dev, "k")
-    v = _rows_out(v, (T, H, D), dtype, dev, "v")
+    shape = (T, H, D)
+    if out is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+        strides = (H * D, D, H * D, D)
+    else:
+        k, v = (_rows_out(t, shape, dtype, dev, n) for t, n in zip(out, "kv"))
+        strides = (*k.stride()[:2], *v.stride()[:2])
     ptr, raw = _call_on(handle, stream, dev)
     _check(lib().sv_kv_read(
         ptr, *cache, H, D, block, pages, _dense(table, i32, (B, cols), "table", dev), cols,
         None if first is None else _dense(first, i32, (B,), "first", dev),
         _dense(cu, i32, (B + 1,), "cu", dev), B, T, k.data_ptr(), v.data_ptr(), _CODE[dtype],
-        k.stride(0), k.stride(1), v.stride(0), v.stride(1), raw), "sv_kv_read")
+        *strides, raw), "sv_kv_read")
     return {"k": k, "v": v}
 
 
@@ -696,44 +699,52 @@ def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e
     be the inputs.  Returns a dict (q, k)."""
     x = k if q is None else q
     dev = _cuda(x, "k" if q is None else "q")
-    if x.dim() != 3 or x.dtype not in _CODE:
+    given = x.dtype
+    if x.dim() != 3 or given not in _CODE:
         raise ValueError("q and k must be bfloat16 or float32 tensors [T, heads, D]")
-    T, _, D = x.shape
+    T, Hq, D = x.shape
+    H, qi, qo, ki, ko = 0, (0, 0, 1), (0, 0), (0, 0, 1), (0, 0)
     if dtype is None:
-        dtype = x.dtype
+        dtype = given
     elif dtype not in _CODE:
         raise ValueError("dtype must be bfloat16 or float32")
-    o = (None, None) if out is None else out
-    heads, src, dst, ins, outs = [], [], [], [], []
-    res = {}
-    for t, to, name in ((q, o[0], "q"), (k, o[1], "k")):
-        if t is None:
-            heads.append(0), src.append(None), dst.append(None)
-            ins += (0, 0)
-            outs += (0, 0)
-            res[name] = None
-            continue
-        if t is not x and (t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or
-                           t.dtype is not x.dtype or t.device != dev):
+    y = z = None
+    if q is None:
+        Hq = 0
+    else:
+        qi = q.stride()
+        if out is None or out[0] is None:
+            y, qo = q.new_empty((T, Hq, D), dtype=dtype), (Hq * D, D)
+        else:
+            y = _rows_out(out[0], q.shape, dtype, dev, "q of out")
+            qo = y.stride()
+    if k is not None:
+        ki = k.stride()
+        if k is not x and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or
+                           k.dtype is not given or k.device != dev):
             raise ValueError("q and k must have one T, D, type and device")
-        if t.stride(2) != 1:
-            raise ValueError("%s: the last dimension must be contiguous" % name)
-        y = res[name] = _rows_out(to, t.shape, dtype, dev, name + " of out")
-        heads.append(t.shape[1]), src.append(t.data_ptr()), dst.append(y.data_ptr())
-        ins += (t.stride(0), t.stride(1))
-        outs += (y.stride(0), y.stride(1))
-    f32, rot = torch.float32, 0
+        H = k.shape[1]
+        if out is None or out[1] is None:
+            z, ko = k.new_empty((T, H, D), dtype=dtype), (H * D, D)
+        else:
+            z = _rows_out(out[1], k.shape, dtype, dev, "k of out")
+            ko = z.stride()
+    if qi[2] != 1 or ki[2] != 1:
+        raise ValueError("q and k: the last dimension must be contiguous")
+    f32, rot, row = torch.float32, 0, (D,)
     if inv_freq is not None:
-        rot = 2 * inv_freq.shape[0]
-        inv_freq = _dense(inv_freq, f32, (rot // 2,), "inv_freq", dev)
-    w = [None if t is None else _dense(t, f32, (D,), n, dev)
-         for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+        rot = inv_freq.shape[0]
+        inv_freq, rot = _dense(inv_freq, f32, (rot,), "inv_freq", dev), 2 * rot
     ptr, raw = _call_on(handle, stream, dev)
     _check(lib().sv_qk_norm_rope(
-        ptr, *src, _CODE[x.dtype], *ins, T, *heads, D, *w, float(eps), inv_freq, rot,
-        1 if interleaved else 0, _dense(pos, torch.int32, (T,), "pos", dev), *dst, _CODE[dtype],
-        *outs, raw), "sv_qk_norm_rope")
-    return res
+        ptr, None if q is None else q.data_ptr(), None if k is None else k.data_ptr(),
+        _CODE[given], qi[0], qi[1], ki[0], ki[1], T, Hq, H, D,
+        None if q_weight is None else _dense(q_weight, f32, row, "q_weight", dev),
+        None if k_weight is None else _dense(k_weight, f32, row, "k_weight", dev), eps,
+        inv_freq, rot, 1 if interleaved else 0, _dense(pos, torch.int32, (T,), "pos", dev),
+        None if y is None else y.data_ptr(), None if z is None else z.data_ptr(), _CODE[dtype],
+        qo[0], qo[1], ko[0], ko[1], raw), "sv_qk_norm_rope")
+    return {"q": y, "k": z}
 
 
 def sv_sample_rows(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
