@@ -58,15 +58,14 @@ constexpr int kPxTile = 128;           // tokens of a tile
 constexpr int kPxRows = kPrefixRows;   // query rows of a unit, two slots of 128
 constexpr int kPxK = 3, kPxV = 2;      // tiles of keys and of values in flight
 constexpr int kPxPieces = 4;           // pieces known ahead
+constexpr int kPxReaders = 14;         // warps that read them
 constexpr int kPxRing = 8;             // tiles whose scales are kept
-constexpr int kPxSoft = 16;            // softmax warps, eight a slot: four for each half of a row
-constexpr int kPxProd = kPxSoft + 4, kPxIssue = kPxSoft + 5;
-constexpr int kPxReaders = kPxSoft + 6;  // warps that read pieces
-constexpr int kPxThreads = 768;        // + 4 converting warps, producer, 2 issuers, 1 idle
-// Registers: the launch gives each thread 80 of the SM's 65,536; the softmax warps take
-// what the others leave.
-constexpr int kPxRegs = 80, kPxSoftRegs = 88, kPxSideRegs = 64;
-static_assert(kPxSoft * 32 * kPxSoftRegs + 256 * kPxSideRegs <= kPxThreads * kPxRegs, "registers");
+constexpr int kPxSoft = 8;             // softmax warps, four a slot
+constexpr int kPxThreads = 512;        // + 4 converting warps, producer, 2 issuers, 1 idle
+// Registers: 128 a thread at launch; the softmax warps, which hold a row's 128
+// scores, take what the others leave (256 * 184 + 256 * 72 = 512 * 128).
+constexpr int kPxRegs = 128, kPxSoftRegs = 184, kPxSideRegs = 72;
+static_assert(256 * kPxSoftRegs + 256 * kPxSideRegs <= kPxThreads * kPxRegs, "registers");
 constexpr float kPxLazy = 8.f;         // log2 of how far a weight may pass 1
 constexpr uint32_t kPxTries = 1u << 16; // of a wait
 constexpr float kPxNone = -1e30f;      // maximum of no tokens
@@ -75,7 +74,6 @@ constexpr float kPxNone = -1e30f;      // maximum of no tokens
 // Which pages are shared.
 // ---------------------------------------------------------------------------
 constexpr int kPrepCtas = 8, kPrepThreads = 512;
-constexpr long long kPxLeast = 8192;
 
 // Row blocks of a head, and costs, in tiles of a slot (1,750 cycles).  What a piece's
 // start and end take (queries, first scores, sums) is counted at the front of a unit.
@@ -193,8 +191,6 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         if (!bad) {
             const int lo = edge(g), hi = edge(g + 1);
             int pages = 0x7FFFFFFF, lead = 0x7FFFFFFF, live = 0;
-            bool many = false;
-            int eights = 0;
             for (int b = lo + lane; b < hi; b += 32) {
                 int n, L;
                 if (!tokens(b, n, L)) pages = 0;
@@ -202,21 +198,12 @@ prefix_prep_kernel(const PrefixJob j, int warps)
                     pages = min(pages, __ldcg(j.skip + b));
                     lead = min(lead, b);
                     ++live;
-                    many |= n * j.G > kTailMax;
-                    eights += min((n * j.G + 7) / 8, 1 << 16);
                 }
             }
             pages = __reduce_min_sync(0xFFFFFFFFu, pages);
             lead = __reduce_min_sync(0xFFFFFFFFu, lead);
             live = __reduce_add_sync(0xFFFFFFFFu, live);
             if (live < 2) pages = 0;  // nothing is shared
-            // What little there is the tail reads sooner for each sequence by itself: 16
-            // tokens of eight rows of a head take it about 2 ns in all, the prefix kernel
-            // some 15 us more than nothing.
-            eights = __reduce_add_sync(0xFFFFFFFFu, eights);
-            if (!__any_sync(0xFFFFFFFFu, many) &&
-                (long long)((pages << shift) / 16) * eights * j.H < kPxLeast)
-                pages = 0;
             const int first = pages ? j.cu[lo] : 0;
             const long long rows = pages ? (long long)(j.cu[hi] - first) * j.G : 0;
             for (int b = lo + lane; b < hi; b += 32) {
@@ -468,8 +455,7 @@ struct PxShared {
     uint64_t piece_full[kPxPieces], piece_empty[kPxPieces];
     uint32_t lost[2][4];               // tokens of a tile with NaN in their value, a bit each
     float c[kPxRows];                  // factor from S to log2 units, per row
-    float m[2][128], l[2][2][128];     // of the two slots, and of the halves of a row
-    float top[2][2][128];              // maxima of the halves
+    float m[2][128], l[2][128];        // of the two slots, where they share rows
 };
 
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float *v)
@@ -683,15 +669,15 @@ __device__ __forceinline__ bool px_next(PxShared *sh, int *err, uint32_t &pieces
     return ok && p.rows > 0;
 }
 
-// Which of 64 tokens a row sees, a bit each: its token is new token i of the sequence,
-// `at` the first of the 64.
+// Which of a tile's 128 tokens a row sees, a bit each: its token is new token i of the
+// sequence, `at` the tile's first token.
 struct PxSees {
-    uint32_t w[2];
+    uint32_t w[4];
     __device__ __forceinline__ PxSees(const PrefixJob &j, const PxPiece &pc, int i, bool live, int at)
     {
         const uint32_t *m = j.mask && live ? j.mask + (int64_t)(pc.first + i) * j.words : nullptr;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             const int p = at + 32 * k, q = p - pc.ctx;  // of the word's first token
             // tokens before the new ones, and before the end
             auto first = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
@@ -713,53 +699,53 @@ struct PxSees {
     }
 };
 
-// One tile of a softmax thread: half of a row's 128 scores to weights, 32 at a time.
-// M (a whole number): the row's running maximum, alike in both halves; l: the half's
-// sum of weights.  Weights are taken against the maximum in use before it is known
-// whether one passes it by too much; a vote of the slot tells, before they are stored
-// over the scores.  Where one does, M moves, the sums so far are scaled by the power
-// of two, and the weights are taken again.
+// One tile of a softmax thread: a row's 128 scores to weights, 64 at a time.
+// M (a whole number), l: the row's running maximum and sum of weights.  Weights are
+// taken against the maximum in use before it is known whether one passes it by too
+// much; where one does, M moves, and what there is of the row (sums, values, the
+// tile's first 64 weights) is scaled by the power of two.
 // same: pages of 64 tokens or more, one scale for the 64.  EDGE: only the tokens of
 // `sees` count, and those of `lost` are NaN.
 // (The factors are taken before the scores, the weights stored after them: loads
 // and stores between would keep the scores' chains from overlapping.)
-// ok: whether this warp's waits have ended well; the slot's warps return alike.
 template <int D, bool EDGE>
 __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
-                                             int slot, int half, int row, uint32_t count, bool first,
-                                             const float4 *sc, bool same, float c, float &M, float &l,
-                                             const uint32_t *sees, const uint32_t *lost, bool ok)
+                                             uint64_t *pv_done, uint32_t count, bool first,
+                                             const float4 *sc, bool same, float c, float &M,
+                                             float &l, const uint32_t *sees, const uint32_t *lost)
 {
-    uint32_t p[32];
-    float add;
-    auto load = [&](int q, float (&s)[32], float4 (&f)[2]) {
-        tc_ld32(s_at + half * 64 + q * 32, s);
-        f[0] = sc[4 * half + 2 * q];
-        f[1] = f[0];
-        if (!same) f[1] = sc[4 * half + 2 * q + 1];
+    bool ok = true;
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+        float s[64];
+        tc_ld32(s_at + q * 64, s);
+        tc_ld32(s_at + q * 64 + 32, s + 32);
+        float4 f[4];
+        f[0] = sc[4 * q];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) {
+            f[k] = f[0];
+            if (!same) f[k] = sc[4 * q + k];
+        }
         tc_wait_ld(s);
         if (EDGE) {
-            const uint32_t see = sees[q], gone = lost[q];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (!(see >> i & 1))
+            for (int i = 0; i < 64; ++i) {
+                const uint32_t see = sees[2 * q + (i >> 5)], gone = lost[2 * q + (i >> 5)];
+                if (!(see >> (i & 31) & 1))
                     s[i] = -INFINITY;
-                else if (gone >> i & 1)
+                else if (gone >> (i & 31) & 1)
                     s[i] = __int_as_float(0x7FC00000);
             }
         }
-    };
+        uint32_t p[32];
+        float add;
 #pragma unroll 1
-    for (;;) {
-        float top = -INFINITY;
-        add = 0.f;
+        for (;;) {
+            float top = -INFINITY;
+            add = 0.f;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float s[32];
-            float4 f[2];
-            load(q, s, f);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const float2 u = make_float2(c * f[k].x, c * f[k].x);
                 const float2 v = make_float2(f[k].y - M, f[k].y - M);
                 float2 sum;
@@ -769,61 +755,66 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
                     top = max3(top, y.x, y.y);
                     const float2 w = make_float2(ex2f(y.x), ex2f(y.y));
                     sum = i ? add2(sum, w) : w;
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                        : "=r"(p[16 * q + 8 * k + i]) : "f"(w.y), "f"(w.x));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[8 * k + i]) : "f"(w.y), "f"(w.x));
                 }
                 add = fmaf(sum.x + sum.y, f[k].z, add);
             }
-        }
-        // (M is unset, at kPxNone, before a row's first token)
-        if (!bar_or(2 + slot, kPxSoft * 16, !ok || top > kPxLazy)) break;
-        // the row's maximum, from the scores themselves
-        float m = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            float s[32];
-            float4 f[2];
-            load(q, s, f);
+            // (M is unset, at kPxNone, before a row's first token)
+            if (!__any_sync(0xFFFFFFFFu, top > kPxLazy)) break;
+            float to = top > kPxLazy ? M + ceilf(top) : M;
+            float scale = pow2_int(M - to);
+            if (M == kPxNone) {
+                // no sum was taken against it: from the scores themselves (it stays where
+                // there are none)
+                float m = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float a = s[16 * k];
+                for (int k = 0; k < 4; ++k) {
+                    float a = s[16 * k], b = s[16 * k + 1];
 #pragma unroll
-                for (int i = 1; i < 15; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
-                m = fmaxf(m, fmaf(fmaxf(a, s[16 * k + 15]), c * f[k].x, f[k].y));
+                    for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
+                    m = fmaxf(m, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
+                }
+                to = m > -INFINITY ? ceilf(m) : M;
+                scale = 1.f;
             }
-        }
-        sh->top[slot][half][row] = m;
-        if (bar_or(2 + slot, kPxSoft * 16, !ok)) return false;
-        m = fmaxf(m, sh->top[slot][half ^ 1][row]);
-        float to = M, scale = 1.f;
-        if (M == kPxNone) {
-            if (m > -INFINITY) to = ceilf(m);
-        } else if (m > M + kPxLazy) {
-            to = ceilf(m);
-            scale = pow2_int(M - to);
-        }
-        M = to;
-        l *= scale;
-        if (!first) {
-            ok = px_wait(sh, err, &sh->pv_done[slot], (count - 1) & 1);
-            tc_fence_after();
+            M = to;
+            l *= scale;
+            if (!first) {
+                ok = ok && px_wait(sh, err, pv_done, (count - 1) & 1);
+                tc_fence_after();
 #pragma unroll 1
-            for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 8) {
-                float o[8];
-                tc_ld8(o_at + i, o);
-                tc_wait_ld(o);
+                for (int i = 0; i < D; i += 8) {
+                    float o[8];
+                    tc_ld8(o_at + i, o);
+                    tc_wait_ld(o);
 #pragma unroll
-                for (int n = 0; n < 8; ++n) o[n] *= scale;
-                tc_st8(o_at + i, o);
+                    for (int n = 0; n < 8; ++n) o[n] *= scale;
+                    tc_st8(o_at + i, o);
+                }
+            }
+            if (q) {
+                tc_wait_st();
+                uint32_t two;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(two) : "f"(scale));
+#pragma unroll 1
+                for (int i = 0; i < 32; i += 8) {
+                    float o[8];
+                    tc_ld8(s_at + i, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+                        o[n] = __uint_as_float(mul_bf16x2(__float_as_uint(o[n]), two));
+                    tc_st8(s_at + i, o);
+                }
             }
             tc_wait_st();
         }
+        l += add;
+        // (over scores that have been taken)
+        tc_st32u(s_at + q * 32, p);
     }
-    l += add;
-    // (over scores that all of the slot have taken)
-    tc_st32u(s_at + half * 32, p);
     tc_wait_st();
-    return true;
+    return ok;
 }
 
 template <int D>
@@ -856,7 +847,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             mbar_init(&sh->drained[i], 1);
             mbar_init(&sh->turn[i], 1);
             mbar_init(&sh->s_full[i], 1);
-                mbar_init(&sh->p_full[i], 8);
+            mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->pv_done[i], 1);
         }
         for (int i = 0; i < kPxRing; ++i) mbar_init(&sh->scales[i], 1);
@@ -868,7 +859,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         mbar_fence_init();
         sh->abort = 0;
     }
-    if (warp == kPxProd) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_u32(&sh->tmem))
                      : "memory");
@@ -887,8 +878,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
 
     if (warp < kPxSoft) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPxSoftRegs));
-        const int slot = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-        const int r = quarter * 32 + lane;
+        const int slot = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_at = lanes + slot * 128, o_at = lanes + 256 + slot * 128;
         uint32_t count = 0;                     // this slot's tiles so far
@@ -914,30 +904,39 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 ok = px_wait(sh, j.err, &sh->scales[ring], ((it + i) / kPxRing) & 1);
                 ok = ok && px_wait(sh, j.err, &sh->s_full[slot], count & 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
                 tc_fence_after();
                 const int at = (pc.t0 + i) * kPxTile;
                 if (__builtin_expect(at + kPxTile <= pc.ctx, 1)) {
-                    ok = px_soft_tile<D, false>(sh, j.err, s_at, o_at, slot, half, r, count, i == from,
-                                                sh->sc[ring], j.block >= 64, c, M, l, nullptr, nullptr, ok);
+                    ok = px_soft_tile<D, false>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
+                                                sh->sc[ring], j.block >= 64, c, M, l, nullptr, nullptr);
                 } else {
                     // (which tokens are lost is known once the values are converted)
                     const uint32_t sb = (it + i) & 1;
-                    ok = ok && px_wait(sh, j.err, &sh->full_b[sb], ((it + i) >> 1) & 1);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    const PxSees sees(j, pc, token, row < pc.rows, at + half * 64);
-                    const uint32_t lost[2] = {sh->lost[sb][2 * half], sh->lost[sb][2 * half + 1]};
-                    ok = px_soft_tile<D, true>(sh, j.err, s_at, o_at, slot, half, r, count, i == from,
-                                               sh->sc[ring], j.block >= 64, c, M, l, sees.w, lost, ok);
+                    ok = px_wait(sh, j.err, &sh->full_b[sb], ((it + i) >> 1) & 1);
+                    const PxSees sees(j, pc, token, row < pc.rows, at);
+                    uint32_t lost[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) lost[k] = sh->lost[sb][k];
+                    ok = __all_sync(0xFFFFFFFFu, ok) &&
+                         px_soft_tile<D, true>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
+                                               sh->sc[ring], j.block >= 64, c, M, l, sees.w, lost);
                 }
+                ok = __all_sync(0xFFFFFFFFu, ok);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full[slot]);
             }
             const bool had = from < n;
             if (had && ok) ok = px_wait(sh, j.err, &sh->pv_done[slot], (count - 1) & 1);
-            if (half == 0) sh->m[slot][r] = M;
-            sh->l[slot][half][r] = l;
-            if (bar_or(1, kPxSoft * 32, !ok)) break;
+            if (!wide) {
+                sh->m[slot][r] = M;
+                sh->l[slot][r] = l;
+            }
+            if (bar_or(1, kPxSoft * 32, !ok)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
             // ---- the piece's sums
             if (tid == 0) {
@@ -950,41 +949,40 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             float *ml = part + (size_t)D * kPxRows + row;
             if (wide) {
 #pragma unroll 1
-                for (int i = half * (D / 2); i < (half + 1) * (D / 2); i += 16) {
-                    float o[16];
-                    tc_ld8(o_at + i, o);
-                    tc_ld8(o_at + i + 8, o + 8);
+                for (int i = 0; i < D; i += 32) {
+                    float o[32];
+                    tc_ld32(o_at + i, o);
                     tc_wait_ld(o);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 8; ++q)
                         to[(i / 4 + q) * kPxRows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
-                if (half == 0) {
-                    ml[0] = M;
-                    ml[kPxRows] = sh->l[slot][0][r] + sh->l[slot][1][r];
-                }
+                ml[0] = M;
+                ml[kPxRows] = l;
             } else {
-                // both slots' sums of a row; a quarter of its elements each
+                // both slots' sums of a row; half of its elements each
                 const float m0 = sh->m[0][r], m1 = n > 1 ? sh->m[1][r] : kPxNone;
                 const float m = fmaxf(m0, m1), f0 = ex2f(m0 - m), f1 = n > 1 ? ex2f(m1 - m) : 0.f;
-                const int part_no = slot * 2 + half;
 #pragma unroll 1
-                for (int i = part_no * (D / 4); i < (part_no + 1) * (D / 4); i += 8) {
-                    float a[8], b[8];
+                for (int i = slot * (D / 2); i < (slot + 1) * (D / 2); i += 16) {
+                    float a[16], b[16];
                     tc_ld8(lanes + 256 + i, a);
-                    if (n > 1) tc_ld8(lanes + 384 + i, b);
+                    tc_ld8(lanes + 256 + i + 8, a + 8);
+                    if (n > 1) {
+                        tc_ld8(lanes + 384 + i, b);
+                        tc_ld8(lanes + 384 + i + 8, b + 8);
+                    }
                     tc_wait_ld(a);
                     if (n > 1) tc_wait_ld(b);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) a[q] = n > 1 ? fmaf(b[q], f1, a[q] * f0) : a[q];
+                    for (int q = 0; q < 16; ++q) a[q] = n > 1 ? fmaf(b[q], f1, a[q] * f0) : a[q];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                    for (int q = 0; q < 4; ++q)
                         to[(i / 4 + q) * kPxRows] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
                 }
-                if (part_no == 0) {
-                    const float l0 = sh->l[0][0][r] + sh->l[0][1][r];
+                if (slot == 0) {
                     ml[0] = m;
-                    ml[kPxRows] = n > 1 ? fmaf(sh->l[1][0][r] + sh->l[1][1][r], f1, l0 * f0) : l0;
+                    ml[kPxRows] = n > 1 ? fmaf(sh->l[1][r], f1, sh->l[0][r] * f0) : sh->l[0][r];
                 }
             }
             tc_fence_before();
@@ -993,7 +991,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxSideRegs));
-        if (warp < kPxProd) {
+        if (warp < 12) {
             // ---- the values to bf16, a token a thread
             const int tk = tid - kPxSoft * 32;
             while (ok && px_next(sh, j.err, pieces, pc, lane)) {
@@ -1047,7 +1045,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     }
                 }
             }
-        } else if (warp == kPxProd) {
+        } else if (warp == 12) {
             // ---- producer: the pieces, and the pages of each tile, looked up 32 at a time
             const int shift = 31 - __clz(j.block), per_tile = kPxTile >> shift;
             const int inner = lane & (per_tile - 1);
@@ -1144,7 +1142,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 for (int i = 0; i < kPxK; ++i) mbar_wait_n(&sh->full_k[i], (it / kPxK) & 1, 1u << 12);
                 for (int i = 0; i < kPxV; ++i) mbar_wait_n(&sh->full_v[i], (it / kPxV) & 1, 1u << 12);
             }
-        } else if (warp < kPxIssue + 2) {
+        } else if (warp < 15) {
             // ---- issuers of the products, one a slot.  A step: the product of the slot's
             // weights with the tile's values, then the scores of its next tile, whose
             // place the weights have held.  (The whole warp walks along, so that
@@ -1153,7 +1151,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             constexpr uint32_t kIdS = kSums | (128u >> 3 << 17) | kM;
             // bf16 both; B with its rows (tokens) as the products' dimension
             constexpr uint32_t kIdO = kSums | 1u << 7 | 1u << 10 | 1u << 16 | ((uint32_t)D >> 3 << 17) | kM;
-            const int slot = __shfl_sync(0xFFFFFFFFu, warp - kPxIssue, 0);
+            const int slot = __shfl_sync(0xFFFFFFFFu, warp - 13, 0);
             const uint32_t col = tmem + slot * 128;
             const uint64_t dk0 = tc_desc(smem_u32(s_k), 16, 8 * D, kSwz);
             const uint64_t dq0 = tc_desc(smem_u32(s_q), 16, 8 * D, kSwz);
@@ -1191,6 +1189,10 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
 #pragma unroll
                         for (int k = 0; k < kPxTile / 16; ++k)
                             tc_mma_ts(col + 256, col + 8 * k, db + 128 * k, kIdO, k || i >= step);
+                        tc_commit(&sh->pv_done[slot]);
+                        // (both slots release a tile)
+                        tc_commit(&sh->empty_b[sb]);
+                        if (!wide) tc_commit(&sh->empty_b[sb]);
                     }
                     if (next && one) {
                         const uint64_t dk = dk0 + st * (kSide >> 4);
@@ -1201,14 +1203,8 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         for (int k = 0; k < D / 32; ++k)
                             tc_mma(col, dq + (kSide >> 4) + 2 * k, dk + 2 * k, kIdS, 1);
                         tc_commit(&sh->s_full[slot]);
-                        // (both slots release a tile)
                         tc_commit(&sh->empty_k[st]);
                         if (!wide) tc_commit(&sh->empty_k[st]);
-                    }
-                    if (now && one) {
-                        tc_commit(&sh->pv_done[slot]);
-                        tc_commit(&sh->empty_b[sb]);
-                        if (!wide) tc_commit(&sh->empty_b[sb]);
                     }
                     if (now && wide) {
                         ++wides;
@@ -1227,7 +1223,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kPxProd) {
+    if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }

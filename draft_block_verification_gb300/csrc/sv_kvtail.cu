@@ -507,7 +507,7 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
     TailSums<D, NT> s;
     s.clear();
     int ref = 0;
-    {
+    if (t.s0 < t.s1) {
         uint32_t x[NT][D / 8];
         float cf[NT][2];
         tail_queries<D, NT>(j, t, lane, x, cf);
