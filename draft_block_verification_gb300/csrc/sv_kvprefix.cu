@@ -75,6 +75,12 @@ constexpr float kPxNone = -1e30f;      // maximum of no tokens
 // ---------------------------------------------------------------------------
 constexpr int kPrepCtas = 8, kPrepThreads = 512;
 
+// What little is shared the tail reads sooner for each sequence by itself: 16 tokens
+// of eight rows of a head take it about 2 ns in all, a run of the prefix kernel some
+// 15 us more than one without work.  (Four sequences of a row, 4,096 shared tokens, 8
+// heads: 33 us against 41.)
+constexpr unsigned long long kPxLeast = 8192;
+
 // Row blocks of a head, and costs, in tiles of a slot (1,750 cycles).  What a piece's
 // start and end take (queries, first scores, sums) is counted at the front of a unit.
 constexpr int kPxUnitCost = 10;
@@ -101,7 +107,8 @@ __device__ __forceinline__ int px_tiles(int end) { return (int)(((long long)end 
 __global__ void __cluster_dims__(kPrepCtas, 1, 1) __launch_bounds__(kPrepThreads)
 prefix_prep_kernel(const PrefixJob j, int warps)
 {
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_many;
+    __shared__ unsigned long long s_shared;
     __shared__ longlong2 s_sum[kPrepThreads / 32];
     __shared__ int2 s_scan[kPrepThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -109,7 +116,7 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     const int shift = 31 - __clz(j.block);
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) s_bad = s_many = 0, s_shared = 0;
     if (blockIdx.x == 0)
         for (int i = tid; i < kTailParts * warps; i += kPrepThreads) j.tail_arrived[i] = 0;
     auto edge = [&](int g) { return j.cu_group ? j.cu_group[g] : g ? j.B : 0; };
@@ -191,6 +198,8 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         if (!bad) {
             const int lo = edge(g), hi = edge(g + 1);
             int pages = 0x7FFFFFFF, lead = 0x7FFFFFFF, live = 0;
+            long long eights = 0;
+            bool many = false;
             for (int b = lo + lane; b < hi; b += 32) {
                 int n, L;
                 if (!tokens(b, n, L)) pages = 0;
@@ -198,6 +207,8 @@ prefix_prep_kernel(const PrefixJob j, int warps)
                     pages = min(pages, __ldcg(j.skip + b));
                     lead = min(lead, b);
                     ++live;
+                    eights += (n * j.G + 7) >> 3;
+                    many |= n * j.G > kTailMax;
                 }
             }
             pages = __reduce_min_sync(0xFFFFFFFFu, pages);
@@ -211,6 +222,9 @@ prefix_prep_kernel(const PrefixJob j, int warps)
                 j.skip[b] = tokens(b, n, L) && n > 0 ? pages : 0;
                 j.seq_group[b] = g;
             }
+            if (many) s_many = 1;
+            if (pages)
+                atomicAdd(&s_shared, (unsigned long long)(eights * j.H * ((pages << shift) >> 4)));
             if (rows > 0) {
                 r.first = first;
                 r.rows = (int)rows;
@@ -221,6 +235,11 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         if (lane == 0) j.span[g] = r;
     }
     __syncthreads();
+    if (!s_many && s_shared < kPxLeast) {
+        for (int b = tid; b < j.B; b += kPrepThreads) j.skip[b] = 0;
+        for (int g = tid; g < j.groups; g += kPrepThreads) j.span[g] = PrefixSpan{};
+        __syncthreads();
+    }
     // the tail's tasks: what is left of each sequence, cut into ranges of `c` stages
     auto left = [&](int b, long long &blocks, int &stages) {
         int n, L;

@@ -21,11 +21,20 @@ def ok(dbv):
     dbv.default_handle(torch.device("cuda", 0)).sync_status()
 
 
+def with_wide(prefix, sizes, after, new, wide):
+    """Few rows behind a short prefix are read for each sequence by itself.  wide:
+    one more sequence, of its own group, whose rows are too many for that; then
+    what is shared is read once, however short."""
+    more = ([0], [1], [70], [9]) if wide else ([],) * 4
+    return [x + y for x, y in zip((prefix, sizes, after, new), more)]
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
 @pytest.mark.parametrize("P", [0, 15, 16, 128, 130, 257, 1000])
-def test_lengths_and_pages(dbv, P, block, D):
-    c = pu.make(P + block, [P], [3], [5, 0, 40], [1, 1, 1], 2, 4, D, block)
+def test_lengths_and_pages(dbv, P, block, D, wide):
+    c = pu.make(P + block, *with_wide([P], [3], [5, 0, 40], [1, 1, 1], wide), 2, 4, D, block)
     pu.check(c, pu.run(dbv, c))
     ok(dbv)
 
@@ -72,13 +81,11 @@ def test_groups(dbv, tree):
 
 def test_bounds_only_say_where_to_look(dbv):
     """Bounds below, at and above what is shared, none, and tables that part early."""
-    c = pu.make(6, [400], [4], [80, 90, 7, 300], [2, 5, 1, 3], 2, 4, 64, 32)
+    c = pu.make(6, [400], [4], [80, 90, 7, 300], [2, 9, 1, 3], 2, 4, 64, 32)
     for p in (0, 31, 32, 100, 399, 416, 10 ** 9, -5):
         pu.check(c, pu.run(dbv, c, prefix_len=pu.dev([p])))
     pu.check(c, pu.run(dbv, c, prefix_len=None, cu_group=None))
     # a sequence whose third page is a copy of its own
-    spare = len(c["codes"][0]) - 1
-    assert spare not in c["table"] or True
     used = set(c["table"].reshape(-1).tolist())
     spare = next(i for i in range(len(c["codes"][0])) if i not in used)
     for a in c["codes"]:
@@ -98,12 +105,14 @@ def test_bounds_only_say_where_to_look(dbv):
     ok(dbv)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("far", [-30, -7, 12, 38])
 @pytest.mark.parametrize("pow2", [True, False])
-def test_value_scales_far_apart(dbv, far, pow2):
+def test_value_scales_far_apart(dbv, far, pow2, wide):
     """Pages of a prefix whose value scales lie far apart: what a row has from
     pages of small scales keeps its bits."""
-    c = pu.make(8, [1100], [3], [0] * 3, [1, 2, 1], 2, 2, 128, 16, pow2=pow2, far=far)
+    c = pu.make(8, *with_wide([1100], [3], [0] * 3, [1, 2, 1], wide), 2, 4, 128, 16, pow2=pow2,
+                far=far)
     # pages of large scales hold zeros; so the output is the others'
     big = np.arange(len(c["codes"][1])) % 2 == (1 if far > 0 else 0)
     c["codes"][1][big] &= 0x80
@@ -117,9 +126,10 @@ def test_value_scales_far_apart(dbv, far, pow2):
     ok(dbv)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("scale", [0.0, -0.088, 1.0, 3e-5])
-def test_softmax_scales(dbv, scale):
-    c = pu.make(9, [600], [3], [30, 0, 5], [3, 1, 4], 2, 3, 64, 64)
+def test_softmax_scales(dbv, scale, wide):
+    c = pu.make(9, *with_wide([600], [3], [30, 0, 5], [3, 1, 4], wide), 2, 4, 64, 64)
     pu.check(c, pu.run(dbv, c, scale=scale), scale)
 
 
@@ -133,10 +143,11 @@ def test_maxima_that_move(dbv):
     pu.check(c, pu.run(dbv, c))
 
 
-def test_rows_that_are_not_finite(dbv):
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_that_are_not_finite(dbv, wide):
     """A query of NaN or infinity gives a row of NaN and no other; so does a new
     token of NaN for the rows that see it."""
-    c = pu.make(11, [500], [3], [10, 0, 3], [4, 6, 5], 2, 2, 128, 32)
+    c = pu.make(11, *with_wide([500], [3], [10, 0, 3], [4, 6, 5], wide), 2, 4, 128, 32)
     c["q"][2, 1, 5] = float("nan")
     c["q"][7, 3, 100] = float("inf")
     got = pu.run(dbv, c)
@@ -150,21 +161,23 @@ def test_rows_that_are_not_finite(dbv):
     c["codes"][1][page, 0, row, 9] = 0x7F
     got = pu.run(dbv, c)["out"].isnan().any(-1)
     want = torch.zeros_like(got)
-    want[7:10, :2] = True  # tokens 3, 4 and 5 of sequence 1, heads of cache head 0
+    want[7:10, :4] = True  # tokens 3, 4 and 5 of sequence 1, heads of cache head 0
     assert torch.equal(got, want)
 
 
-def test_rows_that_see_only_the_prefix(dbv):
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_that_see_only_the_prefix(dbv, wide):
     """A mask that leaves a new token nothing of its own sequence."""
-    c = pu.make(12, [64], [2], [0, 0], [3, 4], 1, 2, 128, 64, tree=True)
+    c = pu.make(12, *with_wide([64], [2], [0, 0], [3, 4], wide), 1, 4, 128, 64, tree=True)
     c["mask"][:] = 0
     pu.check(c, pu.run(dbv, c))
     ok(dbv)
 
 
-def test_strided_queries(dbv):
+@pytest.mark.parametrize("wide", [False, True])
+def test_strided_queries(dbv, wide):
     """Views into a projection, on and off 16 bytes, and a broadcast head."""
-    c = pu.make(13, [300], [3], [5, 6, 7], [2, 1, 4], 2, 2, 64, 16)
+    c = pu.make(13, *with_wide([300], [3], [5, 6, 7], [2, 1, 4], wide), 2, 4, 64, 16)
     q = c["q"]
     T, Hq, D = q.shape
     for width, off in ((3 * Hq * D, 8), (Hq * D + 3, 1)):
