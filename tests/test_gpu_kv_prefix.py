@@ -302,3 +302,52 @@ def test_bad_lengths_and_groups_are_latched(dbv):
     latched()
     pu.check(c, pu.run(dbv, c))
     ok(dbv)
+
+
+@pytest.mark.parametrize("new,H,G,D,block", [([2000, 3, 40], 1, 2, 64, 64), ([700, 900], 2, 1, 128, 16),
+                                             ([1, 33, 16, 17, 32, 8], 2, 1, 128, 32),
+                                             ([4, 5, 4, 5, 1], 1, 8, 64, 128)])
+def test_rows_on_both_sides(dbv, new, H, G, D, block):
+    """Sequences of up to 32 rows a head and of more, in one group; whole prompts."""
+    n = len(new)
+    c = pu.make(n + H, [530], [n], [700 + 50 * i for i in range(n)], new, H, G, D, block)
+    pu.check(c, pu.run(dbv, c))
+    ok(dbv)
+
+
+@pytest.mark.parametrize("after,new,G,D", [([30000, 20000], [1, 1], 3, 128), ([25000], [1], 8, 64),
+                                           ([9000, 17, 40000], [2, 4, 3], 7, 64)])
+@pytest.mark.parametrize("far", [0, 9])
+def test_own_tokens_in_many_ranges(dbv, after, new, G, D, far):
+    """Few sequences with long contexts of their own, which many warps share."""
+    n = len(new)
+    c = pu.make(n + G, [64], [n], after, new, 1, G, D, 64, pow2=far == 0, far=far)
+    pu.check(c, pu.run(dbv, c))
+    ok(dbv)
+
+
+def test_many_sequences(dbv):
+    """Thousands of sequences and groups: more tasks than warps, and spans."""
+    r = np.random.RandomState(3)
+    sizes = [int(x) for x in r.randint(1, 6, 900)]
+    B = sum(sizes)
+    c = pu.make(4, [int(x) for x in r.randint(1, 70, 900)], sizes,
+                [int(x) for x in r.randint(0, 40, B)], [int(x) for x in r.randint(0, 3, B)],
+                1, 2, 64, 16)
+    pu.check(c, pu.run(dbv, c))
+    ok(dbv)
+
+
+@pytest.mark.parametrize("far", [-40, 7, 30])
+def test_own_scales_far_apart(dbv, far):
+    """What a sequence has of its own, behind no prefix: pages of small value scales
+    keep their bits beside pages of large ones that hold zeros."""
+    c = pu.make(20, [0], [3], [700, 45, 130], [1, 3, 8], 2, 4, 128, 16, far=far)
+    big = np.arange(len(c["codes"][1])) % 2 == (1 if far > 0 else 0)
+    c["codes"][1][big] &= 0x80
+    c["scale"][0][:] = 2.0 ** -7
+    got = pu.run(dbv, c)
+    want, _, mag, size = pu.exact(c)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15 * size[..., None]) * mag
+    assert ((got["out"].double() - want).abs() <= tol).all()
+    ok(dbv)
