@@ -714,7 +714,7 @@ def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e
     else:
         qi = q.stride()
         if out is None or out[0] is None:
-            y, qo = q.new_empty((T, Hq, D), dtype=dtype), (Hq * D, D)
+            y, qo = torch.empty((T, Hq, D), dtype=dtype, device=dev), (Hq * D, D)
         else:
             y = _rows_out(out[0], q.shape, dtype, dev, "q of out")
             qo = y.stride()
@@ -725,7 +725,7 @@ def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e
             raise ValueError("q and k must have one T, D, type and device")
         H = k.shape[1]
         if out is None or out[1] is None:
-            z, ko = k.new_empty((T, H, D), dtype=dtype), (H * D, D)
+            z, ko = torch.empty((T, H, D), dtype=dtype, device=dev), (H * D, D)
         else:
             z = _rows_out(out[1], k.shape, dtype, dev, "k of out")
             ko = z.stride()

@@ -1194,8 +1194,8 @@ sv_status sv_qk_norm_rope(sv_handle *h, const void *q, const void *k, sv_dtype d
                  {q_out_token_stride * os, k_out_token_stride * os},
                  {q_out_head_stride * os, k_out_head_stride * os},
                  dtype, out_dtype, T, Hq, H, D, rot, interleaved != 0, {q_weight, k_weight},
-                 inv_freq, eps, pos};
-    return cuda_status(rope_launch(j, (cudaStream_t)stream));
+                 inv_freq, eps, 1.f / (float)D, pos};
+    return cuda_status(rope_launch(j, h->sms, (cudaStream_t)stream));
 }
 
 sv_status sv_sample_rows(sv_handle *h, const void *logits, sv_dtype dtype, int64_t row_stride,

@@ -133,11 +133,11 @@ struct RopeJob {
     int dtype, odtype, T, Hq, H, D, rot, inter;
     const float *weight[2];    // [D] or null
     const float *inv_freq;     // [rot / 2]
-    float eps;
+    float eps, share;          // share: 1 / D
     const int32_t *pos;        // [T], negative: skipped
 };
 constexpr int kRopeMaxD = 512;
-cudaError_t rope_launch(const RopeJob &j, cudaStream_t s);
+cudaError_t rope_launch(const RopeJob &j, int sms, cudaStream_t s);
 
 struct ReadJob {
     const uint8_t *cache[2];

@@ -142,7 +142,11 @@ def test_not_finite_stays_in_its_head(dbv):
 
 @pytest.mark.parametrize("D", [128, 96, 42])
 def test_skipped_tokens_and_places(dbv, D):
-    """Negative positions are left; outputs in place, in views, heads first."""
+    """Negative positions are left; outputs in place, in views, heads first.  (Rows
+    off 16 bytes go another way, which adds and multiplies in another order: their
+    results are within the tolerance, not the same bits.  fp32 sums of D squares in
+    two orders differ by up to D 2^-24, and where that moves a result across the
+    middle of two bf16 values its rounding differs by a step.)"""
     q, k, pos, f, w = inputs(6, 40, 4, 2, D, D)
     pos[3] = -1
     pos[30:] = -1
@@ -152,8 +156,8 @@ def test_skipped_tokens_and_places(dbv, D):
                       device="cuda")[:, 1:1 + 2 * D].unflatten(1, (2, D)))
     check(dbv, q, k, pos, f, *w, out=out)
     live = pos >= 0
-    for o, n in zip(out, "qk"):
-        assert (o[~live] == 5.0).all() and torch.equal(o[live], want[n][live])
+    for o in out:
+        assert (o[~live] == 5.0).all()
     before = [q.clone(), k.clone()]
     got = dbv.sv_qk_norm_rope(q, k, pos, f, q_weight=w[0], k_weight=w[1], out=(q, k))
     for x, b, n in zip((q, k), before, "qk"):
@@ -196,3 +200,39 @@ def test_in_a_graph_and_on_another_stream(dbv):
     other = dbv.sv_qk_norm_rope(q, k, pos, f, q_weight=w[0], k_weight=w[1], stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(out[n], want[n]) and torch.equal(other[n], want[n]) for n in "qk")
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot,off", [(128, 32, 0), (128, 20, 0), (96, 48, 1), (64, 0, 0)])
+def test_what_is_not_rotated_stays_apart(dbv, D, rot, off, inter):
+    """Infinities and NaN: without a norm they reach the other element of their own
+    pair, and none that is not rotated but themselves; the rest keeps its bits."""
+    T = 6
+    whole = torch.randn((T, 2, D + 8), device="cuda").bfloat16()
+    x = whole[:, :, off:off + D]
+    pos = torch.arange(1, T + 1, device="cuda", dtype=torch.int32)
+    f = torch.rand(rot // 2, device="cuda") + 0.1 if rot else None
+    clean = dbv.sv_qk_norm_rope(x, None, pos, f, interleaved=inter)["q"]
+    for d in range(0, D, 5):
+        x[d % T, d % 2, d] = float("inf") if d % 3 else float("nan")
+    bad = ~x.isfinite()
+    reach = bad.clone()
+    i = torch.arange(rot // 2, device="cuda")
+    a, b = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    reach[..., a] |= bad[..., b]
+    reach[..., b] |= bad[..., a]
+    got = dbv.sv_qk_norm_rope(x, None, pos, f, interleaved=inter)["q"]
+    assert torch.equal(~got.isfinite(), reach)
+    assert torch.equal(got[~reach], clean[~reach])
+    assert torch.equal(got[..., rot:].nan_to_num(7.0), x[..., rot:].nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("Hq,H,D,rot,inter", [(32, 8, 128, 128, False), (7, 3, 96, 48, True),
+                                              (1, 40, 64, 64, False), (5, 2, 256, 32, False)])
+@pytest.mark.parametrize("given", [torch.bfloat16, torch.float32])
+def test_many_tokens(dbv, Hq, H, D, rot, inter, given):
+    """So many that a warp takes all of a token's heads."""
+    q, k, pos, f, w = inputs(10, 5000, Hq, H, D, rot, given, far=1 << 20)
+    pos[77] = pos[4999] = -1
+    check(dbv, q, k, pos, f, *w, inter=inter, dtype=torch.bfloat16)
+    check(dbv, q, k, pos, f, w[0], None, inter=inter)
