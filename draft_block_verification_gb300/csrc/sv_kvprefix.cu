@@ -285,10 +285,11 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         many += s_sum[w].y;
     }
     __syncthreads();
-    // a task a warp, of 256 tokens at least; where there are about as many as warps
+    // a task a warp, of 128 tokens at least (four sequences of 1,024: 28 us a call; of
+    // 192 30, of 256 34); where there are about as many as warps
     // before any is cut, only those of twice the mean
     const long long mean = (all + warps - 1) / warps;
-    const int c = (int)max(8LL, 2 * many >= warps ? 2 * mean : mean);
+    const int c = (int)max(4LL, 2 * many >= warps ? 2 * mean : mean);
     if (tid == 0) *j.tail_stages = c;
     int units = 0, parts = 0;
     for (int b0 = 0; b0 < j.B; b0 += kPrepThreads) {

@@ -67,7 +67,7 @@ __device__ __forceinline__ int tail_seq(const PrefixJob &j, int u, int lane)
     int lo = 0, n = j.B;               // among [lo, lo + n)
     while (n > 1) {
         const int step = (n + 31) >> 5, at = lo + lane * step;
-        const bool on = at < lo + n && j.unit0[at] <= u;
+        const bool on = at < lo + n && __ldcg(j.unit0 + at) <= u;
         const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, on));  // (lane 0 is on)
         n = min(step, n - k * step);
         lo += k * step;
@@ -82,13 +82,13 @@ __device__ __forceinline__ TailTask tail_task(const PrefixJob &j, int u, int lan
     t.first = j.cu[t.b];
     t.n = j.cu[t.b + 1] - t.first;
     t.L = j.kv_len[t.b];
-    t.skip = j.skip[t.b];
-    const int c = *j.tail_stages, rows = t.n * j.G;
+    t.skip = __ldcg(j.skip + t.b);
+    const int c = __ldcg(j.tail_stages), rows = t.n * j.G;
     const TailBlocks rb(rows);
     t.own = rows <= kTailMax;
     const int own = t.L - t.skip * j.block, all = t.own ? (own + kTlTile - 1) / kTlTile : 1;
     t.nz = (all + c - 1) / c;
-    const int i = u - j.unit0[t.b], q = i / t.nz;
+    const int i = u - __ldcg(j.unit0 + t.b), q = i / t.nz;
     t.z = i - q * t.nz;
     t.h = q / rb.blocks;
     t.row0 = (q - t.h * rb.blocks) * rb.rows;
@@ -98,7 +98,7 @@ __device__ __forceinline__ TailTask tail_task(const PrefixJob &j, int u, int lan
     const int seen = t.own ? (sees + kTlTile - 1) / kTlTile : 0;
     t.s0 = min(t.z * c, seen);
     t.s1 = min(t.s0 + c, seen);
-    t.part0 = j.part0[t.b] + q * t.nz;
+    t.part0 = __ldcg(j.part0 + t.b) + q * t.nz;
     return t;
 }
 
@@ -537,6 +537,7 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
     for (int n = 0; n < NT; ++n) s.scale(n, out, out);
     // ---- what the prefix kernel left of these rows, its pieces dealt to the ranges: of
     // the group's span and of the sequence's
+    if (t.skip != 0 || !t.own) pdl_wait();
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         if (which ? t.own : t.skip == 0) continue;
@@ -667,9 +668,12 @@ tail_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUtenso
         mbar_fence_init();
     }
     __syncwarp();
-    pdl_wait();
+    // The prefix kernel lets this one start once its own wait for the prep kernel is
+    // over.  So what prep left is there, and CTAs start where the prefix kernel's have
+    // ended; a task waits for all of them only before it reads what they left, and each
+    // warp before it ends.
     pdl_trigger();
-    const int tasks = j.unit0[j.B], step = gridDim.x * kTlWarps;
+    const int tasks = __ldcg(j.unit0 + j.B), step = gridDim.x * kTlWarps;
     uint32_t it = 0;
     bool ok = true;
     // (neighbours in the list, which share a cache head, run side by side)
@@ -680,6 +684,7 @@ tail_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUtenso
         else
             ok = tail_run<D, 2>(j, t, sh, ring, map_k, map_v, lane, it);
     }
+    pdl_wait();
     // after a wait that ran out: copies still in flight land before the exit
     if (!ok)
         for (int i = 0; i < kTlStages; ++i)
