@@ -347,6 +347,13 @@ struct PrefixSpace {
     }
 };
 
+// Sizes within what the kernels count in 32 bits.
+bool prefix_fits(int T, int Hq, int B, int groups, const PrefixSpace &w)
+{
+    return (int64_t)T * Hq <= 0x7FFFFFFF && (int64_t)groups + B <= (1 << 30) &&
+           w.units <= kPrefixMaxUnits;
+}
+
 void fill_common(Job &j, sv_handle *h, const void *src0, sv_dtype dt, int64_t rs, int V)
 {
     memset(&j, 0, sizeof j);
@@ -1065,7 +1072,8 @@ size_t sv_kv_prefix_work_bytes(const sv_handle *h, int T, int Hq, int H, int D, 
 {
     if (!h || T < 0 || B < 0 || Hq < 1 || H < 1 || Hq % H || groups < 1 || (D != 64 && D != 128))
         return 0;
-    return PrefixSpace(h->sms, T, Hq, H, D, B, groups).bytes;
+    const PrefixSpace w(h->sms, T, Hq, H, D, B, groups);
+    return prefix_fits(T, Hq, B, groups, w) ? w.bytes : 0;
 }
 
 sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_stride,
@@ -1095,7 +1103,7 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
         !work || !aligned16(work))
         return SV_ERR_INVALID_ARG;
     const PrefixSpace w(h->sms, T, Hq, H, D, B, groups);
-    if (w.units > kPrefixMaxUnits) return SV_ERR_UNSUPPORTED;
+    if (!prefix_fits(T, Hq, B, groups, w)) return SV_ERR_UNSUPPORTED;
     if (work_bytes < w.bytes) return SV_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_prefix_attention")) return fi;
@@ -1136,6 +1144,10 @@ sv_status sv_kv_read(sv_handle *h, const void *k_cache, const void *v_cache,
     const int esz = dtype == SV_BF16 ? 2 : 4;
     if (!table || !cu || !k || !v || (uintptr_t)k % esz || (uintptr_t)v % esz ||
         k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+        return SV_ERR_INVALID_ARG;
+    // rows that several outputs share
+    if (k == v || (T > 1 && (k_token_stride == 0 || v_token_stride == 0)) ||
+        (H > 1 && (k_head_stride == 0 || v_head_stride == 0)))
         return SV_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_read")) return fi;

@@ -36,8 +36,9 @@
 //   tensor  S0 . . PV0 S0' PV1 S1' ...
 //   slot 0    softmax     softmax
 // A unit of up to 128 rows gives both slots the same queries and every other
-// tile each, and joins the two at its end.  Each softmax thread holds its row's
-// 128 scores; four more warps bring the values to bf16, one fetches, one issues.
+// tile each, and joins the two at its end.  A softmax thread has a row, and takes
+// its 128 scores 64 at a time; four more warps bring the values to bf16, one
+// fetches, two issue (a slot each, taking turns).
 //
 // The running maximum moves lazily: only where a tile's maximum passes it by
 // 2^8 are a row's sums rescaled.
@@ -62,7 +63,7 @@ constexpr int kPxReaders = 14;         // warps that read them
 constexpr int kPxRing = 8;             // tiles whose scales are kept
 constexpr int kPxSoft = 8;             // softmax warps, four a slot
 constexpr int kPxThreads = 512;        // + 4 converting warps, producer, 2 issuers, 1 idle
-// Registers: 128 a thread at launch; the softmax warps, which hold a row's 128
+// Registers: 128 a thread at launch; the softmax warps, which hold 64 of a row's
 // scores, take what the others leave (256 * 184 + 256 * 72 = 512 * 128).
 constexpr int kPxRegs = 128, kPxSoftRegs = 184, kPxSideRegs = 72;
 static_assert(256 * kPxSoftRegs + 256 * kPxSideRegs <= kPxThreads * kPxRegs, "registers");
@@ -107,7 +108,7 @@ __device__ __forceinline__ int px_tiles(int end) { return (int)(((long long)end 
 __global__ void __cluster_dims__(kPrepCtas, 1, 1) __launch_bounds__(kPrepThreads)
 prefix_prep_kernel(const PrefixJob j, int warps)
 {
-    __shared__ int s_bad, s_many;
+    __shared__ int s_bad, s_many, s_lost;
     __shared__ unsigned long long s_shared;
     __shared__ longlong2 s_sum[kPrepThreads / 32];
     __shared__ int2 s_scan[kPrepThreads / 32];
@@ -116,15 +117,16 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     const int shift = 31 - __clz(j.block);
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) s_bad = s_many = 0, s_shared = 0;
+    if (tid == 0) s_bad = s_many = s_lost = 0, s_shared = 0;
     if (blockIdx.x == 0)
         for (int i = tid; i < kTailParts * warps; i += kPrepThreads) j.tail_arrived[i] = 0;
     auto edge = [&](int g) { return j.cu_group ? j.cu_group[g] : g ? j.B : 0; };
+    bool lost = false;
     auto tokens = [&](int b, int &n, int &L) {  // false: lengths out of range
         const int first = j.cu[b], end = j.cu[b + 1];
         L = j.kv_len[b];
         n = end - first;
-        return first >= 0 && end <= j.T && n >= 0 && L >= n &&
+        return !lost && first >= 0 && end <= j.T && n >= 0 && L >= n &&
                ((L + (long long)j.block - 1) >> shift) <= j.cols;
     };
     // leading pages that sequence b has in common with its group's first
@@ -188,8 +190,13 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         const int lo = edge(g), hi = edge(g + 1);
         if (lo < 0 || hi < lo || hi > j.B) s_bad = 1;
     }
+    // Rows of sequences out of order may be more than there are, and than the
+    // workspace has units for: then none is taken.
+    for (int b = tid; b < j.B; b += kPrepThreads)
+        if (j.cu[b + 1] < j.cu[b]) s_lost = 1;
     __syncthreads();
     const bool bad = s_bad;
+    lost = s_lost;
     if (bad && tid == 0) latch(j.err, SV_ERR_DEVICE_BOUNDS);
     if (bad)
         for (int b = tid; b < j.B; b += kPrepThreads) j.skip[b] = j.seq_group[b] = 0;

@@ -51,8 +51,7 @@
  *   sv_verify_spot, sv_packed_step, sv_packed_topk_step,
  *   sv_packed_anyorder_step, sv_kv_plan, sv_kv_append, sv_kv_attention,
  *   sv_kv_prefix_attention, sv_kv_read, sv_qk_norm_rope, sv_sample_rows)
- *   return the
- *   status `code` (1..6) at its launch point,
+ *   return the status `code` (1..6) at its launch point,
  *   after its argument checks and before anything is enqueued.  It is read
  *   at every call; unset, nothing is injected.
  */
@@ -497,17 +496,23 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
  *   the group with new tokens, wholly within prefix_len[g] and within the tokens
  *   before each sequence's new ones.  So the result does not depend on cu_group
  *   and prefix_len; they say where to look.  Groups that share nothing, and
- *   sequences of no group, go the way of sv_kv_attention.
- *   Precision: as sv_kv_attention; on the shared pages a weight is held to 2^-8
- *   of itself and scales may lie any distance apart.
+ *   sequences of no group, are read each by itself.
+ *   Precision: scores, maxima and sums are fp32, a query is held as there.  A
+ *   weight is held to 2^-8 of itself; among a sequence's own tokens, and where
+ *   little is shared, for up to 32 query rows a cache head to 2^-11, down to 2^-19
+ *   of the row's largest product of a weight and a value scale.  Value scales may
+ *   lie any distance apart.  The same call gives the same bits.
+ *   Pages stand in several rows of the table then, which sv_kv_plan does not know:
+ *   a sequence whose cached_len is the shared tokens' gives back what it holds
+ *   beyond them, and with held set to 0 after that no longer the shared ones.
  *   work: device memory of the caller, 16-byte aligned, of the size that
  *     sv_kv_prefix_work_bytes tells for these sizes (0 for sizes that the call
  *     refuses).  Its content is of no consequence before and after; calls that
  *     may run at the same time, captured ones among them, need one each.
  * Errors: SV_ERR_INVALID_ARG (too small a workspace among them);
  * SV_ERR_UNSUPPORTED (D; sizes beyond 32 bits); latched SV_ERR_DEVICE_BOUNDS as
- * sv_kv_attention, and for groups out of order or range (nothing is shared
- * then).
+ * sv_kv_attention, for groups out of order or range (nothing is shared then),
+ * and for cu_new out of order (no row is meaningful then).
  * ------------------------------------------------------------------------- */
 size_t sv_kv_prefix_work_bytes(const sv_handle *h, int T, int Hq, int H, int D, int B,
                                int groups);
@@ -527,9 +532,9 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
  * positions first[b] .. of sequence b (first NULL: 0): each byte's e4m3 value
  * times its page's and head's scale, rounded once (exact in bf16 where the scale
  * is a power of two).  NaN stays NaN.  Rows from cu[B] on are not written.
- * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D, H > 32767); rows whose
- * position or page is out of range latch SV_ERR_DEVICE_BOUNDS and are not
- * written.
+ * Errors: SV_ERR_INVALID_ARG (outputs that are one, strides of 0 among them);
+ * SV_ERR_UNSUPPORTED (D, H > 32767); rows whose position or page is out of range
+ * latch SV_ERR_DEVICE_BOUNDS and are not written.
  * ------------------------------------------------------------------------- */
 sv_status sv_kv_read(sv_handle *h, const void *k_cache, const void *v_cache,
                      const float *k_scale, const float *v_scale, int H, int D, int block,
@@ -550,8 +555,9 @@ sv_status sv_kv_read(sv_handle *h, const void *k_cache, const void *v_cache,
  *     y_a = x'_a cos t - x'_b sin t,  y_b = x'_b cos t + x'_a sin t;
  *   elements from rot on (rot even, 0 to D) are x'.
  * In fp32, rounded once to the outputs' type; an angle is right to 2^-32 of a
- * turn for |inv_freq| < 2 at any position.  (Squares are summed in fp32: heads
- * beyond 2^60 need no norm.)
+ * turn for |inv_freq| < 2 at any position.  Squares are summed in fp32 and
+ * weights multiplied in first: elements and weights of a head with a norm lie
+ * below 2^60.  NaN and infinities reach their pair, with a norm their head.
  * A token with a negative position is skipped (sv_kv_plan's padding).  An output
  * may be its input, with the same type and strides; other overlaps may not be.
  * Errors: SV_ERR_INVALID_ARG; SV_ERR_UNSUPPORTED (D > 512, T (Hq + H) beyond

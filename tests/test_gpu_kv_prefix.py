@@ -351,3 +351,31 @@ def test_own_scales_far_apart(dbv, far):
     tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15 * size[..., None]) * mag
     assert ((got["out"].double() - want).abs() <= tol).all()
     ok(dbv)
+
+
+def test_sequences_out_of_order(dbv):
+    """cu_new that goes back: more rows than there are, in all.  Latched; what lies
+    behind the outputs and the workspace is left alone, and the next call is right."""
+    c = pu.make(21, [64], [1], [20], [40], 2, 2, 128, 16)
+    B = 300
+    d = dict(c, cu=np.append(np.tile([0, 40], B // 2), 0).astype(np.int32),
+             table=np.repeat(c["table"], B, 0), kv=np.repeat(c["kv"], B))
+    a, k = pu.tensors(d)
+    dbv.sv_kv_prefix_attention(*a, **k)
+    h = dbv.default_handle(torch.device("cuda", 0))
+    with pytest.raises(dbv.SVError) as e:
+        h.sync_status()
+    assert e.value.status == dbv.SV_ERR_DEVICE_BOUNDS
+    pu.check(c, pu.run(dbv, c))
+    ok(dbv)
+
+
+def test_masks_of_fewer_words(dbv):
+    """New tokens beyond a mask's words are seen by none."""
+    c = pu.make(22, [96], [3], [5, 0, 9], [70, 40, 3], 2, 2, 64, 32, tree=True)
+    full = c["mask"]
+    c["mask"] = np.ascontiguousarray(full[:, :2])
+    got = pu.run(dbv, c)
+    c["mask"] = full & np.array([2 ** 32 - 1, 2 ** 32 - 1, 0], np.uint32)
+    pu.check(c, got)
+    ok(dbv)

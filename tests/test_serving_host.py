@@ -22,7 +22,8 @@ def prefix_args(**kw):
     (dict(scale=float("inf")), 1), (dict(out=None), 1), (dict(out=OK + 2), 1),
     (dict(T=1 << 30), 5), (dict(cols=1 << 26), 5), (dict(groups=0), 1),
     (dict(group=None, groups=2), 1), (dict(work=None), 1), (dict(work=OK + 8), 1),
-    (dict(size=100), 1), (dict(T=1 << 27, Hq=16, H=16, groups=1 << 27, B=1 << 27), 5)])
+    (dict(size=100), 1), (dict(T=1 << 27, Hq=16, H=16, groups=1 << 27, B=1 << 27), 5),
+    (dict(B=1 << 30), 5), (dict(groups=1 << 30), 5)])
 def test_prefix_refusals(lib, h, kw, want):  # noqa: F811
     assert lib.sv_kv_prefix_attention(h, *prefix_args(**kw)) == want
 
@@ -35,13 +36,14 @@ def test_prefix_work_bytes(lib, h):  # noqa: F811
     assert size(1024, 4, 2, 64, 9, 7) - size(1024, 4, 2, 64, 9, 1) >= 2 * 6 * unit
     assert size(4, 4, 2, 64, 2, 1) < size(4, 4, 2, 128, 2, 1)
     for bad in ((-1, 4, 2, 64, 2, 1), (4, 3, 2, 64, 2, 1), (4, 4, 2, 96, 2, 1),
-                (4, 4, 2, 64, -2, 1), (4, 4, 2, 64, 2, 0)):
+                (4, 4, 2, 64, -2, 1), (4, 4, 2, 64, 2, 0), (1 << 30, 4, 2, 64, 2, 1),
+                (4, 4, 2, 64, 1 << 30, 1)):
         assert size(*bad) == 0
 
 
 def read_args(**kw):
     a = dict(kc=OK, vc=OK, ks=OK, vs=OK, H=2, D=64, block=64, pages=4, table=OK, cols=4,
-             first=None, cu=OK, B=2, T=4, k=OK, v=OK, dtype=1, kt=128, kh=64, vt=128, vh=64,
+             first=None, cu=OK, B=2, T=4, k=OK, v=2 * OK, dtype=1, kt=128, kh=64, vt=128, vh=64,
              stream=None)
     a.update(kw)
     return list(a.values())
@@ -52,7 +54,8 @@ def read_args(**kw):
     (dict(H=40000), 5), (dict(D=96), 5), (dict(block=24), 1), (dict(pages=0), 1),
     (dict(pages=1 << 30), 5), (dict(table=None), 1), (dict(cols=0), 1), (dict(cols=1 << 26), 5),
     (dict(cu=None), 1), (dict(B=-1), 1), (dict(T=-1), 1), (dict(k=None), 1), (dict(v=OK + 1), 1),
-    (dict(dtype=0, k=OK + 2), 1), (dict(dtype=3), 1), (dict(kt=-1), 1), (dict(vh=-1), 1)])
+    (dict(dtype=0, k=OK + 2), 1), (dict(dtype=3), 1), (dict(kt=-1), 1), (dict(vh=-1), 1),
+    (dict(v=OK), 1), (dict(kt=0), 1), (dict(vh=0), 1)])
 def test_read_refusals(lib, h, kw, want):  # noqa: F811
     assert lib.sv_kv_read(h, *read_args(**kw)) == want
 
