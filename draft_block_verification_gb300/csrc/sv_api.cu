@@ -336,8 +336,8 @@ struct PrefixSpace {
         units = H * (2 * rows / kPrefixRows + std::min<int64_t>(groups, std::min(B, T)) +
                      std::min<int64_t>(B, rows / kTailMax));
         units = std::max(units, std::min<int64_t>(2 * units, sms / 2));  // (of half the rows)
-        seq = 0;  // skip, seq_group, part0 [B], unit0 [B + 1], tail_stages
-        span = seq + up(((size_t)4 * B + 2) * sizeof(int32_t));
+        seq = 0;  // skip, seq_group, part0 [B], unit0 [B + 1], tail_stages, next
+        span = seq + up(((size_t)4 * B + 3) * sizeof(int32_t));
         arrived = span + up(((size_t)groups + B + 1) * sizeof(PrefixSpan));
         unit_ctas = arrived + up((size_t)kTailParts * tail_warps(sms) * sizeof(unsigned));
         part_unit = unit_ctas + up((size_t)units * sizeof(int2));
@@ -1115,7 +1115,7 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
                    {k_scale, v_scale}, table, kv_len, cu_new, prefix_len, cu_group, mask, B, T,
                    Hq, H, Hq / H, D, block, pages, cols, groups, mask_words, scale,
                    (uint16_t *)out, lse, seq, seq + B, seq + (size_t)3 * B, seq + (size_t)2 * B,
-                   seq + (size_t)4 * B + 1, (PrefixSpan *)(ws + w.span),
+                   seq + (size_t)4 * B + 1, seq + (size_t)4 * B + 2, (PrefixSpan *)(ws + w.span),
                    (unsigned *)(ws + w.arrived), h->sms, (int2 *)(ws + w.unit_ctas),
                    (int32_t *)(ws + w.part_unit), (float *)(ws + w.part),
                    (float *)(ws + w.tail), h->d_err};

@@ -69,8 +69,9 @@ struct PrefixSpan {
     int first, rows;           // first row of q, query rows a cache head (0: no work)
     int lead, page0;           // the table row, and its first page
     int end, ctx;              // tokens from there on, and those that every row sees
-    long long start;           // where its work starts, in tiles of slots
+    long long start;           // where its work starts, if its units are cut
     int unit0, block;          // its first unit, rows of a unit
+    int loose0, unused;        // units before it that are not cut
 };
 struct PrefixJob {
     const uint16_t *q;         // [T, Hq, D] bf16
@@ -90,6 +91,7 @@ struct PrefixJob {
     int32_t *unit0;            // [B + 1] the tail's tasks of the sequences before
     int32_t *part0;            // [B] its parts
     int32_t *tail_stages;      // of a task, at most
+    int32_t *next;             // of the units that are not cut
     PrefixSpan *span;          // [groups + B + 1]
     unsigned *tail_arrived;    // a counter a part
     // from the prefix kernel

@@ -82,16 +82,18 @@ constexpr int kPrepCtas = 8, kPrepThreads = 512;
 // heads: 33 us against 41.)
 constexpr unsigned long long kPxLeast = 8192;
 
-// Row blocks of a head, and costs, in tiles of a slot (1,750 cycles).  What a piece's
-// start and end take (queries, first scores, sums) is counted at the front of a unit.
-constexpr int kPxUnitCost = 10;
+// Row blocks of a head, and costs, in 400 cycles: a tile of up to 256 rows, one of up
+// to 128, and what a unit takes beside its tiles (queries, first scores, sums), which
+// is counted at its front.
+constexpr int kPxWide = 9, kPxNarrow = 5, kPxUnitCost = 45;
+constexpr int kPxWhole = 130;          // of a unit that is not cut
 struct RowBlocks {
     int blocks, full, last;            // blocks; a tile's cost, in all blocks and in the last
     __device__ __forceinline__ RowBlocks(int rows, int block)
     {
         blocks = (rows + block - 1) / block;
-        full = block > 128 ? 2 : 1;    // one slot's tiles cost half
-        last = rows - (blocks - 1) * block > 128 ? 2 : 1;
+        full = block > 128 ? kPxWide : kPxNarrow;
+        last = rows - (blocks - 1) * block > 128 ? kPxWide : kPxNarrow;
     }
     __device__ __forceinline__ long long unit(int tiles) const
     {
@@ -346,52 +348,73 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     // tail has to read (with as many units as CTAs the halves would only have values
     // brought to bf16 twice).
     const int spans = j.groups + j.B;
-    int big = 0;
+    int big = 0, small = 0;
     for (int g = lane; g < spans; g += 32) {
         const int rows = __ldcg(&j.span[g].rows);
-        if (rows) big += RowBlocks(rows, kPxRows).blocks * j.H;
+        if (!rows) continue;
+        const RowBlocks rb(rows, kPxRows);
+        big += rb.blocks * j.H;
+        if (rb.head(px_tiles(__ldcg(&j.span[g].end))) <= kPxWhole * (long long)rb.blocks)
+            small += rb.blocks * j.H;
     }
     big = __reduce_add_sync(0xFFFFFFFFu, big);
+    small = __reduce_add_sync(0xFFFFFFFFu, small);
     const int block = 4 * big < j.prefix_ctas ? 128 : kPxRows;
+    // Small units, if there are at least as many as CTAs, are not cut: CTAs take them one
+    // by one when their shares of the rest are done.  (CTAs take 240,000 to 330,000
+    // cycles for the same 66 tiles.)
+    const int whole = small >= j.prefix_ctas ? kPxWhole : 0;
     // where each span's work and units start
     long long at = 0;
-    int unit = 0;
+    int unit = 0, loose = 0;
     for (int g0 = 0; g0 < spans; g0 += 32) {
         const int g = g0 + lane;
         long long w = 0;
-        int u = 0;
+        int u = 0, v = 0;
         if (g < spans) {
             const int rows = __ldcg(&j.span[g].rows);
             if (rows) {
                 const RowBlocks rb(rows, block);
-                w = rb.head(px_tiles(__ldcg(&j.span[g].end))) * j.H;
+                const int tiles = px_tiles(__ldcg(&j.span[g].end));
                 u = rb.blocks * j.H;
+                w = rb.head(tiles);
+                if (w <= whole * (long long)rb.blocks) {
+                    v = u;
+                    w = 0;
+                } else {
+                    w *= j.H;
+                }
             }
         }
         long long ws = w;
-        int us = u;
-#pragma unroll
+        int us = u, vs = v;
+#pragma unroll 1
         for (int k = 1; k < 32; k <<= 1) {
             const long long a = __shfl_up_sync(0xFFFFFFFFu, ws, k);
-            const int c = __shfl_up_sync(0xFFFFFFFFu, us, k);
+            const int c = __shfl_up_sync(0xFFFFFFFFu, us, k), d = __shfl_up_sync(0xFFFFFFFFu, vs, k);
             if (lane >= k) {
                 ws += a;
                 us += c;
+                vs += d;
             }
         }
         if (g < spans) {
             j.span[g].start = at + ws - w;
             j.span[g].unit0 = unit + us - u;
+            j.span[g].loose0 = loose + vs - v;
             j.span[g].block = block;
         }
         at += __shfl_sync(0xFFFFFFFFu, ws, 31);
         unit += __shfl_sync(0xFFFFFFFFu, us, 31);
+        loose += __shfl_sync(0xFFFFFFFFu, vs, 31);
     }
     if (lane == 0) {
         PrefixSpan r = {};
         r.start = at;
         r.unit0 = unit;
+        r.loose0 = loose;
         j.span[spans] = r;
+        *j.next = 0;
     }
 }
 
@@ -406,19 +429,28 @@ struct PxPiece {
     __device__ __forceinline__ bool wide() const { return rows > 128; }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
-// A CTA's pieces, found by its producer.  A tile belongs to the share that its first
-// unit of cost lies in.
+// A CTA's pieces, found by its producer.  First its share of the units that are cut: a
+// tile belongs to the share that its first unit of cost lies in.  Then of the others
+// the next one, until none is left.  (Which CTA takes it is not seen in the result.)
 struct PxWalk {
     long long pos, end;
+    int loose;                         // units that are not cut
     __device__ __forceinline__ bool next(const PrefixJob &j, PxPiece &p, int lane)
     {
         for (;;) {
-            if (pos >= end) return false;
-            // the last span that starts at pos or before
+            const bool cut = pos < end;
+            int u = 0;
+            if (!cut) {
+                if (loose == 0) return false;
+                if (lane == 0) u = atomicAdd(j.next, 1);
+                u = __shfl_sync(0xFFFFFFFFu, u, 0);
+                if (u >= loose) return false;
+            }
+            // the last span that starts at pos (or u) or before
             int lo = 0, n = j.groups + j.B;
             while (n > 1) {
                 const int step = (n + 31) >> 5, at = lo + lane * step;
-                const bool on = at < lo + n && j.span[at].start <= pos;
+                const bool on = at < lo + n && (cut ? j.span[at].start <= pos : j.span[at].loose0 <= u);
                 const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, on));  // (lane 0 is on)
                 n = min(step, n - k * step);
                 lo += k * step;
@@ -426,21 +458,27 @@ struct PxWalk {
             const PrefixSpan r = j.span[lo];
             const RowBlocks rb(r.rows, r.block);
             const int tiles = px_tiles(r.end);
-            const long long head = rb.head(tiles), unit = rb.unit(tiles);
-            long long x = pos - r.start;
-            const int h = (int)div_pos(x, head);
-            x -= h * head;
-            const int block = min((int)div_pos(x, unit), rb.blocks - 1);
-            x -= block * unit;
-            const int cost = block == rb.blocks - 1 ? rb.last : rb.full;
-            // a tile lies behind its unit's front
-            const long long front = pos - x + kPxUnitCost;
-            const int t = x <= kPxUnitCost ? 0 : (int)div_pos(x - kPxUnitCost + cost - 1, cost);
-            pos = front + (long long)min(t, tiles) * cost;
-            if (t >= tiles) continue;  // (the unit's last tile starts before the share)
-            if (pos >= end) return false;
-            const int m = (int)min((long long)(tiles - t), div_pos(end - pos + cost - 1, cost));
-            pos += (long long)m * cost;
+            int h, block, t = 0, m = tiles;
+            if (cut) {
+                const long long head = rb.head(tiles), unit = rb.unit(tiles);
+                long long x = pos - r.start;
+                h = (int)div_pos(x, head);
+                x -= h * head;
+                block = min((int)div_pos(x, unit), rb.blocks - 1);
+                x -= block * unit;
+                const int cost = block == rb.blocks - 1 ? rb.last : rb.full;
+                // a tile lies behind its unit's front
+                const long long front = pos - x + kPxUnitCost;
+                t = x <= kPxUnitCost ? 0 : (int)div_pos(x - kPxUnitCost + cost - 1, cost);
+                pos = front + (long long)min(t, tiles) * cost;
+                if (t >= tiles) continue;  // (the unit's last tile starts before the share)
+                if (pos >= end) continue;
+                m = (int)min((long long)(tiles - t), div_pos(end - pos + cost - 1, cost));
+                pos += (long long)m * cost;
+            } else {
+                h = (u - r.loose0) / rb.blocks;
+                block = u - r.loose0 - h * rb.blocks;
+            }
             p.h = h;
             p.row0 = block * r.block;
             p.rows = min(r.block, r.rows - p.row0);
@@ -1077,7 +1115,8 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             const int shift = 31 - __clz(j.block), per_tile = kPxTile >> shift;
             const int inner = lane & (per_tile - 1);
             const long long total = j.span[j.groups + j.B].start;
-            PxWalk walk = {span_at(total, ctas, blockIdx.x), span_at(total, ctas, blockIdx.x + 1)};
+            PxWalk walk = {span_at(total, ctas, blockIdx.x), span_at(total, ctas, blockIdx.x + 1),
+                           j.span[j.groups + j.B].loose0};
             for (bool more = true; ok && more;) {
                 more = walk.next(j, pc, lane);
                 if (!more) pc.rows = 0;
