@@ -43,9 +43,18 @@
 // The running maximum moves lazily: only where a tile's maximum passes it by
 // 2^8 are a row's sums rescaled.
 //
-// Split.  Tiles of all units laid end to end are cut into equal spans, one a
-// CTA.  A unit's piece leaves its sums in the workspace, fp32, four elements of 256
-// rows after the other; the tail kernel adds a unit's pieces.
+// Split.  Tiles of all large units laid end to end are cut into equal shares, one a
+// CTA; small units are taken whole, by the CTAs whose shares are done.  A unit's
+// piece leaves its sums in the workspace, fp32, four elements of 256 rows after the
+// other; the tail kernel adds a unit's pieces.
+//
+// What bounds it.  A slot's tile is a chain: its softmax (1,400 to 2,000 cycles), the
+// products with its weights, the next scores (1,024 of the tensor cores), and what
+// passes between them; two slots, which is what tensor memory holds, make it 3,400
+// cycles a tile of 256 rows at best, of which the tensor cores work 2,048.  A unit
+// takes some 18,000 beside its tiles.  64 sequences of 13 tokens of 32 heads behind
+// 8,192 shared ones and 330 of their own: 175 us of the call's 229; 24 of 4 behind
+// three prefixes of up to 131,072, D = 64: 335 of 387 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -78,15 +87,17 @@ constexpr int kPrepCtas = 8, kPrepThreads = 512;
 
 // What little is shared the tail reads sooner for each sequence by itself: 16 tokens
 // of eight rows of a head take it about 2 ns in all, a run of the prefix kernel some
-// 15 us more than one without work.  (Four sequences of a row, 4,096 shared tokens, 8
-// heads: 33 us against 41.)
+// 15 us more than one without work.  (Four sequences of a token, 1,024 shared ones, 8
+// cache heads of 4 rows: 29 us against 33.)
 constexpr unsigned long long kPxLeast = 8192;
 
 // Row blocks of a head, and costs, in 400 cycles: a tile of up to 256 rows, one of up
 // to 128, and what a unit takes beside its tiles (queries, first scores, sums), which
-// is counted at its front.
+// is counted at its front.  (64 draft blocks / three long documents: with units at a
+// tenth of that 448 / 624 us, at 36 to 56 228 / 387; narrow tiles at half of wide ones
+// 248 / 430 with small units cut, at 6 230 / 398.)
 constexpr int kPxWide = 9, kPxNarrow = 5, kPxUnitCost = 45;
-constexpr int kPxWhole = 130;          // of a unit that is not cut
+constexpr int kPxWhole = 130;          // of a unit that is not cut (90 to 250: equal)
 struct RowBlocks {
     int blocks, full, last;            // blocks; a tile's cost, in all blocks and in the last
     __device__ __forceinline__ RowBlocks(int rows, int block)
@@ -345,8 +356,8 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     if (warp != 0) return;
     // Rows of a unit.  A piece's sums are as many as its rows, whatever its tokens; so
     // where CTAs by far outnumber the units, units of half the rows halve what the
-    // tail has to read (with as many units as CTAs the halves would only have values
-    // brought to bf16 twice).
+    // tail has to read (128 single tokens of 32 heads: 88 us against 90; with as many
+    // units as CTAs the halves would only have values brought to bf16 twice).
     const int spans = j.groups + j.B;
     int big = 0, small = 0;
     for (int g = lane; g < spans; g += 32) {

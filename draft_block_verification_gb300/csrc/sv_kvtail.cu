@@ -28,6 +28,11 @@
 // at most, has fp16's 11 bits down to 2^-19 of the largest, and steps of 2^-30 of it
 // below; value scales may lie any distance apart.
 //
+// What bounds it: one warp's chain of steps, some 435 instructions for 16 tokens and 16
+// rows, three warps to a scheduler.  128 sequences of a token, 32 heads, 320 tokens of
+// their own each, with the join of 16 pieces' sums: 33 of the call's 88 us; four of one
+// token over 1,088: 16 of 29.
+//
 // A warp fetches its own stages of 32 tokens (TMA), two in flight.  Ranges are cut
 // so that every warp of a wave has a task; ranges of the same rows join in the
 // workspace, by the last to arrive, in their order.

@@ -379,3 +379,23 @@ def test_masks_of_fewer_words(dbv):
     c["mask"] = full & np.array([2 ** 32 - 1, 2 ** 32 - 1, 0], np.uint32)
     pu.check(c, got)
     ok(dbv)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_units_that_are_not_cut(dbv, D, tree):
+    """More small units than CTAs, beside some that are cut; the same bits each time,
+    whichever CTA takes them."""
+    r = np.random.RandomState(7)
+    sizes = [40, 1, 30]
+    B = sum(sizes)
+    new = [int(x) for x in r.randint(5, 24, B)]
+    after = [int(x) for x in r.randint(0, 300, B)]
+    after[5], after[50], new[60] = 5000, 4000, 300
+    c = pu.make(23, [900, 50, 2500], sizes, after, new, 4, 4, D, 32, tree=tree)
+    want = pu.run(dbv, c)
+    pu.check(c, want)
+    for _ in range(5):
+        got = pu.run(dbv, c)
+        assert all(torch.equal(got[n], want[n]) for n in want)
+    ok(dbv)
