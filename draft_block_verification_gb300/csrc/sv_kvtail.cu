@@ -84,9 +84,9 @@ __device__ __forceinline__ TailTask tail_task(const PrefixJob &j, int u, int lan
 {
     TailTask t;
     t.b = tail_seq(j, u, lane);
-    t.first = j.cu[t.b];
-    t.n = j.cu[t.b + 1] - t.first;
-    t.L = j.kv_len[t.b];
+    t.first = __ldcg(j.cu + t.b);
+    t.n = __ldcg(j.cu + t.b + 1) - t.first;
+    t.L = __ldcg(j.kv_len + t.b);
     t.skip = __ldcg(j.skip + t.b);
     const int c = __ldcg(j.tail_stages), rows = t.n * j.G;
     const TailBlocks rb(rows);
