@@ -64,7 +64,8 @@ cudaError_t attend_launch(const AttendJob &j, int sms, cudaStream_t s);
 // Attention over a shared prefix: prep finds what is shared and cuts the work, the
 // prefix kernel reads the shared pages, the tail kernel the rest, and joins.
 // A span: pages that query rows read, a group's shared ones or a sequence's own.
-// First the groups', then the sequences', then an entry with the totals.
+// First the groups', then the sequences', then an entry with the totals (rows: the
+// shares that the units are cut into).
 struct PrefixSpan {
     int first, rows;           // first row of q, query rows a cache head (0: no work)
     int lead, page0;           // the table row, and its first page

@@ -44,7 +44,7 @@
 // 2^8 are a row's sums rescaled.
 //
 // Split.  Tiles of all large units laid end to end are cut into equal shares, one a
-// CTA; small units are taken whole, by the CTAs whose shares are done.  A unit's
+// CTA (fewer where units are few: their pieces are added in turn); small units are taken whole, by the CTAs whose shares are done.  A unit's
 // piece leaves its sums in the workspace, fp32, four elements of 256 rows after the
 // other; the tail kernel adds a unit's pieces.
 //
@@ -378,6 +378,7 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     // where each span's work and units start
     long long at = 0;
     int unit = 0, loose = 0;
+    float most = 0.f;                  // of a unit that is cut
     for (int g0 = 0; g0 < spans; g0 += 32) {
         const int g = g0 + lane;
         long long w = 0;
@@ -393,6 +394,7 @@ prefix_prep_kernel(const PrefixJob j, int warps)
                     v = u;
                     w = 0;
                 } else {
+                    most = fmaxf(most, (float)w / (float)rb.blocks);
                     w *= j.H;
                 }
             }
@@ -419,11 +421,19 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         unit += __shfl_sync(0xFFFFFFFFu, us, 31);
         loose += __shfl_sync(0xFFFFFFFFu, vs, 31);
     }
+#pragma unroll 1
+    for (int k = 16; k > 0; k >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, k));
     if (lane == 0) {
         PrefixSpan r = {};
         r.start = at;
         r.unit0 = unit;
         r.loose0 = loose;
+        // A unit's pieces are added one after the other, 0.7 us each (what 3.25 of cost
+        // take): beyond sqrt(cost / 3.25) of them that takes longer than a piece saves.
+        // (One unit of 36 rows over 38,272 tokens: 65 us, in 152 pieces 136;
+        // over 131,072 89 and 165.)
+        const long long least = max(1LL, (long long)sqrtf(3.25f * most));
+        r.rows = (int)min((long long)j.prefix_ctas, max(1LL, at / least));
         j.span[spans] = r;
         *j.next = 0;
     }
@@ -1125,9 +1135,10 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             // ---- producer: the pieces, and the pages of each tile, looked up 32 at a time
             const int shift = 31 - __clz(j.block), per_tile = kPxTile >> shift;
             const int inner = lane & (per_tile - 1);
-            const long long total = j.span[j.groups + j.B].start;
-            PxWalk walk = {span_at(total, ctas, blockIdx.x), span_at(total, ctas, blockIdx.x + 1),
-                           j.span[j.groups + j.B].loose0};
+            const PrefixSpan all = j.span[j.groups + j.B];
+            const int mine = min((int)blockIdx.x, all.rows), next = min(mine + 1, all.rows);
+            PxWalk walk = {span_at(all.start, all.rows, mine), span_at(all.start, all.rows, next),
+                           all.loose0};
             for (bool more = true; ok && more;) {
                 more = walk.next(j, pc, lane);
                 if (!more) pc.rows = 0;
