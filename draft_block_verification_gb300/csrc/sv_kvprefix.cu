@@ -44,9 +44,10 @@
 // 2^8 are a row's sums rescaled.
 //
 // Split.  Tiles of all large units laid end to end are cut into equal shares, one a
-// CTA (fewer where units are few: their pieces are added in turn); small units are taken whole, by the CTAs whose shares are done.  A unit's
-// piece leaves its sums in the workspace, fp32, four elements of 256 rows after the
-// other; the tail kernel adds a unit's pieces.
+// CTA (fewer where units are few: their pieces are added in turn); small units are
+// taken whole, by the CTAs whose shares are done.  A unit's piece leaves its sums in
+// the workspace, fp32, four elements of 256 rows after the other; the tail kernel
+// adds a unit's pieces.
 //
 // What bounds it.  A slot's tile is a chain: its softmax (1,400 to 2,000 cycles), the
 // products with its weights, the next scores (1,024 of the tensor cores), and what

@@ -7,9 +7,9 @@
 // takes the bytes that make 16 bytes of output, so that both the loads and the
 // stores of a warp are whole lines; it has the keys' and the values' loads of
 // kAhead items in flight.  A CTA takes a run of rows and looks up where they
-// lie once, a thread for each row.  506 MB of reads and
-// writes (82,000 tokens of 8 x 128 to bf16) take 79 us, 94 % of the rate of a copy; 17
-// tokens, as a graph, 2.0 us.
+// lie once, a thread for each row.  506 MB of reads and writes (82,000 tokens of
+// 8 x 128 to bf16) take 79 us, 94 % of the rate of a copy; 17 tokens, as a graph,
+// 2.0 us.
 #include "sv_common.cuh"
 #include "sv_kv.cuh"
 
