@@ -26,7 +26,9 @@
 // scale against a power of two of the warp's, which stays within 2^3 of the scale;
 // where it would not, O moves to the new scale, in fp32.  So a weight reaches 2^15
 // at most, has fp16's 11 bits down to 2^-19 of the largest, and steps of 2^-30 of it
-// below; value scales may lie any distance apart.
+// below; value scales may lie any distance apart.  A score is not rounded before M is
+// taken from it, but beyond kTlFar it is, as M has been: the difference of a maximum
+// from itself would else be anything within half a step (16 at 2^28).
 //
 // What bounds it: one warp's chain of steps, some 435 instructions for 16 tokens and 16
 // rows, three warps to a scheduler.  128 sequences of a token, 32 heads, 320 tokens of
@@ -51,6 +53,7 @@ constexpr uint32_t kTlTries = 1u << 20;
 constexpr float kTlNone = -1e30f;      // maximum of no tokens
 constexpr float kTlUnit = 8.f;         // log2 of the weight at M
 constexpr float kTlLazy = 3.f;         // log2 of how far a weight may pass it
+constexpr float kTlFar = 0x1p14f;      // maxima from which on scores are rounded first
 constexpr int kTlNear = 3;             // of how far a value scale may lie from the warp's
 
 struct TailWarp {
@@ -358,7 +361,8 @@ __device__ __forceinline__ void tail_step(const PrefixJob &j, const TailTask &t,
         inv /= fr;
     }
     float z[NT][4];
-    auto scores = [&] {
+    // (rounded: the scores before the maximum is taken from them, as it has been)
+    auto scores = [&](bool rounded) {
         float top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -366,6 +370,10 @@ __device__ __forceinline__ void tail_step(const PrefixJob &j, const TailTask &t,
             const float a0 = lv - s.m[n][0], a1 = lv - s.m[n][1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[n][i] = fmaf(y[n][i], i & 1 ? u1 : u0, i & 1 ? a1 : a0);
+            if (rounded)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    z[n][i] = __fsub_rn(__fmul_rn(y[n][i], i & 1 ? u1 : u0), s.m[n][i & 1]) + lv;
         }
         if (__any_sync(0xFFFFFFFFu, hide != 0))
 #pragma unroll
@@ -378,15 +386,21 @@ __device__ __forceinline__ void tail_step(const PrefixJob &j, const TailTask &t,
             top = fmaxf(top, fmaxf(fmaxf(z[n][0], z[n][1]), fmaxf(z[n][2], z[n][3])));
         return top;
     };
-    if (__any_sync(0xFFFFFFFFu, scores() > lv + kTlLazy)) {
+    auto far = [&] {
+        float m = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) m = fmaxf(m, fmaxf(fabsf(s.m[n][0]), fabsf(s.m[n][1])));
+        return m >= kTlFar;
+    };
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, scores(false) > lv + kTlLazy || far()), 0)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float f[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const float u = cf[n][r] * scale.x;
-                float m = hide >> (4 * n + r) & 1 ? -INFINITY : y[n][r] * u;
-                if (!(hide >> (4 * n + r + 2) & 1)) m = fmaxf(m, y[n][r + 2] * u);
+                float m = hide >> (4 * n + r) & 1 ? -INFINITY : __fmul_rn(y[n][r], u);
+                if (!(hide >> (4 * n + r + 2) & 1)) m = fmaxf(m, __fmul_rn(y[n][r + 2], u));
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
                 const float to = m > s.m[n][r] + kTlLazy ? m : s.m[n][r];
@@ -396,7 +410,7 @@ __device__ __forceinline__ void tail_step(const PrefixJob &j, const TailTask &t,
             }
             s.scale(n, f[0], f[1]);
         }
-        scores();
+        scores(far());
     }
     uint32_t p[NT][2];
 #pragma unroll
