@@ -80,6 +80,7 @@ static_assert(256 * kPxSoftRegs + 256 * kPxSideRegs <= kPxThreads * kPxRegs, "re
 constexpr float kPxLazy = 8.f;         // log2 of how far a weight may pass 1
 constexpr uint32_t kPxTries = 1u << 16; // of a wait
 constexpr float kPxNone = -1e30f;      // maximum of no tokens
+constexpr float kPxFar = 0x1p14f;      // maxima from which on scores are rounded first
 
 // ---------------------------------------------------------------------------
 // Which pages are shared.
@@ -786,11 +787,17 @@ struct PxSees {
     }
 };
 
+__device__ __forceinline__ bool px_far(float M) { return fabsf(M) >= kPxFar && M != kPxNone; }
+
 // One tile of a softmax thread: a row's 128 scores to weights, 64 at a time.
 // M (a whole number), l: the row's running maximum and sum of weights.  Weights are
 // taken against the maximum in use before it is known whether one passes it by too
-// much; where one does, M moves, and what there is of the row (sums, values, the
-// tile's first 64 weights) is scaled by the power of two.
+// much; where one does, M moves, what there is of the row (sums, values, the tile's
+// first 64 weights) is scaled by the power of two, and the 64 weights are taken once
+// more, which is the last time: they do not pass the new M.
+// A score s u is not rounded before M is taken from it, which is right while M's own
+// steps are small.  Beyond kPxFar it is rounded first, as M has been: the difference
+// of a maximum from itself would else be anything within half a step (16 at 2^28).
 // same: pages of 64 tokens or more, one scale for the 64.  EDGE: only the tokens of
 // `sees` count, and those of `lost` are NaN.
 // (The factors are taken before the scores, the weights stored after them: loads
@@ -825,20 +832,25 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
                     s[i] = __int_as_float(0x7FC00000);
             }
         }
+        float u[4], v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            u[k] = c * f[k].x;
+            v[k] = f[k].y - M;
+        }
         uint32_t p[32];
         float add;
 #pragma unroll 1
-        for (;;) {
+        for (bool again = false;; again = true) {
             float top = -INFINITY;
             add = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 u = make_float2(c * f[k].x, c * f[k].x);
-                const float2 v = make_float2(f[k].y - M, f[k].y - M);
+                const float2 u2 = make_float2(u[k], u[k]), v2 = make_float2(v[k], v[k]);
                 float2 sum;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 y = fma2(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), u, v);
+                    const float2 y = fma2(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), u2, v2);
                     top = max3(top, y.x, y.y);
                     const float2 w = make_float2(ex2f(y.x), ex2f(y.y));
                     sum = i ? add2(sum, w) : w;
@@ -847,25 +859,44 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
                 add = fmaf(sum.x + sum.y, f[k].z, add);
             }
             // (M is unset, at kPxNone, before a row's first token)
-            if (!__any_sync(0xFFFFFFFFu, top > kPxLazy)) break;
-            float to = top > kPxLazy ? M + ceilf(top) : M;
-            float scale = pow2_int(M - to);
+            if (__builtin_expect(again || !__any_sync(0xFFFFFFFFu, top > kPxLazy || px_far(M)), 1)) break;
+            // the largest score, rounded (weights of the new M stay below 2^2)
+            float m = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float a = s[16 * k], b = s[16 * k + 1];
+#pragma unroll
+                for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
+                if (f[k].y > -INFINITY) m = fmaxf(m, __fmul_rn(fmaxf(a, b), u[k]));
+            }
+            float to = M, scale = 1.f;
             if (M == kPxNone) {
-                // no sum was taken against it: from the scores themselves (it stays where
-                // there are none)
-                float m = -INFINITY;
+                if (m > -INFINITY) to = ceilf(m);
+            } else if (top > kPxLazy || m - M > kPxLazy) {
+                to = fmaxf(ceilf(m), M);
+                scale = pow2_int(M - to);
+            }
+            if (px_far(to)) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float a = s[16 * k], b = s[16 * k + 1];
 #pragma unroll
-                    for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
-                    m = fmaxf(m, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
+                    for (int i = 16 * k; i < 16 * k + 16; i += 2) {
+                        const float2 z = add2(mul2(make_float2(s[i], s[i + 1]), make_float2(u[k], u[k])),
+                                              make_float2(-to, -to));
+                        s[i] = z.x;
+                        s[i + 1] = z.y;
+                    }
+                    u[k] = 1.f;
+                    v[k] = f[k].y;
                 }
-                to = m > -INFINITY ? ceilf(m) : M;
-                scale = 1.f;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = f[k].y - to;
             }
+            __syncwarp();
             M = to;
             l *= scale;
+            if (!__any_sync(0xFFFFFFFFu, scale != 1.f)) continue;
             if (!first) {
                 ok = ok && px_wait(sh, err, pv_done, (count - 1) & 1);
                 tc_fence_after();

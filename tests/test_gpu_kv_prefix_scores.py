@@ -56,7 +56,7 @@ def check_heights(c, got, scale):
     assert ((gl - lse).abs() <= 2.0 ** -20 * lse.abs() + 2.0 ** -16).all()
 
 
-@pytest.mark.parametrize("wide", [False])
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("pow2", [True, False])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("far", [10, 14, 17, 20, 24, 27, 29, 33, 60])
@@ -68,7 +68,24 @@ def test_scores_far_from_zero(dbv, far, sign, pow2, wide):
     ok(dbv)
 
 
-@pytest.mark.parametrize("wide", [False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [16, 28, 45])
+def test_far_scores_of_many_rows(dbv, far, D):
+    """Draft trees of 40 and prompts: both parts on the prefix kernel, masked tiles, a
+    span cut by many CTAs."""
+    c = pu.make(31 + far, [5000], [5], [200, 0, 17, 300, 64], [40, 33, 90, 60, 45], 1, 3, D, 64,
+                tree=True, pow2=False)
+    scale = two_heights(c, far, far, 1.0)
+    check_heights(c, pu.run(dbv, c, scale=scale), scale)
+    # heights by page, so that maxima move from tile to tile, up and down
+    for p in range(0, len(c["codes"][0]), 3):
+        k = c["codes"][0][p, :, :, 3]
+        k[k != 0x7F] = int(kv_util.e4m3_encode(np.array([128.0]))[0])
+    check_heights(c, pu.run(dbv, c, scale=scale), scale)
+    ok(dbv)
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("spread", [1e5, 1e6, 1e9, 1e15])
 def test_large_queries(dbv, spread, wide):
     """Ordinary keys, large queries.  Which token wins is within a score's error; the
