@@ -789,26 +789,136 @@ struct PxSees {
 
 __device__ __forceinline__ bool px_far(float M) { return fabsf(M) >= kPxFar && M != kPxNone; }
 
+// A tile of rows whose maxima are far from 0, from its half `q` on, 16 scores at a time
+// (what runs seldom is short).  A score s u is not rounded before M is taken from it,
+// which is right while M's own steps are small.  Beyond kPxFar it is rounded first, as M
+// has been: the difference of a maximum from itself would else be anything within half
+// a step (16 at 2^28).  sees, lost: as below, null where all tokens count.
+struct PxRow {
+    float M, l;
+    bool ok;
+};
+template <int D>
+__device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
+                                          uint64_t *pv_done, uint32_t count, bool first, int q,
+                                          const float4 *sc, float c, float M, float l,
+                                          const uint32_t *sees, const uint32_t *lost)
+{
+    bool ok = true;
+#pragma unroll 1
+    for (; q < 2; ++q) {
+        // 16 scores, and which of them count
+        auto scores = [&](int k, float (&x)[16]) {
+            float a[8], b[8];
+            tc_ld8(s_at + q * 64 + 16 * k, a);
+            tc_ld8(s_at + q * 64 + 16 * k + 8, b);
+            tc_wait_ld(a);
+            tc_wait_ld(b);
+            const int at = 2 * q + (k >> 1), up = 16 * (k & 1);
+            const uint32_t gone = lost ? lost[at] >> up : 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] = i < 8 ? a[i & 7] : b[i & 7];
+                if (gone >> i & 1) x[i] = __int_as_float(0x7FC00000);
+            }
+            return sees ? sees[at] >> up : ~0u;
+        };
+        float m = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            float x[16], a = -INFINITY;
+            const uint32_t see = scores(k, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (see >> i & 1) a = fmaxf(a, x[i]);
+            const float4 f = sc[4 * q + k];
+            if (a > -INFINITY && f.y > -INFINITY) m = fmaxf(m, __fmul_rn(a, c * f.x));
+        }
+        float to = M, scale = 1.f;
+        if (M == kPxNone) {
+            if (m > -INFINITY) to = ceilf(m);
+        } else if (m - M > kPxLazy) {
+            to = ceilf(m);
+            scale = pow2_int(M - to);
+        }
+        M = to;
+        l *= scale;
+        if (__any_sync(0xFFFFFFFFu, scale != 1.f)) {
+            if (!first) {
+                ok = ok && px_wait(sh, err, pv_done, (count - 1) & 1);
+                tc_fence_after();
+#pragma unroll 1
+                for (int i = 0; i < D; i += 8) {
+                    float o[8];
+                    tc_ld8(o_at + i, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) o[n] *= scale;
+                    tc_st8(o_at + i, o);
+                }
+            }
+            if (q) {
+                tc_wait_st();
+                uint32_t two;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(two) : "f"(scale));
+#pragma unroll 1
+                for (int i = 0; i < 32; i += 8) {
+                    float o[8];
+                    tc_ld8(s_at + i, o);
+                    tc_wait_ld(o);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+                        o[n] = __uint_as_float(mul_bf16x2(__float_as_uint(o[n]), two));
+                    tc_st8(s_at + i, o);
+                }
+            }
+        }
+        const bool far = px_far(M);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            float x[16], sum = 0.f, p[8];
+            const uint32_t see = scores(k, x);
+            const float4 f = sc[4 * q + k];
+            const float u = c * f.x, v = f.y - M;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                float w[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float y = fmaf(x[i + n], u, v);
+                    if (far) y = __fsub_rn(__fmul_rn(x[i + n], u), M) + f.y;
+                    w[n] = see >> (i + n) & 1 ? ex2f(y) : 0.f;
+                    sum += w[n];
+                }
+                uint32_t two;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(w[1]), "f"(w[0]));
+                p[i / 2] = __uint_as_float(two);
+            }
+            l = fmaf(sum, f.z, l);
+            tc_st8(s_at + q * 32 + 8 * k, p);   // (over scores that have been taken)
+        }
+        tc_wait_st();
+    }
+    return {M, l, ok};
+}
+
 // One tile of a softmax thread: a row's 128 scores to weights, 64 at a time.
 // M (a whole number), l: the row's running maximum and sum of weights.  Weights are
 // taken against the maximum in use before it is known whether one passes it by too
 // much; where one does, M moves, what there is of the row (sums, values, the tile's
 // first 64 weights) is scaled by the power of two, and the 64 weights are taken once
-// more, which is the last time: they do not pass the new M.
-// A score s u is not rounded before M is taken from it, which is right while M's own
-// steps are small.  Beyond kPxFar it is rounded first, as M has been: the difference
-// of a maximum from itself would else be anything within half a step (16 at 2^28).
+// more, which is the last time: they do not pass the new M by 2^2.
+// Returns the half from which on a row's maximum is far from 0 (px_soft_far's), or 2.
 // same: pages of 64 tokens or more, one scale for the 64.  EDGE: only the tokens of
 // `sees` count, and those of `lost` are NaN.
 // (The factors are taken before the scores, the weights stored after them: loads
 // and stores between would keep the scores' chains from overlapping.)
 template <int D, bool EDGE>
-__device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
-                                             uint64_t *pv_done, uint32_t count, bool first,
-                                             const float4 *sc, bool same, float c, float &M,
-                                             float &l, const uint32_t *sees, const uint32_t *lost)
+__device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
+                                            uint64_t *pv_done, uint32_t count, bool first,
+                                            const float4 *sc, bool same, float c, float &M, float &l,
+                                            const uint32_t *sees, const uint32_t *lost, bool &ok)
 {
-    bool ok = true;
 #pragma unroll 1
     for (int q = 0; q < 2; ++q) {
         float s[64];
@@ -832,12 +942,6 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
                     s[i] = __int_as_float(0x7FC00000);
             }
         }
-        float u[4], v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            u[k] = c * f[k].x;
-            v[k] = f[k].y - M;
-        }
         uint32_t p[32];
         float add;
 #pragma unroll 1
@@ -846,11 +950,12 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
             add = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 u2 = make_float2(u[k], u[k]), v2 = make_float2(v[k], v[k]);
+                const float2 u = make_float2(c * f[k].x, c * f[k].x);
+                const float2 v = make_float2(f[k].y - M, f[k].y - M);
                 float2 sum;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 y = fma2(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), u2, v2);
+                    const float2 y = fma2(make_float2(s[16 * k + 2 * i], s[16 * k + 2 * i + 1]), u, v);
                     top = max3(top, y.x, y.y);
                     const float2 w = make_float2(ex2f(y.x), ex2f(y.y));
                     sum = i ? add2(sum, w) : w;
@@ -859,44 +964,29 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
                 add = fmaf(sum.x + sum.y, f[k].z, add);
             }
             // (M is unset, at kPxNone, before a row's first token)
-            if (__builtin_expect(again || !__any_sync(0xFFFFFFFFu, top > kPxLazy || px_far(M)), 1)) break;
-            // the largest score, rounded (weights of the new M stay below 2^2)
-            float m = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float a = s[16 * k], b = s[16 * k + 1];
-#pragma unroll
-                for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
-                if (f[k].y > -INFINITY) m = fmaxf(m, __fmul_rn(fmaxf(a, b), u[k]));
-            }
-            float to = M, scale = 1.f;
+            if (again || !__any_sync(0xFFFFFFFFu, top > kPxLazy)) break;
+            float to = top > kPxLazy ? M + ceilf(top) : M;
+            float scale = pow2_int(M - to);
             if (M == kPxNone) {
-                if (m > -INFINITY) to = ceilf(m);
-            } else if (top > kPxLazy || m - M > kPxLazy) {
-                to = fmaxf(ceilf(m), M);
-                scale = pow2_int(M - to);
-            }
-            if (px_far(to)) {
+                // no sum was taken against it: from the scores themselves (it stays where
+                // there are none)
+                float m = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
+                    float a = s[16 * k], b = s[16 * k + 1];
 #pragma unroll
-                    for (int i = 16 * k; i < 16 * k + 16; i += 2) {
-                        const float2 z = add2(mul2(make_float2(s[i], s[i + 1]), make_float2(u[k], u[k])),
-                                              make_float2(-to, -to));
-                        s[i] = z.x;
-                        s[i + 1] = z.y;
-                    }
-                    u[k] = 1.f;
-                    v[k] = f[k].y;
+                    for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
+                    m = fmaxf(m, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = f[k].y - to;
+                to = m > -INFINITY ? ceilf(m) : M;
+                scale = 1.f;
             }
-            __syncwarp();
+            if (__any_sync(0xFFFFFFFFu, px_far(to))) {
+                tc_wait_st();
+                return q;
+            }
             M = to;
             l *= scale;
-            if (!__any_sync(0xFFFFFFFFu, scale != 1.f)) continue;
             if (!first) {
                 ok = ok && px_wait(sh, err, pv_done, (count - 1) & 1);
                 tc_fence_after();
@@ -932,7 +1022,7 @@ __device__ __forceinline__ bool px_soft_tile(PxShared *sh, int *err, uint32_t s_
         tc_st32u(s_at + q * 32, p);
     }
     tc_wait_st();
-    return ok;
+    return 2;
 }
 
 template <int D>
@@ -1025,20 +1115,38 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 if (!ok) break;
                 tc_fence_after();
                 const int at = (pc.t0 + i) * kPxTile;
-                if (__builtin_expect(at + kPxTile <= pc.ctx, 1)) {
-                    ok = px_soft_tile<D, false>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
-                                                sh->sc[ring], j.block >= 64, c, M, l, nullptr, nullptr);
+                // (maxima far from 0 have a way of their own)
+                int half = __any_sync(0xFFFFFFFFu, px_far(M)) ? 0 : 2;
+                const bool edge = at + kPxTile > pc.ctx;
+                uint32_t seen[4], lost[4];
+                if (__builtin_expect(!edge, 1)) {
+                    if (half)
+                        half = px_soft_tile<D, false>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
+                                                      i == from, sh->sc[ring], j.block >= 64, c, M, l,
+                                                      nullptr, nullptr, ok);
                 } else {
                     // (which tokens are lost is known once the values are converted)
                     const uint32_t sb = (it + i) & 1;
                     ok = px_wait(sh, j.err, &sh->full_b[sb], ((it + i) >> 1) & 1);
                     const PxSees sees(j, pc, token, row < pc.rows, at);
-                    uint32_t lost[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) lost[k] = sh->lost[sb][k];
-                    ok = __all_sync(0xFFFFFFFFu, ok) &&
-                         px_soft_tile<D, true>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count, i == from,
-                                               sh->sc[ring], j.block >= 64, c, M, l, sees.w, lost);
+                    for (int k = 0; k < 4; ++k) {
+                        seen[k] = sees.w[k];
+                        lost[k] = sh->lost[sb][k];
+                    }
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (half && ok)
+                        half = px_soft_tile<D, true>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
+                                                     i == from, sh->sc[ring], j.block >= 64, c, M, l,
+                                                     seen, lost, ok);
+                }
+                if (__builtin_expect(half < 2, 0)) {
+                    const PxRow r = px_soft_far<D>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
+                                                   i == from, half, sh->sc[ring], c, M, l,
+                                                   edge ? seen : nullptr, edge ? lost : nullptr);
+                    M = r.M;
+                    l = r.l;
+                    ok = ok && r.ok;
                 }
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 tc_fence_before();
