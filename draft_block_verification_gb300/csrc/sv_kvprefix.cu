@@ -942,6 +942,13 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
                     s[i] = __int_as_float(0x7FC00000);
             }
         }
+        // (a score that is hidden, -inf, keeps its sign against a factor of 0)
+        float by[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            by[k] = c * f[k].x;
+            if (EDGE && by[k] == 0.f) by[k] = 0x1p-126f;
+        }
         uint32_t p[32];
         float add;
 #pragma unroll 1
@@ -950,7 +957,7 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
             add = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 u = make_float2(c * f[k].x, c * f[k].x);
+                const float2 u = make_float2(by[k], by[k]);
                 const float2 v = make_float2(f[k].y - M, f[k].y - M);
                 float2 sum;
 #pragma unroll
@@ -976,7 +983,7 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
                     float a = s[16 * k], b = s[16 * k + 1];
 #pragma unroll
                     for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
-                    m = fmaxf(m, fmaf(fmaxf(a, b), c * f[k].x, f[k].y));
+                    m = fmaxf(m, fmaf(fmaxf(a, b), by[k], f[k].y));
                 }
                 to = m > -INFINITY ? ceilf(m) : M;
                 scale = 1.f;
@@ -1101,9 +1108,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             bar_or(1, kPxSoft * 32, false);     // the rows' factors are there
             if (lane == 0) mbar_arrive(&sh->q_full);
             const int row = wide ? slot * 128 + r : r;
-            // (a score that is hidden, -inf, keeps its sign against a factor of 0)
-            float c = sh->c[row];
-            if (c == 0.f) c = 1e-38f;
+            const float c = sh->c[row];
             const int token = (pc.row0 + row) / j.G;  // of the span's
             const int step = wide ? 1 : 2, from = wide ? 0 : slot, n = pc.t1 - pc.t0;
             float M = kPxNone, l = 0.f;

@@ -98,3 +98,21 @@ def test_large_queries(dbv, spread, wide):
     assert float(got["out"].abs().max()) <= 448.0 * float(c["scale"][1].max()) * (1 + 2.0 ** -7)
     assert ((got["lse"].double() - lse).abs() <= 2.0 ** -15 * size + 2.0 ** -19 * (1 + lse.abs())).all()
     ok(dbv)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("scale,spread", [(0.0, 1.0), (None, 2.0 ** -110), (-0.1, 2.0 ** -105)])
+def test_hidden_tokens_beside_a_factor_of_zero(dbv, scale, spread, tree, wide):
+    """Scores that are 0 whatever the key, among tiles of new tokens: key scales of
+    2^-40, which a page of zeros has.  Weights are alike for all that a row sees."""
+    prefix, sizes, after, new = with_wide([300], [3], [7, 0, 90], [3, 1, 40], wide)
+    c = pu.make(35, prefix, sizes, after, new, 2, 4, 128, 32, tree=tree, pow2=False, spread=spread)
+    c["scale"][0][::2] = 2.0 ** -40
+    got = pu.run(dbv, c, scale=scale)
+    pu.check(c, got, scale)
+    _, lse, _, _ = pu.exact(c, scale)
+    some = torch.isfinite(lse)
+    assert torch.isfinite(got["lse"][some]).all()
+    assert ((got["lse"][some].double() - lse[some]).abs() <= 2.0 ** -16).all()
+    ok(dbv)
