@@ -3,8 +3,9 @@
 A thin ctypes binding over the C ABI of ``libsv.so`` (declared in
 ``include/sv.h``).  Each function has the C name, takes torch CUDA tensors,
 marshals pointers, sizes and the current CUDA stream, and raises ``SVError``
-on any status other than SV_OK.  Every step of the computation runs in the
-library's kernels; there is no other code path.  The library must have been
+on any status other than SV_OK.  With ``stream=`` a call runs on that stream, and
+what it allocates comes from that stream's memory.  Every step of the computation
+runs in the library's kernels; there is no other code path.  The library must have been
 built (``draft_block_verification_gb300._build.build()``); importing the
 functions when it is missing raises immediately.
 """
@@ -12,6 +13,7 @@ from __future__ import annotations
 
 import atexit
 import ctypes as C
+import functools
 import os
 import sys
 import threading
@@ -232,6 +234,40 @@ def _out(t, shape, dtype, dev):
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
 
 
+def _tensors(x):
+    """The tensors of a call's arguments or results."""
+    if isinstance(x, torch.Tensor):
+        yield x
+    elif isinstance(x, (tuple, list, dict)):
+        for y in x.values() if isinstance(x, dict) else x:
+            yield from _tensors(y)
+
+
+def _on_stream(call):
+    """A call with stream= runs with that stream as torch's current one: what it
+    allocates comes from that stream's memory, not from blocks that work queued on the
+    current stream may still use.  Results may be used and freed on the current stream
+    as before."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        dev = next((t.device for t in _tensors((args, kw)) if t.is_cuda), None)
+        if dev is None:
+            return call(*args, **kw)              # (refused)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
+        now = torch.cuda.current_stream(dev)
+        with torch.cuda.stream(stream):
+            out = call(*args, **kw)
+        if now.cuda_stream != stream.cuda_stream:
+            for t in _tensors(out):
+                t.record_stream(now)
+        return out
+    return on
+
+
+@_on_stream
 def sv_verify_greedy(target, draft_ids, draft_len=None, *, handle=None, stream=None,
                      accept_len=None, next_token=None):
     """Greedy verification; target [B, K+1, V]; returns (accept_len, next_token)."""
@@ -249,6 +285,7 @@ def sv_verify_greedy(target, draft_ids, draft_len=None, *, handle=None, stream=N
     return acc, nxt
 
 
+@_on_stream
 def sv_verify_greedy_static(target, draft_ids, draft_len=None, *, stream=None, accept_len=None,
                             next_token=None, status=None):
     """Greedy verification with the library's fixed scratch (no device
@@ -271,6 +308,7 @@ def sv_verify_greedy_static(target, draft_ids, draft_len=None, *, stream=None, a
     return acc, nxt, st
 
 
+@_on_stream
 def sv_verify_sample(target, draft, draft_ids, draft_len=None, *, T_p=1.0, T_q=1.0,
                      mode=SV_LOSSLESS, lam=1.0, seed=0, pos_base=None, want_rows=True,
                      want_tv=False, handle=None, stream=None):
@@ -307,6 +345,7 @@ def sv_verify_sample(target, draft, draft_ids, draft_len=None, *, T_p=1.0, T_q=1
     return out
 
 
+@_on_stream
 def sv_verify_tree(node_logits, parent, node_pos, node_tok, *, T=0.0, seed=0, pos_base=None,
                    max_depth=None, handle=None, stream=None):
     """Coupled-noise tree verification; node_logits [B, N, V]."""
@@ -331,6 +370,7 @@ def sv_verify_tree(node_logits, parent, node_pos, node_tok, *, T=0.0, seed=0, po
     return out
 
 
+@_on_stream
 def sv_verify_spot(state_logits, parent, node_pos, node_tok, root_mask, *, T=0.0, seed=0,
                    pos_base=None, max_depth=None, handle=None, stream=None):
     """SPOT verification with the target's position selection (see sv.h):
@@ -363,6 +403,7 @@ def sv_verify_spot(state_logits, parent, node_pos, node_tok, root_mask, *, T=0.0
     return out
 
 
+@_on_stream
 def sv_packed_anyorder_step(logits, Kv, W, u, win_pos, order, draft, end_pos, *, eos_id=-1,
                             handle=None, stream=None):
     """One any-order Packed-SS iteration (see sv.h); logits [B, Kv + W, V];
@@ -388,6 +429,7 @@ def sv_packed_anyorder_step(logits, Kv, W, u, win_pos, order, draft, end_pos, *,
     return out
 
 
+@_on_stream
 def sv_packed_step(logits, K, W, prev_draft, prev_len, *, prev_q_at_draft=None,
                    prev_draft_logits=None, prev_q_offset=None, T=0.0, seed=0, it=0,
                    pos_base=None, eos_id=-1, remaining=None, handle=None, stream=None):
@@ -427,6 +469,7 @@ def sv_packed_step(logits, K, W, prev_draft, prev_len, *, prev_q_at_draft=None,
     return out
 
 
+@_on_stream
 def sv_packed_topk_step(logits, K, W, kp, kq, prev_draft, prev_len, prev_q_ids, prev_q_probs,
                         prev_q_offset, *, T=1.0, seed=0, it=0, pos_base=None, eos_id=-1,
                         remaining=None, handle=None, stream=None):
@@ -494,6 +537,7 @@ def _call_on(handle, stream, dev):
     return handle.ptr, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+@_on_stream
 def sv_kv_plan(cached_len, new_len, held, table, free_ids, free_pos, block, max_tokens, *,
                handle=None, stream=None):
     """Places of new tokens in the paged cache (see sv.h): cached_len, new_len,
@@ -538,6 +582,7 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
                    _dense(v_scale, torch.float32, shape[:2], "v_scale", dev))
 
 
+@_on_stream
 def sv_kv_append(k, v, slot, k_cache, v_cache, k_scale, v_scale, *, handle=None, stream=None):
     """Write k, v [T, Hkv, D] (float32 or bfloat16) to the cache's slots
     slot [T] int32 in place (see sv.h); caches [pages, Hkv, block, D]
@@ -559,6 +604,7 @@ def sv_kv_append(k, v, slot, k_cache, v_cache, k_scale, v_scale, *, handle=None,
         "sv_kv_append")
 
 
+@_on_stream
 def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new, *, scale=None,
                     mask=None, want_lse=False, handle=None, stream=None):
     """Attention of the new tokens' queries q [T, Hq, D] (bfloat16) over the
@@ -595,6 +641,7 @@ def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new
     return out
 
 
+@_on_stream
 def sv_kv_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new,
                            prefix_len=None, *, cu_group=None, scale=None, mask=None,
                            want_lse=False, handle=None, stream=None):
@@ -621,8 +668,6 @@ def sv_kv_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len,
         if mask.dim() != 2:
             raise ValueError("mask must be [T, words]")
         words = mask.shape[1]
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
     ptr, raw = _call_on(handle, stream, dev)
     L = lib()
     size = L.sv_kv_prefix_work_bytes(ptr, T, Hq, H, D, B, groups)
@@ -630,8 +675,6 @@ def sv_kv_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len,
     if want_lse:
         out["lse"] = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     work = torch.empty(size, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        work.record_stream(stream)
     _check(L.sv_kv_prefix_attention(
         ptr, q.data_ptr(), q.stride(0), q.stride(1), T, Hq, H, D, *cache, block, pages,
         _dense(table, i32, (B, cols), "table", dev), cols,
@@ -656,6 +699,7 @@ def _rows_out(t, shape, dtype, dev, name):
     return t
 
 
+@_on_stream
 def sv_kv_read(k_cache, v_cache, k_scale, v_scale, table, cu, rows, *, first=None,
                dtype=torch.bfloat16, out=None, handle=None, stream=None):
     """Tokens read back from the paged cache (see sv.h): rows cu[b] .. cu[b + 1]
@@ -689,6 +733,7 @@ def sv_kv_read(k_cache, v_cache, k_scale, v_scale, table, cu, rows, *, first=Non
     return {"k": k, "v": v}
 
 
+@_on_stream
 def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
                     interleaved=False, dtype=None, out=None, handle=None, stream=None):
     """Norms of queries and keys for each head, and the rotation by position, in
@@ -747,6 +792,7 @@ def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e
     return {"q": y, "k": z}
 
 
+@_on_stream
 def sv_sample_rows(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
                    handle=None, stream=None):
     """One draw from each row of logits [R, V] with the filters of sv.h; u,
