@@ -103,6 +103,12 @@ struct PrefixJob {
     float *tail_part;          // sums of ranges
     int *err;
 };
+// Whether a unit's entry tells CTAs.  A CTA of the prefix kernel whose wait ran out leaves
+// no entry of the units it did not get to: there stands what was in the workspace.
+inline __host__ __device__ bool unit_known(int first, int last, int ctas)
+{
+    return first >= 0 && first <= last && last < ctas;
+}
 constexpr int kPrefixRows = 256;                             // query rows of a unit
 constexpr int64_t kPrefixMaxUnits = 1 << 24;
 size_t prefix_part_bytes(int sms, int64_t units, int D);

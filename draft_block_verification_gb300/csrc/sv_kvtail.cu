@@ -574,6 +574,7 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
                 const bool live = row + r < t.rows;
                 unit[r] = gr.unit0 + t.h * blocks + (live ? (at + r) / gr.block : 0);
                 cc[r] = live ? __ldcg(j.unit_ctas + unit[r]) : none;
+                if (!unit_known(cc[r].x, cc[r].y, j.prefix_ctas)) cc[r] = none;
             }
             const int most = max(cc[0].y - cc[0].x, cc[1].y - cc[1].x);
 #pragma unroll 2
