@@ -556,7 +556,6 @@ __device__ __forceinline__ bool tail_run(const PrefixJob &j, const TailTask &t, 
     for (int n = 0; n < NT; ++n) s.scale(n, out, out);
     // ---- what the prefix kernel left of these rows, its pieces dealt to the ranges: of
     // the group's span and of the sequence's
-    if (t.skip != 0 || !t.own) pdl_wait();
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         if (which ? t.own : t.skip == 0) continue;
@@ -688,10 +687,7 @@ tail_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUtenso
         mbar_fence_init();
     }
     __syncwarp();
-    // The prefix kernel lets this one start once its own wait for the prep kernel is
-    // over.  So what prep left is there, and CTAs start where the prefix kernel's have
-    // ended; a task waits for all of them only before it reads what they left, and each
-    // warp before it ends.
+    pdl_wait();
     pdl_trigger();
     const int tasks = __ldcg(j.unit0 + j.B), step = gridDim.x * kTlWarps;
     uint32_t it = 0;
@@ -704,7 +700,6 @@ tail_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUtenso
         else
             ok = tail_run<D, 2>(j, t, sh, ring, map_k, map_v, lane, it);
     }
-    pdl_wait();
     // after a wait that ran out: copies still in flight land before the exit
     if (!ok)
         for (int i = 0; i < kTlStages; ++i)
