@@ -24,20 +24,26 @@
 // of the products, a row's scores lie in one thread's registers, and maxima and
 // sums need no exchange:
 //   S [128 rows x 128 tokens] = Q K^T    in 8 bits: the cache's bytes as they
-//       lie, the query exactly in two e4m3 parts (as in sv_kvattn.cu), added up
-//   O [128 rows x D]         += P V      in bf16: P from tensor memory, V's bytes
-//       brought to bf16 in shared memory
-// A weight is rounded to bf16, within 2^-8 of itself at any size, and a value
-// times the power of two in its page's scale is exact in bf16; what the scale
-// has beside that power goes into the exponent and out of the sum again (as log2
-// and 1 / x).  So the scales' range needs no care.
+//       lie, the query in two e4m3 parts, added up (exact from 2^-9 of the row's
+//       largest element on, within 2^-17 of it below)
+//   O [128 rows x D]         += P V      in fp16: P from tensor memory, V's bytes
+//       brought to fp16 in shared memory
+// Weights are 2^(y - M) with M 2^6 below the maximum that it was taken from, 2^15 at
+// most: fp16's 11 bits down to 2^-19 of the largest, steps of 2^-29 of it below.  Their
+// sum is that of the weights before the rounding.  A value times the power of two in its
+// page's scale, by a power that the piece has in common (the largest of its first pages),
+// is exact in fp16; what the scale has beside the power goes into the exponent
+// and out of the sum again (as log2 and 1 / x).  A tile with a page whose scale lies
+// more than 2^3 above the common one or 2^5 below it would lose small weights' bits to
+// large scales: it is taken in bf16, values and weights, where a weight is within 2^-8
+// of itself at any size.  (All in bf16: the same time, and a weight's 2^-8 in every row.)
 //
 // The products of a slot's tile run under the other slot's softmax:
 //   tensor  S0 . . PV0 S0' PV1 S1' ...
 //   slot 0    softmax     softmax
 // A unit of up to 128 rows gives both slots the same queries and every other
 // tile each, and joins the two at its end.  A softmax thread has a row, and takes
-// its 128 scores 64 at a time; four more warps bring the values to bf16, one
+// its 128 scores 64 at a time; four more warps bring the values to fp16, one
 // fetches, two issue (a slot each, taking turns).
 //
 // The running maximum moves lazily: only where a tile's maximum passes it by
@@ -77,10 +83,13 @@ constexpr int kPxThreads = 512;        // + 4 converting warps, producer, 2 issu
 // scores, take what the others leave (256 * 184 + 256 * 72 = 512 * 128).
 constexpr int kPxRegs = 128, kPxSoftRegs = 184, kPxSideRegs = 72;
 static_assert(256 * kPxSoftRegs + 256 * kPxSideRegs <= kPxThreads * kPxRegs, "registers");
-constexpr float kPxLazy = 8.f;         // log2 of how far a weight may pass 1
+constexpr float kPxUnit = 6.f;         // log2 of the weight of a maximum that M was taken from
+constexpr float kPxMost = 14.f;        // of the largest weight before M moves
+constexpr int kPxAbove = 3, kPxBelow = 5;  // of a value scale about the piece's
 constexpr uint32_t kPxTries = 1u << 16; // of a wait
 constexpr float kPxNone = -1e30f;      // maximum of no tokens
 constexpr float kPxFar = 0x1p14f;      // maxima from which on scores are rounded first
+constexpr float kPxMark = -3e38f;      // stands for one of those: every weight passes it
 
 // ---------------------------------------------------------------------------
 // Which pages are shared.
@@ -359,7 +368,7 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     // Rows of a unit.  A piece's sums are as many as its rows, whatever its tokens; so
     // where CTAs by far outnumber the units, units of half the rows halve what the
     // tail has to read (128 single tokens of 32 heads: 88 us against 90; with as many
-    // units as CTAs the halves would only have values brought to bf16 twice).
+    // units as CTAs the halves would only have values converted twice).
     const int spans = j.groups + j.B;
     int big = 0, small = 0;
     for (int g = lane; g < spans; g += 32) {
@@ -535,10 +544,12 @@ struct PxShared {
     uint64_t s_full[2], p_full[2], pv_done[2], q_full, turn[2], scales[kPxRing], drained[2];
     uint32_t tmem;
     int abort;
-    // for each 16 tokens: the key's scale, log2 of the value scale's fraction (1 to 2)
-    // and its inverse; the scale's power of two, as two factors
+    // for each 16 tokens: the key's scale, log2 of the value scale's fraction (1 to 2),
+    // its inverse, and the log2 once more (the first is infinite where the tile is taken
+    // in bf16); the scale's power of two by the piece's, as two factors
     float4 sc[kPxRing][8];
     uint32_t up[kPxRing][8], more[kPxRing][8];
+    int kind[kPxRing];                 // kPxApart: in bf16; the rest, less 64: the piece's exponent
     PxPiece piece[kPxPieces];          // handed from the producer to the other roles
     uint64_t piece_full[kPxPieces], piece_empty[kPxPieces];
     uint32_t lost[2][4];               // tokens of a tile with NaN in their value, a bit each
@@ -610,6 +621,31 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Two weights, the first in the lower half.
+__device__ __forceinline__ uint32_t weights_f16(float a, float b)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t weights_bf16(float a, float b)
+{
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float by)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return weights_f16(f.x * by, f.y * by);
+}
+
 // Bounded wait that also ends when another role has given up.  A try lets the
 // warp sleep until the phase completes or some 10 us have passed: polling warps
 // would take a quarter of the instruction slots.
@@ -637,11 +673,23 @@ __device__ __forceinline__ bool px_wait(PxShared *sh, int *err, uint64_t *bar, u
 // same steps, subnormals too.  up: 2^(120 + e), twice, e the scale's exponent, of
 // which more than 7 would leave the range (kPxTop).
 constexpr int kPxTop = 7;
+constexpr int kPxApart = 1 << 8;
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t w, uint32_t up, uint32_t &lo, uint32_t &hi)
 {
     constexpr uint32_t kKeep = 0x87F087F0u;
     lo = mul_bf16x2((sign_pairs(w, 0x9180) << 4) & kKeep, up);
     hi = mul_bf16x2((sign_pairs(w, 0xB3A2) << 4) & kKeep, up);
+}
+
+// To fp16 pairs, exactly, NaN too.  up: 2^d, twice.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t up, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    lo = mul_f16x2(lo, up);
+    hi = mul_f16x2(hi, up);
 }
 
 // The piece's queries: hi and lo parts to shared memory, rows of D bytes in the
@@ -789,8 +837,9 @@ struct PxSees {
 
 __device__ __forceinline__ bool px_far(float M) { return fabsf(M) >= kPxFar && M != kPxNone; }
 
-// A tile of rows whose maxima are far from 0, from its half `q` on, 16 scores at a time
-// (what runs seldom is short).  A score s u is not rounded before M is taken from it,
+// A tile whose value scales lie apart (bf: values and weights are bf16), or of rows whose
+// maxima are far from 0, from its half `q` on, 16 scores at a time (what runs seldom is
+// short).  A score s u is not rounded before M is taken from it,
 // which is right while M's own steps are small.  Beyond kPxFar it is rounded first, as M
 // has been: the difference of a maximum from itself would else be anything within half
 // a step (16 at 2^28).  sees, lost: as below, null where all tokens count.
@@ -801,7 +850,7 @@ struct PxRow {
 template <int D>
 __device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
                                           uint64_t *pv_done, uint32_t count, bool first, int q,
-                                          const float4 *sc, float c, float M, float l,
+                                          const float4 *sc, bool bf, float c, float M, float l,
                                           const uint32_t *sees, const uint32_t *lost)
 {
     bool ok = true;
@@ -832,13 +881,13 @@ __device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_
             for (int i = 0; i < 16; ++i)
                 if (see >> i & 1) a = fmaxf(a, x[i]);
             const float4 f = sc[4 * q + k];
-            if (a > -INFINITY && f.y > -INFINITY) m = fmaxf(m, __fmul_rn(a, c * f.x));
+            if (a > -INFINITY && f.w > -INFINITY) m = fmaxf(m, __fmul_rn(a, c * f.x));
         }
         float to = M, scale = 1.f;
         if (M == kPxNone) {
-            if (m > -INFINITY) to = ceilf(m);
-        } else if (m - M > kPxLazy) {
-            to = ceilf(m);
+            if (m > -INFINITY) to = ceilf(m) - kPxUnit;
+        } else if (m - M > kPxMost) {
+            to = ceilf(m) - kPxUnit;
             scale = pow2_int(M - to);
         }
         M = to;
@@ -859,16 +908,17 @@ __device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_
             }
             if (q) {
                 tc_wait_st();
-                uint32_t two;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(two) : "f"(scale));
+                const uint32_t two = weights_bf16(scale, scale);
 #pragma unroll 1
                 for (int i = 0; i < 32; i += 8) {
                     float o[8];
                     tc_ld8(s_at + i, o);
                     tc_wait_ld(o);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
-                        o[n] = __uint_as_float(mul_bf16x2(__float_as_uint(o[n]), two));
+                    for (int n = 0; n < 8; ++n) {
+                        const uint32_t w = __float_as_uint(o[n]);
+                        o[n] = __uint_as_float(bf ? mul_bf16x2(w, two) : scaled_f16(w, scale));
+                    }
                     tc_st8(s_at + i, o);
                 }
             }
@@ -879,20 +929,18 @@ __device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_
             float x[16], sum = 0.f, p[8];
             const uint32_t see = scores(k, x);
             const float4 f = sc[4 * q + k];
-            const float u = c * f.x, v = f.y - M;
+            const float u = c * f.x, v = f.w - M;
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
                 float w[2];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     float y = fmaf(x[i + n], u, v);
-                    if (far) y = __fsub_rn(__fmul_rn(x[i + n], u), M) + f.y;
+                    if (far) y = __fsub_rn(__fmul_rn(x[i + n], u), M) + f.w;
                     w[n] = see >> (i + n) & 1 ? ex2f(y) : 0.f;
                     sum += w[n];
                 }
-                uint32_t two;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(two) : "f"(w[1]), "f"(w[0]));
-                p[i / 2] = __uint_as_float(two);
+                p[i / 2] = __uint_as_float(bf ? weights_bf16(w[0], w[1]) : weights_f16(w[0], w[1]));
             }
             l = fmaf(sum, f.z, l);
             tc_st8(s_at + q * 32 + 8 * k, p);   // (over scores that have been taken)
@@ -966,13 +1014,13 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
                     top = max3(top, y.x, y.y);
                     const float2 w = make_float2(ex2f(y.x), ex2f(y.y));
                     sum = i ? add2(sum, w) : w;
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[8 * k + i]) : "f"(w.y), "f"(w.x));
+                    p[8 * k + i] = weights_f16(w.x, w.y);
                 }
                 add = fmaf(sum.x + sum.y, f[k].z, add);
             }
             // (M is unset, at kPxNone, before a row's first token)
-            if (again || !__any_sync(0xFFFFFFFFu, top > kPxLazy)) break;
-            float to = top > kPxLazy ? M + ceilf(top) : M;
+            if (again || !__any_sync(0xFFFFFFFFu, top > kPxMost)) break;
+            float to = top > kPxMost ? M + (ceilf(top) - kPxUnit) : M;
             float scale = pow2_int(M - to);
             if (M == kPxNone) {
                 // no sum was taken against it: from the scores themselves (it stays where
@@ -985,10 +1033,10 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
                     for (int i = 2; i < 16; i += 2) a = max3(a, s[16 * k + i], s[16 * k + i + 1]);
                     m = fmaxf(m, fmaf(fmaxf(a, b), by[k], f[k].y));
                 }
-                to = m > -INFINITY ? ceilf(m) : M;
+                to = m > -INFINITY ? ceilf(m) - kPxUnit : M;
                 scale = 1.f;
             }
-            if (__any_sync(0xFFFFFFFFu, px_far(to))) {
+            if (__any_sync(0xFFFFFFFFu, px_far(M) || px_far(to))) {
                 tc_wait_st();
                 return q;
             }
@@ -1009,8 +1057,6 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
             }
             if (q) {
                 tc_wait_st();
-                uint32_t two;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(two) : "f"(scale));
 #pragma unroll 1
                 for (int i = 0; i < 32; i += 8) {
                     float o[8];
@@ -1018,7 +1064,7 @@ __device__ __forceinline__ int px_soft_tile(PxShared *sh, int *err, uint32_t s_a
                     tc_wait_ld(o);
 #pragma unroll
                     for (int n = 0; n < 8; ++n)
-                        o[n] = __uint_as_float(mul_bf16x2(__float_as_uint(o[n]), two));
+                        o[n] = __uint_as_float(scaled_f16(__float_as_uint(o[n]), scale));
                     tc_st8(s_at + i, o);
                 }
             }
@@ -1038,7 +1084,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
               const __grid_constant__ CUtensorMap map_v)
 {
     constexpr int kSide = kPxTile * D;          // bytes of a tile's keys (or values)
-    constexpr int kWideV = kPxTile * D * 2;     // in bf16
+    constexpr int kWideV = kPxTile * D * 2;     // in 16 bits
     constexpr uint32_t kSwz = D == 128 ? 2 : 4;
     extern __shared__ char px_raw[];
     __shared__ PxShared shared;
@@ -1111,7 +1157,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             const float c = sh->c[row];
             const int token = (pc.row0 + row) / j.G;  // of the span's
             const int step = wide ? 1 : 2, from = wide ? 0 : slot, n = pc.t1 - pc.t0;
-            float M = kPxNone, l = 0.f;
+            float M = kPxNone, l = 0.f, far = 0.f;
             for (int i = from; i < n && ok; i += step, ++count) {
                 const int ring = (int)((it + i) % kPxRing);
                 ok = px_wait(sh, j.err, &sh->scales[ring], ((it + i) / kPxRing) & 1);
@@ -1120,19 +1166,12 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 if (!ok) break;
                 tc_fence_after();
                 const int at = (pc.t0 + i) * kPxTile;
-                // (maxima far from 0 have a way of their own)
-                int half = __any_sync(0xFFFFFFFFu, px_far(M)) ? 0 : 2;
                 const bool edge = at + kPxTile > pc.ctx;
                 uint32_t seen[4], lost[4];
-                if (__builtin_expect(!edge, 1)) {
-                    if (half)
-                        half = px_soft_tile<D, false>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
-                                                      i == from, sh->sc[ring], j.block >= 64, c, M, l,
-                                                      nullptr, nullptr, ok);
-                } else {
-                    // (which tokens are lost is known once the values are converted)
+                // which tokens a row sees, and are lost (known once the values are converted)
+                auto look = [&] {
                     const uint32_t sb = (it + i) & 1;
-                    ok = px_wait(sh, j.err, &sh->full_b[sb], ((it + i) >> 1) & 1);
+                    ok = ok && px_wait(sh, j.err, &sh->full_b[sb], ((it + i) >> 1) & 1);
                     const PxSees sees(j, pc, token, row < pc.rows, at);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -1140,16 +1179,29 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         lost[k] = sh->lost[sb][k];
                     }
                     ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (half && ok)
+                };
+                int half = 0;
+                if (__builtin_expect(!edge, 1)) {
+                    half = px_soft_tile<D, false>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
+                                                  i == from, sh->sc[ring], j.block >= 64, c, M, l,
+                                                  nullptr, nullptr, ok);
+                } else {
+                    look();
+                    if (ok && !(sh->kind[ring] & kPxApart))
                         half = px_soft_tile<D, true>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
                                                      i == from, sh->sc[ring], j.block >= 64, c, M, l,
                                                      seen, lost, ok);
                 }
+                // (value scales apart, and maxima far from 0, have a way of their own)
                 if (__builtin_expect(half < 2, 0)) {
+                    const bool bf = sh->kind[ring] & kPxApart;
+                    if (bf && !edge) look();
                     const PxRow r = px_soft_far<D>(sh, j.err, s_at, o_at, &sh->pv_done[slot], count,
-                                                   i == from, half, sh->sc[ring], c, M, l,
-                                                   edge ? seen : nullptr, edge ? lost : nullptr);
-                    M = r.M;
+                                                   i == from, half, sh->sc[ring], bf, c,
+                                                   M == kPxMark ? far : M, l, edge || bf ? seen : nullptr,
+                                                   edge || bf ? lost : nullptr);
+                    far = r.M;
+                    M = px_far(far) ? kPxMark : far;
                     l = r.l;
                     ok = ok && r.ok;
                 }
@@ -1158,6 +1210,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full[slot]);
             }
+            if (M == kPxMark) M = far;
             const bool had = from < n;
             if (had && ok) ok = px_wait(sh, j.err, &sh->pv_done[slot], (count - 1) & 1);
             if (!wide) {
@@ -1175,6 +1228,9 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 if (pc.t1 == pc.tiles) j.unit_ctas[pc.unit].y = blockIdx.x;
                 if (!pc.whole()) j.part_unit[2 * blockIdx.x + (pc.t0 == 0 ? 1 : 0)] = pc.unit;
             }
+            // (the values' unit, the piece's power of two)
+            const int e = (sh->kind[(it + n - 1) % kPxRing] & (kPxApart - 1)) - 64;
+            const float unit = __int_as_float((127 + e) << 23);
             float *part = px_part(j, ctas, blockIdx.x, pc.t0, pc.whole(), pc.unit);
             float4 *to = reinterpret_cast<float4 *>(part) + row;
             float *ml = part + (size_t)D * kPxRows + row;
@@ -1185,6 +1241,8 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     tc_ld32(o_at + i, o);
                     tc_wait_ld(o);
 #pragma unroll
+                    for (int q = 0; q < 32; ++q) o[q] *= unit;
+#pragma unroll
                     for (int q = 0; q < 8; ++q)
                         to[(i / 4 + q) * kPxRows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                 }
@@ -1194,6 +1252,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 // both slots' sums of a row; half of its elements each
                 const float m0 = sh->m[0][r], m1 = n > 1 ? sh->m[1][r] : kPxNone;
                 const float m = fmaxf(m0, m1), f0 = ex2f(m0 - m), f1 = n > 1 ? ex2f(m1 - m) : 0.f;
+                const float u0 = f0 * unit, u1 = f1 * unit;
 #pragma unroll 1
                 for (int i = slot * (D / 2); i < (slot + 1) * (D / 2); i += 16) {
                     float a[16], b[16];
@@ -1206,7 +1265,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     tc_wait_ld(a);
                     if (n > 1) tc_wait_ld(b);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) a[q] = n > 1 ? fmaf(b[q], f1, a[q] * f0) : a[q];
+                    for (int q = 0; q < 16; ++q) a[q] = n > 1 ? fmaf(b[q], u1, a[q] * u0) : a[q] * unit;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         to[(i / 4 + q) * kPxRows] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
@@ -1223,7 +1282,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxSideRegs));
         if (warp < 12) {
-            // ---- the values to bf16, a token a thread
+            // ---- the values to fp16 or bf16, a token a thread
             const int tk = tid - kPxSoft * 32;
             while (ok && px_next(sh, j.err, pieces, pc, lane)) {
                 for (int t = pc.t0; t < pc.t1; ++t, ++it) {
@@ -1234,12 +1293,14 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const uint32_t up = sh->up[ring][tk >> 4], more = sh->more[ring][tk >> 4];
-                    constexpr uint32_t kOne = 0x3F803F80u;
-                    const char *src = s_v + st * kSide + tk * D;
+                    const bool bf = sh->kind[ring] & kPxApart;
+                    char *src = s_v + st * kSide + tk * D;
                     char *dst = s_b + sb * kWideV + tk * 128;
                     const int sw = D == 128 ? tk & 7 : (tk >> 1) & 3;
-                    // New tokens may be NaN, which would become numbers here.
-                    if (__builtin_expect((t + 1) * kPxTile > pc.ctx, 0)) {
+                    // New tokens may be NaN, which rows that do not see them would get (0 times
+                    // NaN): cleared, as is what lies behind the last token.  In bf16 NaN would
+                    // become a number.
+                    if (__builtin_expect(bf || (t + 1) * kPxTile > pc.ctx, 0)) {
                         bool nan = false;
 #pragma unroll 1
                         for (int i = 0; i < D / 16; ++i) {
@@ -1248,26 +1309,33 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         }
                         const uint32_t m = __ballot_sync(0xFFFFFFFFu, nan);
                         if (lane == 0) sh->lost[sb][warp - kPxSoft] = m;
+#pragma unroll 1
+                        for (int i = 0; nan && i < D / 16; ++i)
+                            *reinterpret_cast<uint4 *>(src + (i << 4)) = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    auto bring = [&](auto convert) {
 #pragma unroll 2
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(src + ((i ^ sw) << 4));
-                        uint4 a, b;
-                        e4m3_to_bf16(w.x, up, a.x, a.y);
-                        e4m3_to_bf16(w.y, up, a.z, a.w);
-                        e4m3_to_bf16(w.z, up, b.x, b.y);
-                        e4m3_to_bf16(w.w, up, b.z, b.w);
-                        if (more != kOne) {     // a scale of 256 or more
-                            a.x = mul_bf16x2(a.x, more); a.y = mul_bf16x2(a.y, more);
-                            a.z = mul_bf16x2(a.z, more); a.w = mul_bf16x2(a.w, more);
-                            b.x = mul_bf16x2(b.x, more); b.y = mul_bf16x2(b.y, more);
-                            b.z = mul_bf16x2(b.z, more); b.w = mul_bf16x2(b.w, more);
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src + ((i ^ sw) << 4));
+                            uint4 a, b;
+                            convert(w.x, a.x, a.y);
+                            convert(w.y, a.z, a.w);
+                            convert(w.z, b.x, b.y);
+                            convert(w.w, b.z, b.w);
+                            char *at = dst + (i >> 2) * (kPxTile * 128);
+                            const int q = (i & 3) * 2;
+                            *reinterpret_cast<uint4 *>(at + ((q ^ (tk & 7)) << 4)) = a;
+                            *reinterpret_cast<uint4 *>(at + (((q + 1) ^ (tk & 7)) << 4)) = b;
                         }
-                        char *at = dst + (i >> 2) * (kPxTile * 128);
-                        const int q = (i & 3) * 2;
-                        *reinterpret_cast<uint4 *>(at + ((q ^ (tk & 7)) << 4)) = a;
-                        *reinterpret_cast<uint4 *>(at + (((q + 1) ^ (tk & 7)) << 4)) = b;
-                    }
+                    };
+                    if (__builtin_expect(!bf, 1))
+                        bring([&](uint32_t w, uint32_t &lo, uint32_t &hi) { e4m3_to_f16(w, up, lo, hi); });
+                    else
+                        bring([&](uint32_t w, uint32_t &lo, uint32_t &hi) {
+                            e4m3_to_bf16(w, up, lo, hi);
+                            lo = mul_bf16x2(lo, more);
+                            hi = mul_bf16x2(hi, more);
+                        });
                     fence_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -1315,6 +1383,9 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                 float ks, vs, nks, nvs;
                 window(w0, page, ks, vs);
                 window(w0 + 32, npage, nks, nvs);
+                // The piece's power of two: of the largest scale here.
+                auto power = [](float v) { return (int)(__float_as_uint(v) >> 23) - 127; };
+                const int unit = max(__reduce_max_sync(0xFFFFFFFFu, page >= 0 ? power(vs) : -64), -40);
                 for (int t = pc.t0; t < pc.t1; ++t, ++it) {
                     const int p0 = t * per_tile;
                     if (p0 >= w0 + 32) {
@@ -1346,13 +1417,16 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     if (mine) fetch(&map_k, s_k + sk * kSide + inner * j.block * D, &sh->full_k[sk]);
                     // (the tile that had these places is behind the scores of all
                     // but the last tiles)
+                    const int e = live ? power(vs) - unit : 0;
+                    const bool bf = __any_sync(0xFFFFFFFFu, mine && (e > kPxAbove || e < -kPxBelow));
+                    if (lane == 0) sh->kind[ring] = unit + 64 + (bf ? kPxApart : 0);
                     if (mine) {
-                        const uint32_t u = __float_as_uint(vs);
-                        const int e = (int)(u >> 23) - 127;
-                        const float f = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
-                        const float4 sc = live ? make_float4(ks, f == 1.f ? 0.f : log2f(f), 1.f / f, 0.f)
-                                               : make_float4(1.f, -INFINITY, 0.f, 0.f);
-                        const uint32_t up = (uint32_t)(127 + 120 + min(e, kPxTop)) << 7;  // bf16
+                        const float f = __uint_as_float((__float_as_uint(vs) & 0x7FFFFFu) | 0x3F800000u);
+                        const float lg = f == 1.f ? 0.f : log2f(f);
+                        const float4 sc = live ? make_float4(ks, bf ? INFINITY : lg, 1.f / f, lg)
+                                               : make_float4(1.f, -INFINITY, 0.f, -INFINITY);
+                        const uint32_t up = bf ? (uint32_t)(127 + 120 + min(e, kPxTop)) << 7
+                                               : (uint32_t)(15 + e) << 10;
                         const uint32_t more = (uint32_t)(127 + max(e - kPxTop, 0)) << 7;
                         for (int i = 0; i < j.block >> 4; ++i) {
                             sh->sc[ring][inner * (j.block >> 4) + i] = sc;
@@ -1382,8 +1456,9 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
             // descriptors lie in uniform registers; one thread issues.)
             constexpr uint32_t kSums = 1u << 4, kM = 128u >> 4 << 24;  // fp32 sums, M = 128
             constexpr uint32_t kIdS = kSums | (128u >> 3 << 17) | kM;
-            // bf16 both; B with its rows (tokens) as the products' dimension
-            constexpr uint32_t kIdO = kSums | 1u << 7 | 1u << 10 | 1u << 16 | ((uint32_t)D >> 3 << 17) | kM;
+            // fp16 both, or bf16; B with its rows (tokens) as the products' dimension
+            constexpr uint32_t kIdO = kSums | 1u << 16 | ((uint32_t)D >> 3 << 17) | kM;
+            constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;
             const int slot = __shfl_sync(0xFFFFFFFFu, warp - 13, 0);
             const uint32_t col = tmem + slot * 128;
             const uint64_t dk0 = tc_desc(smem_u32(s_k), 16, 8 * D, kSwz);
@@ -1404,8 +1479,10 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                     const uint32_t tn = t + step, st = tn % kPxK;
                     // (the weights last: from then on nothing is in the way)
                     if (next) ok = px_wait(sh, j.err, &sh->full_k[st], (tn / kPxK) & 1);
+                    uint32_t id = kIdO;
                     if (now) {
                         ok = ok && px_wait(sh, j.err, &sh->full_b[sb], (t >> 1) & 1);
+                        if (sh->kind[t % kPxRing] & kPxApart) id |= kBf16;
                         // the slots take turns: one's softmax runs under the other's
                         // products (side by side, both wait for the products, then the
                         // products for both; free to run, one gets a tile ahead and
@@ -1421,7 +1498,7 @@ prefix_kernel(const __grid_constant__ PrefixJob j, const __grid_constant__ CUten
                         const uint64_t db = db0 + sb * (kWideV >> 4);
 #pragma unroll
                         for (int k = 0; k < kPxTile / 16; ++k)
-                            tc_mma_ts(col + 256, col + 8 * k, db + 128 * k, kIdO, k || i >= step);
+                            tc_mma_ts(col + 256, col + 8 * k, db + 128 * k, id, k || i >= step);
                         tc_commit(&sh->pv_done[slot]);
                         // (both slots release a tile)
                         tc_commit(&sh->empty_b[sb]);

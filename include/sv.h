@@ -498,10 +498,12 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
  *   and prefix_len; they say where to look.  Groups that share nothing, and
  *   sequences of no group, are read each by itself.
  *   Precision: scores, maxima and sums are fp32, a query is held as there.  A
- *   weight is held to 2^-8 of itself; among a sequence's own tokens, and where
- *   little is shared, for up to 32 query rows a cache head to 2^-11, down to 2^-19
- *   of the row's largest product of a weight and a value scale.  Value scales may
- *   lie any distance apart.  The same call gives the same bits.
+ *   weight is held to 2^-11 of itself, down to 2^-19 of the row's largest product of
+ *   a weight and a value scale where the scales are alike, to 2^-10 where they lie
+ *   2^8 apart (and within 2^-21 of that product below).  128 tokens with a scale
+ *   more than 2^3 above or 2^5 below those at the start of their part of the work are
+ *   held to 2^-8 instead, at any size.  The same call gives the same bits.  A stored value that is NaN makes the rows that see it NaN in its
+ *   element at least, no others.
  *   Pages stand in several rows of the table then, which sv_kv_plan does not know:
  *   a sequence whose cached_len is the shared tokens' gives back what it holds
  *   beyond them, and with held set to 0 after that no longer the shared ones.
