@@ -63,6 +63,7 @@ struct sv_handle {
     int kv_n = 0, kv_next = 1;  // sets in use; the one that a further stream takes over
     cudaEvent_t ev[2] = {nullptr, nullptr};  // caller-owned (SV_OPT_TIMING_EVENTS)
     bool timing = false;
+    sv_status prefix = SV_OK;  // what sv_kv_prefix_attention answers: its own setup's
     std::mutex mu;
 };
 
@@ -508,8 +509,13 @@ sv_status sv_create(sv_handle **out)
     if (e == cudaSuccess) e = plan_setup();
     if (e == cudaSuccess) e = rows_setup();
     if (e == cudaSuccess) e = attend_setup();
-    if (e == cudaSuccess) e = prefix_setup();
-    if (e == cudaSuccess) e = tail_setup();
+    // (kernels that cannot run as they were compiled are refused there, not here)
+    h->prefix = fault_injected("sv_kv_prefix_setup");
+    if (e == cudaSuccess && h->prefix == SV_OK &&
+        (prefix_setup() != cudaSuccess || tail_setup() != cudaSuccess)) {
+        h->prefix = SV_ERR_UNSUPPORTED;
+        cudaGetLastError();
+    }
     if (e == cudaSuccess) e = cudaMalloc(&h->d_err, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_ctl, C_NCTL * sizeof(unsigned));
     if (e == cudaSuccess) e = cudaMalloc(&h->d_gtab, kGTab * sizeof(float));
@@ -1107,6 +1113,7 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
     if (work_bytes < w.bytes) return SV_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_prefix_attention")) return fi;
+    if (h->prefix != SV_OK) return h->prefix;
     cudaStream_t s = (cudaStream_t)stream;
     char *ws = (char *)work;
     int32_t *seq = (int32_t *)(ws + w.seq);

@@ -53,7 +53,8 @@
  *   sv_kv_prefix_attention, sv_kv_read, sv_qk_norm_rope, sv_sample_rows)
  *   return the status `code` (1..6) at its launch point,
  *   after its argument checks and before anything is enqueued.  It is read
- *   at every call; unset, nothing is injected.
+ *   at every call; unset, nothing is injected.  (sv_kv_prefix_setup, read by
+ *   sv_create: what sv_kv_prefix_attention answers on that handle.)
  */
 #ifndef SV_H
 #define SV_H
@@ -512,7 +513,8 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
  *     refuses).  Its content is of no consequence before and after; calls that
  *     may run at the same time, captured ones among them, need one each.
  * Errors: SV_ERR_INVALID_ARG (too small a workspace among them);
- * SV_ERR_UNSUPPORTED (D; sizes beyond 32 bits); latched SV_ERR_DEVICE_BOUNDS as
+ * SV_ERR_UNSUPPORTED (D; sizes beyond 32 bits; kernels compiled with other
+ * registers than they share out, in a debug build, say); latched SV_ERR_DEVICE_BOUNDS as
  * sv_kv_attention, for groups out of order or range (nothing is shared then),
  * and for cu_new out of order (no row is meaningful then).
  * ------------------------------------------------------------------------- */
