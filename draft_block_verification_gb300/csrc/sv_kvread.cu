@@ -26,6 +26,20 @@ __device__ __forceinline__ float2 e4m3_pair(uint32_t v)
     return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
 
+// A value times its scale, to be rounded to bf16.  Up to 4 times 24 bits: rounded to fp32
+// before, as it is where the scale has all of its bits, a product beside the middle of two
+// steps would fall into it.  So it is rounded to odd there: cut off, and the last bit set
+// where something was.
+__device__ __forceinline__ bool whole_products(float scale)
+{
+    return (__float_as_uint(scale) & 15u) == 0;
+}
+__device__ __forceinline__ float odd_product(float v, float scale)
+{
+    const float p = __fmul_rz(v, scale);
+    return __uint_as_float(__float_as_uint(p) | (fmaf(v, scale, -p) != 0.f ? 1u : 0u));
+}
+
 template <bool F32>
 __device__ __forceinline__ void put(char *dst, uint2 raw, float scale)
 {
@@ -35,12 +49,20 @@ __device__ __forceinline__ void put(char *dst, uint2 raw, float scale)
                make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale));
     } else {
         const float2 c = e4m3_pair(raw.y & 0xFFFFu), d = e4m3_pair(raw.y >> 16);
-        auto two = [&](float2 v) {
+        auto two = [](float x, float y) {
             uint32_t r;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y * scale), "f"(v.x * scale));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
             return r;
         };
-        __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(two(a), two(b), two(c), two(d)));
+        uint4 o;
+        if (__builtin_expect(whole_products(scale), 1)) {
+            o = make_uint4(two(a.x * scale, a.y * scale), two(b.x * scale, b.y * scale),
+                           two(c.x * scale, c.y * scale), two(d.x * scale, d.y * scale));
+        } else {
+            auto odd = [&](float2 v) { return two(odd_product(v.x, scale), odd_product(v.y, scale)); };
+            o = make_uint4(odd(a), odd(b), odd(c), odd(d));
+        }
+        __stcs(reinterpret_cast<uint4 *>(dst), o);
     }
 }
 
@@ -125,12 +147,12 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadJob j, int
 #pragma unroll
                     for (int q = 0; q < kElems; ++q) {
                         const uint32_t b = ((q < 4 ? raw[k][n].x : raw[k][n].y) >> (8 * (q & 3))) & 255;
-                        const float v = e4m3_pair(b).x * sc[k][n];
+                        const float a = e4m3_pair(b).x, s = sc[k][n];
                         if (F32)
-                            reinterpret_cast<float *>(dst)[q] = v;
+                            reinterpret_cast<float *>(dst)[q] = a * s;
                         else
-                            reinterpret_cast<uint16_t *>(dst)[q] =
-                                __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                            reinterpret_cast<uint16_t *>(dst)[q] = __bfloat16_as_ushort(
+                                __float2bfloat16_rn(whole_products(s) ? a * s : odd_product(a, s)));
                     }
                 }
             }
