@@ -13,7 +13,6 @@ from __future__ import annotations
 
 import atexit
 import ctypes as C
-import functools
 import os
 import sys
 import threading
@@ -243,34 +242,31 @@ def _tensors(x):
             yield from _tensors(y)
 
 
-def _on_stream(call):
-    """A call with stream= runs with that stream as torch's current one: what it
-    allocates comes from that stream's memory, not from blocks that work queued on the
-    current stream may still use.  Results may be used and freed on the current stream
-    as before."""
-    @functools.wraps(call)
-    def on(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        dev = next((t.device for t in _tensors((args, kw)) if t.is_cuda), None)
-        if dev is None:
-            return call(*args, **kw)              # (refused)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
-        now = torch.cuda.current_stream(dev)
-        with torch.cuda.stream(stream):
-            out = call(*args, **kw)
-        if now.cuda_stream != stream.cuda_stream:
-            for t in _tensors(out):
-                t.record_stream(now)
-        return out
-    return on
+def _on_stream(stream, call, given):
+    """A call with stream=, `given` its arguments: runs with that stream as torch's
+    current one.  What it allocates comes from that stream's memory, not from blocks that
+    work queued on the current stream may still use.  Results may be used and freed on the
+    current stream as before."""
+    given = dict(given, stream=None)
+    dev = next((t.device for t in _tensors(given) if t.is_cuda), None)
+    if dev is None:
+        return call(**given)                      # (refused)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=dev)
+    now = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        out = call(**given)
+    if now.cuda_stream != stream.cuda_stream:
+        for t in _tensors(out):
+            t.record_stream(now)
+    return out
 
 
-@_on_stream
 def sv_verify_greedy(target, draft_ids, draft_len=None, *, handle=None, stream=None,
                      accept_len=None, next_token=None):
     """Greedy verification; target [B, K+1, V]; returns (accept_len, next_token)."""
+    if stream is not None:
+        return _on_stream(stream, sv_verify_greedy, locals())
     B, K1, V = target.shape
     K = K1 - 1
     dev = target.device
@@ -285,7 +281,6 @@ def sv_verify_greedy(target, draft_ids, draft_len=None, *, handle=None, stream=N
     return acc, nxt
 
 
-@_on_stream
 def sv_verify_greedy_static(target, draft_ids, draft_len=None, *, stream=None, accept_len=None,
                             next_token=None, status=None):
     """Greedy verification with the library's fixed scratch (no device
@@ -293,6 +288,8 @@ def sv_verify_greedy_static(target, draft_ids, draft_len=None, *, stream=None, a
     status); status[0] holds the first device-side error of the call, 0 if
     none.  Pass preallocated outputs to keep the call free of allocations on
     the Python side as well."""
+    if stream is not None:
+        return _on_stream(stream, sv_verify_greedy_static, locals())
     B, K1, V = target.shape
     K = K1 - 1
     dev = target.device
@@ -308,12 +305,13 @@ def sv_verify_greedy_static(target, draft_ids, draft_len=None, *, stream=None, a
     return acc, nxt, st
 
 
-@_on_stream
 def sv_verify_sample(target, draft, draft_ids, draft_len=None, *, T_p=1.0, T_q=1.0,
                      mode=SV_LOSSLESS, lam=1.0, seed=0, pos_base=None, want_rows=True,
                      want_tv=False, handle=None, stream=None):
     """Lossless / lenient speculative sampling; target [B, K+1, V], draft [B, K, V].
     Returns a dict of output tensors (see sv.h)."""
+    if stream is not None:
+        return _on_stream(stream, sv_verify_sample, locals())
     B, K1, V = target.shape
     K = K1 - 1
     dev = target.device
@@ -345,10 +343,11 @@ def sv_verify_sample(target, draft, draft_ids, draft_len=None, *, T_p=1.0, T_q=1
     return out
 
 
-@_on_stream
 def sv_verify_tree(node_logits, parent, node_pos, node_tok, *, T=0.0, seed=0, pos_base=None,
                    max_depth=None, handle=None, stream=None):
     """Coupled-noise tree verification; node_logits [B, N, V]."""
+    if stream is not None:
+        return _on_stream(stream, sv_verify_tree, locals())
     B, N, V = node_logits.shape
     dev = node_logits.device
     code, rs = _rows(node_logits, "node_logits")
@@ -370,12 +369,13 @@ def sv_verify_tree(node_logits, parent, node_pos, node_tok, *, T=0.0, seed=0, po
     return out
 
 
-@_on_stream
 def sv_verify_spot(state_logits, parent, node_pos, node_tok, root_mask, *, T=0.0, seed=0,
                    pos_base=None, max_depth=None, handle=None, stream=None):
     """SPOT verification with the target's position selection (see sv.h):
     state_logits [B, 1+N, L, V]; parent/node_pos/node_tok [B, N] int32;
     root_mask [B] int64 (bit s: position s is masked in the root state)."""
+    if stream is not None:
+        return _on_stream(stream, sv_verify_spot, locals())
     B, S, L, V = state_logits.shape
     N = S - 1
     dev = state_logits.device
@@ -403,11 +403,12 @@ def sv_verify_spot(state_logits, parent, node_pos, node_tok, root_mask, *, T=0.0
     return out
 
 
-@_on_stream
 def sv_packed_anyorder_step(logits, Kv, W, u, win_pos, order, draft, end_pos, *, eos_id=-1,
                             handle=None, stream=None):
     """One any-order Packed-SS iteration (see sv.h); logits [B, Kv + W, V];
     u, end_pos [B]; win_pos, order, draft [B, W] (int32 CUDA tensors)."""
+    if stream is not None:
+        return _on_stream(stream, sv_packed_anyorder_step, locals())
     B, R, V = logits.shape
     if R != Kv + W:
         raise ValueError("logits must be [B, Kv + W, V]")
@@ -429,11 +430,12 @@ def sv_packed_anyorder_step(logits, Kv, W, u, win_pos, order, draft, end_pos, *,
     return out
 
 
-@_on_stream
 def sv_packed_step(logits, K, W, prev_draft, prev_len, *, prev_q_at_draft=None,
                    prev_draft_logits=None, prev_q_offset=None, T=0.0, seed=0, it=0,
                    pos_base=None, eos_id=-1, remaining=None, handle=None, stream=None):
     """One Packed-SS iteration; logits [B, K+W, V]."""
+    if stream is not None:
+        return _on_stream(stream, sv_packed_step, locals())
     B, R, V = logits.shape
     if R != K + W:
         raise ValueError("logits must be [B, K+W, V]")
@@ -469,13 +471,14 @@ def sv_packed_step(logits, K, W, prev_draft, prev_len, *, prev_q_at_draft=None,
     return out
 
 
-@_on_stream
 def sv_packed_topk_step(logits, K, W, kp, kq, prev_draft, prev_len, prev_q_ids, prev_q_probs,
                         prev_q_offset, *, T=1.0, seed=0, it=0, pos_base=None, eos_id=-1,
                         remaining=None, handle=None, stream=None):
     """One Packed-SS iteration with top-k truncated target (kp) and drafter
     (kq) distributions; logits [B, K+W, V]; the previous call's drafter lists
     prev_q_ids / prev_q_probs [B, W, kq] (int32 / float32)."""
+    if stream is not None:
+        return _on_stream(stream, sv_packed_topk_step, locals())
     B, R, V = logits.shape
     if R != K + W:
         raise ValueError("logits must be [B, K+W, V]")
@@ -537,13 +540,14 @@ def _call_on(handle, stream, dev):
     return handle.ptr, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-@_on_stream
 def sv_kv_plan(cached_len, new_len, held, table, free_ids, free_pos, block, max_tokens, *,
                handle=None, stream=None):
     """Places of new tokens in the paged cache (see sv.h): cached_len, new_len,
     held [B] and table [B, cols], free_ids [ring] int32; free_pos [2] int64.
     Updates table and free_ids in place and returns a dict of new tensors
     (kv_len, cu_new, held, free_pos, slot, pos)."""
+    if stream is not None:
+        return _on_stream(stream, sv_kv_plan, locals())
     dev = _cuda(cached_len, "cached_len")
     i32, empty = torch.int32, torch.empty
     B, cap = cached_len.shape[0], int(max_tokens)
@@ -582,11 +586,12 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev):
                    _dense(v_scale, torch.float32, shape[:2], "v_scale", dev))
 
 
-@_on_stream
 def sv_kv_append(k, v, slot, k_cache, v_cache, k_scale, v_scale, *, handle=None, stream=None):
     """Write k, v [T, Hkv, D] (float32 or bfloat16) to the cache's slots
     slot [T] int32 in place (see sv.h); caches [pages, Hkv, block, D]
     float8_e4m3fn, scales [pages, Hkv] float32."""
+    if stream is not None:
+        return _on_stream(stream, sv_kv_append, locals())
     dev = _cuda(k, "k")
     (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     T = k.shape[0]
@@ -604,13 +609,14 @@ def sv_kv_append(k, v, slot, k_cache, v_cache, k_scale, v_scale, *, handle=None,
         "sv_kv_append")
 
 
-@_on_stream
 def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new, *, scale=None,
                     mask=None, want_lse=False, handle=None, stream=None):
     """Attention of the new tokens' queries q [T, Hq, D] (bfloat16) over the
     paged cache (see sv.h); table [B, cols], kv_len [B], cu_new [B + 1] int32;
     mask [T, words] int32 bits over the sequence's new tokens, or None for
     causal.  scale defaults to D ** -0.5.  Returns a dict (out, and lse)."""
+    if stream is not None:
+        return _on_stream(stream, sv_kv_attention, locals())
     dev = _cuda(q, "q")
     (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
@@ -641,7 +647,6 @@ def sv_kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new
     return out
 
 
-@_on_stream
 def sv_kv_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_new,
                            prefix_len=None, *, cu_group=None, scale=None, mask=None,
                            want_lse=False, handle=None, stream=None):
@@ -650,6 +655,8 @@ def sv_kv_prefix_attention(q, k_cache, v_cache, k_scale, v_scale, table, kv_len,
     ([groups + 1] int32; None: all) share at most their first prefix_len[g]
     tokens ([groups] int32; None: as far as their tables agree).  Returns a
     dict (out, and lse)."""
+    if stream is not None:
+        return _on_stream(stream, sv_kv_prefix_attention, locals())
     dev = _cuda(q, "q")
     (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     if q.dim() != 3 or q.shape[2] != D or q.dtype != torch.bfloat16 or q.stride(2) != 1:
@@ -699,13 +706,14 @@ def _rows_out(t, shape, dtype, dev, name):
     return t
 
 
-@_on_stream
 def sv_kv_read(k_cache, v_cache, k_scale, v_scale, table, cu, rows, *, first=None,
                dtype=torch.bfloat16, out=None, handle=None, stream=None):
     """Tokens read back from the paged cache (see sv.h): rows cu[b] .. cu[b + 1]
     - 1 ([B + 1] int32) are positions first[b] on of sequence b (None: 0), in
     bfloat16 or float32.  rows: the outputs' rows; out: (k, v) [rows, Hkv, D] to
     write to.  Returns a dict (k, v); rows from cu[B] on are not written."""
+    if stream is not None:
+        return _on_stream(stream, sv_kv_read, locals())
     dev = _cuda(k_cache, "k_cache")
     (pages, H, block, D), cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     if table.dim() != 2:
@@ -733,7 +741,6 @@ def sv_kv_read(k_cache, v_cache, k_scale, v_scale, table, cu, rows, *, first=Non
     return {"k": k, "v": v}
 
 
-@_on_stream
 def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
                     interleaved=False, dtype=None, out=None, handle=None, stream=None):
     """Norms of queries and keys for each head, and the rotation by position, in
@@ -742,6 +749,8 @@ def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e
     [rot / 2] float32 (None: no rotation), weights [D] float32 (None: no norm).
     dtype: of the outputs (None: the inputs'); out: (q, k) to write to, which may
     be the inputs.  Returns a dict (q, k)."""
+    if stream is not None:
+        return _on_stream(stream, sv_qk_norm_rope, locals())
     x = k if q is None else q
     dev = _cuda(x, "k" if q is None else "q")
     given = x.dtype
@@ -792,12 +801,13 @@ def sv_qk_norm_rope(q, k, pos, inv_freq, *, q_weight=None, k_weight=None, eps=1e
     return {"q": y, "k": z}
 
 
-@_on_stream
 def sv_sample_rows(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None,
                    handle=None, stream=None):
     """One draw from each row of logits [R, V] with the filters of sv.h; u,
     temperature, top_p, min_p [R] float32 and top_k [R] int32 (None: off; for
     the temperature 1).  Returns a dict (token, prob, kept)."""
+    if stream is not None:
+        return _on_stream(stream, sv_sample_rows, locals())
     dev = _cuda(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [R, V]")
