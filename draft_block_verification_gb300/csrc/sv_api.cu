@@ -1105,11 +1105,12 @@ sv_status sv_kv_prefix_attention(sv_handle *h, const void *q, int64_t q_token_st
     if (!kv_cache_ok(k_cache, k_scale) || !kv_cache_ok(v_cache, v_scale))
         return SV_ERR_INVALID_ARG;
     if (T == 0 || B == 0) return SV_OK;
+    // (before the workspace: there is no size for these)
+    const PrefixSpace w(h->sms, T, Hq, H, D, B, groups);
+    if (!prefix_fits(T, Hq, B, groups, w)) return SV_ERR_UNSUPPORTED;
     if (!q || !table || !kv_len || !cu_new || !out || (uintptr_t)q % 2 || !aligned16(out) ||
         !work || !aligned16(work))
         return SV_ERR_INVALID_ARG;
-    const PrefixSpace w(h->sms, T, Hq, H, D, B, groups);
-    if (!prefix_fits(T, Hq, B, groups, w)) return SV_ERR_UNSUPPORTED;
     if (work_bytes < w.bytes) return SV_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(h->mu);
     if (sv_status fi = fault_injected("sv_kv_prefix_attention")) return fi;
