@@ -11,8 +11,9 @@
 // Angles.  What counts is the fraction of a turn: p * (inv_freq / 2 pi) mod 1.
 // inv_freq / 2 pi mod 1 is held as a 64-bit fraction, taken from the float's 24
 // bits times 65 bits of 1 / 2 pi, so that a 64-bit product with the position
-// wraps by itself: for |inv_freq| < 2 the angle is right to 2^-32 of a turn at
-// any position, where an fp32 product would be off by p 2^-25 turns.
+// wraps by itself: for |inv_freq| < 2 the fraction is right to 2^-32 of a turn at
+// any position, where an fp32 product would be off by p 2^-25 turns.  It is rounded
+// to fp32 once, in half turns: 2^-26 of a turn.
 //
 // Bound by DRAM.  A head is D / 16 threads, each with two vectors of eight
 // elements: the two halves of its pairs, so that the rotation needs no

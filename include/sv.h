@@ -558,8 +558,8 @@ sv_status sv_kv_read(sv_handle *h, const void *k_cache, const void *v_cache,
  *     i < rot / 2, are turned by t = pos[token] inv_freq[i]:
  *     y_a = x'_a cos t - x'_b sin t,  y_b = x'_b cos t + x'_a sin t;
  *   elements from rot on (rot even, 0 to D) are x'.
- * In fp32, rounded once to the outputs' type; an angle is right to 2^-32 of a
- * turn for |inv_freq| < 2 at any position.  Squares are summed in fp32 and
+ * In fp32, rounded once to the outputs' type; an angle is right to 2^-26 of a
+ * turn (an fp32 of half turns) for |inv_freq| < 2 at any position.  Squares are summed in fp32 and
  * weights multiplied in first: elements and weights of a head with a norm lie
  * below 2^60.  NaN and infinities reach their pair, with a norm their head.
  * A token with a negative position is skipped (sv_kv_plan's padding).  An output
