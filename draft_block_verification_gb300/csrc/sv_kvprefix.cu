@@ -97,10 +97,12 @@ constexpr float kPxMark = -3e38f;      // stands for one of those: every weight 
 constexpr int kPrepCtas = 8, kPrepThreads = 512;
 
 // What little is shared the tail reads sooner for each sequence by itself: 16 tokens
-// of eight rows of a head take it about 2 ns in all, a run of the prefix kernel some
-// 15 us more than one without work.  (Four sequences of a token, 1,024 shared ones, 8
-// cache heads of 4 rows: 29 us against 33.)
-constexpr unsigned long long kPxLeast = 8192;
+// of eight rows of a head take it 1 to 2 ns in all, a run of the prefix kernel some
+// 15 us more than one without work, and the tail waits for it.  (Single tokens of 32
+// heads, 8 of the cache, as graphs: 16 to 64 behind 1,024 to 256 shared ones 35 to 37 us
+// against 45 to 47; behind twice as many 39 against 47 for 16, 57 against 49 for 64;
+// behind four times as many 48 against 55, and 72 against 51.)
+constexpr unsigned long long kPxLeast = 16384;
 
 // Row blocks of a head, and costs, in 400 cycles: a tile of up to 256 rows, one of up
 // to 128, and what a unit takes beside its tiles (queries, first scores, sums), which
@@ -367,7 +369,7 @@ prefix_prep_kernel(const PrefixJob j, int warps)
     if (warp != 0) return;
     // Rows of a unit.  A piece's sums are as many as its rows, whatever its tokens; so
     // where CTAs by far outnumber the units, units of half the rows halve what the
-    // tail has to read (128 single tokens of 32 heads: 88 us against 90; with as many
+    // tail has to read (128 single tokens of 32 heads: 107 us against 115; with as many
     // units as CTAs the halves would only have values converted twice).
     const int spans = j.groups + j.B;
     int big = 0, small = 0;
