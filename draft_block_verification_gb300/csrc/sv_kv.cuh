@@ -116,8 +116,7 @@ cudaError_t prefix_setup();
 cudaError_t prefix_prep_launch(const PrefixJob &j, int sms, cudaStream_t s);
 cudaError_t prefix_launch(const PrefixJob &j, int sms, cudaStream_t s);
 // Rows a cache head that the tail reads for, at most.  (64 draft blocks of 36 to 68 rows /
-// three long documents of 21 to 35, us: 32 245 / 437, 48 246 / 443, 64 243 / 441, 80 239 /
-// 443.  32 it is, for what a task's rows cost in its queries and sums.)
+// three long documents of 21 to 35, us: 32 239 / 409, 64 281 / 452.)
 constexpr int kTailMax = 32;
 constexpr int kTailTiles = 2;                                // eights of rows of a task
 constexpr int kTailTile = 32;                                // tokens of a stage

@@ -57,11 +57,11 @@
 //
 // What bounds it.  A slot's tile is a chain: its softmax (1,400 to 2,000 cycles), the
 // products with its weights, the next scores (1,024 of the tensor cores), and what
-// passes between them; two slots, which is what tensor memory holds, make it 3,400
-// cycles a tile of 256 rows at best, of which the tensor cores work 2,048.  A unit
-// takes some 18,000 beside its tiles.  64 sequences of 13 tokens of 32 heads behind
-// 8,192 shared ones and 330 of their own: 175 us of the call's 229; 24 of 4 behind
-// three prefixes of up to 131,072, D = 64: 335 of 387 us.
+// passes between them; two slots, which is what tensor memory holds at D = 128 (at 64 a
+// quarter of it is not used), make it 3,400 cycles a tile of 256 rows at best, of which
+// the tensor cores work 2,048.  A unit takes some 18,000 beside its tiles.  64 sequences
+// of 13 tokens of 32 heads behind 8,192 shared ones and 330 of their own: 180 us of the
+// call's 238; 24 of 4 behind three prefixes of up to 131,072, D = 64: 344 of 409 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -106,9 +106,8 @@ constexpr unsigned long long kPxLeast = 16384;
 
 // Row blocks of a head, and costs, in 400 cycles: a tile of up to 256 rows, one of up
 // to 128, and what a unit takes beside its tiles (queries, first scores, sums), which
-// is counted at its front.  (64 draft blocks / three long documents: with units at a
-// tenth of that 448 / 624 us, at 36 to 56 228 / 387; narrow tiles at half of wide ones
-// 248 / 430 with small units cut, at 6 230 / 398.)
+// is counted at its front.  (64 draft blocks / three long documents: 239 / 409 us; units
+// at a ninth of that 239 / 535, narrow tiles at 6 241 / 418.)
 constexpr int kPxWide = 9, kPxNarrow = 5, kPxUnitCost = 45;
 constexpr int kPxWhole = 130;          // of a unit that is not cut (90 to 250: equal)
 struct RowBlocks {
@@ -318,8 +317,8 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         many += s_sum[w].y;
     }
     __syncthreads();
-    // a task a warp, of 128 tokens at least (four sequences of 1,024: 28 us a call; of
-    // 192 30, of 256 34); where there are about as many as warps
+    // a task a warp, of 128 tokens at least (four sequences of 1,024, as a graph: 33 us;
+    // of 192 35, of 256 39); where there are about as many as warps
     // before any is cut, only those of twice the mean
     const long long mean = (all + warps - 1) / warps;
     const int c = (int)max(4LL, 2 * many >= warps ? 2 * mean : mean);
@@ -443,8 +442,8 @@ prefix_prep_kernel(const PrefixJob j, int warps)
         r.loose0 = loose;
         // A unit's pieces are added one after the other, 0.7 us each (what 3.25 of cost
         // take): beyond sqrt(cost / 3.25) of them that takes longer than a piece saves.
-        // (One unit of 36 rows over 38,272 tokens: 65 us, in 152 pieces 136;
-        // over 131,072 89 and 165.)
+        // (One unit of 36 rows over 38,272 tokens: 81 us, in 152 pieces 154;
+        // over 131,072 104 and 178.)
         const long long least = max(1LL, (long long)sqrtf(3.25f * most));
         r.rows = (int)min((long long)j.prefix_ctas, max(1LL, at / least));
         j.span[spans] = r;

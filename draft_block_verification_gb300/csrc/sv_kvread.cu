@@ -8,8 +8,8 @@
 // stores of a warp are whole lines; it has the keys' and the values' loads of
 // kAhead items in flight.  A CTA takes a run of rows and looks up where they
 // lie once, a thread for each row.  506 MB of reads and writes (82,000 tokens of
-// 8 x 128 to bf16) take 79 us, 94 % of the rate of a copy; 17 tokens, as a graph,
-// 2.0 us.
+// 8 x 128 to bf16) take 81 us, 93 % of the rate of a copy (131,072 tokens 112 us as a
+// graph; with scales that need odd_product a fifth more); 17 tokens, as a graph, 2.1 us.
 #include "sv_common.cuh"
 #include "sv_kv.cuh"
 
@@ -67,7 +67,7 @@ __device__ __forceinline__ void put(char *dst, uint2 raw, float scale)
 }
 
 // VEC: output rows start on 16 bytes.  (Else elements are stored one by one: 131,072
-// tokens of 8 x 128 to bf16 take 557 us, with VEC 107.)
+// tokens of 8 x 128 to bf16 take 568 us, with VEC 112.)
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadJob j, int rows)
 {

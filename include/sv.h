@@ -493,6 +493,11 @@ sv_status sv_kv_attention(sv_handle *h, const void *q, int64_t q_token_stride,
  *     group (in order, each in one group at most), or NULL (groups = 1): all.
  *   prefix_len [groups]: a group shares its first prefix_len[g] tokens at most,
  *     or NULL: no bound.
+ *   (It pays where many rows stand behind what is shared: with 32 heads, 8 of the
+ *   cache, of 128, 128 single tokens behind 64 shared ones take 56 us against
+ *   sv_kv_attention's 88, behind 8,192 107 against 318; 64 blocks of 17 drafts
+ *   behind 512 104 against 105, behind 8,192 243 against 330.  4 to 16 single tokens
+ *   are quicker there, 33 us against 27 behind 1,024.)
  *   Shared are the leading pages that the table has alike for all sequences of
  *   the group with new tokens, wholly within prefix_len[g] and within the tokens
  *   before each sequence's new ones.  So the result does not depend on cu_group
