@@ -840,19 +840,19 @@ __device__ __forceinline__ bool px_far(float M) { return fabsf(M) >= kPxFar && M
 
 // A tile whose value scales lie apart (bf: values and weights are bf16), or of rows whose
 // maxima are far from 0, from its half `q` on, 16 scores at a time (what runs seldom is
-// short).  A score s u is not rounded before M is taken from it,
-// which is right while M's own steps are small.  Beyond kPxFar it is rounded first, as M
-// has been: the difference of a maximum from itself would else be anything within half
-// a step (16 at 2^28).  sees, lost: as below, null where all tokens count.
+// short).  A score s u is not rounded before M is taken from it, which is right while M's
+// own steps are small.  Beyond kPxFar it is rounded first, as M has been: the difference
+// of a maximum from itself would else be anything within half a step (16 at 2^28).
+// sees, lost: as below, null where all tokens count.
 struct PxRow {
     float M, l;
     bool ok;
 };
 template <int D>
 __device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_at, uint32_t o_at,
-                                          uint64_t *pv_done, uint32_t count, bool first, int q,
-                                          const float4 *sc, bool bf, float c, float M, float l,
-                                          const uint32_t *sees, const uint32_t *lost)
+                                             uint64_t *pv_done, uint32_t count, bool first, int q,
+                                             const float4 *sc, bool bf, float c, float M, float l,
+                                             const uint32_t *sees, const uint32_t *lost)
 {
     bool ok = true;
 #pragma unroll 1
@@ -956,7 +956,7 @@ __device__ __forceinline__ PxRow px_soft_far(PxShared *sh, int *err, uint32_t s_
 // taken against the maximum in use before it is known whether one passes it by too
 // much; where one does, M moves, what there is of the row (sums, values, the tile's
 // first 64 weights) is scaled by the power of two, and the 64 weights are taken once
-// more, which is the last time: they do not pass the new M by 2^2.
+// more, which is the last time: they do not pass 2^(kPxUnit + 1) against the new M.
 // Returns the half from which on a row's maximum is far from 0 (px_soft_far's), or 2.
 // same: pages of 64 tokens or more, one scale for the 64.  EDGE: only the tokens of
 // `sees` count, and those of `lost` are NaN.
